@@ -41,6 +41,11 @@ GPTQ_Q4_FORMAT_GPTQ_V2 = 1
 GPTQ_Q4_DTYPE_FP16 = 0
 GPTQ_Q4_DTYPE_BF16 = 1
 GPTQ_Q4_DTYPE_FP32 = 2
+GPTQ_Q4_ROPE_PLAIN = 0
+GPTQ_Q4_ROPE_LINEAR = 1
+GPTQ_Q4_ROPE_NTK = 2
+GPTQ_Q4_ROPE_BANDS = 3
+GPTQ_Q4_ROPE_YARN = 4
 
 EXPORTED = [
     "gptq_q4_make", "gptq_q4_set_bias", "gptq_q4_reserve", "gptq_q4_matmul", "gptq_q4_dequant",
@@ -49,10 +54,28 @@ EXPORTED = [
     "gptq_q4_last_status", "gptq_q4_last_error", "gptq_q4_launch_count", "gptq_q4_matmul_noalloc",
     "gptq_q4_set_format", "gptq_q4_debug_wait_probe", "gptq_q4_debug_prefill_plan", "gptq_q4_debug_dispatch", "gptq_q4_make_fused", "gptq_q4_pack",
     "gptq_q4_make8", "gptq_q4_set_act_dtype",
+    "gptq_q4_lora_make", "gptq_q4_lora_set", "gptq_q4_lora_reserve", "gptq_q4_lora_add", "gptq_q4_lora_device_error",
+    "gptq_q4_lora_free",
+    "gptq_q4_attn_make", "gptq_q4_rope_freqs", "gptq_q4_attn_set_rope", "gptq_q4_attn_append", "gptq_q4_attn_attend",
+    "gptq_q4_attn_device_error", "gptq_q4_attn_free",
 ]
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_D = ctypes.c_double
+
+
+class gptq_q4_cache(ctypes.Structure):
+    """One layer's keys and values (see include/gptq_q4.h)."""
+    _fields_ = [("k", _P), ("v", _P), ("pages", _I), ("page_stride", _L)]
+
+
+class gptq_q4_batch(ctypes.Structure):
+    """The requests of one step (see include/gptq_q4.h)."""
+    _fields_ = [("cu_q", _P), ("kv_len", _P), ("table", _P), ("table_stride", _L),
+                ("width", _I), ("batch", _I), ("tokens", _I), ("max_q", _I)]
+
 
 
 def _sig(name, restype, *argtypes):
@@ -87,6 +110,19 @@ _sig("gptq_q4_last_status", _I)
 _sig("gptq_q4_last_error", ctypes.c_char_p)
 _sig("gptq_q4_launch_count", ctypes.c_uint64)
 _sig("gptq_q4_matmul_noalloc", _I, _P, _P, _I, _P, _P)
+_sig("gptq_q4_lora_make", _P, _I, _I, _I, _I, _I)
+_sig("gptq_q4_lora_set", _I, _P, _I, _P, _P, _I, ctypes.c_float, _P)
+_sig("gptq_q4_lora_reserve", _I, _P, _I)
+_sig("gptq_q4_lora_add", _I, _P, _P, _L, _P, _I, _P, _L, _P, _L, _P)
+_sig("gptq_q4_lora_device_error", _I, _P)
+_sig("gptq_q4_lora_free", None, _P)
+_sig("gptq_q4_attn_make", _P, _I, _I, _I, _I, _I)
+_sig("gptq_q4_rope_freqs", _I, _I, _D, _I, _D, _D, _D, _I, _P, _P)
+_sig("gptq_q4_attn_set_rope", _I, _P, _I, _I, _P, _D, _I)
+_sig("gptq_q4_attn_append", _I, _P, _P, _L, _P, _P, _P, _P, _L, _P)
+_sig("gptq_q4_attn_attend", _I, _P, _P, _L, _P, _P, ctypes.c_float, _I, _P, _L, _P)
+_sig("gptq_q4_attn_device_error", _I, _P)
+_sig("gptq_q4_attn_free", None, _P)
 
 GPTQ_Q4_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -260,6 +296,79 @@ def gptq_q4_matmul_noalloc(h: int, x: int, M: int, out: int, stream: int) -> int
     return _check(_lib.gptq_q4_matmul_noalloc(h, x or None, M, out or None, stream or None))
 
 
+def gptq_q4_lora_make(K: int, N: int, slots: int, max_rank: int, dtype: int) -> int:
+    h = _lib.gptq_q4_lora_make(K, N, slots, max_rank, dtype)
+    if not h:
+        raise GPTQ4Error(gptq_q4_last_status(), gptq_q4_last_error())
+    return h
+
+
+def gptq_q4_lora_set(h: int, slot: int, a: int | None, b: int | None, rank: int, scale: float, stream: int) -> int:
+    return _check(_lib.gptq_q4_lora_set(h, slot, a or None, b or None, rank, scale, stream or None))
+
+
+def gptq_q4_lora_reserve(h: int, max_m: int) -> int:
+    return _check(_lib.gptq_q4_lora_reserve(h, max_m))
+
+
+def gptq_q4_lora_add(h: int, x: int, x_stride: int, row_slot: int, M: int, y: int, y_stride: int, out: int,
+                     out_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_lora_add(h, x, x_stride, row_slot, M, y, y_stride, out, out_stride, stream))
+
+
+def gptq_q4_lora_device_error(h: int) -> int:
+    return _check(_lib.gptq_q4_lora_device_error(h))
+
+
+def gptq_q4_lora_free(h: int | None) -> None:
+    if h:
+        _lib.gptq_q4_lora_free(h)
+
+
+def gptq_q4_attn_make(q_heads: int, kv_heads: int, head_dim: int, page_size: int, dtype: int) -> int:
+    h = _lib.gptq_q4_attn_make(q_heads, kv_heads, head_dim, page_size, dtype)
+    if not h:
+        raise GPTQ4Error(gptq_q4_last_status(), gptq_q4_last_error())
+    return h
+
+
+def gptq_q4_rope_freqs(rotary_dim: int, base: float, kind: int, factor: float = 1.0, low: float = 1.0,
+                       high: float = 4.0, original: int = 1):
+    """(angles per position of each pair, length scale) for gptq_q4_attn_set_rope."""
+    f = (_D * max(1, rotary_dim // 2))()
+    scale = _D()
+    _check(_lib.gptq_q4_rope_freqs(rotary_dim, base, kind, factor, low, high, original, f, ctypes.byref(scale)))
+    return list(f), scale.value
+
+
+def gptq_q4_attn_set_rope(h: int, rotary_dim: int, interleaved: int, inv_freq, length_scale: float,
+                          max_pos: int) -> int:
+    """inv_freq: rotary_dim / 2 floats, or None with rotary_dim 0."""
+    f = None if inv_freq is None else (_D * max(1, len(inv_freq)))(*inv_freq)
+    return _check(_lib.gptq_q4_attn_set_rope(h, rotary_dim, interleaved, f, length_scale, max_pos))
+
+
+def gptq_q4_attn_append(h: int, qkv: int, qkv_stride: int, cache: gptq_q4_cache, batch: gptq_q4_batch,
+                        positions: int | None, q_out: int, q_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_append(h, qkv, qkv_stride, ctypes.byref(cache), ctypes.byref(batch), positions,
+                                           q_out, q_stride, stream))
+
+
+def gptq_q4_attn_attend(h: int, q: int, q_stride: int, cache: gptq_q4_cache, batch: gptq_q4_batch, scale: float,
+                        window: int, out: int, out_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_attend(h, q, q_stride, ctypes.byref(cache), ctypes.byref(batch), scale, window,
+                                           out, out_stride, stream))
+
+
+def gptq_q4_attn_device_error(h: int) -> int:
+    return _check(_lib.gptq_q4_attn_device_error(h))
+
+
+def gptq_q4_attn_free(h: int | None) -> None:
+    if h:
+        _lib.gptq_q4_attn_free(h)
+
+
 # --------------------------------------------------------- torch marshalling
 
 class Q4Matrix:
@@ -403,3 +512,16 @@ def gemm_f16(a, b, bias=None):
     gptq_q4_gemm_f16(a.data_ptr(), b.data_ptr(), None if bias is None else bias.data_ptr(), M, K, N,
                      out.data_ptr(), torch.cuda.current_stream().cuda_stream)
     return out
+
+
+# The operators around the projection; their modules need torch when imported.
+_LAZY = {"LoraPool": "adapters", "PagedAttention": "attention", "PagedBatch": "attention", "PagedCache": "attention"}
+
+
+def __getattr__(name):
+    if name in _LAZY:
+        import importlib
+        value = getattr(importlib.import_module(f"{__name__}.{_LAZY[name]}"), name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,105 @@
+"""Low-rank adapters of many requests beside a shared projection.
+
+``LoraPool`` marshals torch CUDA tensors to ``gptq_q4_lora_*`` (see
+include/gptq_q4.h); the library does the work and keeps its own copy of the
+adapters.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (GPTQ4Error, GPTQ_Q4_DTYPE_BF16, GPTQ_Q4_DTYPE_FP16, GPTQ_Q4_DTYPE_FP32, GPTQ_Q4_INVALID_ARGUMENT,
+               gptq_q4_lora_add, gptq_q4_lora_device_error, gptq_q4_lora_free, gptq_q4_lora_make,
+               gptq_q4_lora_reserve, gptq_q4_lora_set)
+
+_CODES = {torch.float16: GPTQ_Q4_DTYPE_FP16, torch.bfloat16: GPTQ_Q4_DTYPE_BF16, torch.float32: GPTQ_Q4_DTYPE_FP32}
+
+
+def _refuse(message: str):
+    raise GPTQ4Error(GPTQ_Q4_INVALID_ARGUMENT, message)
+
+
+def _code(dtype) -> int:
+    if dtype not in _CODES:
+        _refuse(f"dtype {dtype} is not float16 or bfloat16")
+    return _CODES[dtype]
+
+
+def _rows(t, what: str, width: int, dtype, device):
+    """`t` as rows of `width` elements, dense within a row: (tensor [rows, width], row stride)."""
+    if t.dtype != dtype or t.device != device:
+        _refuse(f"{what} is {t.dtype} on {t.device}: {dtype} on {device} is wanted")
+    if t.dim() != 2:
+        t = t.reshape(-1, width) if t.dim() else t.reshape(1, -1)
+    if t.shape[1] != width:
+        _refuse(f"{what} has rows of {t.shape[1]} elements: {width} are wanted")
+    if t.stride(1) != 1:
+        _refuse(f"{what} is not dense within its rows")
+    # one row, or none, has no stride of its own
+    return t, (t.stride(0) if t.shape[0] > 1 else max(width, t.stride(0)) // 8 * 8)
+
+
+class LoraPool:
+    """Up to `slots` adapters of one projection (K inputs, N outputs), each of
+    its own rank up to max_rank; float16 or bfloat16."""
+
+    def __init__(self, K: int, N: int, slots: int, max_rank: int, dtype=torch.float16):
+        self.handle = None
+        self.K, self.N, self.slots, self.max_rank, self.dtype = K, N, slots, max_rank, dtype
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.handle = gptq_q4_lora_make(K, N, slots, max_rank, _code(dtype))
+
+    def set(self, slot: int, a, b, scale: float = 1.0) -> None:
+        """Put an adapter into a slot: a [rank, K], b [N, rank]; the pool keeps a copy."""
+        if a.dim() != 2 or b.dim() != 2 or a.shape[1] != self.K or b.shape != (self.N, a.shape[0]):
+            _refuse(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [rank, {self.K}] and [{self.N}, rank]")
+        for t, what in ((a, "a"), (b, "b")):
+            if t.dtype != self.dtype or t.device != self.device:
+                _refuse(f"{what} is {t.dtype} on {t.device}: {self.dtype} on {self.device} is wanted")
+        a, b = a.contiguous(), b.contiguous()
+        gptq_q4_lora_set(self.handle, slot, a.data_ptr(), b.data_ptr(), a.shape[0], scale,
+                         torch.cuda.current_stream(self.device).cuda_stream)
+
+    def clear(self, slot: int) -> None:
+        gptq_q4_lora_set(self.handle, slot, None, None, 0, 0.0,
+                         torch.cuda.current_stream(self.device).cuda_stream)
+
+    def reserve(self, max_m: int) -> None:
+        gptq_q4_lora_reserve(self.handle, max_m)
+
+    def add(self, x, row_slot, y, out=None):
+        """y plus each row's adapter: x [.., K] is the projection's input, y
+        [.., N] its output, row_slot int32 [rows] each row's slot (negative:
+        none).  out=y adds in place; rows of x, y and out may be strided."""
+        shape = y.shape
+        x2, xs = _rows(x, "x", self.K, self.dtype, self.device)
+        y2, ys = _rows(y, "y", self.N, self.dtype, self.device)
+        M = x2.shape[0]
+        if out is None:
+            o2 = torch.empty((M, self.N), dtype=self.dtype, device=self.device)
+            os_ = self.N
+        else:
+            o2, os_ = _rows(out, "out", self.N, self.dtype, self.device)
+            if o2.data_ptr() != out.data_ptr():
+                _refuse("out cannot be viewed as rows")
+        if y2.shape[0] != M or o2.shape[0] != M or row_slot.numel() != M:
+            _refuse(f"x has {M} rows, y {y2.shape[0]}, out {o2.shape[0]}, row_slot {row_slot.numel()}")
+        if row_slot.dtype != torch.int32 or row_slot.device != self.device or not row_slot.is_contiguous():
+            _refuse(f"row_slot must be contiguous int32 on {self.device}")
+        gptq_q4_lora_add(self.handle, x2.data_ptr(), xs, row_slot.data_ptr(), M, y2.data_ptr(), ys, o2.data_ptr(),
+                         os_, torch.cuda.current_stream(self.device).cuda_stream)
+        return o2.view(shape) if out is None else out
+
+    def device_error(self) -> None:
+        gptq_q4_lora_device_error(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            gptq_q4_lora_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

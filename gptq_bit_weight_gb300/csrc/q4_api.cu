@@ -1024,4 +1024,14 @@ int api_check_matmul_args(gptq_q4_handle h, const void *x, int M, const void *ou
 }
 HandleView api_view(const gptq_q4_s *h) { return view(h); }
 void api_count_launches(int n) { g_launches += static_cast<uint64_t>(n); }
+int api_check_device_ptr(const void *p, int dev, const char *name) { return check_device_ptr(p, dev, name); }
+int api_check_device_sm103(int *dev_out) { return check_device_sm103(dev_out); }
+int api_failf(int code, const char *fmt, ...) {
+    t_status = code;
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_msg, sizeof(t_msg), fmt, ap);
+    va_end(ap);
+    return code;
+}
 }  // namespace q4

@@ -45,4 +45,7 @@ int api_cuda_fail(cudaError_t e, const char *what);
 int api_check_matmul_args(gptq_q4_handle h, const void *x, int M, const void *out);
 HandleView api_view(const gptq_q4_s *h);
 void api_count_launches(int n);
+int api_check_device_ptr(const void *p, int dev, const char *name);
+int api_check_device_sm103(int *dev_out);
+int api_failf(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 }  // namespace q4

@@ -1,0 +1,204 @@
+// C ABI of the adapter pool (gptq_q4_lora_*): argument checks, the pool's
+// memory and its workspace.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include "q4_handle.h"
+#include "q4_serve.h"
+
+struct gptq_q4_lora_s {
+    int device = -1;
+    int K = 0, N = 0, slots = 0, max_rank = 0, dtype = 0;
+    uint16_t *a = nullptr, *b = nullptr;
+    q4::LoraSlot *slot = nullptr;
+    int *status = nullptr;
+    float *t = nullptr;
+    size_t t_rows = 0;
+};
+
+namespace {
+
+using q4::api_cuda_fail;
+using q4::api_failf;
+using q4::api_set_status;
+
+int check(gptq_q4_lora h) {
+    if (!h) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "adapter pool is NULL");
+    int dev = -1;
+    if (cudaError_t e = cudaGetDevice(&dev)) return api_cuda_fail(e, "cudaGetDevice");
+    if (dev != h->device)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "the pool was made on device %d, current device is %d", h->device,
+                         dev);
+    return GPTQ_Q4_OK;
+}
+
+void release(gptq_q4_lora_s *h) {
+    if (!h) return;
+    int cur = -1;
+    cudaGetDevice(&cur);
+    if (h->device >= 0) cudaSetDevice(h->device);
+    cudaDeviceSynchronize();
+    cudaFree(h->a);
+    cudaFree(h->b);
+    cudaFree(h->slot);
+    cudaFree(h->status);
+    cudaFree(h->t);
+    if (cur >= 0) cudaSetDevice(cur);
+    delete h;
+}
+
+q4::LoraView view(const gptq_q4_lora_s *h) {
+    return q4::LoraView{h->K, h->N, h->slots, q4::ceil16(h->max_rank), h->a, h->b, h->slot, h->t, h->status};
+}
+
+int ensure_rows(gptq_q4_lora_s *h, size_t rows, cudaStream_t s, bool sync_alloc) {
+    if (rows <= h->t_rows) return GPTQ_Q4_OK;
+    if (h->t) {
+        if (cudaError_t e = sync_alloc ? cudaFree(h->t) : cudaFreeAsync(h->t, s))
+            return api_cuda_fail(e, "freeing the adapter workspace");
+        h->t = nullptr;
+        h->t_rows = 0;
+    }
+    void *p = nullptr;
+    const size_t bytes = rows * q4::ceil16(h->max_rank) * sizeof(float);
+    if (cudaError_t e = sync_alloc ? cudaMalloc(&p, bytes) : cudaMallocAsync(&p, bytes, s))
+        return api_cuda_fail(e, "allocating the adapter workspace");
+    h->t = static_cast<float *>(p);
+    h->t_rows = rows;
+    return GPTQ_Q4_OK;
+}
+
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype) {
+    if (K <= 0 || N <= 0 || K % 8 || N % 8) {
+        api_failf(GPTQ_Q4_INVALID_ARGUMENT, "K=%d and N=%d must be positive multiples of 8", K, N);
+        return nullptr;
+    }
+    if (slots < 1 || slots > 4096 || max_rank < 1 || max_rank > 256) {
+        api_failf(GPTQ_Q4_INVALID_ARGUMENT, "slots=%d must be in [1, 4096] and max_rank=%d in [1, 256]", slots,
+                  max_rank);
+        return nullptr;
+    }
+    if (dtype != GPTQ_Q4_DTYPE_FP16 && dtype != GPTQ_Q4_DTYPE_BF16) {
+        api_failf(dtype == GPTQ_Q4_DTYPE_FP32 ? GPTQ_Q4_UNSUPPORTED : GPTQ_Q4_INVALID_ARGUMENT,
+                  "dtype=%d: adapters are GPTQ_Q4_DTYPE_FP16 or GPTQ_Q4_DTYPE_BF16", dtype);
+        return nullptr;
+    }
+    int dev = -1;
+    if (q4::api_check_device_sm103(&dev)) return nullptr;
+    gptq_q4_lora_s *h = new (std::nothrow) gptq_q4_lora_s();
+    if (!h) {
+        api_failf(GPTQ_Q4_OUT_OF_MEMORY, "host allocation of the adapter pool failed");
+        return nullptr;
+    }
+    h->device = dev;
+    h->K = K;
+    h->N = N;
+    h->slots = slots;
+    h->max_rank = max_rank;
+    h->dtype = dtype;
+    const size_t each = static_cast<size_t>(slots) * q4::ceil16(max_rank) * 2;
+    cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&h->a), each * K);
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->b), each * N);
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->slot), slots * sizeof(q4::LoraSlot));
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->status), sizeof(int));
+    if (!e) e = cudaMemset(h->slot, 0, slots * sizeof(q4::LoraSlot));
+    if (!e) e = cudaMemset(h->status, 0, sizeof(int));
+    if (!e) e = cudaDeviceSynchronize();
+    if (e) {
+        api_cuda_fail(e, "allocating the adapter pool");
+        release(h);
+        return nullptr;
+    }
+    if (ensure_rows(h, 64, nullptr, true)) {
+        release(h);
+        return nullptr;
+    }
+    api_set_status(GPTQ_Q4_OK, nullptr);
+    return h;
+}
+
+int gptq_q4_lora_set(gptq_q4_lora h, int slot, const void *a, const void *b, int rank, float scale,
+                     cudaStream_t stream) {
+    if (int r = check(h)) return r;
+    if (slot < 0 || slot >= h->slots || rank < 0 || rank > h->max_rank)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "slot=%d must be in [0, %d) and rank=%d in [0, %d]", slot, h->slots,
+                         rank, h->max_rank);
+    if (!(rank ? a && b : !a && !b))
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "a and b must be given for a rank above 0, and NULL for rank 0");
+    if (!std::isfinite(scale)) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "scale is not finite");
+    if (rank) {
+        if (int r = q4::api_check_device_ptr(a, h->device, "a")) return r;
+        if (int r = q4::api_check_device_ptr(b, h->device, "b")) return r;
+        if (reinterpret_cast<uintptr_t>(a) % 2 || reinterpret_cast<uintptr_t>(b) % 2)
+            return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "misaligned a or b");
+    }
+    if (cudaError_t e = q4::launch_lora_set(view(h), h->a, h->b, h->slot, slot, static_cast<const uint16_t *>(a),
+                                            static_cast<const uint16_t *>(b), rank, scale, stream))
+        return api_cuda_fail(e, "adapter copy launch");
+    q4::api_count_launches(1);
+    return api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+int gptq_q4_lora_reserve(gptq_q4_lora h, int max_m) {
+    if (int r = check(h)) return r;
+    if (max_m < 0) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "max_m=%d < 0", max_m);
+    if (cudaError_t e = cudaDeviceSynchronize()) return api_cuda_fail(e, "reserve");
+    if (int r = ensure_rows(h, static_cast<size_t>(max_m), nullptr, true)) return r;
+    return api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int32_t *row_slot, int M, const void *y,
+                     int64_t y_stride, void *out, int64_t out_stride, cudaStream_t stream) {
+    if (int r = check(h)) return r;
+    if (M < 0) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "M=%d < 0", M);
+    if (M == 0) return api_set_status(GPTQ_Q4_OK, nullptr);
+    if (!x || !row_slot || !y || !out)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "x, row_slot, y and out must not be NULL");
+    if (!aligned16(x) || !aligned16(y) || !aligned16(out) || reinterpret_cast<uintptr_t>(row_slot) % 4)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "x, y and out must be 16-byte aligned, row_slot 4-byte");
+    if (x_stride < h->K || y_stride < h->N || out_stride < h->N || x_stride % 8 || y_stride % 8 || out_stride % 8)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "row strides (x %lld, y %lld, out %lld) must be multiples of 8 and at least K=%d, N=%d, N",
+                         static_cast<long long>(x_stride), static_cast<long long>(y_stride),
+                         static_cast<long long>(out_stride), h->K, h->N);
+    if (out == y && out_stride != y_stride)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "out is y but their row strides differ (%lld and %lld)",
+                         static_cast<long long>(out_stride), static_cast<long long>(y_stride));
+    if (int r = ensure_rows(h, static_cast<size_t>(M), stream, false)) return r;
+    const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
+                         static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M};
+    int launches = 0;
+    if (cudaError_t e = q4::launch_lora_add(view(h), c, h->dtype == GPTQ_Q4_DTYPE_BF16, stream, &launches))
+        return api_cuda_fail(e, "adapter launch");
+    q4::api_count_launches(launches);
+    return api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+int gptq_q4_lora_device_error(gptq_q4_lora h) {
+    if (int r = check(h)) return r;
+    int flag = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (!e) e = cudaMemcpy(&flag, h->status, sizeof(int), cudaMemcpyDeviceToHost);
+    if (!e && flag) e = cudaMemset(h->status, 0, sizeof(int));
+    if (e) return api_cuda_fail(e, "reading the pool's status word");
+    if (flag)
+        return api_failf(GPTQ_Q4_DEVICE_FAULT, "adapter kernels reported status 0x%x:%s", flag,
+                         flag & q4::kLoraBadSlot ? " a row_slot entry is not below the number of slots" : "");
+    return api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+void gptq_q4_lora_free(gptq_q4_lora h) {
+    release(h);
+    api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+}  // extern "C"

@@ -1,0 +1,127 @@
+// Handles and launchers of the operators around the projection: the adapter
+// pool (q4_lora*.cu) and paged attention with its cache append (q4_attn*.cu).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/gptq_q4.h"
+
+namespace q4 {
+
+// One adapter of a pool, as the kernels read it.
+struct LoraSlot {
+    int rank;        // of the adapter; 0: empty
+    float scale;
+};
+
+// Status bits of the two handles.
+constexpr int kLoraBadSlot = 0x1;      // row_slot entry >= slots
+constexpr int kAttnBadBatch = 0x1;     // a length outside its range, or cu_q not ascending
+constexpr int kAttnBadPage = 0x2;      // a page index outside the cache
+constexpr int kAttnBadPosition = 0x4;  // a position outside the rotary table
+constexpr int kAttnTimeout = 0x8;      // a bounded wait ran out
+
+constexpr int ceil16(int r) { return (r + 15) / 16 * 16; }
+
+struct LoraView {
+    int K, N, slots, rpad;       // rpad: ceil16(max_rank)
+    const uint16_t *a;           // [slots][rpad][K]; rows rank .. ceil16(rank) - 1 are zero
+    const uint16_t *b;           // [slots][N * rpad]: slot s holds [N][ceil16(rank_s)], padded columns zero
+    const LoraSlot *slot;        // [slots]
+    float *t;                    // [rows][rpad] fp32: scale * x . A^T
+    int *status;
+};
+
+struct LoraCall {
+    const uint16_t *x, *y;
+    uint16_t *out;
+    const int32_t *row_slot;
+    int64_t xs, ys, os;
+    int M;
+};
+
+cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,
+                            const uint16_t *src_b, int rank, float scale, cudaStream_t st);
+cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
+
+// The step's requests and one layer's cache, as the kernels read them.
+struct AttnBatch {
+    const int32_t *cu_q, *kv_len, *table;
+    int64_t table_stride;
+    int width, batch, tokens;
+};
+struct AttnCache {
+    uint16_t *k, *v;
+    int pages;
+    int64_t page_stride;
+};
+struct AttnShape {
+    int hq, hkv, group, d, page, page_log2;
+};
+
+struct AppendCall {
+    const uint16_t *qkv;
+    uint16_t *q_out;
+    int64_t qkv_stride, q_stride;
+    const int32_t *positions;
+    const float2 *rope;          // [max_pos][rot / 2] (cos, sin), NULL: no rotation
+    int rot, interleaved, max_pos;
+    int *status;
+};
+cudaError_t launch_rope_table(float2 *table, const double *inv_freq, double length_scale, int half, int max_pos,
+                              cudaStream_t st);
+cudaError_t launch_attn_append(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AppendCall &a,
+                               bool bf16, cudaStream_t st);
+
+struct AttendCall {
+    const uint16_t *q;
+    uint16_t *out;
+    int64_t q_stride, out_stride;
+    float scale;
+    int window;
+    int max_q;
+    int *status;
+};
+cudaError_t launch_attend(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
+                          cudaStream_t st);
+
+// ------------------------------------------------------------ device helpers
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if constexpr (BF) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&v));
+    else return __half22float2(*reinterpret_cast<__half2 *>(&v));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF) {
+        __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&r);
+    } else {
+        __half2 r = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&r);
+    }
+}
+
+// A request's rows and context length, cut to their ranges: 0 <= q0,
+// q0 + ql <= tokens, 0 <= kv <= width * page.  bad: something had to be cut.
+struct Request {
+    int q0, ql, kv;
+    bool bad;
+};
+__device__ __forceinline__ Request load_request(const AttnBatch &b, int i, int page_log2) {
+    const int a = b.cu_q[i], e = b.cu_q[i + 1], n = b.kv_len[i];
+    const long long cap = static_cast<long long>(b.width) << page_log2;
+    Request r;
+    r.q0 = min(max(a, 0), b.tokens);
+    r.ql = max(min(e, b.tokens) - r.q0, 0);
+    r.kv = static_cast<int>(min(static_cast<long long>(max(n, 0)), cap));
+    r.bad = r.q0 != a || r.q0 + r.ql != e || r.kv != n;
+    return r;
+}
+
+}  // namespace q4

@@ -416,6 +416,184 @@ gptq_q4_handle gptq_q4_make8(const int32_t *qweight, const int32_t *qzeros,
                              const uint16_t *scales, const int32_t *g_idx,
                              int K, int N, int groupsize);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.
+ *
+ *     out[m] = y[m] + scale_a * (x[m] . A_a^T) . B_a^T,   a = row_slot[m]
+ *
+ * A pool holds up to `slots` adapters of one projection (K inputs, N
+ * outputs), each with its own rank; every row of a call names the slot of its
+ * adapter, or a negative number for none.  x and y are the projection's input
+ * and output (gptq_q4_matmul), so one call adds every request's adapter to
+ * the shared product.  For one part of a fused projection, pass that part's
+ * columns of y and out with the fused row strides.
+ *
+ * A pool may be used from one stream at a time (gptq_q4_lora_set and _add
+ * are ordered by the streams they are enqueued on; the sums x . A^T live in
+ * the pool's workspace). */
+typedef struct gptq_q4_lora_s *gptq_q4_lora;
+
+/* An empty pool.  dtype: GPTQ_Q4_DTYPE_FP16 or _BF16, the type of x, y, out,
+ * A and B.  K and N positive multiples of 8, 1 <= slots <= 4096,
+ * 1 <= max_rank <= 256.  Device memory: slots * ceil16(max_rank) * (K + N)
+ * 16-bit values.  Synchronizes.  NULL on error (status and message as for
+ * gptq_q4_make): INVALID_ARGUMENT, UNSUPPORTED (device not sm_103, fp32),
+ * OUT_OF_MEMORY, CUDA_ERROR. */
+gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype);
+
+/* Put an adapter into a slot (it replaces the slot's last one):
+ *   a  device [rank][K], b  device [N][rank], dense, of the pool's type;
+ *   rank 0 with NULL a and b empties the slot.
+ * Copied on `stream`; the caller may change a and b once the stream has
+ * passed this call.  Errors: INVALID_ARGUMENT (NULL, slot or rank out of
+ * range, non-device pointers), CUDA_ERROR. */
+int gptq_q4_lora_set(gptq_q4_lora h, int slot, const void *a, const void *b, int rank, float scale,
+                     cudaStream_t stream);
+
+/* Size the workspace for calls with up to max_m rows (a later call with more
+ * rows grows it on its stream).  Synchronizes.  Errors: INVALID_ARGUMENT,
+ * OUT_OF_MEMORY. */
+int gptq_q4_lora_reserve(gptq_q4_lora h, int max_m);
+
+/* out = y + the adapters' part, as above.
+ *   x         device [M][K], row stride x_stride elements
+ *   row_slot  device int32 [M]: the row's slot; negative or an empty slot: out = y.
+ *             An entry >= slots counts as none and is reported by gptq_q4_lora_device_error
+ *   y, out    device [M][N], row strides y_stride, out_stride; out may be y itself
+ *             (same stride), and must not overlap x or otherwise overlap y
+ * Pointers 16-byte aligned, strides multiples of 8 and at least the row's
+ * length; M = 0 is a no-op.  x . A^T, its products with B and the sum with y
+ * are fp32, rounded once to the output.  Errors: INVALID_ARGUMENT,
+ * OUT_OF_MEMORY (growing the workspace), CUDA_ERROR. */
+int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int32_t *row_slot, int M, const void *y,
+                     int64_t y_stride, void *out, int64_t out_stride, cudaStream_t stream);
+
+/* As gptq_q4_device_error and gptq_q4_free, for a pool. */
+int gptq_q4_lora_device_error(gptq_q4_lora h);
+void gptq_q4_lora_free(gptq_q4_lora h);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions, a paged cache, and attention over it: what lies between
+ * a decoder layer's fused QKV projection and its output projection.
+ *
+ * One handle serves all layers of a model: it holds the table of rotary
+ * cosines and sines, a fixed workspace, and the status word.  It may be used
+ * from one stream at a time.
+ *
+ * The cache of one layer: keys and values in pages of page_size tokens,
+ *   k, v  device [pages][kv_heads][page_size][head_dim], 16-byte aligned;
+ *         page_stride elements from page to page (at least
+ *         kv_heads * page_size * head_dim, a multiple of 8), the rest dense. */
+typedef struct {
+    void *k, *v;
+    int pages;
+    int64_t page_stride;
+} gptq_q4_cache;
+
+/* The requests of one step.  Request b has q_len = cu_q[b+1] - cu_q[b] new
+ * tokens, rows cu_q[b] .. cu_q[b+1]-1 of the step's `tokens` rows, and
+ * kv_len[b] tokens in the cache, the new ones (its last q_len) among them:
+ * new token t has index kv_len - q_len + t in the request's context.  Token j
+ * lies in page table[b][j / page_size], at j % page_size.
+ *   cu_q   device int32 [batch + 1], ascending
+ *   kv_len device int32 [batch], each 0 .. width * page_size
+ *   table  device int32 [batch][width], table_stride elements from row to row;
+ *          only entries of pages that a call reads or writes have to be valid
+ *   max_q  no request has more new tokens (a larger number is allowed and
+ *          changes no result, only which kernel runs)
+ * The arrays are read on the GPU when the call runs.  A length or page index
+ * outside its range is cut to it (no access leaves the caller's arrays),
+ * makes that request's results meaningless, and is reported by
+ * gptq_q4_attn_device_error. */
+typedef struct {
+    const int32_t *cu_q, *kv_len, *table;
+    int64_t table_stride;
+    int width, batch, tokens, max_q;
+} gptq_q4_batch;
+
+typedef struct gptq_q4_attn_s *gptq_q4_attn;
+
+/* A handle for q_heads query heads that share kv_heads key/value heads
+ * (q_heads a multiple of kv_heads, at most 128 query heads for each),
+ * head_dim 64 or 128, page_size a power of two from 8 to 1024; dtype
+ * GPTQ_Q4_DTYPE_FP16 or _BF16: the type of q, k, v and the output.
+ * Synchronizes.  NULL on error: INVALID_ARGUMENT, UNSUPPORTED (head_dim,
+ * page_size, fp32, device not sm_103), OUT_OF_MEMORY, CUDA_ERROR. */
+gptq_q4_attn gptq_q4_attn_make(int q_heads, int kv_heads, int head_dim, int page_size, int dtype);
+
+/* Angles per position for gptq_q4_attn_set_rope; host only, no device call.
+ * inv_freq (host, rotary_dim / 2 doubles): f_i = base^(-2i / rotary_dim), then
+ *   ROPE_PLAIN   as it is
+ *   ROPE_LINEAR  f_i / factor
+ *   ROPE_NTK     base replaced by base * factor^(rotary_dim / (rotary_dim - 2))
+ *   ROPE_BANDS   with r = original * f_i / 2 pi turns over the original context and
+ *                s = clamp((r - low) / (high - low), 0, 1):  s f_i + (1 - s) f_i / factor
+ *   ROPE_YARN    with the pair index d(r) = rotary_dim ln(original / 2 pi r) / (2 ln base) at which a pair makes
+ *                r turns, l = max(floor(d(high)), 0), h = min(ceil(d(low)), rotary_dim - 1) and
+ *                s = 1 - clamp((i - l) / max(h - l, 0.001), 0, 1):  s f_i + (1 - s) f_i / factor
+ * length_scale (host): what the rotated vectors are multiplied by: 1, and
+ * 0.1 ln(factor) + 1 for ROPE_YARN.  factor, low, high and original are read
+ * only where the formula has them.
+ * Errors: INVALID_ARGUMENT (NULL, rotary_dim not even and positive, base <= 1,
+ * factor < 1, high <= low, low <= 0, original < 1, unknown kind). */
+#define GPTQ_Q4_ROPE_PLAIN  0
+#define GPTQ_Q4_ROPE_LINEAR 1
+#define GPTQ_Q4_ROPE_NTK    2
+#define GPTQ_Q4_ROPE_BANDS  3
+#define GPTQ_Q4_ROPE_YARN   4
+int gptq_q4_rope_freqs(int rotary_dim, double base, int kind, double factor, double low, double high, int original,
+                       double *inv_freq, double *length_scale);
+
+/* Rotary positions for gptq_q4_attn_append: pair i of the first rotary_dim
+ * elements of every query and key head turns by position * inv_freq[i] and
+ * is multiplied by length_scale.  Pair i is elements (i, i + rotary_dim / 2),
+ * or (2i, 2i + 1) if interleaved.  inv_freq: host, rotary_dim / 2 doubles.
+ * Builds a table of fp32 cosines and sines for positions 0 .. max_pos - 1
+ * (angles in fp64), 4 * max_pos * rotary_dim bytes.  rotary_dim: even, at most
+ * head_dim, a multiple of 16; 0 turns rotation off again (the state of a new
+ * handle).  Synchronizes.  Errors: INVALID_ARGUMENT, OUT_OF_MEMORY,
+ * CUDA_ERROR. */
+int gptq_q4_attn_set_rope(gptq_q4_attn h, int rotary_dim, int interleaved, const double *inv_freq,
+                          double length_scale, int max_pos);
+
+/* Rotate the step's queries and keys and put keys and values into the cache.
+ *   qkv        device [tokens][(q_heads + 2 kv_heads) * head_dim], row stride
+ *              qkv_stride: the fused projection's output, queries, keys, values
+ *   positions  device int32 [tokens], or NULL: a token's index in its context
+ *   q_out      device [tokens][q_heads * head_dim], row stride q_stride, the
+ *              rotated queries; may be qkv itself (same stride), else must not overlap it
+ * 16-byte aligned, strides multiples of 8.  Rotation in fp32, rounded once.
+ * Rows that no request owns are left alone.  A token whose index is negative
+ * or past the table (kv_len < q_len, say), or whose position is outside
+ * 0 .. max_pos - 1, is not written anywhere and is reported by
+ * gptq_q4_attn_device_error.  Errors: INVALID_ARGUMENT, CUDA_ERROR. */
+int gptq_q4_attn_append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const gptq_q4_cache *cache,
+                        const gptq_q4_batch *batch, const int32_t *positions, void *q_out, int64_t q_stride,
+                        cudaStream_t stream);
+
+/* Attention of the step's new tokens over the cache:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j)
+ * over the tokens j <= i of the request's context, i = kv_len - q_len + t the
+ * token's own index, and, if window > 0, j > i - window.  A row that sees
+ * nothing (i < 0) gets zeros.
+ *   q, out  device [tokens][q_heads * head_dim], row strides q_stride,
+ *           out_stride; 16-byte aligned, strides multiples of 8, not overlapping
+ * Cache slots past kv_len (and pages before the window) are not part of any
+ * result, whatever they hold.  Scores, softmax and sums are fp32; each
+ * weight p is rounded to 16 bits for its product with v; the output is
+ * rounded once.  Rows that no request owns are left alone.  The order of the
+ * sums depends on the lengths of the whole batch, not on timing: the same
+ * call gives the same bits.  Errors: INVALID_ARGUMENT (NULL, sizes, strides,
+ * alignment, scale not finite, window < 0), UNSUPPORTED (batch > 4096),
+ * CUDA_ERROR. */
+int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache *cache,
+                        const gptq_q4_batch *batch, float scale, int window, void *out, int64_t out_stride,
+                        cudaStream_t stream);
+
+/* As gptq_q4_device_error and gptq_q4_free, for an attention handle. */
+int gptq_q4_attn_device_error(gptq_q4_attn h);
+void gptq_q4_attn_free(gptq_q4_attn h);
+
 /* Status and message of the last call made on this host thread.
  * "Inference Backends", "Hardware, dependency, and format requirements":
  * device-validation errors keep the kernel's specific reason (an unsupported
