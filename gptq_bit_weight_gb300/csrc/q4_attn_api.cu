@@ -16,6 +16,9 @@ struct gptq_q4_attn_s {
     int rot = 0, interleaved = 0, max_pos = 0;
     float2 *rope = nullptr;
     int *status = nullptr;
+    float *ws = nullptr;
+    int *tickets = nullptr;
+    int ctas = 0;
 };
 
 namespace {
@@ -54,10 +57,10 @@ int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache *c, const gptq_q4_ba
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "the cache's k and v must be 16-byte aligned and not NULL");
     const int64_t page = static_cast<int64_t>(h->shape.hkv) * h->shape.page * h->shape.d;
-    if (c->pages < 1 || c->page_stride < page || c->page_stride % 8)
+    if (c->pages < 1 || c->page_stride < page || c->page_stride % 8 || c->page_stride >= int64_t{1} << 39)
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
-                         "pages=%d must be positive and page_stride=%lld a multiple of 8, at least %lld", c->pages,
-                         static_cast<long long>(c->page_stride), static_cast<long long>(page));
+                         "pages=%d must be positive and page_stride=%lld a multiple of 8, at least %lld and below 2^39",
+                         c->pages, static_cast<long long>(c->page_stride), static_cast<long long>(page));
     return GPTQ_Q4_OK;
 }
 
@@ -76,6 +79,8 @@ void release(gptq_q4_attn_s *h) {
     cudaDeviceSynchronize();
     cudaFree(h->rope);
     cudaFree(h->status);
+    cudaFree(h->ws);
+    cudaFree(h->tickets);
     if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
@@ -115,6 +120,10 @@ gptq_q4_attn gptq_q4_attn_make(int q_heads, int kv_heads, int head_dim, int page
     h->shape = q4::AttnShape{q_heads, kv_heads, q_heads / kv_heads, head_dim, page_size, log2};
     cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&h->status), sizeof(int));
     if (!e) e = cudaMemset(h->status, 0, sizeof(int));
+    h->ctas = q4::device_sm_count();
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->ws), q4::attend_stream_ws_bytes(h->ctas));
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->tickets), h->ctas * sizeof(int));
+    if (!e) e = cudaMemset(h->tickets, 0, h->ctas * sizeof(int));
     if (!e) e = cudaDeviceSynchronize();
     if (e) {
         api_cuda_fail(e, "allocating the attention handle");
@@ -243,8 +252,8 @@ int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const g
                          static_cast<long long>(q_stride), static_cast<long long>(out_stride),
                          static_cast<long long>(row));
     const q4::AttendCall a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), q_stride, out_stride,
-                           scale, window, batch->max_q, h->status};
-    if (cudaError_t e = q4::launch_attend(s, batch_view(batch), cache_view(cache), a,
+                           scale, window, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
+    if (cudaError_t e = q4::launch_attend_stream(s, batch_view(batch), cache_view(cache), a,
                                           h->dtype == GPTQ_Q4_DTYPE_BF16, stream))
         return api_cuda_fail(e, "attention launch");
     q4::api_count_launches(1);
@@ -257,6 +266,8 @@ int gptq_q4_attn_device_error(gptq_q4_attn h) {
     cudaError_t e = cudaDeviceSynchronize();
     if (!e) e = cudaMemcpy(&flag, h->status, sizeof(int), cudaMemcpyDeviceToHost);
     if (!e && flag) e = cudaMemset(h->status, 0, sizeof(int));
+    // a kernel that gave up may have left pieces uncounted
+    if (!e && (flag & q4::kAttnTimeout)) e = cudaMemset(h->tickets, 0, h->ctas * sizeof(int));
     if (e) return api_cuda_fail(e, "reading the attention handle's status word");
     if (flag)
         return api_failf(GPTQ_Q4_DEVICE_FAULT, "attention kernels reported status 0x%x:%s%s%s%s", flag,

@@ -1,0 +1,207 @@
+// How the attention kernels share out their work.
+//
+// A request's rows (new token x query head of the group, head fastest) are
+// cut into row tiles of `step` rows, its context into key tiles of 2^kt_log2
+// tokens.  An item is one (request, key/value head, row tile); its units are
+// the key tiles its rows can see (one, without work, if they see nothing).
+// All units of a call, item after item, are dealt to the CTAs in equal
+// contiguous runs, so a CTA holds the end of one item, some whole ones and
+// the beginning of another; pieces of a cut item meet in the workspace.
+// Every CTA works the shares out for itself from the lengths in device
+// memory: no host copy of them, no planning launch.
+#pragma once
+#include "q4_serve.h"
+
+namespace q4 {
+
+struct SchedParams {
+    AttnBatch b;
+    int hkv, group, page_log2;
+    int step;        // rows of a row tile
+    int kt_log2;     // log2 of the tokens of a key tile
+    int window;
+};
+
+struct Item {
+    int b, head, tile, tiles;
+    int q0, ql, kv;
+    int t0, t1;      // first and last token of the row tile
+    int lo, hi;      // keys [lo, hi) that some row of the tile sees; hi <= 0: none
+    int first, n;    // key tiles
+    long long u;     // the item's first unit
+};
+
+__device__ __forceinline__ int row_tiles(const SchedParams &p, int ql) {
+    return (ql * p.group + p.step - 1) / p.step;
+}
+
+// The tokens, keys and key tiles of row tile `it.tile`.
+__device__ __forceinline__ void fill_tile(const SchedParams &p, Item &it) {
+    const int r0 = it.tile * p.step, r1 = min(r0 + p.step, it.ql * p.group);
+    it.t0 = r0 / p.group;
+    it.t1 = (r1 - 1) / p.group;
+    const int own = it.kv - it.ql;                   // index of new token 0
+    it.hi = min(own + it.t1 + 1, it.kv);
+    it.lo = p.window > 0 ? max(0, own + it.t0 - p.window + 1) : 0;
+    it.first = it.lo >> p.kt_log2;
+    const int kt = 1 << p.kt_log2;
+    it.n = it.hi > 0 ? ((it.hi + kt - 1) >> p.kt_log2) - it.first : 1;
+}
+
+// Units of row tiles i0, i0 + stride, .. of a request with ql tokens and a context of kv.
+__device__ __forceinline__ long long tile_units(const SchedParams &p, int ql, int kv, int i0, int stride) {
+    Item it;
+    it.ql = ql;
+    it.kv = kv;
+    const int tiles = row_tiles(p, ql);
+    long long sum = 0;
+    for (it.tile = i0; it.tile < tiles; it.tile += stride) {
+        fill_tile(p, it);
+        sum += it.n;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ void load_item_request(const SchedParams &p, Item &it) {
+    const Request r = load_request(p.b, it.b, p.page_log2);
+    it.q0 = r.q0;
+    it.ql = r.ql;
+    it.kv = r.kv;
+    it.tiles = row_tiles(p, r.ql);
+}
+
+// Step to the next item; false after the last.
+__device__ __forceinline__ bool next_item(const SchedParams &p, Item &it) {
+    it.u += it.n;
+    if (++it.tile == it.tiles) {
+        it.tile = 0;
+        if (++it.head == p.hkv) {
+            it.head = 0;
+            do {
+                if (++it.b >= p.b.batch) return false;
+                load_item_request(p, it);
+            } while (it.tiles == 0);
+        }
+    }
+    fill_tile(p, it);
+    return true;
+}
+
+struct Share {
+    long long begin, end;    // units of this CTA
+    long long per;           // units of every CTA but the last with any
+};
+
+// Shared memory of sched_share.
+struct SchedSmem {
+    long long warp_sum[32];
+    int b, head, tile;
+    long long rem, units, u;
+};
+
+// This CTA's share and, if it has one, its first item.  Called by all NT
+// threads of the CTA; `sm` must not be in use before or within the call.
+template <int NT>
+__device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int ctas, int *status, Item &it) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (p.b.batch + NT - 1) / NT;     // requests of a thread, in order
+    long long mine = 0, last = 0;
+    for (int i = 0; i < chunk; ++i) {
+        const int b = tid * chunk + i;
+        Request r{0, 0, 0, false};
+        if (b < p.b.batch) {
+            r = load_request(p.b, b, p.page_log2);
+            if (r.bad && cta == 0) atomicOr(status, kAttnBadBatch);
+        }
+        // a request of many row tiles is summed by the whole warp
+        const bool many = row_tiles(p, r.ql) > 4;
+        last = many ? 0 : tile_units(p, r.ql, r.kv, 0, 1);
+        for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
+            const int who = __ffs(left) - 1;
+            long long s = tile_units(p, __shfl_sync(0xffffffffu, r.ql, who), __shfl_sync(0xffffffffu, r.kv, who), lane, 32);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == who) last = s;
+        }
+        mine += last * p.hkv;
+    }
+    long long upto = mine;                           // inclusive prefix within the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sm.warp_sum[warp] = upto;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sm.warp_sum[w];
+        total += sm.warp_sum[w];
+    }
+    Share s;
+    s.per = max((total + ctas - 1) / ctas, 1ll);
+    s.begin = min(cta * s.per, total);
+    s.end = min(s.begin + s.per, total);
+    before += upto - mine;
+    if (s.begin < s.end && before <= s.begin && s.begin < before + mine) {
+        // this thread's requests hold the first unit: find which
+        long long rem = s.begin - before, units = last;
+        int b = tid * chunk;
+        for (;; ++b) {
+            if (chunk > 1) {
+                const Request r = load_request(p.b, b, p.page_log2);
+                units = tile_units(p, r.ql, r.kv, 0, 1);
+            }
+            if (rem < units * p.hkv) break;
+            rem -= units * p.hkv;
+        }
+        const int head = static_cast<int>(rem / units);
+        sm.b = b;
+        sm.head = head;
+        sm.rem = rem - head * units;
+    }
+    __syncthreads();
+    if (s.begin >= s.end) return s;
+    it.b = sm.b;
+    it.head = sm.head;
+    load_item_request(p, it);
+    if (warp == 0) {
+        // the row tile: a scan over 32 tiles at a time
+        long long rem = sm.rem;
+        for (int base = 0;; base += 32) {
+            it.tile = base + lane;
+            it.n = 0;
+            if (it.tile < it.tiles) fill_tile(p, it);
+            long long pre = it.n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, pre, o);
+                if (lane >= o) pre += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, pre > rem);
+            if (past) {
+                if (lane == __ffs(past) - 1) {
+                    sm.tile = it.tile;
+                    sm.u = s.begin - (rem - (pre - it.n));
+                }
+                break;
+            }
+            if (base + 32 >= it.tiles) {             // cannot be: the sums said otherwise
+                if (lane == 0) {
+                    sm.tile = it.tiles - 1;
+                    sm.u = s.begin;
+                }
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, pre, 31);
+        }
+    }
+    __syncthreads();
+    it.tile = sm.tile;
+    it.u = sm.u;
+    fill_tile(p, it);
+    return s;
+}
+
+}  // namespace q4

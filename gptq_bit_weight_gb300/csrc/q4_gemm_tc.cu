@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "q4_internal.cuh"
+#include "q4_serve.h"
 #include "q4_tc.cuh"
 
 namespace q4 {
@@ -257,6 +258,20 @@ cudaError_t encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *ptr,
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, dt, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_pages(CUtensorMap *map, const void *ptr, const AttnShape &s, const AttnCache &c, uint32_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t d = s.d, page = s.page;
+    const cuuint64_t dims[4] = {d, page, static_cast<cuuint64_t>(s.hkv), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[3] = {d * 2, d * page * 2, static_cast<cuuint64_t>(c.page_stride) * 2};
+    const cuuint32_t box[4] = {64, rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+    // 16-bit values either way: the copy does not look at them
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

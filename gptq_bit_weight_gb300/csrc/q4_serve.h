@@ -1,6 +1,7 @@
 // Handles and launchers of the operators around the projection: the adapter
 // pool (q4_lora*.cu) and paged attention with its cache append (q4_attn*.cu).
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -86,9 +87,17 @@ struct AttendCall {
     int window;
     int max_q;
     int *status;
+    float *ws;                   // pieces of cut items
+    int *tickets;                // [ctas], zero between calls
+    int ctas;                    // one for each SM
 };
-cudaError_t launch_attend(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
-                          cudaStream_t st);
+// few rows for each key/value head (q4_attn_stream.cu)
+size_t attend_stream_ws_bytes(int ctas);
+cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a,
+                                 bool bf16, cudaStream_t st);
+// Tensor map of a cache's keys or values [pages][heads][page][d]: boxes of
+// 64 columns (128 bytes, swizzled) and `rows` tokens (q4_gemm_tc.cu).
+cudaError_t encode_pages(CUtensorMap *map, const void *ptr, const AttnShape &s, const AttnCache &c, uint32_t rows);
 
 // ------------------------------------------------------------ device helpers
 template <bool BF>

@@ -483,7 +483,7 @@ void gptq_q4_lora_free(gptq_q4_lora h);
  * The cache of one layer: keys and values in pages of page_size tokens,
  *   k, v  device [pages][kv_heads][page_size][head_dim], 16-byte aligned;
  *         page_stride elements from page to page (at least
- *         kv_heads * page_size * head_dim, a multiple of 8), the rest dense. */
+ *         kv_heads * page_size * head_dim, a multiple of 8). */
 typedef struct {
     void *k, *v;
     int pages;
