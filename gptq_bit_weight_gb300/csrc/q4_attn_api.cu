@@ -2,6 +2,7 @@
 // (gptq_q4_attn_*): argument checks and the handle's memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -121,7 +122,7 @@ gptq_q4_attn gptq_q4_attn_make(int q_heads, int kv_heads, int head_dim, int page
     cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&h->status), sizeof(int));
     if (!e) e = cudaMemset(h->status, 0, sizeof(int));
     h->ctas = q4::device_sm_count();
-    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->ws), q4::attend_stream_ws_bytes(h->ctas));
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->ws), std::max(q4::attend_stream_ws_bytes(h->ctas), q4::attend_tc_ws_bytes(h->ctas)));
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->tickets), h->ctas * sizeof(int));
     if (!e) e = cudaMemset(h->tickets, 0, h->ctas * sizeof(int));
     if (!e) e = cudaDeviceSynchronize();
@@ -246,15 +247,19 @@ int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const g
     if (!q || !out || !aligned16(q) || !aligned16(out))
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "q and out must be 16-byte aligned and not NULL");
     const int64_t row = static_cast<int64_t>(s.hq) * s.d;
-    if (q_stride < row || q_stride % 8 || out_stride < row || out_stride % 8)
+    if (q_stride < row || q_stride % 8 || out_stride < row || out_stride % 8 ||
+        q_stride >= int64_t{1} << 39)
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
-                         "row strides (q %lld, out %lld) must be multiples of 8 and at least %lld",
+                         "row strides (q %lld, out %lld) must be multiples of 8, at least %lld and below 2^39",
                          static_cast<long long>(q_stride), static_cast<long long>(out_stride),
                          static_cast<long long>(row));
     const q4::AttendCall a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), q_stride, out_stride,
                            scale, window, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
-    if (cudaError_t e = q4::launch_attend_stream(s, batch_view(batch), cache_view(cache), a,
-                                          h->dtype == GPTQ_Q4_DTYPE_BF16, stream))
+    // more query rows for each key than the streaming kernel's largest row tile: the tensor-core kernel
+    // (which takes its maximum before scaling, so a positive scale)
+    const bool chunk = static_cast<int64_t>(batch->max_q) * s.group > 64 && scale > 0.f;
+    if (cudaError_t e = (chunk ? q4::launch_attend_tc : q4::launch_attend_stream)(
+            s, batch_view(batch), cache_view(cache), a, h->dtype == GPTQ_Q4_DTYPE_BF16, stream))
         return api_cuda_fail(e, "attention launch");
     q4::api_count_launches(1);
     return api_set_status(GPTQ_Q4_OK, nullptr);

@@ -1,0 +1,550 @@
+// Attention of chunks of new tokens over the paged cache on the 5th-generation
+// tensor cores (tcgen05), scores and outputs in tensor memory.
+//
+//   scores s = q . k (fp32); reference maximum m and sum l of each row,
+//   p = 2^(c (s - m)), c = scale log2(e), rounded to 16 bits for its product
+//   with v (l sums the unrounded ones); o = sum p v in fp32; o / l rounded
+//   once.  m follows the running maximum only when a row's maximum has risen
+//   by more than 2^8 in p, so the output in tensor memory is rescaled rarely;
+//   p stays below 2^8, within fp16, and l and o stay exact to fp32 either way.
+//
+// One CTA per SM works on two tiles of up to 128 rows at a time (row = token x
+// query head of the group, so the heads that share a key/value head share its
+// tiles) against key tiles of 128 tokens:
+//   warps 0-3, 4-7  softmax of the two row tiles: one thread for each row
+//                   reads its scores (tcgen05.ld), writes p back over them
+//                   as the A operand of the second product (tcgen05.st),
+//                   rescales and, at the end, stores the output
+//   warp 8          loads queries, keys and values by TMA (one box for each
+//                   page and 64 columns) into a ring of half-stages
+//   warp 9          one thread issues tcgen05.mma: while one row tile's
+//                   softmax runs, the tensor cores work on the other's
+//   warp 10         zeroes value rows outside the visible keys in the tiles
+//                   at the edges: such slots hold anything, and 0 x NaN is NaN
+// Every wait is bounded; a wait that runs out sets a status bit and its role
+// goes on without waiting.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "q4_attn_sched.cuh"
+#include "q4_tc.cuh"
+
+namespace q4 {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kKtLog2 = 7, kKt = 1 << kKtLog2;
+constexpr int kThreads = 384;
+constexpr int kLoader = 8, kIssuer = 9, kCleaner = 10;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
+
+template <int D_>
+struct Cfg {
+    static constexpr int D = D_;
+    static constexpr int kHalf = kKt * D * 2;    // bytes of a half-stage: keys or values of a tile
+    static constexpr int kQ = 128 * D * 2;       // of one row tile's queries
+    static constexpr int kMisc = 2048;
+    static constexpr int kRoom = (232448 - 1024 - 2 * kQ - kMisc) / kHalf;
+    static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
+    static constexpr int kSmem = 2 * kQ + kStages * kHalf + kMisc + 1024;
+    static constexpr int kPiece = 2 * 128 * (D + 2);   // floats of a piece in the workspace
+};
+
+struct Args {
+    SchedParams p;
+    AttnCache c;
+    uint16_t *out;
+    int64_t out_stride;
+    float scale;                 // times log2(e), positive
+    int tokens;                  // of a row tile: 128 / group
+    float *ws;                   // [2 * CTAs] pieces
+    int *tickets;                // [CTAs], zero between calls
+    int *status;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+// D += A . B with A in tensor memory: row = lane, two 16-bit values of K in a column.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+#define Q4_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+// 32 columns of the warp's lanes, without waiting for them.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : Q4_R8(r, 0), Q4_R8(r, 8), Q4_R8(r, 16), Q4_R8(r, 24)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : Q4_R8(r, 0), Q4_R8(r, 8)
+        : "r"(taddr)
+        : "memory");
+}
+#undef Q4_R8
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#define Q4_R8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        Q4_R8(r, 0), Q4_R8(r, 8)
+        : "memory");
+}
+#undef Q4_R8
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool wait_all(bool alive, uint32_t bar, uint32_t parity) {
+    if (alive) alive = mbar_wait(bar, parity);
+    return __all_sync(0xffffffffu, alive);
+}
+
+// What of an item falls to this CTA, the same for every role.
+struct Part {
+    int j0, j1;              // its key tiles, counted from it.first
+    bool two;                // the second row tile has rows
+    __device__ Part(const Item &it, const Share &sh, int tokens)
+        : j0(static_cast<int>(max(sh.begin - it.u, 0ll))),
+          j1(static_cast<int>(min(sh.end - it.u, static_cast<long long>(it.n)))),
+          two(it.t1 >= it.t0 + tokens) {}
+};
+
+template <bool BF, class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, Args a) {
+    constexpr int D = C::D, S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *sb = smem_raw + (base - raw);
+    const uint32_t ring = base + 2 * C::kQ, bars = ring + S * C::kHalf;
+    uint8_t *misc = sb + 2 * C::kQ + S * C::kHalf;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (S + s); };
+    auto tail = [&](int s) { return bars + 8u * (2 * S + s); };
+    const uint32_t q_full = bars + 8u * (3 * S), q_empty = q_full + 8, done = q_full + 16;
+    auto s_full = [&](int i) { return q_full + 24 + 8u * i; };
+    auto p_ready = [&](int i) { return q_full + 40 + 8u * i; };
+    auto pv_done = [&](int i) { return q_full + 56 + 8u * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
+    int *last_flag = reinterpret_cast<int *>(misc + 516);
+    SchedSmem &sched = *reinterpret_cast<SchedSmem *>(misc + 1024);
+    static_assert(8 * (3 * S + 9) <= 512 && 1024 + sizeof(SchedSmem) <= C::kMisc, "misc region");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+            mbar_init(tail(s), 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(p_ready(i), 128);
+            mbar_init(pv_done(i), 1);
+        }
+        mbar_init_fence();
+    }
+    if (warp == kIssuer) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tc_fence_before();
+    Item it;
+    const Share sh = sched_share<kThreads>(a.p, sched, blockIdx.x, gridDim.x, a.status, it);   // synchronizes
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool alive = true;
+    // 168 registers a thread at launch: 256 x 200 + 128 x 104 = 384 x 168
+    const bool work = sh.begin < sh.end;
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ---------------------------------------------- softmax: a thread holds a row
+        const int me = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + 128 * me, tO = tmem + lanes + 256 + 128 * me;
+        const float c = a.scale;
+        const int tok = row / a.p.group, head_in = row - tok * a.p.group;
+        int uses = 0;
+        for (bool more = work; more && it.u < sh.end; more = next_item(a.p, it)) {
+            const Part part(it, sh, a.tokens);
+            const bool active = me == 0 || part.two;
+            const int t = it.t0 + me * a.tokens + tok;                 // the row's token
+            const bool valid = active && tok < a.tokens && t <= it.t1;
+            const int lim = valid ? it.kv - it.ql + t : -1;            // last key that the row sees
+            const int lim_lo = a.p.window > 0 ? lim - a.p.window : -1; // keys up to this one are out of the window
+            float m = -INFINITY, l = 0.f;
+            if (it.hi > 0 && active) {
+                // keys that every row of this row tile sees
+                const int own = it.kv - it.ql, ta = it.t0 + me * a.tokens, tb = min(ta + a.tokens - 1, it.t1);
+                const int all_hi = own + ta, all_lo = a.p.window > 0 ? own + tb - a.p.window : -1;
+                for (int j = part.j0; j < part.j1; ++j, ++uses) {
+                    const int key_t = (it.first + j) << kKtLog2;
+                    alive = wait_all(alive, s_full(me), uses & 1);
+                    tc_fence_after();
+                    uint32_t s[128];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, s + 32 * q);
+                    tmem_wait_ld();
+                    if (key_t + kKt - 1 > all_hi || key_t <= all_lo) {
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            if (key_t + e > lim || key_t + e <= lim_lo) s[e] = 0xff800000u;
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    const bool first = j == part.j0;
+                    const bool grows = first ? mx > m : (mx - m) * c > kRescale;
+                    if (__any_sync(0xffffffffu, grows)) {
+                        const float to = grows ? mx : m;
+                        // from a row without any key so far, nothing is kept
+                        const float f = grows ? ex2((m - to) * c) : 1.f;
+                        l *= f;
+                        m = to;
+                        if (!first) {
+                            alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
+                            tc_fence_after();
+#pragma unroll
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + 16 * q, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(tO + 16 * q, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float x = ex2(fmaf(__uint_as_float(s[32 * h + 2 * e]), c, -ref));
+                            const float y = ex2(fmaf(__uint_as_float(s[32 * h + 2 * e + 1]), c, -ref));
+                            sum[2 * (e & 1)] += x;
+                            sum[2 * (e & 1) + 1] += y;
+                            p[e] = pack2<BF>(x, y);
+                        }
+                        tmem_st16(tS + 16 * h, p);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_ready(me));
+                }
+                alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
+                tc_fence_after();
+            }
+            // ------------------------------------------ output, or a piece for the workspace
+            uint16_t *dst = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
+                            (it.head * a.p.group + head_in) * D;
+            const bool whole = part.j0 == 0 && part.j1 == it.n;
+            if (whole) {
+                if (active) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        if (it.hi > 0) {
+                            tmem_ld32(tO + 32 * q, o);
+                            tmem_wait_ld();
+                        }
+                        if (valid)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = l == 0.f ? 0u
+                                                    : pack2<BF>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                                                __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                    }
+                    tc_fence_before();
+                }
+                continue;
+            }
+            const int c0 = static_cast<int>(it.u / sh.per), c1 = static_cast<int>((it.u + it.n - 1) / sh.per);
+            // [D / 4][128] float4 of each row tile, then [2][128] (m, l)
+            auto piece = [&](int cta) { return a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece; };
+            if (active) {
+                float4 *w = reinterpret_cast<float4 *>(piece(blockIdx.x)) + me * 128 * (D / 4) + row;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * q, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        __stcg(w + (8 * q + v) * 128,
+                               make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                                           __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3])));
+                }
+                tc_fence_before();
+                __stcg(reinterpret_cast<float2 *>(piece(blockIdx.x) + 2 * 128 * D) + me * 128 + row, make_float2(m, l));
+                __threadfence();
+            }
+            bar_softmax();
+            if (threadIdx.x == 0) {
+                __threadfence();
+                const int before = atomicAdd(a.tickets + c0, 1);
+                *last_flag = before == c1 - c0;
+                if (before == c1 - c0) a.tickets[c0] = 0;
+                __threadfence();
+            }
+            bar_softmax();
+            if (*reinterpret_cast<volatile int *>(last_flag) && valid) {
+                float top = -INFINITY;
+                auto ml = [&](int cta) {
+                    return __ldcg(reinterpret_cast<const float2 *>(piece(cta) + 2 * 128 * D) + me * 128 + row);
+                };
+                for (int k = c0; k <= c1; ++k) top = fmaxf(top, ml(k).x);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float sum = 0.f;
+                for (int k = c0; k <= c1; ++k) {
+                    const float2 v = ml(k);
+                    sum += v.y * ex2((v.x - ref) * c);
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                    float4 acc[8];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = c0; k <= c1; ++k) {
+                        const float f = ex2((ml(k).x - ref) * c);
+                        const float4 *w = reinterpret_cast<const float4 *>(piece(k)) + me * 128 * (D / 4) + row;
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const float4 x = __ldcg(w + (8 * q + v) * 128);
+                            acc[v].x += x.x * f;
+                            acc[v].y += x.y * f;
+                            acc[v].z += x.z * f;
+                            acc[v].w += x.w * f;
+                        }
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float4 x = acc[2 * v], y = acc[2 * v + 1];
+                        *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * v) =
+                            make_uint4(pack2<BF>(x.x * inv, x.y * inv), pack2<BF>(x.z * inv, x.w * inv),
+                                       pack2<BF>(y.x * inv, y.y * inv), pack2<BF>(y.z * inv, y.w * inv));
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (!work) {
+        } else if (warp == kLoader) {
+            const int pages_log2 = min(a.p.page_log2, kKtLog2), box = 1 << pages_log2;   // tokens of a box
+            const int boxes = kKt >> pages_log2;                                        // of a tile
+            const int q_bytes = a.tokens * a.p.group * D * 2;
+            int seq = 0, items = 0, bad = 0;
+            for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
+                if (it.hi <= 0) continue;
+                const Part part(it, sh, a.tokens);
+                const int32_t *table = a.p.b.table + it.b * a.p.b.table_stride;
+                if (items) alive = wait_all(alive, q_empty, (items - 1) & 1);
+                if (!alive) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, part.two ? 2 * q_bytes : q_bytes);
+                    for (int i = 0; i < (part.two ? 2 : 1); ++i)
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_3d(base + i * C::kQ + h * (128 * 128), &tmQ, q_full, 64 * h, it.head * a.p.group,
+                                        it.q0 + it.t0 + i * a.tokens);
+                }
+                ++items;
+                for (int j = part.j0; j < part.j1; ++j) {
+                    const int key_t = (it.first + j) << kKtLog2, key = key_t + lane * box;
+                    const bool wanted = lane < boxes && key < it.hi && key + box > it.lo;
+                    int page = wanted ? table[key >> a.p.page_log2] : 0;
+                    if (page < 0 || page >= a.c.pages) {
+                        bad = kAttnBadPage;
+                        page = 0;
+                    }
+                    const bool edge = key_t + kKt > it.hi || key_t < it.lo;
+                    const int bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * box * D * 2;
+                    const int row = key & ((1 << a.p.page_log2) - 1);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++seq) {
+                        const int s = seq % S;
+                        if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
+                        if (!alive) break;
+                        const uint32_t bar = kv && edge ? tail(s) : full(s);
+                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        __syncwarp();
+                        if (wanted)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_4d(ring + s * C::kHalf + h * (kKt * 128) + lane * box * 128, kv ? &tmV : &tmK, bar,
+                                            64 * h, row, it.head, page);
+                    }
+                    if (!alive) break;
+                }
+                if (!alive) break;
+            }
+            if (bad) atomicOr(a.status, bad);
+            if (!alive) {
+                // let the copies in flight land before the CTA can exit
+                if (items) mbar_wait(q_full, (items - 1) & 1);
+                for (int i = max(seq - S, 0); i < seq; ++i) mbar_wait(full(i % S), (i / S) & 1);
+            }
+        } else if (warp == kIssuer) {
+            if (lane == 0) {
+                constexpr uint32_t fmt = BF ? (1u << 7) | (1u << 10) : 0u;         // A and B bf16
+                constexpr uint32_t id_qk = idesc_f16(128, kKt, false) | fmt, id_pv = idesc_f16(128, D, true) | fmt;
+                int tiles = 0, items = 0, uses[2] = {0, 0};
+                auto wait = [&](uint32_t bar, int n) {
+                    if (alive) alive = mbar_wait(bar, n & 1);
+                    tc_fence_after();
+                };
+                auto qk = [&](int i, int seq) {
+                    const uint32_t kb = ring + (seq % S) * C::kHalf;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                        umma_f16(tmem + 128 * i, smem_desc_sw128(base + i * C::kQ + off, 16, 1024),
+                                 smem_desc_sw128(kb + off, 16, 1024), id_qk, kk != 0);
+                    }
+                    umma_commit(s_full(i));
+                };
+                auto pv = [&](int i, int seq, bool first) {
+                    const uint32_t vb = ring + (seq % S) * C::kHalf;
+#pragma unroll
+                    for (int kk = 0; kk < kKt / 16; ++kk)
+                        umma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
+                                    smem_desc_sw128(vb + kk * 2048, kKt * 128, 1024), id_pv, !first || kk != 0);
+                    umma_commit(pv_done(i));
+                };
+                for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
+                    if (it.hi <= 0) continue;
+                    const Part part(it, sh, a.tokens);
+                    const int n = part.j1 - part.j0, two = part.two ? 2 : 1;
+                    wait(q_full, items++);
+                    wait(full(2 * tiles % S), 2 * tiles / S);
+                    for (int i = 0; i < two; ++i) qk(i, 2 * tiles);
+                    umma_commit(empty(2 * tiles % S));
+                    if (n == 1) umma_commit(q_empty);
+                    for (int j = 0; j < n; ++j, ++tiles) {
+                        const int sv = 2 * tiles + 1, sk = 2 * tiles + 2;
+                        const bool next = j + 1 < n;
+                        wait(full(sv % S), sv / S);
+                        if (next) wait(full(sk % S), sk / S);
+                        for (int i = 0; i < two; ++i) {
+                            wait(p_ready(i), uses[i]++);
+                            pv(i, sv, j == 0);
+                            if (next) qk(i, sk);
+                        }
+                        umma_commit(empty(sv % S));
+                        if (next) umma_commit(empty(sk % S));
+                        if (j + 2 == n) umma_commit(q_empty);
+                    }
+                }
+                umma_commit(done);
+                if (!mbar_wait(done, 0)) alive = false;
+            }
+        } else if (warp == kCleaner) {
+            int seq = 1;
+            uint32_t turn = 0;                               // parity of each slot's tail barrier
+            for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
+                if (it.hi <= 0) continue;
+                const Part part(it, sh, a.tokens);
+                for (int j = part.j0; j < part.j1; ++j, seq += 2) {
+                    const int key_t = (it.first + j) << kKtLog2, s = seq % S;
+                    if (key_t + kKt <= it.hi && key_t >= it.lo) continue;
+                    alive = wait_all(alive, tail(s), (turn >> s) & 1);
+                    turn ^= 1u << s;
+                    uint8_t *v = sb + 2 * C::kQ + s * C::kHalf;
+                    auto zero = [&](int r0, int r1) {
+                        for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                *reinterpret_cast<uint4 *>(v + h * (kKt * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+                    };
+                    zero(0, min(max(it.lo - key_t, 0), kKt));
+                    zero(max(min(it.hi - key_t, kKt), 0), kKt);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(s));
+                }
+            }
+        }
+    }
+    if (!alive) atomicOr(a.status, kAttnTimeout);
+    __syncthreads();
+    if (warp == kIssuer) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <class C>
+cudaError_t launch(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
+                   cudaStream_t st) {
+    CUtensorMap tq, tk, tv;
+    const int tokens = 128 / s.group;
+    const uint32_t box = std::min(s.page, kKt);
+    cudaError_t e = encode_queries(&tq, a.q, s, a.q_stride, b.tokens, tokens);
+    if (!e) e = encode_pages(&tk, c.k, s, c, box);
+    if (!e) e = encode_pages(&tv, c.v, s, c, box);
+    if (e) return e;
+    Args args{{b, s.hkv, s.group, s.page_log2, 2 * tokens * s.group, kKtLog2, a.window}, c, a.out, a.out_stride,
+              a.scale * 1.4426950408889634f, tokens, a.ws, a.tickets, a.status};
+    auto kernel = bf16 ? attend_tc_kernel<true, C> : attend_tc_kernel<false, C>;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem))) return e;
+    kernel<<<a.ctas, kThreads, C::kSmem, st>>>(tq, tk, tv, args);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_tc_ws_bytes(int ctas) { return static_cast<size_t>(2) * ctas * Cfg<128>::kPiece * sizeof(float); }
+
+cudaError_t launch_attend_tc(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
+                             cudaStream_t st) {
+    return s.d == 64 ? launch<Cfg<64>>(s, b, c, a, bf16, st) : launch<Cfg<128>>(s, b, c, a, bf16, st);
+}
+
+}  // namespace q4

@@ -95,6 +95,14 @@ struct AttendCall {
 size_t attend_stream_ws_bytes(int ctas);
 cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a,
                                  bool bf16, cudaStream_t st);
+// chunks (q4_attn_tc.cu); scale > 0
+size_t attend_tc_ws_bytes(int ctas);
+cudaError_t launch_attend_tc(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
+                             cudaStream_t st);
+// Tensor map of the queries [tokens][heads][d]: boxes of 64 columns, a
+// group's heads and `rows` tokens.
+cudaError_t encode_queries(CUtensorMap *map, const void *ptr, const AttnShape &s, int64_t stride, int tokens,
+                           uint32_t rows);
 // Tensor map of a cache's keys or values [pages][heads][page][d]: boxes of
 // 64 columns (128 bytes, swizzled) and `rows` tokens (q4_gemm_tc.cu).
 cudaError_t encode_pages(CUtensorMap *map, const void *ptr, const AttnShape &s, const AttnCache &c, uint32_t rows);
