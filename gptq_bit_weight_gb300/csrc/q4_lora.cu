@@ -1,88 +1,421 @@
 // Low-rank adapters of many requests beside a shared projection:
 //     out[m] = y[m] + scale_a (x[m] . A_a^T) . B_a^T,   a = row_slot[m].
 // Two launches: the sums t[m][r] = scale_a x[m] . A_a[r] in fp32, then the
-// product with B and the sum with y, rounded once.
+// product with B and the sum with y, rounded once.  The second begins while
+// the first runs (programmatic dependent launch) and waits for t only.
+//
+// Here: the adapters' private layout, and the kernels for few rows (single
+// tokens, decode steps).  A call of few rows is bound by reading the adapters
+// in use, or by latency; so each block of ranks (first launch) or columns
+// (second) of one adapter is one CTA's, which gathers the rows that use the
+// adapter, streams its weights straight into mma.sync fragments, once, with
+// 16-byte loads, and needs no other CTA's result.
+//
+// Layout: 8 x 8 blocks of 16-bit values, 8 rows of 16 bytes (the
+// tensor-core "core matrix").
+//   A (r, k): [k / 64][r / 8][k % 64 / 8][r % 8][k % 8], ranks padded with
+//             zeros to a multiple of 16, k to a multiple of 64
+//   B (n, r): [n / 8][r / 8][n % 8][r % 8], ranks padded the same way
+// A warp's fragment load (8 rows x 4 blocks along the sum) is 512 contiguous
+// bytes of A, and any run of columns of B or 64 columns of A is contiguous
+// for a bulk copy.  The sum's index may be permuted as long as both operands
+// agree: lane (g, q) takes the 8 consecutive values of block q in row g,
+// which are the k slots {2q, 2q+1, 2q+8, 2q+9} of two k16 steps.
+#include <algorithm>
 #include <cstdint>
 
-#include "q4_serve.h"
+#include "q4_lora.cuh"
 
 namespace q4 {
+
+bool pdl_enabled();
+
 namespace {
 
-// Copies one adapter into its slot: A rows padded with zero rows to a rank
-// that is a multiple of 16, B rows padded with zeros the same way.
+// Copies one adapter into its slot.
 __global__ void lora_set_kernel(uint16_t *a, uint16_t *b, LoraSlot *slot, const uint16_t *src_a,
                                 const uint16_t *src_b, int K, int N, int rank, int r16, float scale) {
-    const size_t na = static_cast<size_t>(r16) * K, nb = static_cast<size_t>(r16) * N;
+    const size_t na = static_cast<size_t>(r16) * ceil64(K), nb = static_cast<size_t>(r16) * N;
     const size_t step = static_cast<size_t>(gridDim.x) * blockDim.x;
     const size_t i0 = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    for (size_t i = i0; i < na; i += step) a[i] = i / K < static_cast<size_t>(rank) ? src_a[i] : 0;
-    for (size_t i = i0; i < nb; i += step) {
-        const size_t n = i / r16;
-        const int r = static_cast<int>(i - n * r16);
-        b[i] = r < rank ? src_b[n * rank + r] : 0;
+    const int rg = r16 / 8;
+    for (size_t i = i0; i < na; i += step) {             // [k / 64][r / 8][k % 64 / 8][r % 8][k % 8]
+        const int e = i & 7, r8 = i >> 3 & 7, kg = i >> 6 & 7;
+        const size_t u = i >> 9;
+        const int r = static_cast<int>(u % rg) * 8 + r8;
+        const size_t k = u / rg * 64 + kg * 8 + e;
+        a[i] = r < rank && k < static_cast<size_t>(K) ? src_a[static_cast<size_t>(r) * K + k] : 0;
+    }
+    for (size_t i = i0; i < nb; i += step) {             // [n / 8][r / 8][n % 8][r % 8]
+        const int e = i & 7, n8 = i >> 3 & 7;
+        const size_t u = i >> 6;
+        const int r = static_cast<int>(u % rg) * 8 + e;
+        b[i] = r < rank ? src_b[(u / rg * 8 + n8) * rank + r] : 0;
     }
     if (i0 == 0) *slot = LoraSlot{rank, scale};
 }
 
-__device__ __forceinline__ int row_adapter(const LoraView &v, const LoraCall &c, int m, LoraSlot *s) {
-    const int slot = c.row_slot[m];
-    if (slot >= v.slots) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(v.status, kLoraBadSlot);
-        return -1;
-    }
-    if (slot < 0) return -1;
-    *s = v.slot[slot];
-    return s->rank > 0 ? slot : -1;
-}
+constexpr int kRows = 64;            // rows of a call's chunk that one CTA looks over
+constexpr int kWarps = 8;
 
-// One warp for each (row, rank): a dot product over K.
-template <bool BF>
-__global__ void __launch_bounds__(256) lora_shrink_kernel(LoraView v, LoraCall c) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m = blockIdx.y, r = blockIdx.x * 8 + warp;
-    LoraSlot s;
-    const int slot = row_adapter(v, c, m, &s);
-    if (slot < 0 || r >= ceil16(s.rank)) return;
-    const uint4 *x = reinterpret_cast<const uint4 *>(c.x + m * c.xs);
-    const uint4 *a = reinterpret_cast<const uint4 *>(v.a + (static_cast<size_t>(slot) * v.rpad + r) * v.K);
-    float acc = 0.f;
-    for (int k = lane; k < v.K / 8; k += 32) {
-        const uint4 p = x[k], q = a[k];
-        const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 u = unpack2<BF>(pw[e]), w = unpack2<BF>(qw[e]);
-            acc = fmaf(u.x, w.x, fmaf(u.y, w.y, acc));
+// The rows of chunk [m0, m0 + 64), by adapter.  An adapter in use is a class,
+// in the order of its first row; the rows without one are a class as well.
+struct Classes {
+    int slot[kRows], rank[kRows];    // of each class; rank padded to 16, 0: no adapter
+    int first[kRows + 1];            // its first place in `row`
+    int units[kRows + 1];            // units of work of earlier classes
+    int row[kRows];                  // chunk-relative rows, class after class
+    int n;
+    int s_slot[kRows], s_lead[kRows];
+};
+// Called by the whole CTA.  work(rows, rank): the units of a class.
+template <class Work>
+__device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &c, int m0, Classes &k, Work work) {
+    const int i = threadIdx.x;
+    int slot = -2, rank = 0;                             // -2: no row, -1: no adapter
+    if (i < kRows) {
+        if (m0 + i < c.M) {
+            slot = c.row_slot[m0 + i];
+            if (slot >= v.slots) {
+                atomicOr(v.status, kLoraBadSlot);
+                slot = -1;
+            }
+            slot = max(slot, -1);
+            if (slot >= 0) rank = ceil16(v.slot[slot].rank);
+        }
+        k.s_slot[i] = slot;
+    }
+    __syncthreads();
+    int lead = kRows, at = 0;                            // the first row of the same slot; rows of it before this one
+    if (i < kRows) {
+#pragma unroll 16
+        for (int j = 0; j < kRows; ++j) {
+            const bool same = k.s_slot[j] == slot;
+            lead = min(lead, same ? j : kRows);
+            at += same && j < i;
+        }
+        k.s_lead[i] = slot == -2 ? kRows : lead;
+    }
+    __syncthreads();
+    if (i < kRows && slot != -2) {
+        int id = 0, before = 0, count = 0;               // classes and rows with an earlier first row
+#pragma unroll 16
+        for (int j = 0; j < kRows; ++j) {
+            const int l = k.s_lead[j];
+            before += l < lead;
+            id += l == j && l < lead;
+            count += l == lead;
+        }
+        k.row[before + at] = i;
+        if (lead == i) {
+            k.slot[id] = slot;
+            k.rank[id] = rank;
+            k.first[id] = before;
+            k.first[id + 1] = before + count;            // the next class writes the same
+            k.units[id + 1] = work(count, rank);
         }
     }
+    if (i == 0) k.units[0] = 0;
+    const int leads = __syncthreads_count(i < kRows && slot != -2 && lead == i);
+    if (i < 32) {                                        // prefix sums of the units
+        int a = i < leads ? k.units[i + 1] : 0, b = i + 32 < leads ? k.units[i + 33] : 0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) v.t[static_cast<size_t>(m) * v.rpad + r] = acc * s.scale;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+            if (i >= o) {
+                a += x;
+                b += y;
+            }
+        }
+        b += __shfl_sync(0xffffffffu, a, 31);
+        k.units[i + 1] = a;
+        k.units[i + 33] = b;
+        if (i == 0) k.n = leads;
+    }
+    __syncthreads();
+}
+// The class of a unit, by a whole warp.
+__device__ __forceinline__ int class_of(const Classes &k, int unit) {
+    const int lane = threadIdx.x & 31;
+    return __popc(__ballot_sync(0xffffffffu, k.units[lane + 1] <= unit)) +
+           __popc(__ballot_sync(0xffffffffu, k.units[lane + 33] <= unit));
 }
 
-// One thread for each output column of a row.
 template <bool BF>
-__global__ void __launch_bounds__(256) lora_expand_kernel(LoraView v, LoraCall c) {
-    const int m = blockIdx.y, n = 2 * (blockIdx.x * blockDim.x + threadIdx.x);
-    LoraSlot s{0, 0.f};
-    const int slot = row_adapter(v, c, m, &s);
-    if (n >= v.N) return;
-    const uint32_t y = *reinterpret_cast<const uint32_t *>(c.y + m * c.ys + n);
-    float2 acc = make_float2(0.f, 0.f);
-    if (slot >= 0) {
-        const int r16 = ceil16(s.rank);
-        const uint16_t *b = v.b + static_cast<size_t>(slot) * v.N * v.rpad + static_cast<size_t>(n) * r16;
-        const float *t = v.t + static_cast<size_t>(m) * v.rpad;
-        for (int r = 0; r < r16; r += 2) {
-            const float2 p = unpack2<BF>(*reinterpret_cast<const uint32_t *>(b + r));
-            const float2 q = unpack2<BF>(*reinterpret_cast<const uint32_t *>(b + r16 + r));
-            acc.x = fmaf(t[r], p.x, fmaf(t[r + 1], p.y, acc.x));
-            acc.y = fmaf(t[r], q.x, fmaf(t[r + 1], q.y, acc.y));
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 ldg_stream(const uint16_t *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// t of 16 ranks for 8 NT rows, this warp's part of K: ranks are the MMA's
+// rows, the call's rows its columns.
+template <bool BF, int NT>
+__device__ __forceinline__ void shrink_rows(const LoraView &v, const LoraCall &c, const uint16_t *a, int rg,
+                                            const int *s_rows, int n, int first, int step, float *red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const uint16_t *x[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) x[i] = 8 * i + g < n ? c.x + s_rows[8 * i + g] * c.xs + 8 * q : nullptr;
+    float acc[NT][4] = {};
+    const int steps = (v.K + 31) / 32, blocks = v.K / 8;             // of 32 values of k; of 8
+    constexpr int U = NT <= 2 ? 4 : 2;
+    for (int i0 = first; i0 < steps; i0 += U * step) {
+        uint4 w[U][2], p[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step;
+            w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
+            if (i < steps) {
+                const uint16_t *at = a + (static_cast<size_t>(i >> 1) * rg * 8 + (i & 1) * 4 + q) * 64 + g * 8;
+                w[u][0] = ldg_stream(at);
+                w[u][1] = ldg_stream(at + 512);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                p[u][j] = make_uint4(0, 0, 0, 0);
+                if (i < steps && 4 * i + q < blocks && x[j]) p[u][j] = *reinterpret_cast<const uint4 *>(x[j] + 32 * i);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                mma16816<BF>(acc[j], w[u][0].x, w[u][1].x, w[u][0].y, w[u][1].y, p[u][j].x, p[u][j].y);
+                mma16816<BF>(acc[j], w[u][0].z, w[u][1].z, w[u][0].w, w[u][1].w, p[u][j].z, p[u][j].w);
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        reinterpret_cast<float4 *>(red)[(j * kWarps + warp) * 32 + lane] =
+            make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+}
+
+// Grid: (clusters over the chunk's (class, block of 16 ranks) units x CTAs of
+// a cluster along K, chunks of 64 rows).  Few: at most 16 rows in all, for
+// fewer registers.
+template <bool BF, bool Few>
+__global__ void __launch_bounds__(32 * kWarps) lora_shrink_kernel(LoraView v, LoraCall c, int ck) {
+    __shared__ Classes k;
+    __shared__ __align__(16) float red[kRows / 8 * kWarps * 128];
+    __shared__ __align__(16) float sum[kRows / 8 * 128];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int part = blockIdx.x % ck, warp = threadIdx.x >> 5, m0 = blockIdx.y * kRows;
+    find_classes(v, c, m0, k, [](int, int rank) { return rank / 16; });
+    c.x += m0 * c.xs;
+    v.t += static_cast<size_t>(m0) * v.rpad;
+    // every CTA of a cluster takes the same way through this loop
+    for (int unit = blockIdx.x / ck; unit < k.units[k.n]; unit += gridDim.x / ck) {
+        const int id = class_of(k, unit), slot = k.slot[id], rank = k.rank[id], n = k.first[id + 1] - k.first[id];
+        const int r0 = 16 * (unit - k.units[id]), nt = (n + 7) / 8;
+        const int *s_rows = k.row + k.first[id];
+        const uint16_t *a = v.a + static_cast<size_t>(slot) * v.rpad * ceil64(v.K) + static_cast<size_t>(r0) * 64;
+        const int first = part * kWarps + warp, step = ck * kWarps, rg = rank / 8;
+        if (nt == 1) shrink_rows<BF, 1>(v, c, a, rg, s_rows, n, first, step, red);
+        else if (Few || nt == 2) shrink_rows<BF, 2>(v, c, a, rg, s_rows, n, first, step, red);
+        else if (nt <= 4) shrink_rows<BF, 4>(v, c, a, rg, s_rows, n, first, step, red);
+        else shrink_rows<BF, 8>(v, c, a, rg, s_rows, n, first, step, red);
+        __syncthreads();
+        // the warps' parts of K in order, then the cluster's
+        for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += red[(e >> 7) * kWarps * 128 + w * 128 + (e & 127)];
+            sum[e] = s;
+        }
+        auto cluster_sync = [] {
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        };
+        if (ck > 1) cluster_sync();
+        else __syncthreads();
+        if (part == 0) {
+            const float scale = v.slot[slot].scale;
+            for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
+                float s = sum[e];
+                for (int p = 1; p < ck; ++p) {
+                    uint32_t from;
+                    float o;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                        : "=r"(from)
+                        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(sum + e))), "r"(p));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(from) : "memory");
+                    s += o;
+                }
+                // element e of the MMA's result: lane (g, q), value v: rank g + 8 (v / 2), row 2 q + v % 2
+                const int lane = e >> 2 & 31, row = (e >> 7) * 8 + 2 * (lane & 3) + (e & 1);
+                if (row < n)
+                    v.t[static_cast<size_t>(s_rows[row]) * v.rpad + r0 + (lane >> 2) + 8 * (e >> 1 & 1)] = s * scale;
+            }
+        }
+        if (ck > 1) cluster_sync();                      // nobody goes on while its sums are read
+        else __syncthreads();
+    }
+}
+
+// out = y + t . B^T.  A unit is 32 columns of 16 rows of a class; every warp
+// takes an equal run of units, class after class, and keeps t of its 16 rows
+// in registers as MMA fragments, high and low part.  Rows are the MMA's rows,
+// columns its columns, in the order that gives a thread 8 consecutive ones.
+template <bool BF>
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v, LoraCall c) {
+    __shared__ Classes k;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int m0 = blockIdx.y * kRows, nb = (v.N + 31) / 32;
+    find_classes(v, c, m0, k, [](int rows, int) { return (rows + 15) / 16; });
+    c.y += m0 * c.ys;
+    c.out += m0 * c.os;
+    v.t += static_cast<size_t>(m0) * v.rpad;
+    const int warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+    const int64_t units = static_cast<int64_t>(k.units[k.n]) * nb;
+    int64_t u = units * me / warps;
+    const int64_t end = units * (me + 1) / warps;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    {
+        while (u < end) {
+            const int group = static_cast<int>(u / nb), b0 = static_cast<int>(u % nb);
+            const int b1 = static_cast<int>(min(static_cast<int64_t>(nb), b0 + (end - u)));
+            u += b1 - b0;
+            const int id = class_of(k, group), rank = k.rank[id], steps = (rank + 31) / 32, rg = rank / 8;
+            const int r0 = k.first[id] + 16 * (group - k.units[id]) + g, r1 = k.first[id + 1];
+            const uint16_t *b = v.b + (rank ? static_cast<size_t>(k.slot[id]) * v.rpad * v.N : 0);
+            const bool have[2] = {r0 < r1, r0 + 8 < r1};
+            const int64_t row[2] = {have[0] ? k.row[r0] : 0, have[1] ? k.row[r0 + 8] : 0};
+            if (rank == 0 && c.out == c.y) continue;
+            // t of 32 ranks: the lane's 8 ranks of its two rows
+            float x[2][8];
+            auto load = [&](int s) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 p = make_float4(0.f, 0.f, 0.f, 0.f), r = p;
+                    if (have[h] && 32 * s + 8 * q < rank) {
+                        const float4 *t = reinterpret_cast<const float4 *>(v.t + row[h] * v.rpad + 32 * s + 8 * q);
+                        p = __ldcg(t);
+                        r = __ldcg(t + 1);
+                    }
+                    x[h][0] = p.x, x[h][1] = p.y, x[h][2] = p.z, x[h][3] = p.w;
+                    x[h][4] = r.x, x[h][5] = r.y, x[h][6] = r.z, x[h][7] = r.w;
+                }
+            };
+            float up[2] = {1.f, 1.f}, down[2] = {1.f, 1.f};
+            if constexpr (!BF) {
+                float top[2] = {0.f, 0.f};
+                for (int s = 0; s < steps; ++s) {
+                    load(s);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top[h] = fmaxf(top[h], fabsf(x[h][e]));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                    up[h] = split_scale_of(top[h]);
+                    down[h] = 1.f / up[h];               // a power of two: exact
+                }
+            }
+            uint32_t f[2][4][4];                         // fragments of 64 ranks: [32 ranks][k16 half, part][register]
+            auto fragments = [&](int s, uint32_t (&o)[4][4]) {
+                load(s);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float y0 = x[h][e] * down[h], y1 = x[h][e + 1] * down[h];
+                        const uint16_t h0 = to16<BF>(y0), h1 = to16<BF>(y1);
+                        const int half = e >> 2, reg = (e >> 1 & 1) * 2 + h;
+                        o[2 * half][reg] = h0 | static_cast<uint32_t>(h1) << 16;
+                        o[2 * half + 1][reg] = split_low<BF>(y0, h0) | static_cast<uint32_t>(split_low<BF>(y1, h1)) << 16;
+                    }
+            };
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (s < steps) fragments(s, f[s]);
+            for (int blk = b0; blk < b1; ++blk) {
+                const int col = 32 * blk + 8 * q;        // the thread's 8 columns of out
+                uint4 y[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    y[h] = make_uint4(0, 0, 0, 0);
+                    if (have[h] && col < v.N) y[h] = *reinterpret_cast<const uint4 *>(c.y + row[h] * c.ys + col);
+                }
+                float acc[4][4] = {};
+                auto product = [&](int s, const uint32_t (&t)[4][4]) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // MMA column g of tile j is column 8 (g / 2) + 2 j + g % 2 of the 32
+                        const int cg = 4 * blk + (g >> 1), in = 2 * j + (g & 1), kb = 4 * s + q;
+                        w[j] = make_uint4(0, 0, 0, 0);
+                        if (cg * 8 < v.N && kb < rg) w[j] = ldg_stream(b + (static_cast<size_t>(cg) * rg + kb) * 64 + in * 8);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma16816<BF>(acc[j], t[i][0], t[i][1], t[i][2], t[i][3], i < 2 ? w[j].x : w[j].z,
+                                         i < 2 ? w[j].y : w[j].w);
+                };
+                if (steps > 0) product(0, f[0]);
+                if (steps > 1) product(1, f[1]);
+                for (int s = 2; s < steps; ++s) {        // ranks past 64: their fragments are made anew
+                    uint32_t more[4][4];
+                    fragments(s, more);
+                    product(s, more);
+                }
+                if (col >= v.N) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!have[h]) continue;
+                    uint32_t *yw = reinterpret_cast<uint32_t *>(&y[h]);
+                    if (rank)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 o = unpack2<BF>(yw[j]);
+                            yw[j] = pack2<BF>(fmaf(acc[j][2 * h], up[h], o.x), fmaf(acc[j][2 * h + 1], up[h], o.y));
+                        }
+                    *reinterpret_cast<uint4 *>(c.out + row[h] * c.os + col) = y[h];
+                }
+            }
         }
     }
-    const float2 yy = unpack2<BF>(y);
-    *reinterpret_cast<uint32_t *>(c.out + m * c.os + n) = pack2<BF>(yy.x + acc.x, yy.y + acc.y);
+}
+
+template <class... P, class... T>
+cudaError_t start(void (*k)(P...), dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t st,
+                  T... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (dependent && pdl_enabled()) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 }  // namespace
@@ -90,35 +423,47 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(LoraView v, LoraCall c
 cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,
                             const uint16_t *src_b, int rank, float scale, cudaStream_t st) {
     const int r16 = ceil16(rank);
-    const size_t n = static_cast<size_t>(r16) * (v.K > v.N ? v.K : v.N);
-    const int grid = static_cast<int>(n / 256 + 1 < 1216 ? n / 256 + 1 : 1216);
-    lora_set_kernel<<<grid, 256, 0, st>>>(a + static_cast<size_t>(s) * v.rpad * v.K,
+    const size_t n = static_cast<size_t>(r16) * std::max(ceil64(v.K), v.N);
+    const int grid = static_cast<int>(std::min<size_t>(n / 256 + 1, 1216));
+    lora_set_kernel<<<grid, 256, 0, st>>>(a + static_cast<size_t>(s) * v.rpad * ceil64(v.K),
                                           b + static_cast<size_t>(s) * v.rpad * v.N, slot + s, src_a, src_b, v.K, v.N,
                                           rank, r16, scale);
     return cudaGetLastError();
 }
 
 cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
-    for (int m0 = 0; m0 < c.M; m0 += 65535) {          // rows are the grid's y dimension
+    const int chunks_all = (c.M + kRows - 1) / kRows;
+    for (int c0 = 0; c0 < chunks_all; c0 += 65535) {     // chunks are the grid's y dimension
         LoraCall d = c;
         LoraView w = v;
-        d.M = c.M - m0 < 65535 ? c.M - m0 : 65535;
+        const int64_t m0 = static_cast<int64_t>(c0) * kRows;
+        const int chunks = std::min(chunks_all - c0, 65535);
+        d.M = static_cast<int>(std::min<int64_t>(c.M - m0, static_cast<int64_t>(chunks) * kRows));
         d.x += m0 * c.xs;
         d.y += m0 * c.ys;
         d.out += m0 * c.os;
         d.row_slot += m0;
-        w.t += static_cast<size_t>(m0) * v.rpad;
-        const dim3 gs(v.rpad / 8, d.M), ge((v.N + 511) / 512, d.M);
-        if (bf16) {
-            lora_shrink_kernel<true><<<gs, 256, 0, st>>>(w, d);
-            lora_expand_kernel<true><<<ge, 256, 0, st>>>(w, d);
-        } else {
-            lora_shrink_kernel<false><<<gs, 256, 0, st>>>(w, d);
-            lora_expand_kernel<false><<<ge, 256, 0, st>>>(w, d);
-        }
+        w.t += m0 * v.rpad;
+        const int rows = std::min(d.M, kRows);
+        // (class, 16 ranks) units that one chunk can hold; K is split over a cluster while that leaves SMs idle
+        const int units = std::min(rows, v.slots) * (v.rpad / 16);
+        const int gx = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, 1216 / chunks)));
+        int ck = 1;
+        while (ck < 8 && static_cast<int64_t>(gx) * chunks * ck < 304 && v.K / (ck * 2) >= 1024) ck *= 2;
+        // two CTAs for each SM, as long as every warp has a unit
+        const int groups = (rows + 15) / 16 + std::min(rows, v.slots + 1);
+        const int64_t most = static_cast<int64_t>(groups) * ((v.N + 31) / 32);
+        const int ex = static_cast<int>(std::min<int64_t>((most + kWarps - 1) / kWarps, std::max(1, 304 / chunks)));
+        const dim3 gs(gx * ck, chunks), ge(ex, chunks);
+        const bool few = rows <= 16;
+        auto shrink = bf16 ? (few ? lora_shrink_kernel<true, true> : lora_shrink_kernel<true, false>)
+                           : (few ? lora_shrink_kernel<false, true> : lora_shrink_kernel<false, false>);
+        cudaError_t e = start(shrink, gs, 32 * kWarps, 0, ck, false, st, w, d, ck);
+        if (!e) e = start(bf16 ? lora_expand_kernel<true> : lora_expand_kernel<false>, ge, 32 * kWarps, 0, 1, true, st, w, d);
+        if (e) return e;
         *launches += 2;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace q4

@@ -106,7 +106,7 @@ gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype)
     h->max_rank = max_rank;
     h->dtype = dtype;
     const size_t each = static_cast<size_t>(slots) * q4::ceil16(max_rank) * 2;
-    cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&h->a), each * K);
+    cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&h->a), each * q4::ceil64(K));
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->b), each * N);
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->slot), slots * sizeof(q4::LoraSlot));
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->status), sizeof(int));

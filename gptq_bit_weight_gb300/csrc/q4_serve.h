@@ -28,11 +28,12 @@ constexpr int kAttnBadPosition = 0x4;  // a position outside the rotary table
 constexpr int kAttnTimeout = 0x8;      // a bounded wait ran out
 
 constexpr int ceil16(int r) { return (r + 15) / 16 * 16; }
+constexpr int ceil64(int k) { return (k + 63) / 64 * 64; }
 
 struct LoraView {
     int K, N, slots, rpad;       // rpad: ceil16(max_rank)
-    const uint16_t *a;           // [slots][rpad][K]; rows rank .. ceil16(rank) - 1 are zero
-    const uint16_t *b;           // [slots][N * rpad]: slot s holds [N][ceil16(rank_s)], padded columns zero
+    const uint16_t *a;           // [slots][rpad * ceil64(K)], layout in q4_lora.cu
+    const uint16_t *b;           // [slots][rpad * N]
     const LoraSlot *slot;        // [slots]
     float *t;                    // [rows][rpad] fp32: scale * x . A^T
     int *status;

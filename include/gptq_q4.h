@@ -435,7 +435,7 @@ typedef struct gptq_q4_lora_s *gptq_q4_lora;
 
 /* An empty pool.  dtype: GPTQ_Q4_DTYPE_FP16 or _BF16, the type of x, y, out,
  * A and B.  K and N positive multiples of 8, 1 <= slots <= 4096,
- * 1 <= max_rank <= 256.  Device memory: slots * ceil16(max_rank) * (K + N)
+ * 1 <= max_rank <= 256.  Device memory: slots * ceil16(max_rank) * (ceil64(K) + N)
  * 16-bit values.  Synchronizes.  NULL on error (status and message as for
  * gptq_q4_make): INVALID_ARGUMENT, UNSUPPORTED (device not sm_103, fp32),
  * OUT_OF_MEMORY, CUDA_ERROR. */
