@@ -9,8 +9,8 @@ from __future__ import annotations
 import torch
 
 from . import (GPTQ4Error, GPTQ_Q4_DTYPE_BF16, GPTQ_Q4_DTYPE_FP16, GPTQ_Q4_DTYPE_FP32, GPTQ_Q4_INVALID_ARGUMENT,
-               gptq_q4_lora_add, gptq_q4_lora_device_error, gptq_q4_lora_free, gptq_q4_lora_make,
-               gptq_q4_lora_reserve, gptq_q4_lora_set)
+               _check, _lib, gptq_q4_lora_device_error, gptq_q4_lora_free, gptq_q4_lora_make, gptq_q4_lora_reserve,
+               gptq_q4_lora_set)
 
 _CODES = {torch.float16: GPTQ_Q4_DTYPE_FP16, torch.bfloat16: GPTQ_Q4_DTYPE_BF16, torch.float32: GPTQ_Q4_DTYPE_FP32}
 
@@ -25,18 +25,26 @@ def _code(dtype) -> int:
     return _CODES[dtype]
 
 
+# A small call's host time is most of it: these two spare a call a Stream object and a wrapper.
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_add = _lib.gptq_q4_lora_add
+
+
 def _rows(t, what: str, width: int, dtype, device):
     """`t` as rows of `width` elements, dense within a row: (tensor [rows, width], row stride)."""
     if t.dtype != dtype or t.device != device:
         _refuse(f"{what} is {t.dtype} on {t.device}: {dtype} on {device} is wanted")
     if t.dim() != 2:
         t = t.reshape(-1, width) if t.dim() else t.reshape(1, -1)
-    if t.shape[1] != width:
-        _refuse(f"{what} has rows of {t.shape[1]} elements: {width} are wanted")
-    if t.stride(1) != 1:
+    rows, have = t.shape
+    stride, inner = t.stride()
+    if have != width:
+        _refuse(f"{what} has rows of {have} elements: {width} are wanted")
+    if inner != 1:
         _refuse(f"{what} is not dense within its rows")
     # one row, or none, has no stride of its own
-    return t, (t.stride(0) if t.shape[0] > 1 else max(width, t.stride(0)) // 8 * 8)
+    return t, rows, stride if rows > 1 else width
 
 
 class LoraPool:
@@ -58,11 +66,11 @@ class LoraPool:
                 _refuse(f"{what} is {t.dtype} on {t.device}: {self.dtype} on {self.device} is wanted")
         a, b = a.contiguous(), b.contiguous()
         gptq_q4_lora_set(self.handle, slot, a.data_ptr(), b.data_ptr(), a.shape[0], scale,
-                         torch.cuda.current_stream(self.device).cuda_stream)
+                         _stream(self.device.index))
 
     def clear(self, slot: int) -> None:
         gptq_q4_lora_set(self.handle, slot, None, None, 0, 0.0,
-                         torch.cuda.current_stream(self.device).cuda_stream)
+                         _stream(self.device.index))
 
     def reserve(self, max_m: int) -> None:
         gptq_q4_lora_reserve(self.handle, max_m)
@@ -71,24 +79,24 @@ class LoraPool:
         """y plus each row's adapter: x [.., K] is the projection's input, y
         [.., N] its output, row_slot int32 [rows] each row's slot (negative:
         none).  out=y adds in place; rows of x, y and out may be strided."""
-        shape = y.shape
-        x2, xs = _rows(x, "x", self.K, self.dtype, self.device)
-        y2, ys = _rows(y, "y", self.N, self.dtype, self.device)
-        M = x2.shape[0]
+        dtype, device = self.dtype, self.device
+        x2, M, xs = _rows(x, "x", self.K, dtype, device)
+        y2, my, ys = _rows(y, "y", self.N, dtype, device)
         if out is None:
-            o2 = torch.empty((M, self.N), dtype=self.dtype, device=self.device)
-            os_ = self.N
+            out = torch.empty(y.shape, dtype=dtype, device=device)
+            at, mo, os_ = out.data_ptr(), my, self.N
         else:
-            o2, os_ = _rows(out, "out", self.N, self.dtype, self.device)
-            if o2.data_ptr() != out.data_ptr():
+            o2, mo, os_ = _rows(out, "out", self.N, dtype, device)
+            at = o2.data_ptr()
+            if at != out.data_ptr():
                 _refuse("out cannot be viewed as rows")
-        if y2.shape[0] != M or o2.shape[0] != M or row_slot.numel() != M:
-            _refuse(f"x has {M} rows, y {y2.shape[0]}, out {o2.shape[0]}, row_slot {row_slot.numel()}")
-        if row_slot.dtype != torch.int32 or row_slot.device != self.device or not row_slot.is_contiguous():
-            _refuse(f"row_slot must be contiguous int32 on {self.device}")
-        gptq_q4_lora_add(self.handle, x2.data_ptr(), xs, row_slot.data_ptr(), M, y2.data_ptr(), ys, o2.data_ptr(),
-                         os_, torch.cuda.current_stream(self.device).cuda_stream)
-        return o2.view(shape) if out is None else out
+        if my != M or mo != M or row_slot.numel() != M:
+            _refuse(f"x has {M} rows, y {my}, out {mo}, row_slot {row_slot.numel()}")
+        if row_slot.dtype != torch.int32 or row_slot.device != device or not row_slot.is_contiguous():
+            _refuse(f"row_slot must be contiguous int32 on {device}")
+        _check(_add(self.handle, x2.data_ptr(), xs, row_slot.data_ptr(), M, y2.data_ptr(), ys, at, os_,
+                    _stream(device.index)))
+        return out
 
     def device_error(self) -> None:
         gptq_q4_lora_device_error(self.handle)

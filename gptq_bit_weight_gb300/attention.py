@@ -7,12 +7,16 @@ include/gptq_q4.h): ``PagedCache`` is one layer's keys and values,
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import (GPTQ_Q4_ROPE_BANDS, GPTQ_Q4_ROPE_LINEAR, GPTQ_Q4_ROPE_NTK, GPTQ_Q4_ROPE_PLAIN, GPTQ_Q4_ROPE_YARN,
-               gptq_q4_attn_append, gptq_q4_attn_attend, gptq_q4_attn_device_error, gptq_q4_attn_free,
-               gptq_q4_attn_make, gptq_q4_attn_set_rope, gptq_q4_batch, gptq_q4_cache, gptq_q4_rope_freqs)
-from .adapters import _code, _refuse, _rows
+               _check, _lib, gptq_q4_attn_device_error, gptq_q4_attn_free, gptq_q4_attn_make, gptq_q4_attn_set_rope,
+               gptq_q4_batch, gptq_q4_cache, gptq_q4_rope_freqs)
+from .adapters import _code, _refuse, _rows, _stream
+
+_append, _attend = _lib.gptq_q4_attn_append, _lib.gptq_q4_attn_attend
 
 _KINDS = {"none": GPTQ_Q4_ROPE_PLAIN, "linear": GPTQ_Q4_ROPE_LINEAR, "ntk": GPTQ_Q4_ROPE_NTK,
           "bands": GPTQ_Q4_ROPE_BANDS, "yarn": GPTQ_Q4_ROPE_YARN}
@@ -28,7 +32,9 @@ class PagedCache:
         if k.stride()[1:] != inner or v.stride()[1:] != inner or k.stride(0) != v.stride(0):
             _refuse("k and v must be dense within a page, with one stride from page to page")
         self.k, self.v = k, v
+        self.kind = (k.dtype, k.device, *k.shape[1:])
         self.struct = gptq_q4_cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0))
+        self.ref = ctypes.byref(self.struct)
 
 
 class PagedBatch:
@@ -47,10 +53,11 @@ class PagedBatch:
             _refuse(f"cu_q {tuple(cu_q.shape)}, kv_len {tuple(kv_len.shape)} and table {tuple(table.shape)} "
                     "must be [batch + 1], [batch] and [batch, width]")
         self.tensors = (cu_q, kv_len, table)
-        self.tokens = tokens
+        self.tokens, self.device = tokens, cu_q.device
         stride = table.stride(0) if batch > 1 else max(table.stride(0), table.shape[1])
         self.struct = gptq_q4_batch(cu_q.data_ptr(), kv_len.data_ptr(), table.data_ptr(), stride, table.shape[1],
                                     batch, tokens, tokens if max_q is None else max_q)
+        self.ref = ctypes.byref(self.struct)
 
 
 class PagedAttention:
@@ -64,6 +71,7 @@ class PagedAttention:
         self.device = torch.device("cuda", torch.cuda.current_device())
         self.handle = gptq_q4_attn_make(q_heads, kv_heads, head_dim, page_size, _code(dtype))
         self._q_width = q_heads * head_dim
+        self._kind = (dtype, self.device, kv_heads, page_size, head_dim)
         self._scale = head_dim ** -0.5
 
     def set_rope(self, rotary_dim: int, max_pos: int, base: float = 10000.0, interleaved: bool = False,
@@ -83,58 +91,61 @@ class PagedAttention:
                               scale if length_scale is None else length_scale, max_pos)
 
     def _check(self, cache: PagedCache, batch: PagedBatch) -> None:
-        k = cache.k
-        if k.dtype != self.dtype or k.device != self.device or \
-                k.shape[1:] != (self.kv_heads, self.page_size, self.head_dim):
-            _refuse(f"the cache is {k.dtype} {tuple(k.shape)} on {k.device}: {self.dtype} [pages, {self.kv_heads}, "
+        if cache.kind != self._kind:
+            dtype, device, *shape = cache.kind
+            _refuse(f"the cache is {dtype} {['pages', *shape]} on {device}: {self.dtype} ['pages', {self.kv_heads}, "
                     f"{self.page_size}, {self.head_dim}] on {self.device} is wanted")
-        if batch.tensors[0].device != self.device:
-            _refuse(f"the batch is on {batch.tensors[0].device}, the handle on {self.device}")
+        if batch.device != self.device:
+            _refuse(f"the batch is on {batch.device}, the handle on {self.device}")
 
     def append(self, qkv, cache: PagedCache, batch: PagedBatch, positions=None, q_out=None):
         """Rotate queries and keys and put keys and values into the cache; qkv
         [tokens, (q_heads + 2 kv_heads) head_dim].  Returns the rotated
         queries [tokens, q_heads, head_dim]."""
         self._check(cache, batch)
-        x, xs = _rows(qkv, "qkv", (self.q_heads + 2 * self.kv_heads) * self.head_dim, self.dtype, self.device)
+        x, rows, xs = _rows(qkv, "qkv", (self.q_heads + 2 * self.kv_heads) * self.head_dim, self.dtype, self.device)
         if q_out is None:
-            q_out = torch.empty((x.shape[0], self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
-        q, qs = self._token_rows(q_out, "q_out")
-        if x.shape[0] != batch.tokens or q.shape[0] != batch.tokens:
-            _refuse(f"qkv has {x.shape[0]} rows and q_out {q.shape[0]}, the batch {batch.tokens} tokens")
+            q_out = torch.empty((rows, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            q, q_rows, qs = q_out, rows, self._q_width
+        else:
+            q, q_rows, qs = self._token_rows(q_out, "q_out")
+        if rows != batch.tokens or q_rows != batch.tokens:
+            _refuse(f"qkv has {rows} rows and q_out {q_rows}, the batch {batch.tokens} tokens")
         if positions is not None and (positions.dtype != torch.int32 or positions.device != self.device or
                                       positions.numel() != batch.tokens or not positions.is_contiguous()):
             _refuse(f"positions must be contiguous int32 [{batch.tokens}] on {self.device}")
-        gptq_q4_attn_append(self.handle, x.data_ptr(), xs, cache.struct, batch.struct,
-                            None if positions is None else positions.data_ptr(), q.data_ptr(), qs,
-                            torch.cuda.current_stream(self.device).cuda_stream)
+        _check(_append(self.handle, x.data_ptr(), xs, cache.ref, batch.ref,
+                       None if positions is None else positions.data_ptr(), q.data_ptr(), qs,
+                       _stream(self.device.index)))
         return q_out
 
     def attend(self, q, cache: PagedCache, batch: PagedBatch, scale: float | None = None, window: int = 0, out=None):
         """Attention of the new tokens' queries q [tokens, q_heads, head_dim]
         over the cache; scale defaults to head_dim ** -0.5, window 0 is none."""
         self._check(cache, batch)
-        x, xs = self._token_rows(q, "q")
+        x, rows, xs = self._token_rows(q, "q")
         if out is None:
-            out = torch.empty((x.shape[0], self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
-        o, os_ = self._token_rows(out, "out")
-        if x.shape[0] != batch.tokens or o.shape[0] != batch.tokens:
-            _refuse(f"q has {x.shape[0]} rows and out {o.shape[0]}, the batch {batch.tokens} tokens")
-        gptq_q4_attn_attend(self.handle, x.data_ptr(), xs, cache.struct, batch.struct,
-                            self._scale if scale is None else scale, window, o.data_ptr(), os_,
-                            torch.cuda.current_stream(self.device).cuda_stream)
+            out = torch.empty((rows, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            o, o_rows, os_ = out, rows, self._q_width
+        else:
+            o, o_rows, os_ = self._token_rows(out, "out")
+        if rows != batch.tokens or o_rows != batch.tokens:
+            _refuse(f"q has {rows} rows and out {o_rows}, the batch {batch.tokens} tokens")
+        _check(_attend(self.handle, x.data_ptr(), xs, cache.ref, batch.ref, self._scale if scale is None else scale,
+                       window, o.data_ptr(), os_, _stream(self.device.index)))
         return out
 
     def _token_rows(self, t, what: str):
         """[tokens, q_heads, head_dim] (a view of wider rows allowed) or [tokens, q_heads * head_dim]."""
-        if t.dim() == 3:
-            if t.shape[1] != self.q_heads or t.shape[2] != self.head_dim or t.stride(1) != self.head_dim or \
-                    t.stride(2) != 1:
-                _refuse(f"{what} {tuple(t.shape)} must be [tokens, {self.q_heads}, {self.head_dim}], dense in a token")
-            if t.dtype != self.dtype or t.device != self.device:
-                _refuse(f"{what} is {t.dtype} on {t.device}: {self.dtype} on {self.device} is wanted")
-            return t, (t.stride(0) if t.shape[0] > 1 else self._q_width)
-        return _rows(t, what, self._q_width, self.dtype, self.device)
+        if t.dim() != 3:
+            return _rows(t, what, self._q_width, self.dtype, self.device)
+        rows, heads, width = t.shape
+        stride, s1, s2 = t.stride()
+        if heads != self.q_heads or width != self.head_dim or s1 != width or s2 != 1:
+            _refuse(f"{what} {tuple(t.shape)} must be [tokens, {self.q_heads}, {self.head_dim}], dense in a token")
+        if t.dtype != self.dtype or t.device != self.device:
+            _refuse(f"{what} is {t.dtype} on {t.device}: {self.dtype} on {self.device} is wanted")
+        return t, rows, stride if rows > 1 else self._q_width
 
     def device_error(self) -> None:
         gptq_q4_attn_device_error(self.handle)
