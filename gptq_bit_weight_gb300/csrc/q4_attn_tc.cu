@@ -82,6 +82,19 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
+// One lane of a converged warp.  The compiler knows a region behind it to be
+// one thread's, so the operands of tcgen05.mma go to uniform registers
+// directly; behind a test of the lane number each MMA took some 90 cycles to
+// issue, more than the 64 that it runs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
 // D += A . B with A in tensor memory: row = lane, two 16-bit values of K in a column.
 __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -128,6 +141,33 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ uint64_t pair_bits(uint32_t x, uint32_t y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x), "r"(y));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool wait_all(bool alive, uint32_t bar, uint32_t parity) {
     if (alive) alive = mbar_wait(bar, parity);
@@ -190,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool alive = true;
-    // 168 registers a thread at launch: 256 x 200 + 128 x 104 = 384 x 168
+    // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168
     const bool work = sh.begin < sh.end;
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------------------------------------- softmax: a thread holds a row
         const int me = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -222,13 +262,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, s + 32 * q);
                     tmem_wait_ld();
                     if (key_t + kKt - 1 > all_hi || key_t <= all_lo) {
+                        // visible keys of 32 as bits: those up to lim, without those up to lim_lo
+                        auto upto = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
 #pragma unroll
-                        for (int e = 0; e < 128; ++e)
-                            if (key_t + e > lim || key_t + e <= lim_lo) s[e] = 0xff800000u;
+                        for (int q = 0; q < 4; ++q) {
+                            const int k0 = key_t + 32 * q - 1;
+                            const uint32_t seen = upto(lim - k0) & ~upto(lim_lo - k0);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) s[32 * q + e] = 0xff800000u;
+                        }
                     }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float top[4];
 #pragma unroll
-                    for (int e = 0; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
+                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+#pragma unroll
+                    for (int e = 8; e < 128; e += 2)
+                        top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     const bool first = j == part.j0;
                     const bool grows = first ? mx > m : (mx - m) * c > kRescale;
@@ -253,21 +303,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m * c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t p[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float x = ex2(fmaf(__uint_as_float(s[32 * h + 2 * e]), c, -ref));
-                            const float y = ex2(fmaf(__uint_as_float(s[32 * h + 2 * e + 1]), c, -ref));
-                            sum[2 * (e & 1)] += x;
-                            sum[2 * (e & 1) + 1] += y;
-                            p[e] = pack2<BF>(x, y);
+                            const float2 x = unpair(fma2(pair_bits(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, ref2));
+                            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                            sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
+                            p[e] = pack2<BF>(y.x, y.y);
                         }
                         tmem_st16(tS + 16 * h, p);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 total = unpair(add2(sum[0], sum[1]));
+                    l += total.x + total.y;
                     tmem_wait_st();
                     tc_fence_before();
                     mbar_arrive(p_ready(me));
@@ -375,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (!work) {
         } else if (warp == kLoader) {
             const int pages_log2 = min(a.p.page_log2, kKtLog2), box = 1 << pages_log2;   // tokens of a box
@@ -431,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = max(seq - S, 0); i < seq; ++i) mbar_wait(full(i % S), (i / S) & 1);
             }
         } else if (warp == kIssuer) {
-            if (lane == 0) {
+            if (elect_one()) {
                 constexpr uint32_t fmt = BF ? (1u << 7) | (1u << 10) : 0u;         // A and B bf16
                 constexpr uint32_t id_qk = idesc_f16(128, kKt, false) | fmt, id_pv = idesc_f16(128, D, true) | fmt;
                 int tiles = 0, items = 0, uses[2] = {0, 0};
