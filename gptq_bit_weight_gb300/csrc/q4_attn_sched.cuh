@@ -87,6 +87,12 @@ __device__ __forceinline__ bool next_item(const SchedParams &p, Item &it) {
     return true;
 }
 
+// a / b for a >= 0, b > 0 and a result in int; 32-bit where both fit.
+__device__ __forceinline__ int div_units(long long a, long long b) {
+    if (((a | b) >> 31) == 0) return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+    return static_cast<int>(a / b);
+}
+
 struct Share {
     long long begin, end;    // units of this CTA
     long long per;           // units of every CTA but the last with any
@@ -95,8 +101,8 @@ struct Share {
 // Shared memory of sched_share.
 struct SchedSmem {
     long long warp_sum[32];
-    int b, head, tile;
-    long long rem, units, u;
+    int b, head, tile, q0, ql, kv;
+    long long rem, u;
 };
 
 // This CTA's share and, if it has one, its first item.  Called by all NT
@@ -106,9 +112,10 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = (p.b.batch + NT - 1) / NT;     // requests of a thread, in order
     long long mine = 0, last = 0;
+    Request r{0, 0, 0, false};
     for (int i = 0; i < chunk; ++i) {
         const int b = tid * chunk + i;
-        Request r{0, 0, 0, false};
+        r = Request{0, 0, 0, false};
         if (b < p.b.batch) {
             r = load_request(p.b, b, p.page_log2);
             if (r.bad && cta == 0) atomicOr(status, kAttnBadBatch);
@@ -140,7 +147,8 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
         total += sm.warp_sum[w];
     }
     Share s;
-    s.per = max((total + ctas - 1) / ctas, 1ll);
+    s.per = total + ctas < 1ll << 31 ? max(static_cast<uint32_t>(total + ctas - 1) / static_cast<uint32_t>(ctas), 1u)
+                                     : (total + ctas - 1) / ctas;
     s.begin = min(cta * s.per, total);
     s.end = min(s.begin + s.per, total);
     before += upto - mine;
@@ -150,22 +158,28 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
         int b = tid * chunk;
         for (;; ++b) {
             if (chunk > 1) {
-                const Request r = load_request(p.b, b, p.page_log2);
+                r = load_request(p.b, b, p.page_log2);
                 units = tile_units(p, r.ql, r.kv, 0, 1);
             }
             if (rem < units * p.hkv) break;
             rem -= units * p.hkv;
         }
-        const int head = static_cast<int>(rem / units);
+        const int head = div_units(rem, units);
         sm.b = b;
         sm.head = head;
         sm.rem = rem - head * units;
+        sm.q0 = r.q0;
+        sm.ql = r.ql;
+        sm.kv = r.kv;
     }
     __syncthreads();
     if (s.begin >= s.end) return s;
     it.b = sm.b;
     it.head = sm.head;
-    load_item_request(p, it);
+    it.q0 = sm.q0;
+    it.ql = sm.ql;
+    it.kv = sm.kv;
+    it.tiles = row_tiles(p, it.ql);
     if (warp == 0) {
         // the row tile: a scan over 32 tiles at a time
         long long rem = sm.rem;

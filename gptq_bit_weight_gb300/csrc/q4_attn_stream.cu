@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             continue;
         }
-        const int c0 = static_cast<int>(it.u / sh.per), c1 = static_cast<int>((it.u + it.n - 1) / sh.per);
+        const int c0 = div_units(it.u, sh.per), c1 = div_units(it.u + it.n - 1, sh.per);
         auto piece = [&](int cta) { return a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece; };
         if (wk == 0) {
             float *w = piece(blockIdx.x);

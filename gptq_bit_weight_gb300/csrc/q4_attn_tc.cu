@@ -13,8 +13,8 @@
 // tiles) against key tiles of 128 tokens:
 //   warps 0-3, 4-7  softmax of the two row tiles: one thread for each row
 //                   reads its scores (tcgen05.ld), writes p back over them
-//                   as the A operand of the second product (tcgen05.st),
-//                   rescales and, at the end, stores the output
+//                   as the A operand of the second product (tcgen05.st), in
+//                   two halves, rescales and, at the end, stores the output
 //   warp 8          loads queries, keys and values by TMA (one box for each
 //                   page and 64 columns) into a ring of half-stages
 //   warp 9          one thread issues tcgen05.mma: while one row tile's
@@ -38,8 +38,9 @@ namespace {
 using namespace tc;
 
 constexpr int kKtLog2 = 7, kKt = 1 << kKtLog2;
-constexpr int kThreads = 384;
-constexpr int kLoader = 8, kIssuer = 9, kCleaner = 10;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+constexpr int kLoader = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kCleaner = kSoftmaxWarps + 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
 
@@ -48,7 +49,7 @@ struct Cfg {
     static constexpr int D = D_;
     static constexpr int kHalf = kKt * D * 2;    // bytes of a half-stage: keys or values of a tile
     static constexpr int kQ = 128 * D * 2;       // of one row tile's queries
-    static constexpr int kMisc = 2048;
+    static constexpr int kMisc = 1024;
     static constexpr int kRoom = (232448 - 1024 - 2 * kQ - kMisc) / kHalf;
     static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
     static constexpr int kSmem = 2 * kQ + kStages * kHalf + kMisc + 1024;
@@ -168,6 +169,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float row_max(const uint32_t (&s)[128]) {
+    float top[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+#pragma unroll
+    for (int e = 16; e < 128; e += 2)
+        top[e >> 1 & 7] = max3(top[e >> 1 & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+    return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
+}
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool wait_all(bool alive, uint32_t bar, uint32_t parity) {
     if (alive) alive = mbar_wait(bar, parity);
@@ -201,13 +211,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto s_full = [&](int i) { return q_full + 24 + 8u * i; };
     auto p_ready = [&](int i) { return q_full + 40 + 8u * i; };
     auto pv_done = [&](int i) { return q_full + 56 + 8u * i; };
+    auto p_half = [&](int i) { return q_full + 72 + 8u * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
-    int *last_flag = reinterpret_cast<int *>(misc + 516);
-    SchedSmem &sched = *reinterpret_cast<SchedSmem *>(misc + 1024);
-    static_assert(8 * (3 * S + 9) <= 512 && 1024 + sizeof(SchedSmem) <= C::kMisc, "misc region");
+    int *last_flags = reinterpret_cast<int *>(misc + 1016);             // of the first and the last item
+    SchedSmem &sched = *reinterpret_cast<SchedSmem *>(misc + 520);
+    static_assert(8 * (3 * S + 11) <= 512 && 520 + sizeof(SchedSmem) <= 1016, "misc region");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        for (const CUtensorMap *map : {&tmQ, &tmK, &tmV}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
@@ -218,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(done, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
+            mbar_init(p_half(i), 128);
             mbar_init(p_ready(i), 128);
             mbar_init(pv_done(i), 1);
         }
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true;
     // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168
     const bool work = sh.begin < sh.end;
-    if (warp < 8) {
+    if (warp < kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------------------------------------- softmax: a thread holds a row
         const int me = warp >> 2, row = threadIdx.x & 127;
@@ -273,50 +286,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!(seen >> e & 1)) s[32 * q + e] = 0xff800000u;
                         }
                     }
-                    float top[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-#pragma unroll
-                    for (int e = 8; e < 128; e += 2)
-                        top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     const bool first = j == part.j0;
-                    const bool grows = first ? mx > m : (mx - m) * c > kRescale;
-                    if (__any_sync(0xffffffffu, grows)) {
+                    if (first) m = row_max(s);
+                    // The reference is the last tile's, so no exponential waits for this tile's maximum, which
+                    // is found beside the first half of them; only if it is too large they are done again.
+                    uint64_t sum[2];
+                    auto exponentials = [&](int half) {
+                        const float ref = m == -INFINITY ? 0.f : m * c;
+                        const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+#pragma unroll
+                        for (int h = 2 * half; h < 2 * half + 2; ++h) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 x = unpair(fma2(pair_bits(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, ref2));
+                                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                                sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
+                                p[e] = pack2<BF>(y.x, y.y);
+                            }
+                            tmem_st16(tS + 16 * h, p);
+                        }
+                    };
+                    for (;;) {
+                        sum[0] = sum[1] = 0;
+                        exponentials(0);
+                        if (first) break;
+                        const float mx = row_max(s);
+                        const bool grows = (mx - m) * c > kRescale;
+                        if (!__any_sync(0xffffffffu, grows)) break;
                         const float to = grows ? mx : m;
                         // from a row without any key so far, nothing is kept
                         const float f = grows ? ex2((m - to) * c) : 1.f;
                         l *= f;
                         m = to;
-                        if (!first) {
-                            alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
-                            tc_fence_after();
+                        alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
+                        tc_fence_after();
 #pragma unroll
-                            for (int q = 0; q < D / 16; ++q) {
-                                uint32_t o[16];
-                                tmem_ld16(tO + 16 * q, o);
-                                tmem_wait_ld();
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * q, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st16(tO + 16 * q, o);
-                            }
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(tO + 16 * q, o);
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m * c;
-                    const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
-                    uint64_t sum[2] = {0, 0};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 x = unpair(fma2(pair_bits(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, ref2));
-                            const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                            sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
-                            p[e] = pack2<BF>(y.x, y.y);
-                        }
-                        tmem_st16(tS + 16 * h, p);
-                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_half(me));
+                    exponentials(1);
                     const float2 total = unpair(add2(sum[0], sum[1]));
                     l += total.x + total.y;
                     tmem_wait_st();
@@ -329,101 +347,117 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------ output, or a piece for the workspace
             uint16_t *dst = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                             (it.head * a.p.group + head_in) * D;
-            const bool whole = part.j0 == 0 && part.j1 == it.n;
-            if (whole) {
+            auto store = [&](const float *o, float inv, int q) {       // 32 columns
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * v) =
+                        make_uint4(pack2<BF>(o[8 * v] * inv, o[8 * v + 1] * inv), pack2<BF>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
+                                   pack2<BF>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
+                                   pack2<BF>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+            };
+            if (part.j0 == 0 && part.j1 == it.n) {
                 if (active) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
+                        float o[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
                         if (it.hi > 0) {
-                            tmem_ld32(tO + 32 * q, o);
+                            tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(o));
                             tmem_wait_ld();
                         }
-                        if (valid)
+                        if (l == 0.f)                    // a row that sees nothing
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = l == 0.f ? 0u
-                                                    : pack2<BF>(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                                                __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        if (valid) store(o, inv, q);
                     }
                     tc_fence_before();
                 }
                 continue;
             }
-            const int c0 = static_cast<int>(it.u / sh.per), c1 = static_cast<int>((it.u + it.n - 1) / sh.per);
-            // [D / 4][128] float4 of each row tile, then [2][128] (m, l)
+            const int me_cta = blockIdx.x;
+            const int c0 = div_units(it.u, sh.per), c1 = div_units(it.u + it.n - 1, sh.per);
+            // of each row tile [D / 4][128] float4, then [2][128] (m, l)
             auto piece = [&](int cta) { return a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece; };
-            if (active) {
-                float4 *w = reinterpret_cast<float4 *>(piece(blockIdx.x)) + me * 128 * (D / 4) + row;
-#pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * q, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        __stcg(w + (8 * q + v) * 128,
-                               make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                           __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3])));
-                }
-                tc_fence_before();
-                __stcg(reinterpret_cast<float2 *>(piece(blockIdx.x) + 2 * 128 * D) + me * 128 + row, make_float2(m, l));
-                __threadfence();
-            }
-            bar_softmax();
+            auto columns = [&](int cta, int q) {
+                return reinterpret_cast<float4 *>(piece(cta)) + (me * (D / 4) + 8 * q) * 128 + row;
+            };
+            auto ml = [&](int cta) { return reinterpret_cast<float2 *>(piece(cta) + 2 * 128 * D) + me * 128 + row; };
+            int *last_flag = last_flags + (it.u >= sh.begin);
+            // if every other piece is there already, this one need not be written
             if (threadIdx.x == 0) {
+                const int there = *reinterpret_cast<volatile int *>(a.tickets + c0);
                 __threadfence();
-                const int before = atomicAdd(a.tickets + c0, 1);
-                *last_flag = before == c1 - c0;
-                if (before == c1 - c0) a.tickets[c0] = 0;
-                __threadfence();
+                *last_flag = there == c1 - c0;
             }
             bar_softmax();
-            if (*reinterpret_cast<volatile int *>(last_flag) && valid) {
-                float top = -INFINITY;
-                auto ml = [&](int cta) {
-                    return __ldcg(reinterpret_cast<const float2 *>(piece(cta) + 2 * 128 * D) + me * 128 + row);
-                };
-                for (int k = c0; k <= c1; ++k) top = fmaxf(top, ml(k).x);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float sum = 0.f;
-                for (int k = c0; k <= c1; ++k) {
-                    const float2 v = ml(k);
-                    sum += v.y * ex2((v.x - ref) * c);
-                }
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    float4 acc[8];
+            bool last = *reinterpret_cast<volatile int *>(last_flag);
+            if (!last) {
+                if (active) {
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = c0; k <= c1; ++k) {
-                        const float f = ex2((ml(k).x - ref) * c);
-                        const float4 *w = reinterpret_cast<const float4 *>(piece(k)) + me * 128 * (D / 4) + row;
+                    for (int q = 0; q < D / 32; ++q) {
+                        float o[32];
+                        tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(o));
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            const float4 x = __ldcg(w + (8 * q + v) * 128);
-                            acc[v].x += x.x * f;
-                            acc[v].y += x.y * f;
-                            acc[v].z += x.z * f;
-                            acc[v].w += x.w * f;
-                        }
+                        for (int v = 0; v < 8; ++v)
+                            __stcg(columns(me_cta, q) + v * 128, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
                     }
+                    __stcg(ml(me_cta), make_float2(m, l));
+                    __threadfence();
+                }
+                bar_softmax();
+                if (threadIdx.x == 0) {
+                    __threadfence();
+                    *last_flag = atomicAdd(a.tickets + c0, 1) == c1 - c0;
+                    __threadfence();
+                }
+                bar_softmax();
+                last = *reinterpret_cast<volatile int *>(last_flag);
+            }
+            if (last) {
+                // the pieces in the order of their CTAs, this one's from tensor memory
+                if (threadIdx.x == 0) a.tickets[c0] = 0;
+                if (active) {
+                    float top = m;
+                    for (int k = c0; k <= c1; ++k)
+                        if (k != me_cta) top = fmaxf(top, __ldcg(ml(k)).x);
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float sum = 0.f;
+                    for (int k = c0; k <= c1; ++k) {
+                        const float2 v = k == me_cta ? make_float2(m, l) : __ldcg(ml(k));
+                        sum += v.y * ex2((v.x - ref) * c);
+                    }
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        float acc[32];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const float4 x = acc[2 * v], y = acc[2 * v + 1];
-                        *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * v) =
-                            make_uint4(pack2<BF>(x.x * inv, x.y * inv), pack2<BF>(x.z * inv, x.w * inv),
-                                       pack2<BF>(y.x * inv, y.y * inv), pack2<BF>(y.z * inv, y.w * inv));
+                        for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+                        for (int k = c0; k <= c1; ++k) {
+                            float x[32], f;
+                            if (k == me_cta) {
+                                tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(x));
+                                tmem_wait_ld();
+                                f = ex2((m - ref) * c);
+                            } else {
+#pragma unroll
+                                for (int v = 0; v < 8; ++v) {
+                                    const float4 y = __ldcg(columns(k, q) + v * 128);
+                                    x[4 * v] = y.x, x[4 * v + 1] = y.y, x[4 * v + 2] = y.z, x[4 * v + 3] = y.w;
+                                }
+                                f = ex2((__ldcg(ml(k)).x - ref) * c);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) acc[e] += x[e] * f;
+                        }
+                        if (valid) store(acc, inv, q);
                     }
                 }
             }
+            tc_fence_before();
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -500,12 +534,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     umma_commit(s_full(i));
                 };
-                auto pv = [&](int i, int seq, bool first) {
+                auto pv = [&](int i, int seq, bool first) {          // each half of p as soon as it is there
                     const uint32_t vb = ring + (seq % S) * C::kHalf;
 #pragma unroll
-                    for (int kk = 0; kk < kKt / 16; ++kk)
-                        umma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
-                                    smem_desc_sw128(vb + kk * 2048, kKt * 128, 1024), id_pv, !first || kk != 0);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t bar = half ? p_ready(i) : p_half(i);
+                        if (alive) alive = mbar_poll(bar, uses[i] & 1);
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            umma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
+                                        smem_desc_sw128(vb + kk * 2048, kKt * 128, 1024), id_pv, !first || kk != 0);
+                    }
+                    ++uses[i];
                     umma_commit(pv_done(i));
                 };
                 for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
@@ -523,7 +564,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         wait(full(sv % S), sv / S);
                         if (next) wait(full(sk % S), sk / S);
                         for (int i = 0; i < two; ++i) {
-                            wait(p_ready(i), uses[i]++);
                             pv(i, sv, j == 0);
                             if (next) qk(i, sk);
                         }
