@@ -14,12 +14,25 @@
 
 namespace q4 {
 
+// x / d for 0 <= x < 2^31 with m = 2^32 / d rounded down: the high product is
+// the quotient or one less.  (The compiler's division is some 25 instructions,
+// and the walk over the items is in every role.)
+struct FastDiv {
+    uint32_t d, m;
+    __host__ __device__ explicit FastDiv(int d_) : d(d_), m(d_ > 1 ? static_cast<uint32_t>((1ull << 32) / d_) : 0xffffffffu) {}
+    __device__ __forceinline__ int operator()(int x) const {
+        const uint32_t q = __umulhi(static_cast<uint32_t>(x), m);
+        return static_cast<int>(q + (static_cast<uint32_t>(x) - q * d >= d));
+    }
+};
+
 struct SchedParams {
     AttnBatch b;
-    int hkv, group, page_log2;
-    int step;        // rows of a row tile
-    int kt_log2;     // log2 of the tokens of a key tile
-    int window;
+    int hkv, page_log2, window;
+    int kt_log2;      // log2 of the tokens of a key tile
+    FastDiv group;    // query heads of a key/value head
+    int step_log2;    // log2 of the rows of a row tile, or -1:
+    FastDiv tokens;   // tokens of a row tile, where tiles hold whole tokens
 };
 
 struct Item {
@@ -32,14 +45,20 @@ struct Item {
 };
 
 __device__ __forceinline__ int row_tiles(const SchedParams &p, int ql) {
-    return (ql * p.group + p.step - 1) / p.step;
+    if (p.step_log2 < 0) return p.tokens(ql + static_cast<int>(p.tokens.d) - 1);
+    return (ql * static_cast<int>(p.group.d) + (1 << p.step_log2) - 1) >> p.step_log2;
 }
 
 // The tokens, keys and key tiles of row tile `it.tile`.
 __device__ __forceinline__ void fill_tile(const SchedParams &p, Item &it) {
-    const int r0 = it.tile * p.step, r1 = min(r0 + p.step, it.ql * p.group);
-    it.t0 = r0 / p.group;
-    it.t1 = (r1 - 1) / p.group;
+    if (p.step_log2 < 0) {
+        it.t0 = it.tile * static_cast<int>(p.tokens.d);
+        it.t1 = min(it.t0 + static_cast<int>(p.tokens.d), it.ql) - 1;
+    } else {
+        const int r0 = it.tile << p.step_log2, r1 = min(r0 + (1 << p.step_log2), it.ql * static_cast<int>(p.group.d));
+        it.t0 = p.group(r0);
+        it.t1 = p.group(r1 - 1);
+    }
     const int own = it.kv - it.ql;                   // index of new token 0
     it.hi = min(own + it.t1 + 1, it.kv);
     it.lo = p.window > 0 ? max(0, own + it.t0 - p.window + 1) : 0;
@@ -55,6 +74,7 @@ __device__ __forceinline__ long long tile_units(const SchedParams &p, int ql, in
     it.kv = kv;
     const int tiles = row_tiles(p, ql);
     long long sum = 0;
+#pragma unroll 1
     for (it.tile = i0; it.tile < tiles; it.tile += stride) {
         fill_tile(p, it);
         sum += it.n;
@@ -77,6 +97,7 @@ __device__ __forceinline__ bool next_item(const SchedParams &p, Item &it) {
         it.tile = 0;
         if (++it.head == p.hkv) {
             it.head = 0;
+#pragma unroll 1
             do {
                 if (++it.b >= p.b.batch) return false;
                 load_item_request(p, it);
@@ -113,6 +134,7 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
     const int chunk = (p.b.batch + NT - 1) / NT;     // requests of a thread, in order
     long long mine = 0, last = 0;
     Request r{0, 0, 0, false};
+#pragma unroll 1
     for (int i = 0; i < chunk; ++i) {
         const int b = tid * chunk + i;
         r = Request{0, 0, 0, false};
@@ -156,6 +178,7 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
         // this thread's requests hold the first unit: find which
         long long rem = s.begin - before, units = last;
         int b = tid * chunk;
+#pragma unroll 1
         for (;; ++b) {
             if (chunk > 1) {
                 r = load_request(p.b, b, p.page_log2);
@@ -183,6 +206,7 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
     if (warp == 0) {
         // the row tile: a scan over 32 tiles at a time
         long long rem = sm.rem;
+#pragma unroll 1
         for (int base = 0;; base += 32) {
             it.tile = base + lane;
             it.n = 0;

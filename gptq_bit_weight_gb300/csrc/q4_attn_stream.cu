@@ -7,9 +7,9 @@
 //   p = 2^(s - m) rounded to 16 bits for its product with v (l sums the
 //   unrounded ones), o = sum p v in fp32; o / l rounded once.
 //
-// One CTA per SM.  Warp 8 loads key tiles of 128 tokens by TMA, one box for
-// each page and 64 columns, into a ring of half-stages (keys, values, keys,
-// ..).  The other eight warps split each tile's tokens (and, from 64 rows on,
+// One CTA per SM.  Warps 8 and 9 load key tiles of 128 tokens by TMA, keys and
+// values, one box for each page and 64 columns, into a ring of half-stages
+// (keys, values, keys, ..).  The other eight warps split each tile's tokens (and, from 64 rows on,
 // the rows) and keep maximum, sum and output of their own; they join at the
 // end of an item.  Items cut by the shares join through the workspace: the
 // CTA whose piece arrives last adds the pieces in order.
@@ -18,8 +18,7 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "q4_attn_sched.cuh"
-#include "q4_tc.cuh"
+#include "q4_attn_tma.cuh"
 
 namespace q4 {
 
@@ -27,9 +26,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kKtLog2 = 7, kKt = 1 << kKtLog2;
 constexpr int kWarps = 8;                       // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kThreads = 32 * (kWarps + 2);     // and two loaders
 
 template <int D_, int MT_, int WR_>
 struct Cfg {
@@ -38,6 +36,7 @@ struct Cfg {
     static constexpr int WR = WR_;              // warps along the rows
     static constexpr int WK = kWarps / WR;      // warps along the keys
     static constexpr int RT = 16 * MT * WR;     // rows of a row tile
+    static constexpr int kRtLog2 = RT == 16 ? 4 : RT == 32 ? 5 : 6;
     static constexpr int KPW = kKt / WK;        // keys of a warp in a tile
     static constexpr int kHalf = kKt * D * 2;   // bytes of a half-stage
     static constexpr int kQ = RT * D * 2;       // query fragments, double-buffered
@@ -61,15 +60,6 @@ struct Args {
     int *tickets;                // [CTAs], zero between calls
     int *status;
 };
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-        "[%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -97,12 +87,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4 &a, uint32_t
             : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
-// A bounded wait by a whole warp; once one has run out, no more waiting: the
-// roles go through their loops, on whatever is there, and the CTA ends.
-__device__ __forceinline__ bool wait_all(bool alive, uint32_t bar, uint32_t parity) {
-    if (alive) alive = mbar_wait(bar, parity);
-    return __all_sync(0xffffffffu, alive);
-}
 // 2^x; 2^-inf = 0.
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -132,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        for (const CUtensorMap *map : {&tmK, &tmV}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int s = 0; s < S; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), kWarps);
@@ -142,55 +127,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Share sh = sched_share<kThreads>(a.p, sched, blockIdx.x, gridDim.x, a.status, it);
     if (sh.begin >= sh.end) return;
 
-    if (warp == kWarps) {
-        // -------------------------------------------------- loader
-        const int pages_log2 = min(a.p.page_log2, kKtLog2), box = 1 << pages_log2;   // tokens of a box
-        const int boxes = kKt >> pages_log2;                                        // of a tile
-        int seq = 0, bad = 0;
+    if (warp >= kWarps) {
+        // -------------------------------------------------- loaders: keys, values
+        const bool values = warp > kWarps;
+        int seq = values, bad = 0;
         bool alive = true;
-        for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
+        for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
             if (it.hi <= 0) continue;
             const int j0 = static_cast<int>(max(sh.begin - it.u, 0ll));
             const int j1 = static_cast<int>(min(sh.end - it.u, static_cast<long long>(it.n)));
-            const int32_t *table = a.p.b.table + it.b * a.p.b.table_stride;
-            for (int j = j0; j < j1; ++j) {
-                const int key = ((it.first + j) << kKtLog2) + lane * box;
-                const bool wanted = lane < boxes && key < it.hi && key + box > it.lo;
-                int page = wanted ? table[key >> a.p.page_log2] : 0;
-                if (page < 0 || page >= a.c.pages) {
-                    bad = kAttnBadPage;
-                    page = 0;
-                }
-                const int bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * box * D * 2;
-                const int row = key & ((1 << a.p.page_log2) - 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++seq) {
-                    const int s = seq % S;
-                    if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
-                    if (!alive) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
-                    __syncwarp();
-                    if (wanted)
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_4d(base + s * C::kHalf + h * (kKt * 128) + lane * box * 128, kv ? &tmV : &tmK,
-                                        full(s), 64 * h, row, it.head, page);
-                }
+            const PageWalk walk(a.p, it, a.c.pages);
+            TilePages next = walk.tile(it, j0, bad);
+            for (int j = j0; j < j1; ++j, seq += 2) {
+                const TilePages t = next;
+                if (j + 1 < j1) next = walk.tile(it, j + 1, bad);            // on its way while this one waits
+                const int s = seq % S;
+                if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
                 if (!alive) break;
+                walk.copy<D>(t, base + s * C::kHalf, values ? &tmV : &tmK, full(s), it.head);
             }
-            if (!alive) break;
         }
         if (bad) atomicOr(a.status, bad);
         if (!alive) {
             // a consumer stopped answering: let the copies in flight land before the CTA can exit
             if (lane == 0) atomicOr(a.status, kAttnTimeout);
-            for (int i = max(seq - S, 0); i < seq; ++i) mbar_wait(full(i % S), (i / S) & 1);
+            for (int i = seq - 2; i >= 0 && i > seq - 2 - S; i -= 2) wait_bounded(full(i % S), (i / S) & 1);
         }
         return;
     }
 
     // ------------------------------------------------------ consumers
     const int wr = warp % WR, wk = warp / WR, g = lane >> 2, t4 = lane & 3;
-    const int group = a.p.group;
+    const int group = a.p.group.d;
     bool alive = true;
     int seq = 0, buf = 0;
     for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it), buf ^= 1) {
@@ -205,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 2; ++h) {
                 const int r = f / KS * 16 + g + 8 * h;
                 if (r < rows) {
-                    const int rr = it.tile * C::RT + r, t = rr / group;
+                    const int rr = it.tile * C::RT + r, t = a.p.group(rr);
                     const uint16_t *src = a.q + static_cast<int64_t>(it.q0 + t) * a.q_stride +
                                           (it.head * group + rr - t * group) * D + f % KS * 16 + 2 * t4;
                     w[h] = *reinterpret_cast<const uint32_t *>(src);
@@ -227,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m[i][h] = -INFINITY;
                 l[i][h] = 0.f;
                 const int r = it.tile * C::RT + (wr * MT + i) * 16 + g + 8 * h;
-                lim[i][h] = it.kv - it.ql + min(r / group, it.t1);
+                lim[i][h] = it.kv - it.ql + min(a.p.group(r), it.t1);
             }
         }
         const int lim_min = it.kv - it.ql + it.t0, lim_max = it.kv - it.ql + it.t1;
@@ -409,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto store = [&](int i_global, int n, int h, float x, float y, float inv) {
             const int r = i_global * 16 + g + 8 * h;
             if (r >= rows || r >= C::RT) return;
-            const int rr = it.tile * C::RT + r, t = rr / group;
+            const int rr = it.tile * C::RT + r, t = a.p.group(rr);
             *reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                                           (it.head * group + rr - t * group) * D + 8 * n + 2 * t4) =
                 pack2<BF>(x * inv, y * inv);
@@ -495,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <class C>
 cudaError_t launch(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
                    const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
-    Args args{{b, s.hkv, s.group, s.page_log2, C::RT, kKtLog2, a.window}, c, a.q, a.out, a.q_stride, a.out_stride,
+    Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), C::kRtLog2, FastDiv(1)}, c, a.q, a.out, a.q_stride, a.out_stride,
               a.scale * 1.4426950408889634f, s.hq, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_stream_kernel<true, C> : attend_stream_kernel<false, C>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);

@@ -1,22 +1,23 @@
 // Attention of chunks of new tokens over the paged cache on the 5th-generation
 // tensor cores (tcgen05), scores and outputs in tensor memory.
 //
-//   scores s = q . k (fp32); reference maximum m and sum l of each row,
+//   scores s = q . k (fp32); reference m and sum l of each row,
 //   p = 2^(c (s - m)), c = scale log2(e), rounded to 16 bits for its product
 //   with v (l sums the unrounded ones); o = sum p v in fp32; o / l rounded
-//   once.  m follows the running maximum only when a row's maximum has risen
-//   by more than 2^8 in p, so the output in tensor memory is rescaled rarely;
-//   p stays below 2^8, within fp16, and l and o stay exact to fp32 either way.
+//   once.  m is the maximum of the first key tile, and is raised to a later
+//   tile's only when the p of a tile sum to more than 2^12: any m at or
+//   below the row's maximum gives the same result as long as p fits 16 bits,
+//   so most tiles need no maximum and no rescaling of the output.
 //
 // One CTA per SM works on two tiles of up to 128 rows at a time (row = token x
 // query head of the group, so the heads that share a key/value head share its
 // tiles) against key tiles of 128 tokens:
 //   warps 0-3, 4-7  softmax of the two row tiles: one thread for each row
 //                   reads its scores (tcgen05.ld), writes p back over them
-//                   as the A operand of the second product (tcgen05.st), in
-//                   two halves, rescales and, at the end, stores the output
-//   warp 8          loads queries, keys and values by TMA (one box for each
-//                   page and 64 columns) into a ring of half-stages
+//                   as the A operand of the second product (tcgen05.st),
+//                   rescales and, at the end, stores the output
+//   warps 8, 11     load queries and keys, and values, by TMA (one box for
+//                   each page and 64 columns) into a ring of half-stages
 //   warp 9          one thread issues tcgen05.mma: while one row tile's
 //                   softmax runs, the tensor cores work on the other's
 //   warp 10         zeroes value rows outside the visible keys in the tiles
@@ -28,8 +29,7 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "q4_attn_sched.cuh"
-#include "q4_tc.cuh"
+#include "q4_attn_tma.cuh"
 
 namespace q4 {
 
@@ -37,10 +37,9 @@ namespace {
 
 using namespace tc;
 
-constexpr int kKtLog2 = 7, kKt = 1 << kKtLog2;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
-constexpr int kLoader = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kCleaner = kSoftmaxWarps + 2;
+constexpr int kKeys = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kCleaner = kSoftmaxWarps + 2, kValues = kSoftmaxWarps + 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
 
@@ -74,27 +73,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
             dst),
         "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-        "[%2];" ::"r"(dst),
-        "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-// One lane of a converged warp.  The compiler knows a region behind it to be
-// one thread's, so the operands of tcgen05.mma go to uniform registers
-// directly; behind a test of the lane number each MMA took some 90 cycles to
-// issue, more than the 64 that it runs.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p = 0;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
 }
 // D += A . B with A in tensor memory: row = lane, two 16-bit values of K in a column.
 __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -169,20 +147,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-__device__ __forceinline__ float row_max(const uint32_t (&s)[128]) {
-    float top[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-#pragma unroll
-    for (int e = 16; e < 128; e += 2)
-        top[e >> 1 & 7] = max3(top[e >> 1 & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-    return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
-}
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool wait_all(bool alive, uint32_t bar, uint32_t parity) {
-    if (alive) alive = mbar_wait(bar, parity);
-    return __all_sync(0xffffffffu, alive);
-}
 
 // What of an item falls to this CTA, the same for every role.
 struct Part {
@@ -211,11 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto s_full = [&](int i) { return q_full + 24 + 8u * i; };
     auto p_ready = [&](int i) { return q_full + 40 + 8u * i; };
     auto pv_done = [&](int i) { return q_full + 56 + 8u * i; };
-    auto p_half = [&](int i) { return q_full + 72 + 8u * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
     int *last_flags = reinterpret_cast<int *>(misc + 1016);             // of the first and the last item
     SchedSmem &sched = *reinterpret_cast<SchedSmem *>(misc + 520);
-    static_assert(8 * (3 * S + 11) <= 512 && 520 + sizeof(SchedSmem) <= 1016, "misc region");
+    static_assert(8 * (3 * S + 13) <= 512 && 520 + sizeof(SchedSmem) <= 1016, "misc region");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -230,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(done, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
-            mbar_init(p_half(i), 128);
             mbar_init(p_ready(i), 128);
             mbar_init(pv_done(i), 1);
         }
@@ -243,8 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool alive = true;
-    // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168
     const bool work = sh.begin < sh.end;
+    // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168
     if (warp < kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------------------------------------- softmax: a thread holds a row
@@ -252,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + 128 * me, tO = tmem + lanes + 256 + 128 * me;
         const float c = a.scale;
-        const int tok = row / a.p.group, head_in = row - tok * a.p.group;
+        const int tok = a.p.group(row), head_in = row - tok * a.p.group.d;
         int uses = 0;
         for (bool more = work; more && it.u < sh.end; more = next_item(a.p, it)) {
             const Part part(it, sh, a.tokens);
@@ -286,55 +249,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!(seen >> e & 1)) s[32 * q + e] = 0xff800000u;
                         }
                     }
+                    float top[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+#pragma unroll
+                    for (int e = 8; e < 128; e += 2)
+                        top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     const bool first = j == part.j0;
-                    if (first) m = row_max(s);
-                    // The reference is the last tile's, so no exponential waits for this tile's maximum, which
-                    // is found beside the first half of them; only if it is too large they are done again.
-                    uint64_t sum[2];
-                    auto exponentials = [&](int half) {
-                        const float ref = m == -INFINITY ? 0.f : m * c;
-                        const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
-#pragma unroll
-                        for (int h = 2 * half; h < 2 * half + 2; ++h) {
-                            uint32_t p[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float2 x = unpair(fma2(pair_bits(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, ref2));
-                                const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                                sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
-                                p[e] = pack2<BF>(y.x, y.y);
-                            }
-                            tmem_st16(tS + 16 * h, p);
-                        }
-                    };
-                    for (;;) {
-                        sum[0] = sum[1] = 0;
-                        exponentials(0);
-                        if (first) break;
-                        const float mx = row_max(s);
-                        const bool grows = (mx - m) * c > kRescale;
-                        if (!__any_sync(0xffffffffu, grows)) break;
+                    const bool grows = first ? mx > m : (mx - m) * c > kRescale;
+                    if (__any_sync(0xffffffffu, grows)) {
                         const float to = grows ? mx : m;
                         // from a row without any key so far, nothing is kept
                         const float f = grows ? ex2((m - to) * c) : 1.f;
                         l *= f;
                         m = to;
-                        alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
-                        tc_fence_after();
+                        if (!first) {
+                            alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
+                            tc_fence_after();
 #pragma unroll
-                        for (int q = 0; q < D / 16; ++q) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * q, o);
-                            tmem_wait_ld();
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + 16 * q, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(tO + 16 * q, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(tO + 16 * q, o);
+                            }
                         }
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(p_half(me));
-                    exponentials(1);
+                    const float ref = m == -INFINITY ? 0.f : m * c;
+                    const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 x = unpair(fma2(pair_bits(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), c2, ref2));
+                            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                            sum[e & 1] = add2(sum[e & 1], pair(y.x, y.y));
+                            p[e] = pack2<BF>(y.x, y.y);
+                        }
+                        tmem_st16(tS + 16 * h, p);
+                    }
                     const float2 total = unpair(add2(sum[0], sum[1]));
                     l += total.x + total.y;
                     tmem_wait_st();
@@ -346,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ------------------------------------------ output, or a piece for the workspace
             uint16_t *dst = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
-                            (it.head * a.p.group + head_in) * D;
+                            (it.head * static_cast<int>(a.p.group.d) + head_in) * D;
             auto store = [&](const float *o, float inv, int q) {       // 32 columns
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
@@ -462,58 +420,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (!work) {
-        } else if (warp == kLoader) {
-            const int pages_log2 = min(a.p.page_log2, kKtLog2), box = 1 << pages_log2;   // tokens of a box
-            const int boxes = kKt >> pages_log2;                                        // of a tile
-            const int q_bytes = a.tokens * a.p.group * D * 2;
-            int seq = 0, items = 0, bad = 0;
-            for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
+        } else if (warp == kKeys || warp == kValues) {
+            const bool values = warp == kValues;
+            const int q_bytes = a.tokens * a.p.group.d * D * 2;
+            int seq = values, items = 0, bad = 0;            // slots alternate between keys and values
+            for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
                 if (it.hi <= 0) continue;
                 const Part part(it, sh, a.tokens);
-                const int32_t *table = a.p.b.table + it.b * a.p.b.table_stride;
-                if (items) alive = wait_all(alive, q_empty, (items - 1) & 1);
-                if (!alive) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(q_full, part.two ? 2 * q_bytes : q_bytes);
-                    for (int i = 0; i < (part.two ? 2 : 1); ++i)
-                        for (int h = 0; h < D / 64; ++h)
-                            tma_load_3d(base + i * C::kQ + h * (128 * 128), &tmQ, q_full, 64 * h, it.head * a.p.group,
-                                        it.q0 + it.t0 + i * a.tokens);
-                }
-                ++items;
-                for (int j = part.j0; j < part.j1; ++j) {
-                    const int key_t = (it.first + j) << kKtLog2, key = key_t + lane * box;
-                    const bool wanted = lane < boxes && key < it.hi && key + box > it.lo;
-                    int page = wanted ? table[key >> a.p.page_log2] : 0;
-                    if (page < 0 || page >= a.c.pages) {
-                        bad = kAttnBadPage;
-                        page = 0;
-                    }
-                    const bool edge = key_t + kKt > it.hi || key_t < it.lo;
-                    const int bytes = __popc(__ballot_sync(0xffffffffu, wanted)) * box * D * 2;
-                    const int row = key & ((1 << a.p.page_log2) - 1);
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++seq) {
-                        const int s = seq % S;
-                        if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
-                        if (!alive) break;
-                        const uint32_t bar = kv && edge ? tail(s) : full(s);
-                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                        __syncwarp();
-                        if (wanted)
-                            for (int h = 0; h < D / 64; ++h)
-                                tma_load_4d(ring + s * C::kHalf + h * (kKt * 128) + lane * box * 128, kv ? &tmV : &tmK, bar,
-                                            64 * h, row, it.head, page);
-                    }
+                if (!values) {
+                    if (items) alive = wait_all(alive, q_empty, (items - 1) & 1);
                     if (!alive) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(q_full, part.two ? 2 * q_bytes : q_bytes);
+                        for (int i = 0; i < (part.two ? 2 : 1); ++i)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(base + i * C::kQ + h * (128 * 128), &tmQ, q_full, 64 * h, it.head * a.p.group.d,
+                                            it.q0 + it.t0 + i * a.tokens);
+                    }
+                    __syncwarp();
+                    ++items;
                 }
-                if (!alive) break;
+                const PageWalk walk(a.p, it, a.c.pages);
+                TilePages next = walk.tile(it, part.j0, bad);
+                for (int j = part.j0; j < part.j1; ++j, seq += 2) {
+                    const TilePages t = next;
+                    if (j + 1 < part.j1) next = walk.tile(it, j + 1, bad);       // on its way while this one waits
+                    const int s = seq % S, key_t = (it.first + j) << kKtLog2;
+                    if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
+                    if (!alive) break;
+                    const bool edge = values && (key_t + kKt > it.hi || key_t < it.lo);
+                    walk.copy<D>(t, ring + s * C::kHalf, values ? &tmV : &tmK, edge ? tail(s) : full(s), it.head);
+                }
             }
             if (bad) atomicOr(a.status, bad);
             if (!alive) {
                 // let the copies in flight land before the CTA can exit
-                if (items) mbar_wait(q_full, (items - 1) & 1);
-                for (int i = max(seq - S, 0); i < seq; ++i) mbar_wait(full(i % S), (i / S) & 1);
+                if (items) wait_bounded(q_full, (items - 1) & 1);
+                for (int i = seq - 2; i >= 0 && i > seq - 2 - S; i -= 2) {
+                    wait_bounded(full(i % S), (i / S) & 1);
+                    if (values) wait_bounded(tail(i % S), 0);
+                }
             }
         } else if (warp == kIssuer) {
             if (elect_one()) {
@@ -521,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t id_qk = idesc_f16(128, kKt, false) | fmt, id_pv = idesc_f16(128, D, true) | fmt;
                 int tiles = 0, items = 0, uses[2] = {0, 0};
                 auto wait = [&](uint32_t bar, int n) {
-                    if (alive) alive = mbar_wait(bar, n & 1);
+                    if (alive) alive = wait_bounded(bar, n & 1);
                     tc_fence_after();
                 };
                 auto qk = [&](int i, int seq) {
@@ -534,19 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     umma_commit(s_full(i));
                 };
-                auto pv = [&](int i, int seq, bool first) {          // each half of p as soon as it is there
+                auto pv = [&](int i, int seq, bool first) {
                     const uint32_t vb = ring + (seq % S) * C::kHalf;
+                    wait(p_ready(i), uses[i]++);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t bar = half ? p_ready(i) : p_half(i);
-                        if (alive) alive = mbar_poll(bar, uses[i] & 1);
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            umma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
-                                        smem_desc_sw128(vb + kk * 2048, kKt * 128, 1024), id_pv, !first || kk != 0);
-                    }
-                    ++uses[i];
+                    for (int kk = 0; kk < kKt / 16; ++kk)
+                        umma_f16_ta(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
+                                    smem_desc_sw128(vb + kk * 2048, kKt * 128, 1024), id_pv, !first || kk != 0);
                     umma_commit(pv_done(i));
                 };
                 for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
@@ -573,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 umma_commit(done);
-                if (!mbar_wait(done, 0)) alive = false;
+                if (!wait_bounded(done, 0)) alive = false;
             }
         } else if (warp == kCleaner) {
             int seq = 1;
@@ -621,7 +561,7 @@ cudaError_t launch(const AttnShape &s, const AttnBatch &b, const AttnCache &c, c
     if (!e) e = encode_pages(&tk, c.k, s, c, box);
     if (!e) e = encode_pages(&tv, c.v, s, c, box);
     if (e) return e;
-    Args args{{b, s.hkv, s.group, s.page_log2, 2 * tokens * s.group, kKtLog2, a.window}, c, a.out, a.out_stride,
+    Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), -1, FastDiv(2 * tokens)}, c, a.out, a.out_stride,
               a.scale * 1.4426950408889634f, tokens, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_tc_kernel<true, C> : attend_tc_kernel<false, C>;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem))) return e;
