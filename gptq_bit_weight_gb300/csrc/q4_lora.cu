@@ -32,9 +32,11 @@ bool pdl_enabled();
 
 namespace {
 
+__global__ void lora_slot_kernel(LoraSlot *slot, int rank, float scale) { *slot = LoraSlot{rank, scale, 1}; }
+
 // Copies one adapter into its slot.
 __global__ void lora_set_kernel(uint16_t *a, uint16_t *b, LoraSlot *slot, const uint16_t *src_a,
-                                const uint16_t *src_b, int K, int N, int rank, int r16, float scale) {
+                                const uint16_t *src_b, int K, int N, int rank, int r16, uint16_t exponent) {
     const size_t na = static_cast<size_t>(r16) * ceil64(K), nb = static_cast<size_t>(r16) * N;
     const size_t step = static_cast<size_t>(gridDim.x) * blockDim.x;
     const size_t i0 = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -51,8 +53,8 @@ __global__ void lora_set_kernel(uint16_t *a, uint16_t *b, LoraSlot *slot, const 
         const size_t u = i >> 6;
         const int r = static_cast<int>(u % rg) * 8 + e;
         b[i] = r < rank ? src_b[(u / rg * 8 + n8) * rank + r] : 0;
+        if ((b[i] & exponent) == exponent) slot->finite = 0;         // an infinity or NaN
     }
-    if (i0 == 0) *slot = LoraSlot{rank, scale};
 }
 
 constexpr int kRows = 64;            // rows of a call's chunk that one CTA looks over
@@ -421,13 +423,15 @@ cudaError_t start(void (*k)(P...), dim3 grid, int threads, int smem, int cluster
 }  // namespace
 
 cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,
-                            const uint16_t *src_b, int rank, float scale, cudaStream_t st) {
+                            const uint16_t *src_b, int rank, float scale, bool bf16, cudaStream_t st) {
     const int r16 = ceil16(rank);
     const size_t n = static_cast<size_t>(r16) * std::max(ceil64(v.K), v.N);
     const int grid = static_cast<int>(std::min<size_t>(n / 256 + 1, 1216));
-    lora_set_kernel<<<grid, 256, 0, st>>>(a + static_cast<size_t>(s) * v.rpad * ceil64(v.K),
-                                          b + static_cast<size_t>(s) * v.rpad * v.N, slot + s, src_a, src_b, v.K, v.N,
-                                          rank, r16, scale);
+    lora_slot_kernel<<<1, 1, 0, st>>>(slot + s, rank, scale);
+    if (rank)
+        lora_set_kernel<<<grid, 256, 0, st>>>(a + static_cast<size_t>(s) * v.rpad * ceil64(v.K),
+                                              b + static_cast<size_t>(s) * v.rpad * v.N, slot + s, src_a, src_b, v.K,
+                                              v.N, rank, r16, bf16 ? 0x7f80 : 0x7c00);
     return cudaGetLastError();
 }
 

@@ -2,6 +2,7 @@
 // memory and its workspace.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -17,6 +18,7 @@ struct gptq_q4_lora_s {
     int *status = nullptr;
     float *t = nullptr;
     size_t t_rows = 0;
+    int sms = 0;
 };
 
 namespace {
@@ -71,6 +73,12 @@ int ensure_rows(gptq_q4_lora_s *h, size_t rows, cudaStream_t s, bool sync_alloc)
     return GPTQ_Q4_OK;
 }
 
+// Rows of sums that a call of at most M rows needs: one each, or, with K in
+// up to 8 parts on tiles of 128 rows, at most as many tiles as SMs.
+size_t sum_rows(const gptq_q4_lora_s *h, size_t M) {
+    return std::max(M, std::min(8 * M, static_cast<size_t>(h->sms) * 128));
+}
+
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace
@@ -105,6 +113,7 @@ gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype)
     h->slots = slots;
     h->max_rank = max_rank;
     h->dtype = dtype;
+    h->sms = q4::device_sm_count();
     const size_t each = static_cast<size_t>(slots) * q4::ceil16(max_rank) * 2;
     cudaError_t e = cudaMalloc(reinterpret_cast<void **>(&h->a), each * q4::ceil64(K));
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->b), each * N);
@@ -118,7 +127,7 @@ gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype)
         release(h);
         return nullptr;
     }
-    if (ensure_rows(h, 64, nullptr, true)) {
+    if (ensure_rows(h, sum_rows(h, 64), nullptr, true)) {
         release(h);
         return nullptr;
     }
@@ -142,9 +151,10 @@ int gptq_q4_lora_set(gptq_q4_lora h, int slot, const void *a, const void *b, int
             return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "misaligned a or b");
     }
     if (cudaError_t e = q4::launch_lora_set(view(h), h->a, h->b, h->slot, slot, static_cast<const uint16_t *>(a),
-                                            static_cast<const uint16_t *>(b), rank, scale, stream))
+                                            static_cast<const uint16_t *>(b), rank, scale,
+                                            h->dtype == GPTQ_Q4_DTYPE_BF16, stream))
         return api_cuda_fail(e, "adapter copy launch");
-    q4::api_count_launches(1);
+    q4::api_count_launches(rank ? 2 : 1);
     return api_set_status(GPTQ_Q4_OK, nullptr);
 }
 
@@ -152,7 +162,7 @@ int gptq_q4_lora_reserve(gptq_q4_lora h, int max_m) {
     if (int r = check(h)) return r;
     if (max_m < 0) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "max_m=%d < 0", max_m);
     if (cudaError_t e = cudaDeviceSynchronize()) return api_cuda_fail(e, "reserve");
-    if (int r = ensure_rows(h, static_cast<size_t>(max_m), nullptr, true)) return r;
+    if (int r = ensure_rows(h, sum_rows(h, static_cast<size_t>(max_m)), nullptr, true)) return r;
     return api_set_status(GPTQ_Q4_OK, nullptr);
 }
 
@@ -173,12 +183,17 @@ int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int3
     if (out == y && out_stride != y_stride)
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "out is y but their row strides differ (%lld and %lld)",
                          static_cast<long long>(out_stride), static_cast<long long>(y_stride));
-    if (int r = ensure_rows(h, static_cast<size_t>(M), stream, false)) return r;
+    if (int r = ensure_rows(h, sum_rows(h, static_cast<size_t>(M)), stream, false)) return r;
     const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
                          static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M};
-    int launches = 0;
-    if (cudaError_t e = q4::launch_lora_add(view(h), c, h->dtype == GPTQ_Q4_DTYPE_BF16, stream, &launches))
-        return api_cuda_fail(e, "adapter launch");
+    // from 65 rows on whole tiles of 128 rows; ranks over 128 do not fit them
+    const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
+    const q4::LoraTcPlan plan = q4::plan_lora_tc(view(h), M, h->sms);
+    int launches = 2;
+    cudaError_t e;
+    if (M > 64 && plan.ok) e = q4::launch_lora_tc(view(h), c, plan, h->t, h->sms, bf16, stream);
+    else launches = 0, e = q4::launch_lora_add(view(h), c, bf16, stream, &launches);
+    if (e) return api_cuda_fail(e, "adapter launch");
     q4::api_count_launches(launches);
     return api_set_status(GPTQ_Q4_OK, nullptr);
 }
@@ -191,8 +206,9 @@ int gptq_q4_lora_device_error(gptq_q4_lora h) {
     if (!e && flag) e = cudaMemset(h->status, 0, sizeof(int));
     if (e) return api_cuda_fail(e, "reading the pool's status word");
     if (flag)
-        return api_failf(GPTQ_Q4_DEVICE_FAULT, "adapter kernels reported status 0x%x:%s", flag,
-                         flag & q4::kLoraBadSlot ? " a row_slot entry is not below the number of slots" : "");
+        return api_failf(GPTQ_Q4_DEVICE_FAULT, "adapter kernels reported status 0x%x:%s%s", flag,
+                         flag & q4::kLoraBadSlot ? " a row_slot entry is not below the number of slots;" : "",
+                         flag & q4::kLoraTimeout ? " a bounded wait ran out;" : "");
     return api_set_status(GPTQ_Q4_OK, nullptr);
 }
 

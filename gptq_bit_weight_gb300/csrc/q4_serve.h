@@ -18,10 +18,12 @@ namespace q4 {
 struct LoraSlot {
     int rank;        // of the adapter; 0: empty
     float scale;
+    int finite;      // no infinity or NaN in B
 };
 
 // Status bits of the two handles.
 constexpr int kLoraBadSlot = 0x1;      // row_slot entry >= slots
+constexpr int kLoraTimeout = 0x2;      // a bounded wait ran out
 constexpr int kAttnBadBatch = 0x1;     // a length outside its range, or cu_q not ascending
 constexpr int kAttnBadPage = 0x2;      // a page index outside the cache
 constexpr int kAttnBadPosition = 0x4;  // a position outside the rotary table
@@ -48,8 +50,17 @@ struct LoraCall {
 };
 
 cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,
-                            const uint16_t *src_b, int rank, float scale, cudaStream_t st);
+                            const uint16_t *src_b, int rank, float scale, bool bf16, cudaStream_t st);
+// few rows, and ranks over 128 (q4_lora.cu)
 cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
+// many rows (q4_lora_tc.cu): `part` holds parts x rows x rpad fp32 sums
+struct LoraTcPlan {
+    bool ok;
+    int tiles, parts, blocks_each;
+};
+LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms);
+cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, float *part, int sms, bool bf16,
+                           cudaStream_t st);
 
 // The step's requests and one layer's cache, as the kernels read them.
 struct AttnBatch {

@@ -50,6 +50,8 @@ def reference(x, y, rows, ads, K):
 
 def check(got, ref, tol, what):
     err = (got.double().cpu() - ref).abs()
+    if not err.numel():
+        return
     worst = float((err / tol.clamp(min=1e-300)).max())
     assert bool((err <= tol).all()), f"{what}: worst error / tolerance {worst:.3f}"
 
@@ -76,6 +78,9 @@ CASES = [  # (M, K, N, ranks, rows: "one", "mixed", "runs")
     (1031, 2048, 776, [32], "one"),
     (1500, 200, 136, [16, 64, 40, 8, 24], "runs"),
     (300, 192, 200, [256, 200], "runs"),
+    (130, 456, 392, [16] * 24, "mixed"),
+    (128, 64, 64, [64], "one"),
+    (513, 4104, 1160, [128, 16, 100], "mixed"),
 ]
 
 
@@ -174,6 +179,28 @@ def test_large_sums_and_foreign_nan(q4, M):
     clean = torch.tensor([i for i in range(M) if i not in (1, 3)])
     check(out[clean], ref[clean], tol[clean], "beside NaN")
     assert not torch.isfinite(out[1]).any() and not torch.isfinite(out[3]).any()
+
+
+@pytest.mark.parametrize("M", [9, 200])
+def test_a_broken_adapter_stays_with_its_rows(q4, M):
+    """An infinity in one adapter's B, NaN in another's A: rows of other adapters, and of none, in the same tile."""
+    K, N, dtype = 320, 400, torch.bfloat16
+    g = torch.Generator().manual_seed(13)
+    ads = adapters(g, [16, 16, 32, 64], K, N, dtype)
+    rows = row_slots(g, M, 4, "mixed")
+    x, y = torch.randn(M, K, generator=g).to(dtype), torch.randn(M, N, generator=g).to(dtype)
+    ref, tol = reference(x, y, rows, ads, K)
+    ads[1][1][7, 3] = float("inf")
+    ads[2][0][5, 11] = float("nan")
+    pool = pool_of(q4, ads, K, N, 4, 64, dtype)
+    out = pool.add(x.to(DEV), rows.to(DEV), y.to(DEV)).cpu()
+    whole = (rows != 1) & (rows != 2)
+    check(out[whole], ref[whole], tol[whole], "beside broken adapters")
+    assert torch.isnan(out[rows == 2]).all()
+    bad, fine = out[rows == 1][:, 7], out[rows == 1][:, :7]
+    assert not torch.isfinite(bad).any()
+    check(fine, ref[rows == 1][:, :7], tol[rows == 1][:, :7], "other columns of a broken adapter")
+    pool.device_error()
 
 
 def test_slot_out_of_range_is_reported(q4):
