@@ -43,7 +43,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;           // rows of a tile, and columns in the second launch
-constexpr int kCap = 128;            // ranks of a pass of the second launch
+constexpr int kCap = 176;            // ranks of a pass of the second launch: what two B tiles have room for
 constexpr int kShrinkCap = 256;      // of the first
 
 // The adapters of a tile's rows.
@@ -268,10 +268,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
 
 // ----------------------------------------------------------- second launch
 constexpr int kExpandThreads = 320;  // warps 0-3 and 4-7 turn by turn, 8 loads, 9 issues the MMAs
+// An even number of y stages: each is then one set's, which waits for every use of it.  A set that saw only
+// every other use could take the phase before for its own.
 constexpr int kYStages = 4, kYBytes = kTile * kTile * 2;
+static_assert(kYStages % 2 == 0, "a y stage belongs to one set of warps");
 constexpr int kBStages = 2, kBBytes = kTile * kCap * 2;
 constexpr int kExpandSmem = kYStages * kYBytes + kBStages * kBBytes + 256 + 512 + static_cast<int>(sizeof(TileInfo)) + 1024;
-constexpr uint32_t kLow = kCap / 2;  // column of the low part of t
+constexpr uint32_t kLow = 128;       // column of the low part of t
 constexpr uint32_t kD = 256;         // of the sums, two buffers of 128
 
 // A unit is 128 columns of a row tile; each CTA takes an equal run of units, row tile after row tile.

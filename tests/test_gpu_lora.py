@@ -80,6 +80,7 @@ CASES = [  # (M, K, N, ranks, rows: "one", "mixed", "runs")
     (300, 192, 200, [256, 200], "runs"),
     (130, 456, 392, [16] * 24, "mixed"),
     (128, 64, 64, [64], "one"),
+    (1280, 64, 24576, [16, 8], "runs"),      # a dozen column tiles for each SM
     (513, 4104, 1160, [128, 16, 100], "mixed"),
 ]
 
