@@ -2,7 +2,6 @@
 // memory and its workspace.
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -65,18 +64,12 @@ int ensure_rows(gptq_q4_lora_s *h, size_t rows, cudaStream_t s, bool sync_alloc)
         h->t_rows = 0;
     }
     void *p = nullptr;
-    const size_t bytes = rows * q4::ceil16(h->max_rank) * sizeof(float);
+    const size_t bytes = rows * (q4::ceil16(h->max_rank) + 1) * sizeof(float);
     if (cudaError_t e = sync_alloc ? cudaMalloc(&p, bytes) : cudaMallocAsync(&p, bytes, s))
         return api_cuda_fail(e, "allocating the adapter workspace");
     h->t = static_cast<float *>(p);
     h->t_rows = rows;
     return GPTQ_Q4_OK;
-}
-
-// Rows of sums that a call of at most M rows needs: one each, or, with K in
-// up to 8 parts on tiles of 128 rows, at most as many tiles as SMs.
-size_t sum_rows(const gptq_q4_lora_s *h, size_t M) {
-    return std::max(M, std::min(8 * M, static_cast<size_t>(h->sms) * 128));
 }
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -127,7 +120,7 @@ gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype)
         release(h);
         return nullptr;
     }
-    if (ensure_rows(h, sum_rows(h, 64), nullptr, true)) {
+    if (ensure_rows(h, 64, nullptr, true)) {
         release(h);
         return nullptr;
     }
@@ -162,7 +155,7 @@ int gptq_q4_lora_reserve(gptq_q4_lora h, int max_m) {
     if (int r = check(h)) return r;
     if (max_m < 0) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "max_m=%d < 0", max_m);
     if (cudaError_t e = cudaDeviceSynchronize()) return api_cuda_fail(e, "reserve");
-    if (int r = ensure_rows(h, sum_rows(h, static_cast<size_t>(max_m)), nullptr, true)) return r;
+    if (int r = ensure_rows(h, static_cast<size_t>(max_m), nullptr, true)) return r;
     return api_set_status(GPTQ_Q4_OK, nullptr);
 }
 
@@ -183,15 +176,15 @@ int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int3
     if (out == y && out_stride != y_stride)
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "out is y but their row strides differ (%lld and %lld)",
                          static_cast<long long>(out_stride), static_cast<long long>(y_stride));
-    if (int r = ensure_rows(h, sum_rows(h, static_cast<size_t>(M)), stream, false)) return r;
+    if (int r = ensure_rows(h, static_cast<size_t>(M), stream, false)) return r;
     const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
                          static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M};
-    // from 65 rows on whole tiles of 128 rows; ranks over 128 do not fit them
+    // from 65 rows on tiles of 128 rows; the highest ranks do not fit them
     const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
     const q4::LoraTcPlan plan = q4::plan_lora_tc(view(h), M, h->sms);
     int launches = 2;
     cudaError_t e;
-    if (M > 64 && plan.ok) e = q4::launch_lora_tc(view(h), c, plan, h->t, h->sms, bf16, stream);
+    if (M > 64 && plan.ok) e = q4::launch_lora_tc(view(h), c, plan, h->sms, bf16, stream);
     else launches = 0, e = q4::launch_lora_add(view(h), c, bf16, stream, &launches);
     if (e) return api_cuda_fail(e, "adapter launch");
     q4::api_count_launches(launches);

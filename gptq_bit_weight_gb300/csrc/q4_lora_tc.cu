@@ -10,12 +10,13 @@
 // Prompts come in runs, so a tile has one or two; a tile of many costs a
 // product each, and still one pass over x and y.
 //
-//   first   t'[part][m][r] = x[m] . A[r] over a part of K: x tiles by TMA,
-//           adapter tiles by bulk copy, fp32 sums in tensor memory
-//   second  t = scale sum of the parts, as two 16-bit parts (high, low), is
-//           the A operand in tensor memory; B tiles by bulk copy; the sums
-//           of 128 x 128 outputs in two tensor memory buffers; y tiles are
-//           loaded, added to, rounded in place and stored by TMA
+//   first   t[m][r] = scale x[m] . A[r]: x tiles by TMA, adapter tiles by
+//           bulk copy, fp32 sums in tensor memory; K in parts over a cluster,
+//           which adds them and leaves t as two 16-bit parts (high, low)
+//   second  both parts of t are the A operand in tensor memory; B tiles by
+//           bulk copy; the sums of 128 x 128 outputs in two tensor memory
+//           buffers; y tiles are loaded, added to, rounded in place and
+//           stored by TMA
 //
 // Adapters that a tile cannot hold at once (over kCap ranks in the second
 // launch), and adapters with an infinity or NaN, which must not meet another
@@ -44,7 +45,7 @@ using namespace tc;
 
 constexpr int kTile = 128;           // rows of a tile, and columns in the second launch
 constexpr int kCap = 176;            // ranks of a pass of the second launch: what two B tiles have room for
-constexpr int kShrinkCap = 256;      // of the first
+constexpr int kShrinkCap = 176;      // of the first
 
 // The adapters of a tile's rows.
 struct TileInfo {
@@ -146,22 +147,35 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t sr
 // ------------------------------------------------------------ first launch
 constexpr int kShrinkThreads = 192;  // warps 0-3 read the sums, 4 loads, 5 issues the MMAs
 constexpr int kXBytes = kTile * 128, kABytes = kShrinkCap * 128, kShrinkStage = kXBytes + kABytes;
-constexpr int kShrinkStages = 4;
-constexpr int kShrinkSmem = kShrinkStages * kShrinkStage + 256 + static_cast<int>(sizeof(TileInfo)) + 1024;
+constexpr int kShrinkMaxStages = 5;
+constexpr uint32_t kShrinkCols = 256;
+constexpr int kShrinkMisc = 256 + static_cast<int>(sizeof(TileInfo)) + 1024;
+// The sums of the tile's rows, [128][rpad + 4] fp32, lie behind the ring.
+__host__ __device__ constexpr int sums_bytes(int rpad) { return kTile * (rpad + 4) * 4; }
+__host__ __device__ constexpr int shrink_stages(int rpad) {
+    const int n = (232448 - kShrinkMisc - sums_bytes(rpad)) / kShrinkStage;
+    return n < kShrinkMaxStages ? n : kShrinkMaxStages;
+}
 
-// Grid: (parts of K, row tiles).  part [parts][rows][rpad].
+// Grid: (parts of K, row tiles), the parts of a tile in one cluster: each sums
+// its share of the tile's rows over the parts, in their order, and splits
+// scale times the sum into its two 16-bit parts.
+// t16 [rows][2][rpad]: high and low parts; up [rows]: what they have been divided by.
 template <bool BF>
 __global__ void __launch_bounds__(kShrinkThreads, 1)
-    shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, LoraView v, LoraCall c, float *part, int blocks_each) {
-    constexpr int S = kShrinkStages;
+    shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, LoraView v, LoraCall c, uint16_t *t16, float *up,
+                     int blocks_each, int S) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t *misc = smem_raw + (base - raw) + S * kShrinkStage;
-    const uint32_t bars = base + S * kShrinkStage;
+    uint8_t *sb = smem_raw + (base - raw);
+    float *sums = reinterpret_cast<float *>(sb + S * kShrinkStage);
+    const int pitch = v.rpad + 4;
+    uint8_t *misc = sb + S * kShrinkStage + sums_bytes(v.rpad);
+    const uint32_t bars = base + S * kShrinkStage + sums_bytes(v.rpad);
     auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (S + s); };
-    const uint32_t d_full = bars + 16 * S, d_empty = d_full + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 16 * S + 16);
+    auto empty = [&](int s) { return bars + 8u * (kShrinkMaxStages + s); };
+    const uint32_t d_full = bars + 16 * kShrinkMaxStages, d_empty = d_full + 8;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 16 * kShrinkMaxStages + 16);
     TileInfo &k = *reinterpret_cast<TileInfo *>(misc + 256);
     const int warp = threadIdx.x >> 5;
     const int m0 = blockIdx.y * kTile;
@@ -176,7 +190,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         mbar_init(d_empty, 128);
         mbar_init_fence();
     }
-    if (warp == 5) tmem_alloc(smem_u32(tmem_slot), kShrinkCap);
+    if (warp == 5) tmem_alloc(smem_u32(tmem_slot), kShrinkCols);
     tc_fence_before();
     build_info(v, c, m0, kShrinkCap, false, k);                      // synchronizes
     tc_fence_after();
@@ -238,7 +252,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         }
     } else {
         const int row = threadIdx.x, mine = k.cls[row];
-        float *dst = part + (static_cast<size_t>(blockIdx.x) * c.M + m0 + row) * v.rpad;
+        float *dst = sums + row * pitch;
         for (int p = 0, c0 = 0; p < k.passes; ++p) {
             alive = wait_all(alive, d_full, p & 1);
             tc_fence_after();
@@ -250,7 +264,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                     if (mine == c0)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            __stcg(reinterpret_cast<uint4 *>(dst + r) + e, make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+                            *(reinterpret_cast<uint4 *>(dst + r) + e) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                 }
             }
             tc_fence_before();
@@ -262,12 +276,66 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     if (warp == 5) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, kShrinkCap);
+        tmem_dealloc(tmem, kShrinkCols);
     }
+    auto cluster_sync = [] {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    };
+    cluster_sync();
+    // rows part, part + parts, ..: a warp holds a row, a lane two of each 64 ranks
+    const int parts = gridDim.x, lane = threadIdx.x & 31;
+    for (int row = blockIdx.x + parts * warp; row < kTile; row += parts * (kShrinkThreads / 32)) {
+        const int mine = k.cls[row];
+        if (mine < 0) continue;
+        const int rank = k.rank[mine];
+        const float scale = v.slot[k.slot[mine]].scale;
+        float2 x[3];                                     // kShrinkCap ranks
+        float top = 0.f;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+            x[g] = make_float2(0.f, 0.f);
+            const int r = 64 * g + 2 * lane;
+            if (r < rank) {
+                const uint32_t at = smem_u32(sums + row * pitch + r);
+#pragma unroll 4
+                for (int q = 0; q < parts; ++q) {
+                    uint32_t from;
+                    float2 y;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(q));
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(from) : "memory");
+                    x[g].x += y.x;
+                    x[g].y += y.y;
+                }
+                x[g].x *= scale;
+                x[g].y *= scale;
+            }
+            top = fmaxf(top, fmaxf(fabsf(x[g].x), fabsf(x[g].y)));
+        }
+        float by = 1.f;
+        if constexpr (!BF) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            by = split_scale_of(top);
+        }
+        const float down = 1.f / by;                     // a power of two: exact
+        uint16_t *dst = t16 + static_cast<size_t>(m0 + row) * 2 * v.rpad;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+            const int r = 64 * g + 2 * lane;
+            if (r >= rank) continue;
+            const float y0 = x[g].x * down, y1 = x[g].y * down;
+            const uint16_t h0 = to16<BF>(y0), h1 = to16<BF>(y1);
+            *reinterpret_cast<uint32_t *>(dst + r) = h0 | static_cast<uint32_t>(h1) << 16;
+            *reinterpret_cast<uint32_t *>(dst + v.rpad + r) =
+                split_low<BF>(y0, h0) | static_cast<uint32_t>(split_low<BF>(y1, h1)) << 16;
+        }
+        if (lane == 0) up[m0 + row] = by;
+    }
+    cluster_sync();                                      // nobody leaves while its sums are read
 }
 
 // ----------------------------------------------------------- second launch
-constexpr int kExpandThreads = 320;  // warps 0-3 and 4-7 turn by turn, 8 loads, 9 issues the MMAs
+constexpr int kExpandThreads = 352;  // warps 0-3 and 4-7 turn by turn, 8 loads y, 9 issues the MMAs, 10 loads B
 // An even number of y stages: each is then one set's, which waits for every use of it.  A set that saw only
 // every other use could take the phase before for its own.
 constexpr int kYStages = 4, kYBytes = kTile * kTile * 2;
@@ -281,7 +349,7 @@ constexpr uint32_t kD = 256;         // of the sums, two buffers of 128
 template <bool BF>
 __global__ void __launch_bounds__(kExpandThreads, 1)
     expand_tc_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmO, LoraView v,
-                     LoraCall c, const float *part, int parts) {
+                     LoraCall c, const uint16_t *t16, const float *up_of) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sb = smem_raw + (base - raw);
@@ -345,61 +413,29 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             if (warp < 4 && ranks) {
                 const int row = threadIdx.x, mine = k.cls[row];
                 const bool in = mine >= c0 && mine < c1;
-                const int rank = in ? k.rank[mine] : 0;
-                const float scale = in ? v.slot[k.slot[mine]].scale : 0.f;
-                const float *src = part + static_cast<size_t>(m0 + row) * v.rpad;
-                const size_t step = static_cast<size_t>(c.M) * v.rpad;
-                auto load = [&](int r, float (&x)[16]) {             // 16 ranks, the parts of K in order
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-                    if (r < rank)
-#pragma unroll 4
-                        for (int q = 0; q < parts; ++q)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + q * step + r) + e);
-                                x[4 * e] += y.x;
-                                x[4 * e + 1] += y.y;
-                                x[4 * e + 2] += y.z;
-                                x[4 * e + 3] += y.w;
-                            }
-                };
-                float up = 1.f;
-                if constexpr (!BF) {
-                    float top = 0.f;
-#pragma unroll 1
-                    for (int r = 0; r < rank; r += 16) {
-                        float x[16];
-                        load(r, x);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e] * scale));
-                    }
-                    up = split_scale_of(top);
-                }
-                const float factor = scale / up;                     // up is a power of two
-                s_up[row] = up;
+                const uint16_t *src = t16 + static_cast<size_t>(m0 + row) * 2 * v.rpad;
+                s_up[row] = in ? __ldcg(up_of + m0 + row) : 1.f;
                 for (int i = c0; i < c1; ++i)
 #pragma unroll 1
-                    for (int r = 0; r < k.rank[i]; r += 16) {
-                        float x[16];
-                        uint32_t hi[8], lo[8];
-                        if (__any_sync(0xffffffffu, mine == i)) {
-                            load(r, x);
+                    for (int r0 = 0; r0 < k.rank[i]; r0 += 64) {
+                        uint4 h[4][2], l[4][2];          // 64 ranks, all on their way together; zero in other rows
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float y0 = x[2 * e] * factor, y1 = x[2 * e + 1] * factor;
-                                const uint16_t h0 = to16<BF>(y0), h1 = to16<BF>(y1);
-                                const uint32_t h = h0 | static_cast<uint32_t>(h1) << 16;
-                                const uint32_t l = split_low<BF>(y0, h0) | static_cast<uint32_t>(split_low<BF>(y1, h1)) << 16;
-                                hi[e] = mine == i ? h : 0;
-                                lo[e] = mine == i ? l : 0;
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                h[q][e] = l[q][e] = make_uint4(0, 0, 0, 0);
+                                if (mine == i && r0 + 16 * q < k.rank[i]) {
+                                    h[q][e] = __ldcg(reinterpret_cast<const uint4 *>(src + r0 + 16 * q) + e);
+                                    l[q][e] = __ldcg(reinterpret_cast<const uint4 *>(src + v.rpad + r0 + 16 * q) + e);
+                                }
                             }
-                        } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0;
-                        }
-                        tmem_st8(tmem + lanes + (k.off[i] + r) / 2, hi);
-                        tmem_st8(tmem + lanes + kLow + (k.off[i] + r) / 2, lo);
+                        for (int q = 0; q < 4; ++q)
+                            if (r0 + 16 * q < k.rank[i]) {
+                                const uint32_t col = (k.off[i] + r0) / 2 + 8 * q;
+                                tmem_st8(tmem + lanes + col, reinterpret_cast<const uint32_t(&)[8]>(h[q]));
+                                tmem_st8(tmem + lanes + kLow + col, reinterpret_cast<const uint32_t(&)[8]>(l[q]));
+                            }
                     }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
@@ -410,15 +446,26 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             if (warp == 8) {
                 const CUtensorMap *from = p ? &tmO : &tmY;           // a later pass goes on from the output
                 for (int n = a0; n < a1; ++n) {
-                    const int i = job + n - a0, s = i % kYStages, t = i & 1;
+                    const int i = job + n - a0, s = i % kYStages;
                     if (i >= kYStages) alive = wait_all(alive, y_empty(s), ((i / kYStages) & 1) ^ 1);
-                    if (i >= 2) alive = wait_all(alive, b_empty(t), ((i >> 1) & 1) ^ 1);
                     if (!alive) break;
                     if (elect_one()) {
                         const int halves = v.N - n * kTile > 64 ? 2 : 1;
                         mbar_arrive_expect_tx(y_full(s), halves * (kYBytes / 2));
                         for (int h = 0; h < halves; ++h)
                             tma_load_2d(base + s * kYBytes + h * (kYBytes / 2), from, y_full(s), n * kTile + 64 * h, m0);
+                    }
+                    __syncwarp();
+                }
+                if (!alive)
+                    for (int i = max(job + a1 - a0 - kYStages, 0); i < job + a1 - a0; ++i)
+                        wait_bounded(y_full(i % kYStages), (i / kYStages) & 1);
+            } else if (warp == 10) {
+                for (int n = a0; n < a1; ++n) {
+                    const int i = job + n - a0, t = i & 1;
+                    if (i >= 2) alive = wait_all(alive, b_empty(t), ((i >> 1) & 1) ^ 1);
+                    if (!alive) break;
+                    if (elect_one()) {
                         const int groups = min(kTile, v.N - n * kTile) / 8;
                         mbar_arrive_expect_tx(b_full(t), groups * ranks * 16);   // no adapter: no bytes
 #pragma unroll 1
@@ -431,8 +478,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     __syncwarp();
                 }
                 if (!alive)
-                    for (int i = max(job + a1 - a0 - kYStages, 0); i < job + a1 - a0; ++i)
-                        wait_bounded(y_full(i % kYStages), (i / kYStages) & 1);
+                    for (int i = max(job + a1 - a0 - 2, 0); i < job + a1 - a0; ++i) wait_bounded(b_full(i & 1), (i >> 1) & 1);
             } else if (warp == 9) {
                 if (elect_one()) {
                     constexpr uint32_t idesc = idesc_f16(128, kTile, false) | (BF ? (1u << 7) | (1u << 10) : 0u);
@@ -528,7 +574,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 
 LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms) {
     LoraTcPlan p;
-    p.ok = v.rpad <= kCap;
+    p.ok = v.rpad <= kCap && v.rpad <= kShrinkCap;
     p.tiles = (M + kTile - 1) / kTile;
     const int blocks = (v.K + 63) / 64;
     // parts of K: as many CTAs as fill the GPU once, at least four blocks of 64 each
@@ -538,7 +584,7 @@ LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms) {
     return p;
 }
 
-cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, float *part, int sms, bool bf16,
+cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, int sms, bool bf16,
                            cudaStream_t st) {
     CUtensorMap tx, ty, to;
     const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;        // 16-bit values either way
@@ -548,21 +594,31 @@ cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPla
     if (e) return e;
     auto shrink = bf16 ? shrink_tc_kernel<true> : shrink_tc_kernel<false>;
     auto expand = bf16 ? expand_tc_kernel<true> : expand_tc_kernel<false>;
-    if ((e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem))) return e;
+    const int S = shrink_stages(v.rpad), smem = S * kShrinkStage + sums_bytes(v.rpad) + kShrinkMisc;
+    if ((e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))) return e;
     if ((e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem))) return e;
-    shrink<<<dim3(p.parts, p.tiles), kShrinkThreads, kShrinkSmem, st>>>(tx, v, c, part, p.blocks_each);
-    if ((e = cudaGetLastError())) return e;
+    // t16 takes the place of the fp32 sums of the few-row kernels, the rows' scales come behind
+    uint16_t *t16 = reinterpret_cast<uint16_t *>(v.t);
+    float *up = v.t + static_cast<size_t>(c.M) * v.rpad;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.parts;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.parts, p.tiles);
+    cfg.blockDim = dim3(kShrinkThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, shrink, tx, v, c, t16, up, p.blocks_each, S))) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(sms, static_cast<int64_t>(p.tiles) * ((v.N + kTile - 1) / kTile))));
     cfg.blockDim = dim3(kExpandThreads);
     cfg.dynamicSmemBytes = kExpandSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, expand, ty, to, v, c, static_cast<const float *>(part), p.parts);
+    return cudaLaunchKernelEx(&cfg, expand, ty, to, v, c, static_cast<const uint16_t *>(t16), static_cast<const float *>(up));
 }
 
 }  // namespace q4

@@ -37,7 +37,7 @@ struct LoraView {
     const uint16_t *a;           // [slots][rpad * ceil64(K)], layout in q4_lora.cu
     const uint16_t *b;           // [slots][rpad * N]
     const LoraSlot *slot;        // [slots]
-    float *t;                    // [rows][rpad] fp32: scale * x . A^T
+    float *t;                    // [rows][rpad] fp32: scale * x . A^T; and room for one more each row
     int *status;
 };
 
@@ -53,13 +53,13 @@ cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlo
                             const uint16_t *src_b, int rank, float scale, bool bf16, cudaStream_t st);
 // few rows, and ranks over 128 (q4_lora.cu)
 cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
-// many rows (q4_lora_tc.cu): `part` holds parts x rows x rpad fp32 sums
+// many rows (q4_lora_tc.cu)
 struct LoraTcPlan {
     bool ok;
     int tiles, parts, blocks_each;
 };
 LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms);
-cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, float *part, int sms, bool bf16,
+cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, int sms, bool bf16,
                            cudaStream_t st);
 
 // The step's requests and one layer's cache, as the kernels read them.
