@@ -397,10 +397,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const int n1 = static_cast<int>(min(static_cast<int64_t>(cols), n0 + (u_end - u)));
         u += n1 - n0;
         build_info(v, c, m0, kCap, true, k);
-        if (!waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");       // the sums of the first launch
-            waited = true;
-        }
         // With one pass (or none) the tile's whole run is one stretch; with more, each (unit, pass) is.
         const bool single = k.passes <= 1;
         for (int stretch = 0; stretch < (single ? 1 : (n1 - n0) * k.passes); ++stretch) {
@@ -410,6 +406,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             while (c0 < k.n && k.pass[c0] < p) ++c0;
             for (c1 = c0; c1 < k.n && k.pass[c1] == p; ++c1) ranks += k.rank[c1];
             // -------------------------------- t of the pass into tensor memory: a thread holds a row
+            if (warp < 4 && !waited) {                               // y and B need not wait for the first launch
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                waited = true;
+            }
             if (warp < 4 && ranks) {
                 const int row = threadIdx.x, mine = k.cls[row];
                 const bool in = mine >= c0 && mine < c1;
@@ -439,9 +439,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
-            tc_fence_before();
-            __syncthreads();
-            tc_fence_after();
+            if (warp < 8 || warp == 9) {
+                tc_fence_before();
+                asm volatile("bar.sync 3, 288;" ::: "memory");
+                tc_fence_after();
+            }
             // -------------------------------- the stretch's jobs
             if (warp == 8) {
                 const CUtensorMap *from = p ? &tmO : &tmY;           // a later pass goes on from the output
