@@ -210,7 +210,7 @@ __device__ __forceinline__ void shrink_rows(const LoraView &v, const LoraCall &c
 // a cluster along K, chunks of 64 rows).  Few: at most 16 rows in all, for
 // fewer registers.
 template <bool BF, bool Few>
-__global__ void __launch_bounds__(32 * kWarps) lora_shrink_kernel(LoraView v, LoraCall c, int ck) {
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v, LoraCall c, int ck) {
     __shared__ Classes k;
     __shared__ __align__(16) float red[kRows / 8 * kWarps * 128];
     __shared__ __align__(16) float sum[kRows / 8 * 128];
@@ -284,6 +284,22 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v,
     const int64_t units = static_cast<int64_t>(k.units[k.n]) * nb;
     int64_t u = units * me / warps;
     const int64_t end = units * (me + 1) / warps;
+    // B and y of the warp's units into L2 while the first launch runs
+    auto prefetch = [](const uint16_t *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); };
+    for (int64_t w = u; w < end;) {
+        const int group = static_cast<int>(w / nb), b0 = static_cast<int>(w % nb);
+        const int b1 = static_cast<int>(min(static_cast<int64_t>(nb), b0 + (end - w)));
+        w += b1 - b0;
+        const int id = class_of(k, group), rank = k.rank[id];
+        const int r0 = k.first[id] + 16 * (group - k.units[id]), n = min(16, k.first[id + 1] - r0);
+        if (rank) {
+            const uint16_t *b = v.b + static_cast<size_t>(k.slot[id]) * v.rpad * v.N;
+            const int64_t last = static_cast<int64_t>(min(32 * b1, v.N)) * rank;
+            for (int64_t e = static_cast<int64_t>(32 * b0) * rank + 64 * lane; e < last; e += 64 * 32) prefetch(b + e);
+        }
+        for (int e = lane; e < n * (b1 - b0); e += 32)
+            prefetch(c.y + k.row[r0 + e % n] * c.ys + 32 * (b0 + e / n));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     {
         while (u < end) {
@@ -449,11 +465,12 @@ cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cud
         d.row_slot += m0;
         w.t += m0 * v.rpad;
         const int rows = std::min(d.M, kRows);
-        // (class, 16 ranks) units that one chunk can hold; K is split over a cluster while that leaves SMs idle
+        // (class, 16 ranks) units that one chunk can hold, and two CTAs for each SM over them; K is split over a
+        // cluster where the units alone are fewer
         const int units = std::min(rows, v.slots) * (v.rpad / 16);
-        const int gx = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, 1216 / chunks)));
-        int ck = 1;
-        while (ck < 8 && static_cast<int64_t>(gx) * chunks * ck < 304 && v.K / (ck * 2) >= 1024) ck *= 2;
+        int ck = 8;
+        while (ck > 1 && (static_cast<int64_t>(units) * chunks * ck > 2 * 304 || v.K / ck < 512)) ck /= 2;
+        const int gx = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, 304 / (static_cast<int64_t>(ck) * chunks))));
         // two CTAs for each SM, as long as every warp has a unit
         const int groups = (rows + 15) / 16 + std::min(rows, v.slots + 1);
         const int64_t most = static_cast<int64_t>(groups) * ((v.N + 31) / 32);
