@@ -48,7 +48,7 @@ struct Cfg {
     static constexpr int D = D_;
     static constexpr int kHalf = kKt * D * 2;    // bytes of a half-stage: keys or values of a tile
     static constexpr int kQ = 128 * D * 2;       // of one row tile's queries
-    static constexpr int kMisc = 1024;
+    static constexpr int kMisc = 2048;
     static constexpr int kRoom = (232448 - 1024 - 2 * kQ - kMisc) / kHalf;
     static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
     static constexpr int kSmem = 2 * kQ + kStages * kHalf + kMisc + 1024;
@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
     int *last_flags = reinterpret_cast<int *>(misc + 1016);             // of the first and the last item
     SchedSmem &sched = *reinterpret_cast<SchedSmem *>(misc + 520);
+    float2 *s_ml = reinterpret_cast<float2 *>(misc + 1024);             // [128]: (m, l) of the second buffer
     static_assert(8 * (3 * S + 13) <= 512 && 520 + sizeof(SchedSmem) <= 1016, "misc region");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,17 +220,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         int uses = 0;
         for (bool more = work; more && it.u < sh.end; more = next_item(a.p, it)) {
             const Part part(it, sh, a.tokens);
-            const bool active = me == 0 || part.two;
-            const int t = it.t0 + me * a.tokens + tok;                 // the row's token
-            const bool valid = active && tok < a.tokens && t <= it.t1;
-            const int lim = valid ? it.kv - it.ql + t : -1;            // last key that the row sees
+            // With one row tile only, the two buffers take its key tiles in turn and are merged at the end.
+            const bool turns = !part.two, joins = turns && part.j1 - part.j0 > 1;
+            const bool active = me == 0 || !turns;
+            const int ta = it.t0 + (turns ? 0 : me * a.tokens), t = ta + tok;    // the row tile's first token, the row's
+            const bool mine = tok < a.tokens && t <= it.t1, valid = active && mine;
+            const int lim = mine ? it.kv - it.ql + t : -1;             // last key that the row sees
             const int lim_lo = a.p.window > 0 ? lim - a.p.window : -1; // keys up to this one are out of the window
             float m = -INFINITY, l = 0.f;
-            if (it.hi > 0 && active) {
+            if (it.hi > 0 && (active || joins)) {
                 // keys that every row of this row tile sees
-                const int own = it.kv - it.ql, ta = it.t0 + me * a.tokens, tb = min(ta + a.tokens - 1, it.t1);
+                const int own = it.kv - it.ql, tb = min(ta + a.tokens - 1, it.t1);
+                const int first_j = part.j0 + (turns ? me : 0), step = turns ? 2 : 1;
                 const int all_hi = own + ta, all_lo = a.p.window > 0 ? own + tb - a.p.window : -1;
-                for (int j = part.j0; j < part.j1; ++j, ++uses) {
+                for (int j = first_j; j < part.j1; j += step, ++uses) {
                     const int key_t = (it.first + j) << kKtLog2;
                     alive = wait_all(alive, s_full(me), uses & 1);
                     tc_fence_after();
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 8; e < 128; e += 2)
                         top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    const bool first = j == part.j0;
+                    const bool first = j == first_j;
                     const bool grows = first ? mx > m : (mx - m) * c > kRescale;
                     if (__any_sync(0xffffffffu, grows)) {
                         const float to = grows ? mx : m;
@@ -301,6 +305,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
                 tc_fence_after();
+                if (joins) {
+                    if (me == 1) s_ml[row] = make_float2(m, l);
+                    tc_fence_before();
+                    bar_softmax();
+                    tc_fence_after();
+                    if (me == 0) {
+                        const float2 v = s_ml[row];
+                        const float top = fmaxf(m, v.x), ref = top == -INFINITY ? 0.f : top;
+                        const float f0 = ex2((m - ref) * c), f1 = ex2((v.x - ref) * c);
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t x[16], y[16];
+                            tmem_ld16(tO + 16 * q, x);
+                            tmem_ld16(tO + 128 + 16 * q, y);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
+                            tmem_st16(tO + 16 * q, x);
+                        }
+                        tmem_wait_st();
+                        m = top;
+                        l = l * f0 + v.y * f1;
+                    }
+                    tc_fence_before();
+                    bar_softmax();                       // the second buffer has been read
+                    tc_fence_after();
+                }
             }
             // ------------------------------------------ output, or a piece for the workspace
             uint16_t *dst = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
@@ -470,12 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (alive) alive = wait_bounded(bar, n & 1);
                     tc_fence_after();
                 };
-                auto qk = [&](int i, int seq) {
+                auto qk = [&](int i, int tile, int seq) {            // scores buffer i = row tile's queries . keys
                     const uint32_t kb = ring + (seq % S) * C::kHalf;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-                        umma_f16(tmem + 128 * i, smem_desc_sw128(base + i * C::kQ + off, 16, 1024),
+                        umma_f16(tmem + 128 * i, smem_desc_sw128(base + tile * C::kQ + off, 16, 1024),
                                  smem_desc_sw128(kb + off, 16, 1024), id_qk, kk != 0);
                     }
                     umma_commit(s_full(i));
@@ -492,24 +524,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it)) {
                     if (it.hi <= 0) continue;
                     const Part part(it, sh, a.tokens);
-                    const int n = part.j1 - part.j0, two = part.two ? 2 : 1;
+                    // two row tiles: both against each key tile; one: its key tiles take the buffers in turn
+                    const bool turns = !part.two;
+                    const int n = part.j1 - part.j0, ahead = turns ? 2 : 1, each = turns ? 1 : 2;
                     wait(q_full, items++);
-                    wait(full(2 * tiles % S), 2 * tiles / S);
-                    for (int i = 0; i < two; ++i) qk(i, 2 * tiles);
-                    umma_commit(empty(2 * tiles % S));
-                    if (n == 1) umma_commit(q_empty);
+                    for (int j = 0; j < min(ahead, n); ++j) {
+                        const int sk = 2 * (tiles + j);
+                        wait(full(sk % S), sk / S);
+                        for (int i = 0; i < each; ++i) qk(turns ? j : i, i, sk);
+                        umma_commit(empty(sk % S));
+                    }
+                    if (n <= ahead) umma_commit(q_empty);
                     for (int j = 0; j < n; ++j, ++tiles) {
-                        const int sv = 2 * tiles + 1, sk = 2 * tiles + 2;
-                        const bool next = j + 1 < n;
+                        const int sv = 2 * tiles + 1, sk = 2 * (tiles + ahead);
+                        const bool next = j + ahead < n;
                         wait(full(sv % S), sv / S);
-                        if (next) wait(full(sk % S), sk / S);
-                        for (int i = 0; i < two; ++i) {
-                            pv(i, sv, j == 0);
-                            if (next) qk(i, sk);
+                        for (int i = 0; i < each; ++i) {
+                            const int buf = turns ? j & 1 : i;
+                            pv(buf, sv, j < ahead);
+                            if (!next) continue;
+                            if (i == 0) wait(full(sk % S), sk / S);
+                            qk(buf, i, sk);
                         }
                         umma_commit(empty(sv % S));
                         if (next) umma_commit(empty(sk % S));
-                        if (j + 2 == n) umma_commit(q_empty);
+                        if (j + ahead + 1 == n) umma_commit(q_empty);
                     }
                 }
                 umma_commit(done);
