@@ -390,11 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float o[32];
                         tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(o));
                         tmem_wait_ld();
+                        if (valid)                       // the other rows are not anybody's
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            __stcg(columns(me_cta, q) + v * 128, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
+                            for (int v = 0; v < 8; ++v)
+                                __stcg(columns(me_cta, q) + v * 128, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
                     }
-                    __stcg(ml(me_cta), make_float2(m, l));
+                    if (valid) __stcg(ml(me_cta), make_float2(m, l));
                     __threadfence();
                 }
                 bar_softmax();
@@ -412,11 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (active) {
                     float top = m;
                     for (int k = c0; k <= c1; ++k)
-                        if (k != me_cta) top = fmaxf(top, __ldcg(ml(k)).x);
+                        if (k != me_cta && valid) top = fmaxf(top, __ldcg(ml(k)).x);
                     const float ref = top == -INFINITY ? 0.f : top;
                     float sum = 0.f;
                     for (int k = c0; k <= c1; ++k) {
-                        const float2 v = k == me_cta ? make_float2(m, l) : __ldcg(ml(k));
+                        const float2 v = k == me_cta || !valid ? make_float2(m, l) : __ldcg(ml(k));
                         sum += v.y * ex2((v.x - ref) * c);
                     }
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -435,10 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             } else {
 #pragma unroll
                                 for (int v = 0; v < 8; ++v) {
-                                    const float4 y = __ldcg(columns(k, q) + v * 128);
+                                    const float4 y = valid ? __ldcg(columns(k, q) + v * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
                                     x[4 * v] = y.x, x[4 * v + 1] = y.y, x[4 * v + 2] = y.z, x[4 * v + 3] = y.w;
                                 }
-                                f = ex2((__ldcg(ml(k)).x - ref) * c);
+                                f = valid ? ex2((__ldcg(ml(k)).x - ref) * c) : 0.f;
+                                __syncwarp();
                             }
 #pragma unroll
                             for (int e = 0; e < 32; ++e) acc[e] += x[e] * f;
