@@ -275,11 +275,12 @@ int gptq_q4_attn_device_error(gptq_q4_attn h) {
     if (!e && (flag & q4::kAttnTimeout)) e = cudaMemset(h->tickets, 0, h->ctas * sizeof(int));
     if (e) return api_cuda_fail(e, "reading the attention handle's status word");
     if (flag)
-        return api_failf(GPTQ_Q4_DEVICE_FAULT, "attention kernels reported status 0x%x:%s%s%s%s", flag,
+        return api_failf(GPTQ_Q4_DEVICE_FAULT, "attention kernels reported status 0x%x:%s%s%s%s%s", flag,
                          flag & q4::kAttnBadBatch ? " a length or row range outside its limits;" : "",
                          flag & q4::kAttnBadPage ? " a page index outside the cache;" : "",
                          flag & q4::kAttnBadPosition ? " a position outside the rotary table;" : "",
-                         flag & q4::kAttnTimeout ? " a bounded wait ran out;" : "");
+                         flag & q4::kAttnTimeout ? " a bounded wait ran out;" : "",
+                         flag & q4::kAttnTooLong ? " more work than one call can count;" : "");
     return api_set_status(GPTQ_Q4_OK, nullptr);
 }
 

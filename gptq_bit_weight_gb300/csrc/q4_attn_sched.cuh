@@ -41,7 +41,7 @@ struct Item {
     int t0, t1;      // first and last token of the row tile
     int lo, hi;      // keys [lo, hi) that some row of the tile sees; hi <= 0: none
     int first, n;    // key tiles
-    long long u;     // the item's first unit
+    int u;           // the item's first unit
 };
 
 __device__ __forceinline__ int row_tiles(const SchedParams &p, int ql) {
@@ -108,22 +108,16 @@ __device__ __forceinline__ bool next_item(const SchedParams &p, Item &it) {
     return true;
 }
 
-// a / b for a >= 0, b > 0 and a result in int; 32-bit where both fit.
-__device__ __forceinline__ int div_units(long long a, long long b) {
-    if (((a | b) >> 31) == 0) return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
-    return static_cast<int>(a / b);
-}
-
 struct Share {
-    long long begin, end;    // units of this CTA
-    long long per;           // units of every CTA but the last with any
+    int begin, end;          // units of this CTA
+    uint32_t per;            // units of every CTA but the last with any
 };
 
 // Shared memory of sched_share.
 struct SchedSmem {
     long long warp_sum[32];
     int b, head, tile, q0, ql, kv;
-    long long rem, u;
+    int rem, u;
 };
 
 // This CTA's share and, if it has one, its first item.  Called by all NT
@@ -163,34 +157,38 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
     if (lane == 31) sm.warp_sum[warp] = upto;
     __syncthreads();
     long long before = 0, total = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += sm.warp_sum[w];
         total += sm.warp_sum[w];
     }
+    if (total >= 1ll << 31) {                        // units are counted in 32 bits: the call is not done
+        if (cta == 0 && tid == 0) atomicOr(status, kAttnTooLong);
+        total = 0;
+    }
     Share s;
-    s.per = total + ctas < 1ll << 31 ? max(static_cast<uint32_t>(total + ctas - 1) / static_cast<uint32_t>(ctas), 1u)
-                                     : (total + ctas - 1) / ctas;
-    s.begin = min(cta * s.per, total);
-    s.end = min(s.begin + s.per, total);
+    s.per = max((static_cast<uint32_t>(total) + ctas - 1) / ctas, 1u);
+    s.begin = static_cast<int>(min(static_cast<long long>(cta) * s.per, total));
+    s.end = static_cast<int>(min(s.begin + static_cast<long long>(s.per), total));
     before += upto - mine;
     if (s.begin < s.end && before <= s.begin && s.begin < before + mine) {
         // this thread's requests hold the first unit: find which
-        long long rem = s.begin - before, units = last;
+        uint32_t rem = static_cast<uint32_t>(s.begin - before);
+        uint32_t units = static_cast<uint32_t>(last);
         int b = tid * chunk;
 #pragma unroll 1
         for (;; ++b) {
             if (chunk > 1) {
                 r = load_request(p.b, b, p.page_log2);
-                units = tile_units(p, r.ql, r.kv, 0, 1);
+                units = static_cast<uint32_t>(tile_units(p, r.ql, r.kv, 0, 1));
             }
             if (rem < units * p.hkv) break;
             rem -= units * p.hkv;
         }
-        const int head = div_units(rem, units);
+        const int head = static_cast<int>(rem / units);
         sm.b = b;
         sm.head = head;
-        sm.rem = rem - head * units;
+        sm.rem = static_cast<int>(rem - head * units);
         sm.q0 = r.q0;
         sm.ql = r.ql;
         sm.kv = r.kv;
@@ -205,16 +203,16 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
     it.tiles = row_tiles(p, it.ql);
     if (warp == 0) {
         // the row tile: a scan over 32 tiles at a time
-        long long rem = sm.rem;
+        int rem = sm.rem;
 #pragma unroll 1
         for (int base = 0;; base += 32) {
             it.tile = base + lane;
             it.n = 0;
             if (it.tile < it.tiles) fill_tile(p, it);
-            long long pre = it.n;
+            int pre = it.n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, pre, o);
+                const int v = __shfl_up_sync(0xffffffffu, pre, o);
                 if (lane >= o) pre += v;
             }
             const unsigned past = __ballot_sync(0xffffffffu, pre > rem);

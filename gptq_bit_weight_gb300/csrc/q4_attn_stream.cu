@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool alive = true;
         for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
             if (it.hi <= 0) continue;
-            const int j0 = static_cast<int>(max(sh.begin - it.u, 0ll));
-            const int j1 = static_cast<int>(min(sh.end - it.u, static_cast<long long>(it.n)));
+            const int j0 = max(sh.begin - it.u, 0);
+            const int j1 = min(sh.end - it.u, it.n);
             const PageWalk walk(a.p, it, a.c.pages);
             TilePages next = walk.tile(it, j0, bad);
             for (int j = j0; j < j1; ++j, seq += 2) {
@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true;
     int seq = 0, buf = 0;
     for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it), buf ^= 1) {
-        const int j0 = static_cast<int>(max(sh.begin - it.u, 0ll));
-        const int j1 = static_cast<int>(min(sh.end - it.u, static_cast<long long>(it.n)));
+        const int j0 = max(sh.begin - it.u, 0);
+        const int j1 = min(sh.end - it.u, it.n);
         const int rows = it.ql * group - it.tile * C::RT;             // of this tile: min(rows, RT)
         // query rows, as MMA fragments
         uint4 *qf = sq + buf * (C::kQ / 16);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 1);
                 l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 2);
             }
-#pragma unroll
+#pragma unroll 1
         for (int half = WK / 2; half; half >>= 1) {
             if (wk >= half && wk < 2 * half) {
                 const int slot = (wk - half) * WR + wr;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             continue;
         }
-        const int c0 = div_units(it.u, sh.per), c1 = div_units(it.u + it.n - 1, sh.per);
+        const int c0 = static_cast<uint32_t>(it.u) / sh.per, c1 = static_cast<uint32_t>(it.u + it.n - 1) / sh.per;
         auto piece = [&](int cta) { return a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece; };
         if (wk == 0) {
             float *w = piece(blockIdx.x);
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float r0 = ref_of(top0), r1 = ref_of(top1);
             float acc[2][4] = {}, l0 = 0.f, l1 = 0.f;
-#pragma unroll 4
+#pragma unroll 2
             for (int c = c0; c <= c1; ++c) {
                 const float4 *w = reinterpret_cast<const float4 *>(piece(c));
                 const float4 v = __ldcg(w + C::RT * D / 4 + ig * 8 + g);

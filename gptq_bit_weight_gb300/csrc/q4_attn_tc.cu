@@ -154,8 +154,8 @@ struct Part {
     int j0, j1;              // its key tiles, counted from it.first
     bool two;                // the second row tile has rows
     __device__ Part(const Item &it, const Share &sh, int tokens)
-        : j0(static_cast<int>(max(sh.begin - it.u, 0ll))),
-          j1(static_cast<int>(min(sh.end - it.u, static_cast<long long>(it.n)))),
+        : j0(max(sh.begin - it.u, 0)),
+          j1(min(sh.end - it.u, it.n)),
           two(it.t1 >= it.t0 + tokens) {}
 };
 
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             const int me_cta = blockIdx.x;
-            const int c0 = div_units(it.u, sh.per), c1 = div_units(it.u + it.n - 1, sh.per);
+            const int c0 = static_cast<uint32_t>(it.u) / sh.per, c1 = static_cast<uint32_t>(it.u + it.n - 1) / sh.per;
             // of each row tile [D / 4][128] float4, then [2][128] (m, l)
             auto piece = [&](int cta) { return a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece; };
             auto columns = [&](int cta, int q) {

@@ -82,19 +82,24 @@ struct PageWalk {
     template <int D>
     __device__ __forceinline__ void copy(const TilePages &t, uint32_t dst, const CUtensorMap *map, uint32_t bar,
                                          int head) const {
-        int page[16];                    // a tile has at most 16 pages
-#pragma unroll
-        for (int i = 0; i < 16; ++i) page[i] = __shfl_sync(0xffffffffu, t.page, i);
-        if (elect_one()) {
-            tc::mbar_arrive_expect_tx(bar, __popc(t.wanted) * (D * 2) << box_log2);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (t.wanted >> i & 1)
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
-                        tma_load_4d(dst + h * (kKt * 128) + (i << box_log2) * 128, map, bar, 64 * h, t.row, head, page[i]);
-        }
+        if (elect_one()) tc::mbar_arrive_expect_tx(bar, __popc(t.wanted) * (D * 2) << box_log2);
         __syncwarp();
+#pragma unroll 1
+        for (int i0 = 0; i0 < (kKt >> box_log2); i0 += 4) {      // a tile has 1 to 16 pages
+            int page[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) page[i] = __shfl_sync(0xffffffffu, t.page, i0 + i);
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (t.wanted >> (i0 + i) & 1)
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_4d(dst + h * (kKt * 128) + ((i0 + i) << box_log2) * 128, map, bar, 64 * h, t.row, head,
+                                        page[i]);
+            }
+            __syncwarp();
+        }
     }
 };
 

@@ -28,6 +28,7 @@ constexpr int kAttnBadBatch = 0x1;     // a length outside its range, or cu_q no
 constexpr int kAttnBadPage = 0x2;      // a page index outside the cache
 constexpr int kAttnBadPosition = 0x4;  // a position outside the rotary table
 constexpr int kAttnTimeout = 0x8;      // a bounded wait ran out
+constexpr int kAttnTooLong = 0x10;     // 2^31 or more units of work in a call
 
 constexpr int ceil16(int r) { return (r + 15) / 16 * 16; }
 constexpr int ceil64(int k) { return (k + 63) / 64 * 64; }
@@ -137,14 +138,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // A request's rows and context length, cut to their ranges: 0 <= q0,
-// q0 + ql <= tokens, 0 <= kv <= width * page.  bad: something had to be cut.
+// q0 + ql <= tokens, 0 <= kv <= width * page and 2^30.  bad: something had to be cut.
 struct Request {
     int q0, ql, kv;
     bool bad;
 };
 __device__ __forceinline__ Request load_request(const AttnBatch &b, int i, int page_log2) {
     const int a = b.cu_q[i], e = b.cu_q[i + 1], n = b.kv_len[i];
-    const long long cap = static_cast<long long>(b.width) << page_log2;
+    const long long cap = min(static_cast<long long>(b.width) << page_log2, 1ll << 30);
     Request r;
     r.q0 = min(max(a, 0), b.tokens);
     r.ql = max(min(e, b.tokens) - r.q0, 0);

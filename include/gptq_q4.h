@@ -496,7 +496,7 @@ typedef struct {
  * new token t has index kv_len - q_len + t in the request's context.  Token j
  * lies in page table[b][j / page_size], at j % page_size.
  *   cu_q   device int32 [batch + 1], ascending
- *   kv_len device int32 [batch], each 0 .. width * page_size
+ *   kv_len device int32 [batch], each 0 .. width * page_size, at most 2^30
  *   table  device int32 [batch][width], table_stride elements from row to row;
  *          only entries of pages that a call reads or writes have to be valid
  *   max_q  no request has more new tokens (a larger number is allowed and
@@ -583,7 +583,11 @@ int gptq_q4_attn_append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, con
  * weight p is rounded to 16 bits for its product with v; the output is
  * rounded once.  Rows that no request owns are left alone.  The order of the
  * sums depends on the lengths of the whole batch, not on timing: the same
- * call gives the same bits.  Errors: INVALID_ARGUMENT (NULL, sizes, strides,
+ * call gives the same bits.  A NaN or infinity in a key reaches the rows that
+ * see it; one in a value may reach earlier new tokens of the same chunk too
+ * (their weight for it is 0, and 0 times it is NaN).  A call of more than 2^31
+ * tiles of work (a prompt of over a million tokens at once) is not done and
+ * reported by gptq_q4_attn_device_error.  Errors: INVALID_ARGUMENT (NULL, sizes, strides,
  * alignment, scale not finite, window < 0), UNSUPPORTED (batch > 4096),
  * CUDA_ERROR. */
 int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache *cache,

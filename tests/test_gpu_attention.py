@@ -294,6 +294,23 @@ def test_lengths_and_pages_out_of_range_are_reported(q4, max_q):
     att.device_error()
 
 
+@pytest.mark.parametrize("max_q", [1, 100000])
+def test_more_work_than_a_call_counts_is_reported_and_not_done(q4, max_q):
+    """2^31 tiles of work, from lengths alone: nothing is read or written."""
+    heads, D, page = 128, 64, 1024
+    i32 = torch.int32
+    att = q4.PagedAttention(heads, heads, D, page)
+    k = torch.zeros(1, heads, page, D, dtype=torch.float16, device=DEV)
+    batch = q4.PagedBatch(torch.tensor([0, 600], dtype=i32, device=DEV), torch.tensor([2 ** 30], dtype=i32, device=DEV),
+                          torch.zeros(1, 2 ** 20, dtype=i32, device=DEV), tokens=600, max_q=max_q)
+    out = torch.full((600, heads, D), 5.0, dtype=torch.float16, device=DEV)
+    att.attend(torch.zeros_like(out), q4.PagedCache(k, k), batch, out=out)
+    with pytest.raises(q4.GPTQ4Error) as e:
+        att.device_error()
+    assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
+    assert (out == 5).all()
+
+
 # ------------------------------------------------------------------ append
 
 def rotate_reference(x, pos, freqs, length, interleaved, dtype):
