@@ -329,8 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 1);
                 l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 2);
             }
+        // (of a single short tile only the first warps have keys)
+        const int held = j1 - j0 > 1 ? WK : min(WK, (max(it.hi - ((it.first + j0) << kKtLog2), 1) + C::KPW - 1) / C::KPW);
 #pragma unroll 1
         for (int half = WK / 2; half; half >>= 1) {
+            if (half >= held) continue;
             if (wk >= half && wk < 2 * half) {
                 const int slot = (wk - half) * WR + wr;
 #pragma unroll
