@@ -1,7 +1,10 @@
 // Attention of few new tokens over the paged cache: single tokens of a decode
 // step, drafts of a few tokens.  The cache is streamed once through shared
-// memory and the products run on mma.sync: with at most 64 query rows for
-// each key the call is bound by reading the cache, not by the tensor cores.
+// memory and the products run on mma.sync in tiles of 16 query rows (token x
+// query head of the group): bound by reading the cache, not by the tensor
+// cores.  64 requests of up to 8192 tokens, 64 heads over 8: 131 us, 6.2 TB/s;
+// two of 131071 and about 100000: 103 us, 6.3 TB/s; one of 777, 32 heads: 12
+// us, latency (lengths, page table, keys, the join of the pieces).
 //
 //   scores s = scale log2(e) q . k in fp32; running maximum m and sum l,
 //   p = 2^(s - m) rounded to 16 bits for its product with v (l sums the
@@ -9,10 +12,11 @@
 //
 // One CTA per SM.  Warps 8 and 9 load key tiles of 128 tokens by TMA, keys and
 // values, one box for each page and 64 columns, into a ring of half-stages
-// (keys, values, keys, ..).  The other eight warps split each tile's tokens (and, from 64 rows on,
-// the rows) and keep maximum, sum and output of their own; they join at the
-// end of an item.  Items cut by the shares join through the workspace: the
-// CTA whose piece arrives last adds the pieces in order.
+// (keys, values, keys, ..).  The other eight warps split each tile's tokens,
+// 16 each, and keep maximum, sum and output of their own, so a tile needs no
+// synchronization among them; they join at the end of an item.  Items cut by
+// the shares join through the workspace: the CTA whose piece arrives last adds
+// the pieces in order.
 #include <cuda.h>
 
 #include <algorithm>
@@ -29,23 +33,20 @@ using namespace tc;
 constexpr int kWarps = 8;                       // consumer warps
 constexpr int kThreads = 32 * (kWarps + 2);     // and two loaders
 
-template <int D_, int MT_, int WR_>
+constexpr int kRows = 16, kRowsLog2 = 4;        // rows of a row tile: one m16 MMA tile
+constexpr int kKeys = kKt / kWarps;             // keys of a warp in a tile
+
+template <int D_>
 struct Cfg {
     static constexpr int D = D_;
-    static constexpr int MT = MT_;              // m16 tiles of rows of a warp
-    static constexpr int WR = WR_;              // warps along the rows
-    static constexpr int WK = kWarps / WR;      // warps along the keys
-    static constexpr int RT = 16 * MT * WR;     // rows of a row tile
-    static constexpr int kRtLog2 = RT == 16 ? 4 : RT == 32 ? 5 : 6;
-    static constexpr int KPW = kKt / WK;        // keys of a warp in a tile
     static constexpr int kHalf = kKt * D * 2;   // bytes of a half-stage
-    static constexpr int kQ = RT * D * 2;       // query fragments, double-buffered
-    static constexpr int kMerge = kWarps / 2 * MT * 16 * D * 4 + kWarps / 2 * MT * 4 * 32 * 4;
+    static constexpr int kQ = kRows * D * 2;    // query fragments, double-buffered
+    static constexpr int kMerge = kWarps / 2 * (kRows * D * 4 + 4 * 32 * 4);
     static constexpr int kMisc = 1024;
     static constexpr int kRoom = 232448 - 1024 - 2 * kQ - kMerge - kMisc;
-    static constexpr int kStages = kRoom / kHalf > 6 ? 6 : kRoom / kHalf;
+    static constexpr int kStages = kRoom / kHalf > 10 ? 10 : kRoom / kHalf;
     static constexpr int kSmem = kStages * kHalf + 2 * kQ + kMerge + kMisc + 1024;
-    static constexpr int kPiece = RT * (D + 2);  // floats of a piece in the workspace
+    static constexpr int kPiece = kRows * (D + 2);   // floats of a piece in the workspace
 };
 
 struct Args {
@@ -55,7 +56,6 @@ struct Args {
     uint16_t *out;
     int64_t q_stride, out_stride;
     float scale;                 // times log2(e)
-    int hq;
     float *ws;                   // [2 * CTAs] pieces
     int *tickets;                // [CTAs], zero between calls
     int *status;
@@ -99,13 +99,13 @@ __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.f :
 template <bool BF, class C>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Args a) {
-    constexpr int D = C::D, MT = C::MT, WR = C::WR, WK = C::WK, KS = D / 16, NT = D / 8, S = C::kStages;
+    constexpr int D = C::D, KS = D / 16, NT = D / 8, S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sb = smem_raw + (base - raw);
-    uint4 *sq = reinterpret_cast<uint4 *>(sb + S * C::kHalf);                     // [2][MT * WR][KS][32]
-    float4 *so = reinterpret_cast<float4 *>(sb + S * C::kHalf + 2 * C::kQ);       // [kWarps / 2][MT][NT][32]
-    float *sml = reinterpret_cast<float *>(so + kWarps / 2 * MT * NT * 32);       // [kWarps / 2][MT][4][32]
+    uint4 *sq = reinterpret_cast<uint4 *>(sb + S * C::kHalf);                     // [2][KS][32]
+    float4 *so = reinterpret_cast<float4 *>(sb + S * C::kHalf + 2 * C::kQ);       // [kWarps / 2][NT][32]
+    float *sml = reinterpret_cast<float *>(so + kWarps / 2 * NT * 32);            // [kWarps / 2][4][32]
     uint8_t *misc = sb + S * C::kHalf + 2 * C::kQ + C::kMerge;
     const uint32_t bar0 = base + S * C::kHalf + 2 * C::kQ + C::kMerge;
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -157,25 +157,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ------------------------------------------------------ consumers
-    const int wr = warp % WR, wk = warp / WR, g = lane >> 2, t4 = lane & 3;
-    const int group = a.p.group.d;
+    const int g = lane >> 2, t4 = lane & 3, group = a.p.group.d;
     bool alive = true;
     int seq = 0, buf = 0;
     for (bool more = true; more && it.u < sh.end; more = next_item(a.p, it), buf ^= 1) {
         const int j0 = max(sh.begin - it.u, 0);
         const int j1 = min(sh.end - it.u, it.n);
-        const int rows = it.ql * group - it.tile * C::RT;             // of this tile: min(rows, RT)
+        const int r_first = it.tile * kRows, rows = it.ql * group - r_first;       // of this tile: min(rows, 16)
         // query rows, as MMA fragments
         uint4 *qf = sq + buf * (C::kQ / 16);
-        for (int f = warp; f < MT * WR * KS; f += kWarps) {
+        for (int f = warp; f < KS; f += kWarps) {
             uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = f / KS * 16 + g + 8 * h;
+                const int r = g + 8 * h;
                 if (r < rows) {
-                    const int rr = it.tile * C::RT + r, t = a.p.group(rr);
+                    const int rr = r_first + r, t = a.p.group(rr);
                     const uint16_t *src = a.q + static_cast<int64_t>(it.q0 + t) * a.q_stride +
-                                          (it.head * group + rr - t * group) * D + f % KS * 16 + 2 * t4;
+                                          (it.head * group + rr - t * group) * D + f * 16 + 2 * t4;
                     w[h] = *reinterpret_cast<const uint32_t *>(src);
                     w[h + 2] = *reinterpret_cast<const uint32_t *>(src + 8);
                 }
@@ -184,235 +183,190 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_consumers();
 
-        float o[MT][NT][4], m[MT][2], l[MT][2];
-        int lim[MT][2];                                                // last key that a row sees
+        float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        int lim[2];                                                    // last key that a row sees
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                m[i][h] = -INFINITY;
-                l[i][h] = 0.f;
-                const int r = it.tile * C::RT + (wr * MT + i) * 16 + g + 8 * h;
-                lim[i][h] = it.kv - it.ql + min(a.p.group(r), it.t1);
-            }
-        }
+        for (int h = 0; h < 2; ++h) lim[h] = it.kv - it.ql + min(a.p.group(r_first + g + 8 * h), it.t1);
         const int lim_min = it.kv - it.ql + it.t0, lim_max = it.kv - it.ql + it.t1;
         if (it.hi > 0) {
             for (int j = j0; j < j1; ++j, seq += 2) {
                 const int sk = seq % S, sv = (seq + 1) % S;
-                const int key_w = ((it.first + j) << kKtLog2) + wk * C::KPW;    // the warp's first key
+                const int key0 = ((it.first + j) << kKtLog2) + warp * kKeys;       // the warp's first key
                 alive = wait_all(alive, full(sk), (seq / S) & 1);
                 const uint32_t kb = base + sk * C::kHalf, vb = base + sv * C::kHalf;
-                uint4 pf[MT];
+                const bool some = key0 < it.hi && key0 + kKeys > it.lo;
+                float s[2][4] = {};
+                if (some) {
 #pragma unroll
-                for (int sub = 0; sub < C::KPW / 16; ++sub) {
-                    const int key0 = key_w + 16 * sub;
-                    const bool some = key0 < it.hi && key0 + 16 > it.lo;
-                    float s[MT][2][4];
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.f;
-                    if (some) {
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            // keys 0-7 x d 0-7, keys 0-7 x d 8-15, keys 8-15 x d 0-7, keys 8-15 x d 8-15
-                            const int row = wk * C::KPW + 16 * sub + (lane & 7) + (lane >> 4) * 8;
-                            const int ch = 2 * (k & 3) + ((lane >> 3) & 1);
-                            uint32_t b[4];
-                            ldsm4(kb + (k >> 2) * (kKt * 128) + row * 128 + ((ch ^ (row & 7)) << 4), b);
-#pragma unroll
-                            for (int i = 0; i < MT; ++i) {
-                                const uint4 q = qf[((wr * MT + i) * KS + k) * 32 + lane];
-                                mma16816<BF>(s[i][0], q, b[0], b[1]);
-                                mma16816<BF>(s[i][1], q, b[2], b[3]);
-                            }
-                        }
+                    for (int k = 0; k < KS; ++k) {
+                        // keys 0-7 x d 0-7, keys 0-7 x d 8-15, keys 8-15 x d 0-7, keys 8-15 x d 8-15
+                        const int row = warp * kKeys + (lane & 7) + (lane >> 4) * 8;
+                        const int ch = 2 * (k & 3) + ((lane >> 3) & 1);
+                        uint32_t b[4];
+                        ldsm4(kb + (k >> 2) * (kKt * 128) + row * 128 + ((ch ^ (row & 7)) << 4), b);
+                        const uint4 q = qf[k * 32 + lane];
+                        mma16816<BF>(s[0], q, b[0], b[1]);
+                        mma16816<BF>(s[1], q, b[2], b[3]);
                     }
-                    const bool edge = key0 + 15 > lim_min || (a.p.window > 0 && key0 <= lim_max - a.p.window);
+                }
+                const bool edge = key0 + kKeys - 1 > lim_min || (a.p.window > 0 && key0 <= lim_max - a.p.window);
+                float top[2] = {-INFINITY, -INFINITY}, keep[2];
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        float top[2] = {-INFINITY, -INFINITY};
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float x = s[i][n][e] * a.scale;
-                                if (edge) {
-                                    const int key = key0 + 8 * n + 2 * t4 + (e & 1), lm = lim[i][e >> 1];
-                                    if (key > lm || (a.p.window > 0 && key <= lm - a.p.window)) x = -INFINITY;
-                                }
-                                s[i][n][e] = x;
-                                top[e >> 1] = fmaxf(top[e >> 1], x);
-                            }
-                        float keep[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-                            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-                            top[h] = fmaxf(top[h], m[i][h]);
-                            keep[h] = ex2(m[i][h] - ref_of(top[h]));
-                            m[i][h] = top[h];
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[n][e] * a.scale;
+                        if (edge) {
+                            const int key = key0 + 8 * n + 2 * t4 + (e & 1), lm = lim[e >> 1];
+                            if (key > lm || (a.p.window > 0 && key <= lm - a.p.window)) x = -INFINITY;
                         }
-                        if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                o[i][n][0] *= keep[0];
-                                o[i][n][1] *= keep[0];
-                                o[i][n][2] *= keep[1];
-                                o[i][n][3] *= keep[1];
-                            }
-                            l[i][0] *= keep[0];
-                            l[i][1] *= keep[1];
-                        }
-                        const float r0 = ref_of(m[i][0]), r1 = ref_of(m[i][1]);
-                        float p[2][4];
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            p[n][0] = ex2(s[i][n][0] - r0);
-                            p[n][1] = ex2(s[i][n][1] - r0);
-                            p[n][2] = ex2(s[i][n][2] - r1);
-                            p[n][3] = ex2(s[i][n][3] - r1);
-                            l[i][0] += p[n][0] + p[n][1];
-                            l[i][1] += p[n][2] + p[n][3];
-                        }
-                        pf[i] = make_uint4(pack2<BF>(p[0][0], p[0][1]), pack2<BF>(p[0][2], p[0][3]),
-                                           pack2<BF>(p[1][0], p[1][1]), pack2<BF>(p[1][2], p[1][3]));
+                        s[n][e] = x;
+                        top[e >> 1] = fmaxf(top[e >> 1], x);
                     }
-                    if (sub == C::KPW / 16 - 1) {          // the warp has read its keys
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty(sk));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                    top[h] = fmaxf(top[h], m[h]);
+                    keep[h] = ex2(m[h] - ref_of(top[h]));
+                    m[h] = top[h];
+                }
+                if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        o[n][0] *= keep[0];
+                        o[n][1] *= keep[0];
+                        o[n][2] *= keep[1];
+                        o[n][3] *= keep[1];
                     }
-                    if (sub == 0) alive = wait_all(alive, full(sv), ((seq + 1) / S) & 1);
-                    if (some) {
-                        // slots past the visible keys hold anything: their values must not meet a weight of 0
-                        const bool trim = key0 + 16 > it.hi || key0 < it.lo;
-                        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    l[0] *= keep[0];
+                    l[1] *= keep[1];
+                }
+                const float r0 = ref_of(m[0]), r1 = ref_of(m[1]);
+                float p[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    p[n][0] = ex2(s[n][0] - r0);
+                    p[n][1] = ex2(s[n][1] - r0);
+                    p[n][2] = ex2(s[n][2] - r1);
+                    p[n][3] = ex2(s[n][3] - r1);
+                    l[0] += p[n][0] + p[n][1];
+                    l[1] += p[n][2] + p[n][3];
+                }
+                const uint4 pf = make_uint4(pack2<BF>(p[0][0], p[0][1]), pack2<BF>(p[0][2], p[0][3]),
+                                            pack2<BF>(p[1][0], p[1][1]), pack2<BF>(p[1][2], p[1][3]));
+                alive = wait_all(alive, full(sv), ((seq + 1) / S) & 1);
+                if (some) {
+                    // slots past the visible keys hold anything: their values must not meet a weight of 0
+                    const bool trim = key0 + kKeys > it.hi || key0 < it.lo;
+                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    if (trim) {
+                        auto in = [&](int key) { return key >= it.lo && key < it.hi; };
+                        const int k0 = key0 + 2 * t4;
+                        keep0 = (in(k0) ? 0xffffu : 0u) | (in(k0 + 1) ? 0xffff0000u : 0u);
+                        keep1 = (in(k0 + 8) ? 0xffffu : 0u) | (in(k0 + 9) ? 0xffff0000u : 0u);
+                    }
+#pragma unroll
+                    for (int n2 = 0; n2 < NT / 2; ++n2) {
+                        // keys 0-7 x d 0-7, keys 8-15 x d 0-7, keys 0-7 x d 8-15, keys 8-15 x d 8-15
+                        const int row = warp * kKeys + (lane & 7) + ((lane >> 3) & 1) * 8;
+                        const int ch = 2 * (n2 & 3) + (lane >> 4);
+                        uint32_t b[4];
+                        ldsm4t(vb + (n2 >> 2) * (kKt * 128) + row * 128 + ((ch ^ (row & 7)) << 4), b);
                         if (trim) {
-                            auto in = [&](int key) { return key >= it.lo && key < it.hi; };
-                            const int k0 = key0 + 2 * t4;
-                            keep0 = (in(k0) ? 0xffffu : 0u) | (in(k0 + 1) ? 0xffff0000u : 0u);
-                            keep1 = (in(k0 + 8) ? 0xffffu : 0u) | (in(k0 + 9) ? 0xffff0000u : 0u);
+                            b[0] &= keep0;
+                            b[1] &= keep1;
+                            b[2] &= keep0;
+                            b[3] &= keep1;
                         }
-#pragma unroll
-                        for (int n2 = 0; n2 < NT / 2; ++n2) {
-                            // keys 0-7 x d 0-7, keys 8-15 x d 0-7, keys 0-7 x d 8-15, keys 8-15 x d 8-15
-                            const int row = wk * C::KPW + 16 * sub + (lane & 7) + ((lane >> 3) & 1) * 8;
-                            const int ch = 2 * (n2 & 3) + (lane >> 4);
-                            uint32_t b[4];
-                            ldsm4t(vb + (n2 >> 2) * (kKt * 128) + row * 128 + ((ch ^ (row & 7)) << 4), b);
-                            if (trim) {
-                                b[0] &= keep0;
-                                b[1] &= keep1;
-                                b[2] &= keep0;
-                                b[3] &= keep1;
-                            }
-#pragma unroll
-                            for (int i = 0; i < MT; ++i) {
-                                mma16816<BF>(o[i][2 * n2], pf[i], b[0], b[1]);
-                                mma16816<BF>(o[i][2 * n2 + 1], pf[i], b[2], b[3]);
-                            }
-                        }
+                        mma16816<BF>(o[2 * n2], pf, b[0], b[1]);
+                        mma16816<BF>(o[2 * n2 + 1], pf, b[2], b[3]);
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty(sv));
+                if (lane == 0) {
+                    mbar_arrive(empty(sk));
+                    mbar_arrive(empty(sv));
+                }
             }
         }
         // ---------------------------------------- the warps' parts of the keys, joined in a fixed order
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 1);
-                l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 2);
-            }
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
         // (of a single short tile only the first warps have keys)
-        const int held = j1 - j0 > 1 ? WK : min(WK, (max(it.hi - ((it.first + j0) << kKtLog2), 1) + C::KPW - 1) / C::KPW);
+        const int held = j1 - j0 > 1 ? kWarps : min(kWarps, (max(it.hi - ((it.first + j0) << kKtLog2), 1) + kKeys - 1) / kKeys);
 #pragma unroll 1
-        for (int half = WK / 2; half; half >>= 1) {
+        for (int half = kWarps / 2; half; half >>= 1) {
             if (half >= held) continue;
-            if (wk >= half && wk < 2 * half) {
-                const int slot = (wk - half) * WR + wr;
+            if (warp >= half && warp < 2 * half) {
+                const int slot = warp - half;
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        so[((slot * MT + i) * NT + n) * 32 + lane] =
-                            make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
-                    float *ml = sml + (slot * MT + i) * 128 + lane;
-                    ml[0] = m[i][0];
-                    ml[32] = m[i][1];
-                    ml[64] = l[i][0];
-                    ml[96] = l[i][1];
-                }
+                for (int n = 0; n < NT; ++n) so[(slot * NT + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+                float *ml = sml + slot * 128 + lane;
+                ml[0] = m[0];
+                ml[32] = m[1];
+                ml[64] = l[0];
+                ml[96] = l[1];
             }
             bar_consumers();
-            if (wk < half) {
-                const int slot = wk * WR + wr;
+            if (warp < half) {
+                const float *ml = sml + warp * 128 + lane;
+                float mine[2], other[2];
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const float *ml = sml + (slot * MT + i) * 128 + lane;
-                    float mine[2], other[2];
+                for (int h = 0; h < 2; ++h) {
+                    const float mo = ml[32 * h], top = fmaxf(m[h], mo), r = ref_of(top);
+                    mine[h] = ex2(m[h] - r);
+                    other[h] = ex2(mo - r);
+                    m[h] = top;
+                    l[h] = l[h] * mine[h] + ml[64 + 32 * h] * other[h];
+                }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float mo = ml[32 * h], top = fmaxf(m[i][h], mo), r = ref_of(top);
-                        mine[h] = ex2(m[i][h] - r);
-                        other[h] = ex2(mo - r);
-                        m[i][h] = top;
-                        l[i][h] = l[i][h] * mine[h] + ml[64 + 32 * h] * other[h];
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float4 v = so[((slot * MT + i) * NT + n) * 32 + lane];
-                        o[i][n][0] = o[i][n][0] * mine[0] + v.x * other[0];
-                        o[i][n][1] = o[i][n][1] * mine[0] + v.y * other[0];
-                        o[i][n][2] = o[i][n][2] * mine[1] + v.z * other[1];
-                        o[i][n][3] = o[i][n][3] * mine[1] + v.w * other[1];
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    const float4 v = so[(warp * NT + n) * 32 + lane];
+                    o[n][0] = o[n][0] * mine[0] + v.x * other[0];
+                    o[n][1] = o[n][1] * mine[0] + v.y * other[0];
+                    o[n][2] = o[n][2] * mine[1] + v.z * other[1];
+                    o[n][3] = o[n][3] * mine[1] + v.w * other[1];
                 }
             }
             bar_consumers();
         }
         // ---------------------------------------- output, or a piece for the workspace
-        auto store = [&](int i_global, int n, int h, float x, float y, float inv) {
-            const int r = i_global * 16 + g + 8 * h;
-            if (r >= rows || r >= C::RT) return;
-            const int rr = it.tile * C::RT + r, t = a.p.group(rr);
+        auto store = [&](int n, int h, float x, float y, float inv) {
+            const int r = g + 8 * h;
+            if (r >= rows) return;
+            const int rr = r_first + r, t = a.p.group(rr);
             *reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                                           (it.head * group + rr - t * group) * D + 8 * n + 2 * t4) =
                 pack2<BF>(x * inv, y * inv);
         };
         auto inverse = [](float sum) { return sum == 0.f ? 0.f : 1.f / sum; };
         if (j0 == 0 && j1 == it.n) {
-            if (wk == 0)
+            if (warp == 0) {
+                const float i0 = inverse(l[0]), i1 = inverse(l[1]);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const float i0 = inverse(l[i][0]), i1 = inverse(l[i][1]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        store(wr * MT + i, n, 0, o[i][n][0], o[i][n][1], i0);
-                        store(wr * MT + i, n, 1, o[i][n][2], o[i][n][3], i1);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    store(n, 0, o[n][0], o[n][1], i0);
+                    store(n, 1, o[n][2], o[n][3], i1);
                 }
+            }
             continue;
         }
+        // [NT][32] float4 fragments, then (m, l) of rows g and g + 8
         const int c0 = static_cast<uint32_t>(it.u) / sh.per, c1 = static_cast<uint32_t>(it.u + it.n - 1) / sh.per;
-        auto piece = [&](int cta) { return a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece; };
-        if (wk == 0) {
-            float *w = piece(blockIdx.x);
-            float4 *wo = reinterpret_cast<float4 *>(w);
-            float4 *wml = wo + C::RT * D / 4;
+        auto piece = [&](int cta) {
+            return reinterpret_cast<float4 *>(a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece);
+        };
+        if (warp == 0) {
+            float4 *w = piece(blockIdx.x);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int ig = wr * MT + i;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    __stcg(wo + (ig * NT + n) * 32 + lane, make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]));
-                if (t4 == 0) __stcg(wml + ig * 8 + g, make_float4(m[i][0], m[i][1], l[i][0], l[i][1]));
-            }
+            for (int n = 0; n < NT; ++n) __stcg(w + n * 32 + lane, make_float4(o[n][0], o[n][1], o[n][2], o[n][3]));
+            if (t4 == 0) __stcg(w + NT * 32 + g, make_float4(m[0], m[1], l[0], l[1]));
             __threadfence();
         }
         bar_consumers();
@@ -425,39 +379,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_consumers();
         if (!*reinterpret_cast<volatile int *>(last_flag)) continue;
-        for (int f = warp; f < MT * WR * (NT / 2); f += kWarps) {
-            const int ig = f / (NT / 2), n0 = f % (NT / 2) * 2;
+        for (int n = 2 * warp; n < NT; n += 2 * kWarps) {
             float top0 = -INFINITY, top1 = -INFINITY;
             for (int c = c0; c <= c1; ++c) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(c)) + C::RT * D / 4 + ig * 8 + g);
+                const float4 v = __ldcg(piece(c) + NT * 32 + g);
                 top0 = fmaxf(top0, v.x);
                 top1 = fmaxf(top1, v.y);
             }
             const float r0 = ref_of(top0), r1 = ref_of(top1);
-            float acc[2][4] = {}, l0 = 0.f, l1 = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), bcc = acc;
+            float l0 = 0.f, l1 = 0.f;
 #pragma unroll 2
             for (int c = c0; c <= c1; ++c) {
-                const float4 *w = reinterpret_cast<const float4 *>(piece(c));
-                const float4 v = __ldcg(w + C::RT * D / 4 + ig * 8 + g);
-                const float4 x = __ldcg(w + (ig * NT + n0) * 32 + lane), y = __ldcg(w + (ig * NT + n0 + 1) * 32 + lane);
+                const float4 *w = piece(c);
+                const float4 v = __ldcg(w + NT * 32 + g), x = __ldcg(w + n * 32 + lane), y = __ldcg(w + (n + 1) * 32 + lane);
                 const float f0 = ex2(v.x - r0), f1 = ex2(v.y - r1);
                 l0 += v.z * f0;
                 l1 += v.w * f1;
-                acc[0][0] += x.x * f0;
-                acc[0][1] += x.y * f0;
-                acc[0][2] += x.z * f1;
-                acc[0][3] += x.w * f1;
-                acc[1][0] += y.x * f0;
-                acc[1][1] += y.y * f0;
-                acc[1][2] += y.z * f1;
-                acc[1][3] += y.w * f1;
+                acc.x += x.x * f0;
+                acc.y += x.y * f0;
+                acc.z += x.z * f1;
+                acc.w += x.w * f1;
+                bcc.x += y.x * f0;
+                bcc.y += y.y * f0;
+                bcc.z += y.z * f1;
+                bcc.w += y.w * f1;
             }
             const float i0 = inverse(l0), i1 = inverse(l1);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                store(ig, n0 + e, 0, acc[e][0], acc[e][1], i0);
-                store(ig, n0 + e, 1, acc[e][2], acc[e][3], i1);
-            }
+            store(n, 0, acc.x, acc.y, i0);
+            store(n, 1, acc.z, acc.w, i1);
+            store(n + 1, 0, bcc.x, bcc.y, i0);
+            store(n + 1, 1, bcc.z, bcc.w, i1);
         }
     }
     if (!alive && lane == 0) atomicOr(a.status, kAttnTimeout);
@@ -465,36 +417,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class C>
 cudaError_t launch(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
-                   const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st) {
-    Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), C::kRtLog2, FastDiv(1)}, c, a.q, a.out, a.q_stride, a.out_stride,
-              a.scale * 1.4426950408889634f, s.hq, a.ws, a.tickets, a.status};
-    auto kernel = bf16 ? attend_stream_kernel<true, C> : attend_stream_kernel<false, C>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+                   cudaStream_t st) {
+    CUtensorMap tk, tv;
+    const uint32_t box = std::min(s.page, kKt);
+    cudaError_t e = encode_pages(&tk, c.k, s, c, box);
+    if (!e) e = encode_pages(&tv, c.v, s, c, box);
     if (e) return e;
+    Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), kRowsLog2, FastDiv(1)},
+              c, a.q, a.out, a.q_stride, a.out_stride, a.scale * 1.4426950408889634f, a.ws, a.tickets, a.status};
+    auto kernel = bf16 ? attend_stream_kernel<true, C> : attend_stream_kernel<false, C>;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem))) return e;
     kernel<<<a.ctas, kThreads, C::kSmem, st>>>(tk, tv, args);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attend_stream_ws_bytes(int ctas) { return static_cast<size_t>(2) * ctas * Cfg<128, 2, 2>::kPiece * sizeof(float); }
+size_t attend_stream_ws_bytes(int ctas) { return static_cast<size_t>(2) * ctas * Cfg<128>::kPiece * sizeof(float); }
 
 cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a,
                                  bool bf16, cudaStream_t st) {
-    CUtensorMap tk, tv;
-    const uint32_t box = std::min(s.page, kKt);
-    cudaError_t e = encode_pages(&tk, c.k, s, c, box);
-    if (!e) e = encode_pages(&tv, c.v, s, c, box);
-    if (e) return e;
-    // row tiles of 16, 32 or 64 rows: the smallest that holds a request's
-    const int64_t rows = static_cast<int64_t>(a.max_q) * s.group;
-    auto go = [&](auto d) {
-        constexpr int D = decltype(d)::value;
-        if (rows <= 16) return launch<Cfg<D, 1, 1>>(s, b, c, a, bf16, tk, tv, st);
-        if (rows <= 32) return launch<Cfg<D, 2, 1>>(s, b, c, a, bf16, tk, tv, st);
-        return launch<Cfg<D, 2, 2>>(s, b, c, a, bf16, tk, tv, st);
-    };
-    return s.d == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
+    return s.d == 64 ? launch<Cfg<64>>(s, b, c, a, bf16, st) : launch<Cfg<128>>(s, b, c, a, bf16, st);
 }
 
 }  // namespace q4
