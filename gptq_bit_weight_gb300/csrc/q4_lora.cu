@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
         if (ck > 1) cluster_sync();
         else __syncthreads();
         if (part == 0) {
-            const float scale = v.slot[slot].scale;
+            const LoraSlot info = v.slot[slot];
             for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
                 float s = sum[e];
                 for (int p = 1; p < ck; ++p) {
@@ -258,8 +258,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
                 }
                 // element e of the MMA's result: lane (g, q), value v: rank g + 8 (v / 2), row 2 q + v % 2
                 const int lane = e >> 2 & 31, row = (e >> 7) * 8 + 2 * (lane & 3) + (e & 1);
-                if (row < n)
-                    v.t[static_cast<size_t>(s_rows[row]) * v.rpad + r0 + (lane >> 2) + 8 * (e >> 1 & 1)] = s * scale;
+                const int r = r0 + (lane >> 2) + 8 * (e >> 1 & 1);
+                // a rank of the padding would be NaN in a row of x with an infinity
+                if (row < n) v.t[static_cast<size_t>(s_rows[row]) * v.rpad + r] = r < info.rank ? s * info.scale : 0.f;
             }
         }
         if (ck > 1) cluster_sync();                      // nobody goes on while its sums are read

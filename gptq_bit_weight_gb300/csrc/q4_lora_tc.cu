@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         const int mine = k.cls[row];
         if (mine < 0) continue;
         const int rank = k.rank[mine];
-        const float scale = v.slot[k.slot[mine]].scale;
+        const LoraSlot info = v.slot[k.slot[mine]];
         float2 x[3];                                     // kShrinkCap ranks
         float top = 0.f;
 #pragma unroll
@@ -306,8 +306,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                     x[g].x += y.x;
                     x[g].y += y.y;
                 }
-                x[g].x *= scale;
-                x[g].y *= scale;
+                // a rank of the padding would be NaN in a row of x with an infinity
+                x[g].x = r < info.rank ? x[g].x * info.scale : 0.f;
+                x[g].y = r + 1 < info.rank ? x[g].y * info.scale : 0.f;
             }
             top = fmaxf(top, fmaxf(fabsf(x[g].x), fabsf(x[g].y)));
         }

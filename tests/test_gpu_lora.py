@@ -182,6 +182,26 @@ def test_large_sums_and_foreign_nan(q4, M):
     assert not torch.isfinite(out[1]).any() and not torch.isfinite(out[3]).any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M", [3, 400])
+def test_an_infinity_keeps_its_sign(q4, M, dtype):
+    """An adapter of rank 1, stored with 15 ranks of zeros beside it: infinity in x times those is NaN."""
+    K, N = 128, 264
+    g = torch.Generator().manual_seed(14)
+    away = lambda *n: (lambda t: (t.sign() * (t.abs() + 0.1)).to(dtype))(torch.randn(*n, generator=g))
+    a, b = away(1, K), away(N, 1)
+    x, y = torch.randn(M, K, generator=g).to(dtype), torch.randn(M, N, generator=g).to(dtype)
+    x[1, 5] = float("inf")
+    rows = torch.zeros(M, dtype=torch.int32)
+    ref, tol = reference(x, y, rows, [(a, b, 0.5)], K)
+    assert torch.isinf(ref[1]).all()
+    pool = pool_of(q4, [(a, b, 0.5)], K, N, 1, 1, dtype)
+    out = pool.add(x.to(DEV), rows.to(DEV), y.to(DEV)).double().cpu()
+    assert torch.equal(out[1], ref[1])
+    clean = torch.arange(M) != 1
+    check(out[clean], ref[clean], tol[clean], "other rows")
+
+
 @pytest.mark.parametrize("M", [9, 200])
 def test_a_broken_adapter_stays_with_its_rows(q4, M):
     """An infinity in one adapter's B, NaN in another's A: rows of other adapters, and of none, in the same tile."""
