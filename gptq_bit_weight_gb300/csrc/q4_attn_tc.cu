@@ -4,10 +4,9 @@
 //   scores s = q . k (fp32); reference m and sum l of each row,
 //   p = 2^(c (s - m)), c = scale log2(e), rounded to 16 bits for its product
 //   with v (l sums the unrounded ones); o = sum p v in fp32; o / l rounded
-//   once.  m is the maximum of the first key tile, and is raised to a later
-//   tile's only when the p of a tile sum to more than 2^12: any m at or
-//   below the row's maximum gives the same result as long as p fits 16 bits,
-//   so most tiles need no maximum and no rescaling of the output.
+//   once.  m is the maximum of the row's first key tile, and is raised to a
+//   later tile's only when that is more than 2^8 away: any m gives the same
+//   result as long as p fits 16 bits, so most tiles rescale no output.
 //
 // One CTA per SM works on two tiles of up to 128 rows at a time (row = token x
 // query head of the group, so the heads that share a key/value head share its
@@ -146,7 +145,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // What of an item falls to this CTA, the same for every role.
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(done, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
-            mbar_init(p_ready(i), 128);
+            mbar_init(p_ready(i), 4);
             mbar_init(pv_done(i), 1);
         }
         mbar_init_fence();
@@ -301,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += total.x + total.y;
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(p_ready(me));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready(me));
                 }
                 alive = wait_all(alive, pv_done(me), (uses - 1) & 1);
                 tc_fence_after();
