@@ -68,12 +68,13 @@ struct Classes {
     int units[kRows + 1];            // units of work of earlier classes
     int row[kRows];                  // chunk-relative rows, class after class
     int n;
-    int s_slot[kRows], s_lead[kRows];
+    __align__(16) int s_slot[kRows]; // while it is built
+    int s_lead[2], s_count[kRows], s_units[kRows];
 };
 // Called by the whole CTA.  work(rows, rank): the units of a class.
 template <class Work>
 __device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &c, int m0, Classes &k, Work work) {
-    const int i = threadIdx.x;
+    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
     int slot = -2, rank = 0;                             // -2: no row, -1: no adapter
     if (i < kRows) {
         if (m0 + i < c.M) {
@@ -83,56 +84,67 @@ __device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &
                 slot = -1;
             }
             slot = max(slot, -1);
-            if (slot >= 0) rank = ceil16(v.slot[slot].rank);
         }
         k.s_slot[i] = slot;
+        k.s_count[i] = k.s_units[i] = 0;
+        if (slot >= 0) rank = ceil16(v.slot[slot].rank);
     }
     __syncthreads();
-    int lead = kRows, at = 0;                            // the first row of the same slot; rows of it before this one
+    uint32_t same[2] = {0, 0};                           // the rows of the same slot
+    int lead = 0;
     if (i < kRows) {
-#pragma unroll 16
-        for (int j = 0; j < kRows; ++j) {
-            const bool same = k.s_slot[j] == slot;
-            lead = min(lead, same ? j : kRows);
-            at += same && j < i;
+#pragma unroll
+        for (int j = 0; j < kRows / 4; ++j) {
+            const int4 o = reinterpret_cast<const int4 *>(k.s_slot)[j];
+            same[j / 8] |= (o.x == slot ? 1u : 0u) << (4 * j & 31) | (o.y == slot ? 2u : 0u) << (4 * j & 31) |
+                           (o.z == slot ? 4u : 0u) << (4 * j & 31) | (o.w == slot ? 8u : 0u) << (4 * j & 31);
         }
-        k.s_lead[i] = slot == -2 ? kRows : lead;
+        lead = same[0] ? __ffs(same[0]) - 1 : 31 + __ffs(same[1]);
+        const unsigned leads = __ballot_sync(0xffffffffu, slot != -2 && lead == i);
+        if (lane == 0) k.s_lead[warp] = leads;
     }
     __syncthreads();
+    auto below = [](uint32_t m, int n) { return __popc(n >= 32 ? m : m & ((1u << n) - 1)); };
+    auto earlier = [&](const auto *m, int n) { return below(m[0], n) + (n > 32 ? below(m[1], n - 32) : 0); };
+    int id = 0;
     if (i < kRows && slot != -2) {
-        int id = 0, before = 0, count = 0;               // classes and rows with an earlier first row
-#pragma unroll 16
-        for (int j = 0; j < kRows; ++j) {
-            const int l = k.s_lead[j];
-            before += l < lead;
-            id += l == j && l < lead;
-            count += l == lead;
-        }
-        k.row[before + at] = i;
+        id = earlier(k.s_lead, lead);
         if (lead == i) {
+            const int count = __popc(same[0]) + __popc(same[1]);
             k.slot[id] = slot;
             k.rank[id] = rank;
-            k.first[id] = before;
-            k.first[id + 1] = before + count;            // the next class writes the same
-            k.units[id + 1] = work(count, rank);
+            k.s_count[id] = count;
+            k.s_units[id] = work(count, rank);
         }
     }
-    if (i == 0) k.units[0] = 0;
-    const int leads = __syncthreads_count(i < kRows && slot != -2 && lead == i);
-    if (i < 32) {                                        // prefix sums of the units
-        int a = i < leads ? k.units[i + 1] : 0, b = i + 32 < leads ? k.units[i + 33] : 0;
+    __syncthreads();
+    if (i < kRows) {                                     // prefix sums, by either warp for itself
+        int rows[2] = {k.s_count[lane], k.s_count[lane + 32]}, units[2] = {k.s_units[lane], k.s_units[lane + 32]};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-            if (i >= o) {
-                a += x;
-                b += y;
+        for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int x = __shfl_up_sync(0xffffffffu, rows[h], o), y = __shfl_up_sync(0xffffffffu, units[h], o);
+                if (lane >= o) {
+                    rows[h] += x;
+                    units[h] += y;
+                }
             }
+        rows[1] += __shfl_sync(0xffffffffu, rows[0], 31);
+        units[1] += __shfl_sync(0xffffffffu, units[0], 31);
+        if (warp == 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                k.first[lane + 32 * h + 1] = rows[h];
+                k.units[lane + 32 * h + 1] = units[h];
+            }
+        if (i == 0) {
+            k.first[0] = k.units[0] = 0;
+            k.n = __popc(k.s_lead[0]) + __popc(k.s_lead[1]);
         }
-        b += __shfl_sync(0xffffffffu, a, 31);
-        k.units[i + 1] = a;
-        k.units[i + 33] = b;
-        if (i == 0) k.n = leads;
+        // the row's place: the rows of the classes before its own, and its own class's before it
+        const int upto[2] = {__shfl_sync(0xffffffffu, rows[0], id & 31), __shfl_sync(0xffffffffu, rows[1], id & 31)};
+        if (slot != -2) k.row[upto[id >> 5] - k.s_count[id] + earlier(same, i)] = i;
     }
     __syncthreads();
 }
@@ -164,11 +176,13 @@ __device__ __forceinline__ uint4 ldg_stream(const uint16_t *p) {
 }
 
 // t of 16 ranks for 8 NT rows, this warp's part of K: ranks are the MMA's
-// rows, the call's rows its columns.
+// rows, the call's rows its columns.  Row tile j's 16 x 8 sums go to
+// red[j pitch ..]: element e of the MMA's result, lane (g, q), value v, is
+// rank g + 8 (v / 2), row 2 q + v % 2.
 template <bool BF, int NT>
 __device__ __forceinline__ void shrink_rows(const LoraView &v, const LoraCall &c, const uint16_t *a, int rg,
-                                            const int *s_rows, int n, int first, int step, float *red) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+                                            const int *s_rows, int n, int first, int step, float4 *red, int pitch) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const uint16_t *x[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) x[i] = 8 * i + g < n ? c.x + s_rows[8 * i + g] * c.xs + 8 * q : nullptr;
@@ -201,9 +215,21 @@ __device__ __forceinline__ void shrink_rows(const LoraView &v, const LoraCall &c
             }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-        reinterpret_cast<float4 *>(red)[(j * kWarps + warp) * 32 + lane] =
-            make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    for (int j = 0; j < NT; ++j) red[j * pitch + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// *p of the cluster's CTA `rank`.
+__device__ __forceinline__ float load_of(const float *p, int rank) {
+    uint32_t from;
+    float x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(from)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(from) : "memory");
+    return x;
 }
 
 // Grid: (clusters over the chunk's (class, block of 16 ranks) units x CTAs of
@@ -226,10 +252,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
         const int *s_rows = k.row + k.first[id];
         const uint16_t *a = v.a + static_cast<size_t>(slot) * v.rpad * ceil64(v.K) + static_cast<size_t>(r0) * 64;
         const int first = part * kWarps + warp, step = ck * kWarps, rg = rank / 8;
-        if (nt == 1) shrink_rows<BF, 1>(v, c, a, rg, s_rows, n, first, step, red);
-        else if (Few || nt == 2) shrink_rows<BF, 2>(v, c, a, rg, s_rows, n, first, step, red);
-        else if (nt <= 4) shrink_rows<BF, 4>(v, c, a, rg, s_rows, n, first, step, red);
-        else shrink_rows<BF, 8>(v, c, a, rg, s_rows, n, first, step, red);
+        float4 *mine = reinterpret_cast<float4 *>(red) + 32 * warp;
+        if (nt == 1) shrink_rows<BF, 1>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+        else if (Few || nt == 2) shrink_rows<BF, 2>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+        else if (nt <= 4) shrink_rows<BF, 4>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+        else shrink_rows<BF, 8>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
         __syncthreads();
         // the warps' parts of K in order, then the cluster's
         for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
@@ -238,25 +265,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
             for (int w = 0; w < kWarps; ++w) s += red[(e >> 7) * kWarps * 128 + w * 128 + (e & 127)];
             sum[e] = s;
         }
-        auto cluster_sync = [] {
-            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        };
         if (ck > 1) cluster_sync();
         else __syncthreads();
         if (part == 0) {
             const LoraSlot info = v.slot[slot];
             for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
                 float s = sum[e];
-                for (int p = 1; p < ck; ++p) {
-                    uint32_t from;
-                    float o;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                        : "=r"(from)
-                        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(sum + e))), "r"(p));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(from) : "memory");
-                    s += o;
-                }
-                // element e of the MMA's result: lane (g, q), value v: rank g + 8 (v / 2), row 2 q + v % 2
+                for (int p = 1; p < ck; ++p) s += load_of(sum + e, p);
                 const int lane = e >> 2 & 31, row = (e >> 7) * 8 + 2 * (lane & 3) + (e & 1);
                 const int r = r0 + (lane >> 2) + 8 * (e >> 1 & 1);
                 // a rank of the padding would be NaN in a row of x with an infinity
@@ -272,24 +287,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
 // takes an equal run of units, class after class, and keeps t of its 16 rows
 // in registers as MMA fragments, high and low part.  Rows are the MMA's rows,
 // columns its columns, in the order that gives a thread 8 consecutive ones.
-template <bool BF>
-__global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v, LoraCall c) {
-    __shared__ Classes k;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int m0 = blockIdx.y * kRows, nb = (v.N + 31) / 32;
-    find_classes(v, c, m0, k, [](int rows, int) { return (rows + 15) / 16; });
-    c.y += m0 * c.ys;
-    c.out += m0 * c.os;
-    v.t += static_cast<size_t>(m0) * v.rpad;
-    const int warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
-    const int64_t units = static_cast<int64_t>(k.units[k.n]) * nb;
-    int64_t u = units * me / warps;
-    const int64_t end = units * (me + 1) / warps;
-    // B and y of the warp's units into L2 while the first launch runs
+struct Run {
+    int nb;                  // column blocks of a group of 16 rows
+    int64_t u, end;          // the warp's units
+    __device__ Run(const Classes &k, int N) : nb((N + 31) / 32) {
+        const int warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + (threadIdx.x >> 5);
+        const int64_t units = static_cast<int64_t>(k.units[k.n]) * nb;
+        u = units * me / warps;
+        end = units * (me + 1) / warps;
+    }
+};
+// B and y of the warp's units into L2.
+__device__ __forceinline__ void prefetch_units(const LoraView &v, const LoraCall &c, const Classes &k, const Run &run) {
+    const int lane = threadIdx.x & 31, nb = run.nb;
     auto prefetch = [](const uint16_t *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); };
-    for (int64_t w = u; w < end;) {
+    for (int64_t w = run.u; w < run.end;) {
         const int group = static_cast<int>(w / nb), b0 = static_cast<int>(w % nb);
-        const int b1 = static_cast<int>(min(static_cast<int64_t>(nb), b0 + (end - w)));
+        const int b1 = static_cast<int>(min(static_cast<int64_t>(nb), b0 + (run.end - w)));
         w += b1 - b0;
         const int id = class_of(k, group), rank = k.rank[id];
         const int r0 = k.first[id] + 16 * (group - k.units[id]), n = min(16, k.first[id + 1] - r0);
@@ -301,117 +315,204 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v,
         for (int e = lane; e < n * (b1 - b0); e += 32)
             prefetch(c.y + k.row[r0 + e % n] * c.ys + 32 * (b0 + e / n));
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    {
-        while (u < end) {
-            const int group = static_cast<int>(u / nb), b0 = static_cast<int>(u % nb);
-            const int b1 = static_cast<int>(min(static_cast<int64_t>(nb), b0 + (end - u)));
-            u += b1 - b0;
-            const int id = class_of(k, group), rank = k.rank[id], steps = (rank + 31) / 32, rg = rank / 8;
-            const int r0 = k.first[id] + 16 * (group - k.units[id]) + g, r1 = k.first[id + 1];
-            const uint16_t *b = v.b + (rank ? static_cast<size_t>(k.slot[id]) * v.rpad * v.N : 0);
-            const bool have[2] = {r0 < r1, r0 + 8 < r1};
-            const int64_t row[2] = {have[0] ? k.row[r0] : 0, have[1] ? k.row[r0 + 8] : 0};
-            if (rank == 0 && c.out == c.y) continue;
-            // t of 32 ranks: the lane's 8 ranks of its two rows
-            float x[2][8];
-            auto load = [&](int s) {
+}
+// t: [row][pitch] in global memory, written by another launch, or in shared memory.
+template <bool BF, bool Shared>
+__device__ __forceinline__ void expand_units(const LoraView &v, const LoraCall &c, const Classes &k, const Run &run,
+                                             const float *t, int pitch) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, nb = run.nb;
+    auto load4 = [](const float4 *p) {
+        if constexpr (Shared) return *p;
+        else return __ldcg(p);
+    };
+    const int64_t end = run.end;
+    for (int64_t u = run.u; u < end;) {
+        const int group = static_cast<int>(u / nb), b0 = static_cast<int>(u % nb);
+        const int b1 = static_cast<int>(min(static_cast<int64_t>(nb), b0 + (end - u)));
+        u += b1 - b0;
+        const int id = class_of(k, group), rank = k.rank[id], steps = (rank + 31) / 32, rg = rank / 8;
+        const int r0 = k.first[id] + 16 * (group - k.units[id]) + g, r1 = k.first[id + 1];
+        const uint16_t *b = v.b + (rank ? static_cast<size_t>(k.slot[id]) * v.rpad * v.N : 0);
+        const bool have[2] = {r0 < r1, r0 + 8 < r1};
+        const int64_t row[2] = {have[0] ? k.row[r0] : 0, have[1] ? k.row[r0 + 8] : 0};
+        if (rank == 0 && c.out == c.y) continue;
+        // t of 32 ranks: the lane's 8 ranks of its two rows
+        float x[2][8];
+        auto load = [&](int s) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float4 p = make_float4(0.f, 0.f, 0.f, 0.f), r = p;
-                    if (have[h] && 32 * s + 8 * q < rank) {
-                        const float4 *t = reinterpret_cast<const float4 *>(v.t + row[h] * v.rpad + 32 * s + 8 * q);
-                        p = __ldcg(t);
-                        r = __ldcg(t + 1);
-                    }
-                    x[h][0] = p.x, x[h][1] = p.y, x[h][2] = p.z, x[h][3] = p.w;
-                    x[h][4] = r.x, x[h][5] = r.y, x[h][6] = r.z, x[h][7] = r.w;
+            for (int h = 0; h < 2; ++h) {
+                float4 p = make_float4(0.f, 0.f, 0.f, 0.f), r = p;
+                if (have[h] && 32 * s + 8 * q < rank) {
+                    const float4 *at = reinterpret_cast<const float4 *>(t + row[h] * pitch + 32 * s + 8 * q);
+                    p = load4(at);
+                    r = load4(at + 1);
                 }
-            };
-            float up[2] = {1.f, 1.f}, down[2] = {1.f, 1.f};
-            if constexpr (!BF) {
-                float top[2] = {0.f, 0.f};
-                for (int s = 0; s < steps; ++s) {
-                    load(s);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top[h] = fmaxf(top[h], fabsf(x[h][e]));
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-                    up[h] = split_scale_of(top[h]);
-                    down[h] = 1.f / up[h];               // a power of two: exact
-                }
+                x[h][0] = p.x, x[h][1] = p.y, x[h][2] = p.z, x[h][3] = p.w;
+                x[h][4] = r.x, x[h][5] = r.y, x[h][6] = r.z, x[h][7] = r.w;
             }
-            uint32_t f[2][4][4];                         // fragments of 64 ranks: [32 ranks][k16 half, part][register]
-            auto fragments = [&](int s, uint32_t (&o)[4][4]) {
+        };
+        float up[2] = {1.f, 1.f}, down[2] = {1.f, 1.f};
+        if constexpr (!BF) {
+            float top[2] = {0.f, 0.f};
+            for (int s = 0; s < steps; ++s) {
                 load(s);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float y0 = x[h][e] * down[h], y1 = x[h][e + 1] * down[h];
-                        const uint16_t h0 = to16<BF>(y0), h1 = to16<BF>(y1);
-                        const int half = e >> 2, reg = (e >> 1 & 1) * 2 + h;
-                        o[2 * half][reg] = h0 | static_cast<uint32_t>(h1) << 16;
-                        o[2 * half + 1][reg] = split_low<BF>(y0, h0) | static_cast<uint32_t>(split_low<BF>(y1, h1)) << 16;
-                    }
-            };
+                    for (int e = 0; e < 8; ++e) top[h] = fmaxf(top[h], fabsf(x[h][e]));
+            }
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (s < steps) fragments(s, f[s]);
-            for (int blk = b0; blk < b1; ++blk) {
-                const int col = 32 * blk + 8 * q;        // the thread's 8 columns of out
-                uint4 y[2];
+            for (int h = 0; h < 2; ++h) {
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                up[h] = split_scale_of(top[h]);
+                down[h] = 1.f / up[h];               // a power of two: exact
+            }
+        }
+        uint32_t f[2][4][4];                         // fragments of 64 ranks: [32 ranks][k16 half, part][register]
+        auto fragments = [&](int s, uint32_t (&o)[4][4]) {
+            load(s);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    y[h] = make_uint4(0, 0, 0, 0);
-                    if (have[h] && col < v.N) y[h] = *reinterpret_cast<const uint4 *>(c.y + row[h] * c.ys + col);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float y0 = x[h][e] * down[h], y1 = x[h][e + 1] * down[h];
+                    const uint16_t h0 = to16<BF>(y0), h1 = to16<BF>(y1);
+                    const int half = e >> 2, reg = (e >> 1 & 1) * 2 + h;
+                    o[2 * half][reg] = h0 | static_cast<uint32_t>(h1) << 16;
+                    o[2 * half + 1][reg] = split_low<BF>(y0, h0) | static_cast<uint32_t>(split_low<BF>(y1, h1)) << 16;
                 }
-                float acc[4][4] = {};
-                auto product = [&](int s, const uint32_t (&t)[4][4]) {
-                    uint4 w[4];
+        };
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (s < steps) fragments(s, f[s]);
+        for (int blk = b0; blk < b1; ++blk) {
+            const int col = 32 * blk + 8 * q;        // the thread's 8 columns of out
+            uint4 y[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                y[h] = make_uint4(0, 0, 0, 0);
+                if (have[h] && col < v.N) y[h] = *reinterpret_cast<const uint4 *>(c.y + row[h] * c.ys + col);
+            }
+            float acc[4][4] = {};
+            auto product = [&](int s, const uint32_t (&t)[4][4]) {
+                uint4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // MMA column g of tile j is column 8 (g / 2) + 2 j + g % 2 of the 32
+                    const int cg = 4 * blk + (g >> 1), in = 2 * j + (g & 1), kb = 4 * s + q;
+                    w[j] = make_uint4(0, 0, 0, 0);
+                    if (cg * 8 < v.N && kb < rg) w[j] = ldg_stream(b + (static_cast<size_t>(cg) * rg + kb) * 64 + in * 8);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma16816<BF>(acc[j], t[i][0], t[i][1], t[i][2], t[i][3], i < 2 ? w[j].x : w[j].z,
+                                     i < 2 ? w[j].y : w[j].w);
+            };
+            if (steps > 0) product(0, f[0]);
+            if (steps > 1) product(1, f[1]);
+            for (int s = 2; s < steps; ++s) {        // ranks past 64: their fragments are made anew
+                uint32_t more[4][4];
+                fragments(s, more);
+                product(s, more);
+            }
+            if (col >= v.N) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!have[h]) continue;
+                uint32_t *yw = reinterpret_cast<uint32_t *>(&y[h]);
+                if (rank)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        // MMA column g of tile j is column 8 (g / 2) + 2 j + g % 2 of the 32
-                        const int cg = 4 * blk + (g >> 1), in = 2 * j + (g & 1), kb = 4 * s + q;
-                        w[j] = make_uint4(0, 0, 0, 0);
-                        if (cg * 8 < v.N && kb < rg) w[j] = ldg_stream(b + (static_cast<size_t>(cg) * rg + kb) * 64 + in * 8);
+                        const float2 o = unpack2<BF>(yw[j]);
+                        yw[j] = pack2<BF>(fmaf(acc[j][2 * h], up[h], o.x), fmaf(acc[j][2 * h + 1], up[h], o.y));
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma16816<BF>(acc[j], t[i][0], t[i][1], t[i][2], t[i][3], i < 2 ? w[j].x : w[j].z,
-                                         i < 2 ? w[j].y : w[j].w);
-                };
-                if (steps > 0) product(0, f[0]);
-                if (steps > 1) product(1, f[1]);
-                for (int s = 2; s < steps; ++s) {        // ranks past 64: their fragments are made anew
-                    uint32_t more[4][4];
-                    fragments(s, more);
-                    product(s, more);
-                }
-                if (col >= v.N) continue;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!have[h]) continue;
-                    uint32_t *yw = reinterpret_cast<uint32_t *>(&y[h]);
-                    if (rank)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 o = unpack2<BF>(yw[j]);
-                            yw[j] = pack2<BF>(fmaf(acc[j][2 * h], up[h], o.x), fmaf(acc[j][2 * h + 1], up[h], o.y));
-                        }
-                    *reinterpret_cast<uint4 *>(c.out + row[h] * c.os + col) = y[h];
-                }
+                *reinterpret_cast<uint4 *>(c.out + row[h] * c.os + col) = y[h];
             }
         }
     }
 }
+
+template <bool BF>
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v, LoraCall c) {
+    __shared__ Classes k;
+    const int m0 = blockIdx.y * kRows;
+    find_classes(v, c, m0, k, [](int rows, int) { return (rows + 15) / 16; });
+    c.y += m0 * c.ys;
+    c.out += m0 * c.os;
+    const Run run(k, v.N);
+    prefetch_units(v, c, k, run);                        // while the first launch runs
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    expand_units<BF, false>(v, c, k, run, v.t + static_cast<size_t>(m0) * v.rpad, v.rpad);
+}
+
+// Both products in one launch, for a single row whose adapter has few values:
+// every cluster forms all of t for itself, its CTAs a part of K each, and its
+// warps then have their share of the columns.  At 4096 x 4096, rank 16, the
+// GPU takes 5.4 us instead of 7.3 and a call from the host 9.5 instead of 12;
+// at 8192 x 28672, rank 64, the GPU 5.8 instead of 8.4.  The same with the
+// classes of two to four rows was no faster than two launches (4 rows of 4096 x
+// 11008, rank 16: 9.2 and 8.5 us; 3 rows, rank 64: 14 and 9.7).
+constexpr int kOneCtas = 8;          // of a cluster
+constexpr int kOneClusters = 16;     // at most: one wave
+constexpr int kOneRank = 256;
+constexpr int64_t kOneValues = 1 << 19;      // of A
+template <bool BF>
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_one_kernel(LoraView v, LoraCall c) {
+    __shared__ Classes k;
+    __shared__ __align__(16) float part[kOneRank / 16 * 128];                // [16 ranks, part of K][128]
+    __shared__ __align__(16) float t[kOneRank];
+    const int warp = threadIdx.x >> 5, cta = blockIdx.x % kOneCtas;
+    int slot = c.row_slot[0];
+    if (slot >= v.slots) {
+        if (threadIdx.x == 0) atomicOr(v.status, kLoraBadSlot);
+        slot = -1;
+    }
+    slot = max(slot, -1);
+    LoraSlot info{0, 0.f, 1};
+    if (slot >= 0) info = v.slot[slot];
+    const int rank = ceil16(info.rank);
+    if (threadIdx.x <= kRows) k.units[threadIdx.x] = threadIdx.x > 0;        // one class, of one row
+    if (threadIdx.x == 0) {
+        k.n = 1;
+        k.slot[0] = slot;
+        k.rank[0] = rank;
+        k.first[0] = k.row[0] = 0;
+        k.first[1] = 1;
+    }
+    __syncthreads();
+    const Run run(k, v.N);
+    prefetch_units(v, c, k, run);
+    const int units = rank / 16, split = max(1, kWarps / max(units, 1));     // warps of 16 ranks along K
+    for (int job = warp; job < units * split; job += kWarps)
+        shrink_rows<BF, 1>(v, c, v.a + static_cast<size_t>(slot) * v.rpad * ceil64(v.K) + static_cast<size_t>(job / split) * 1024,
+                           rank / 8, k.row, 1, cta * split + job % split, kOneCtas * split,
+                           reinterpret_cast<float4 *>(part) + job * 32, 0);
+    __syncthreads();
+    // the warps' parts of K in order, then the cluster's; a thread has a rank, at its place as shrink_rows left it
+    const int r = threadIdx.x;
+    float *at = part + r / 16 * split * 128 + (r & 7) * 16 + (r >> 3 & 1) * 2;
+    if (r < rank)
+        for (int w = 1; w < split; ++w) *at += at[w * 128];
+    __syncwarp();
+    cluster_sync();
+    if (r < rank) {
+        float x[kOneCtas], sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < kOneCtas; ++p) x[p] = load_of(at, p);
+#pragma unroll
+        for (int p = 0; p < kOneCtas; ++p) sum += x[p];
+        t[r] = r < info.rank ? sum * info.scale : 0.f;
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");    // nobody leaves while its sums are read
+    expand_units<BF, true>(v, c, k, run, t, 0);
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+static_assert(kOneRank <= 32 * kWarps && kOneRank / 16 >= kWarps, "a thread for each rank, a part for every warp");
 
 template <class... P, class... T>
 cudaError_t start(void (*k)(P...), dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t st,
@@ -453,6 +554,12 @@ cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlo
 }
 
 cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
+    if (c.M == 1 && v.rpad <= kOneRank && static_cast<int64_t>(v.rpad) * v.K <= kOneValues) {
+        const int clusters = std::min((v.N + 32 * kWarps * kOneCtas - 1) / (32 * kWarps * kOneCtas), kOneClusters);
+        *launches += 1;
+        return start(bf16 ? lora_one_kernel<true> : lora_one_kernel<false>, dim3(clusters * kOneCtas), 32 * kWarps, 0,
+                     kOneCtas, false, st, v, c);
+    }
     const int chunks_all = (c.M + kRows - 1) / kRows;
     for (int c0 = 0; c0 < chunks_all; c0 += 65535) {     // chunks are the grid's y dimension
         LoraCall d = c;

@@ -82,6 +82,14 @@ CASES = [  # (M, K, N, ranks, rows: "one", "mixed", "runs")
     (128, 64, 64, [64], "one"),
     (1280, 64, 24576, [16, 8], "runs"),      # a dozen column tiles for each SM
     (513, 4104, 1160, [128, 16, 100], "mixed"),
+    (1, 1000, 1288, [16], "one"),            # one row of a small adapter: one launch
+    (1, 2056, 328, [40], "one"),
+    (1, 96, 4104, [24, 5], "mixed"),
+    (1, 2048, 264, [256], "one"),
+    (1, 8, 40968, [100], "one"),
+    (1, 4096, 512, [256], "one"),            # and of a larger one: two
+    (4, 1000, 1288, [16] * 10, "mixed"),
+    (16, 4096, 512, [33, 16, 64], "mixed"),
 ]
 
 
