@@ -59,6 +59,7 @@ __global__ void lora_set_kernel(uint16_t *a, uint16_t *b, LoraSlot *slot, const 
 
 constexpr int kRows = 64;            // rows of a call's chunk that one CTA looks over
 constexpr int kWarps = 8;
+constexpr int kCluster = 8;          // CTAs that split K, at most
 
 // The rows of chunk [m0, m0 + 64), by adapter.  An adapter in use is a class,
 // in the order of its first row; the rows without one are a class as well.
@@ -270,8 +271,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
         if (part == 0) {
             const LoraSlot info = v.slot[slot];
             for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
-                float s = sum[e];
-                for (int p = 1; p < ck; ++p) s += load_of(sum + e, p);
+                float x[kCluster], s = 0.f;              // on their way together, added in order
+#pragma unroll
+                for (int p = 0; p < kCluster; ++p) x[p] = p < ck ? load_of(sum + e, p) : 0.f;
+#pragma unroll
+                for (int p = 0; p < kCluster; ++p) s += x[p];
                 const int lane = e >> 2 & 31, row = (e >> 7) * 8 + 2 * (lane & 3) + (e & 1);
                 const int r = r0 + (lane >> 2) + 8 * (e >> 1 & 1);
                 // a rank of the padding would be NaN in a row of x with an infinity
@@ -576,7 +580,7 @@ cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cud
         // (class, 16 ranks) units that one chunk can hold, and two CTAs for each SM over them; K is split over a
         // cluster where the units alone are fewer
         const int units = std::min(rows, v.slots) * (v.rpad / 16);
-        int ck = 8;
+        int ck = kCluster;
         while (ck > 1 && (static_cast<int64_t>(units) * chunks * ck > 2 * 304 || v.K / ck < 512)) ck /= 2;
         const int gx = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, 304 / (static_cast<int64_t>(ck) * chunks))));
         // two CTAs for each SM, as long as every warp has a unit
