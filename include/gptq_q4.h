@@ -462,9 +462,11 @@ int gptq_q4_lora_reserve(gptq_q4_lora h, int max_m);
  *   y, out    device [M][N], row strides y_stride, out_stride; out may be y itself
  *             (same stride), and must not overlap x or otherwise overlap y
  * Pointers 16-byte aligned, strides multiples of 8 and at least the row's
- * length; M = 0 is a no-op.  x . A^T, its products with B and the sum with y
- * are fp32, rounded once to the output.  Errors: INVALID_ARGUMENT,
- * OUT_OF_MEMORY (growing the workspace), CUDA_ERROR. */
+ * length; M = 0 is a no-op.  Sums are fp32 and the output is rounded once;
+ * x . A^T goes into its product with B as two 16-bit parts, which hold it to
+ * 2^-16 (bf16) or 2^-22 (fp16) of itself.  Infinities and NaN in x, y or an
+ * adapter reach the rows that they belong to and no other.  Errors:
+ * INVALID_ARGUMENT, OUT_OF_MEMORY (growing the workspace), CUDA_ERROR. */
 int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int32_t *row_slot, int M, const void *y,
                      int64_t y_stride, void *out, int64_t out_stride, cudaStream_t stream);
 

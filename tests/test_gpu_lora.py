@@ -210,7 +210,7 @@ def test_an_infinity_keeps_its_sign(q4, M, dtype):
     check(out[clean], ref[clean], tol[clean], "other rows")
 
 
-@pytest.mark.parametrize("M", [9, 200])
+@pytest.mark.parametrize("M", [9, 200, 500])
 def test_a_broken_adapter_stays_with_its_rows(q4, M):
     """An infinity in one adapter's B, NaN in another's A: rows of other adapters, and of none, in the same tile."""
     K, N, dtype = 320, 400, torch.bfloat16
