@@ -367,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int n = 0; n < NT; ++n) __stcg(w + n * 32 + lane, make_float4(o[n][0], o[n][1], o[n][2], o[n][3]));
             if (t4 == 0) __stcg(w + NT * 32 + g, make_float4(m[0], m[1], l[0], l[1]));
-            __threadfence();
         }
         bar_consumers();
         if (threadIdx.x == 0) {

@@ -416,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 __stcg(columns(me_cta, q) + v * 128, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
                     }
                     if (valid) __stcg(ml(me_cta), make_float2(m, l));
-                    __threadfence();
                 }
                 bar_softmax();
                 if (threadIdx.x == 0) {
@@ -593,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < each; ++i) {
                             const int buf = turns ? j & 1 : i;
                             pv(buf, sv, j < ahead);
+                            if (i == each - 1) umma_commit(empty(sv % S));       // not after waiting for keys
                             if (!next) continue;
                             if (i == 0) wait(full(sk % S), sk / S);
                             qk(buf, i, sk);
                         }
-                        umma_commit(empty(sv % S));
                         if (next) umma_commit(empty(sk % S));
                         if (j + ahead + 1 == n) umma_commit(q_empty);
                     }
