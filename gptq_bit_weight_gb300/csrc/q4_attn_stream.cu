@@ -370,11 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_consumers();
         if (threadIdx.x == 0) {
-            __threadfence();
-            const int before = atomicAdd(a.tickets + c0, 1);
+            const int before = count_piece(a.tickets + c0);
             *last_flag = before == c1 - c0;
             if (before == c1 - c0) a.tickets[c0] = 0;
-            __threadfence();
         }
         bar_consumers();
         if (!*reinterpret_cast<volatile int *>(last_flag)) continue;

@@ -22,12 +22,13 @@
 //   warp 10         zeroes value rows outside the visible keys in the tiles
 //                   at the edges: such slots hold anything, and 0 x NaN is NaN
 // Two row tiles, because one alone leaves the tensor cores idle during its
-// softmax; 208 registers for the softmax threads (a row of 128 scores each) and
-// 88 for the others add up to the launch's 384 x 168.  4096 tokens over 16384,
+// softmax; 184 registers for the softmax threads (a row of 128 scores each) and
+// 136 for the others add up to the launch's 384 x 168 (with 208 and 88 the
+// loaders and the issuer spill: 32 requests of 4 tokens 58 us instead of 54.5).  4096 tokens over 16384,
 // 64 heads over 8 of 128: 1120 to 1150 us, 1.7 PFLOP/s, what the tensor cores
-// sustain under the power limit; 512 over 8192: 100 us (1.33 PFLOP/s: start,
+// sustain under the power limit; 512 over 8192: 98 us (1.36 PFLOP/s: start,
 // last wave and the join of the pieces); 384 together with 47 single tokens of
-// others: 125 us, units of single tokens bound by the ring of loads (2 us a
+// others: 111 us, units of single tokens bound by the ring of loads (1.3 us a
 // tile).  Heads of 64, 4096 over 16384, 32 over 8: 463 us, bound by the softmax
 // warps' own chain (with columns of their own for the weights, so that the next
 // scores never wait for the second product: 503).
@@ -221,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     bool alive = true;
     const bool work = sh.begin < sh.end;
-    // 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168
+    // 168 registers a thread at launch: 256 x 184 + 128 x 136 = 384 x 168
     if (warp < kSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---------------------------------------------- softmax: a thread holds a row
         const int me = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -419,9 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 bar_softmax();
                 if (threadIdx.x == 0) {
-                    __threadfence();
-                    *last_flag = atomicAdd(a.tickets + c0, 1) == c1 - c0;
-                    __threadfence();
+                    *last_flag = count_piece(a.tickets + c0) == c1 - c0;
                 }
                 bar_softmax();
                 last = *reinterpret_cast<volatile int *>(last_flag);
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
         if (!work) {
         } else if (warp == kKeys || warp == kValues) {
             const bool values = warp == kValues;

@@ -49,6 +49,14 @@ __device__ __forceinline__ bool wait_all(bool alive, uint32_t bar, uint32_t pari
     return __all_sync(0xffffffffu, alive);
 }
 
+// Counts a piece in the workspace, by one thread behind a barrier: what the CTA wrote before is there for whoever
+// counts later.
+__device__ __forceinline__ int count_piece(int *ticket) {
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+    return before;
+}
+
 // The pages of one key tile, as a loader warp holds them: lane i has page i.
 struct TilePages {
     int page;                // this lane's
