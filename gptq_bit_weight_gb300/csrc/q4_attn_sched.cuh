@@ -120,11 +120,101 @@ struct SchedSmem {
     int rem, u;
 };
 
+// Units of a lane's request (or of none: ql 0), by a whole warp.
+__device__ __forceinline__ long long request_units(const SchedParams &p, const Request &r) {
+    // a request of many row tiles is summed by all lanes
+    const bool many = row_tiles(p, r.ql) > 4;
+    long long units = many ? 0 : tile_units(p, r.ql, r.kv, 0, 1);
+    const int lane = threadIdx.x & 31;
+    for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
+        const int who = __ffs(left) - 1;
+        long long s = tile_units(p, __shfl_sync(0xffffffffu, r.ql, who), __shfl_sync(0xffffffffu, r.kv, who), lane, 32);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == who) units = s;
+    }
+    return units;
+}
+__device__ __forceinline__ long long prefix_sum(long long v) {       // inclusive, within a warp
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+__device__ __forceinline__ Share share_of(long long total, int cta, int ctas, int *status) {
+    if (total >= 1ll << 31) {                        // units are counted in 32 bits: the call is not done
+        if (cta == 0 && threadIdx.x == 0) atomicOr(status, kAttnTooLong);
+        total = 0;
+    }
+    Share s;
+    s.per = max((static_cast<uint32_t>(total) + ctas - 1) / ctas, 1u);
+    s.begin = static_cast<int>(min(static_cast<long long>(cta) * s.per, total));
+    s.end = static_cast<int>(min(s.begin + static_cast<long long>(s.per), total));
+    return s;
+}
+// The row tile of it's request and head that holds unit `rem` of theirs, by a
+// whole warp; `at` is that unit's number.  Sets it.tile and it.u.
+__device__ __forceinline__ void find_tile(const SchedParams &p, Item &it, int rem, int at) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int base = 0;; base += 32) {
+        it.tile = base + lane;
+        it.n = 0;
+        if (it.tile < it.tiles) fill_tile(p, it);
+        int pre = it.n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, pre, o);
+            if (lane >= o) pre += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, pre > rem);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            it.tile = base + who;
+            it.u = at - (rem - __shfl_sync(0xffffffffu, pre - it.n, who));
+            return;
+        }
+        if (base + 32 >= it.tiles) {                 // cannot be: the sums said otherwise
+            it.tile = it.tiles - 1;
+            it.u = at;
+            return;
+        }
+        rem -= __shfl_sync(0xffffffffu, pre, 31);
+    }
+}
+
 // This CTA's share and, if it has one, its first item.  Called by all NT
-// threads of the CTA; `sm` must not be in use before or within the call.
+// threads of the CTA, which it synchronizes; `sm` must not be in use before or
+// within the call.  A call of up to 32 requests is short, and this is at its
+// head: every warp works its share out for itself.
 template <int NT>
 __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int ctas, int *status, Item &it) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.b.batch <= 32) {
+        Request r{0, 0, 0, false};
+        if (lane < p.b.batch) r = load_request(p.b, lane, p.page_log2);
+        if (r.bad && cta == 0 && warp == 0) atomicOr(status, kAttnBadBatch);
+        const long long units = request_units(p, r), mine = units * p.hkv, upto = prefix_sum(mine);
+        const Share s = share_of(__shfl_sync(0xffffffffu, upto, 31), cta, ctas, status);
+        if (s.begin < s.end) {
+            const int who = __ffs(__ballot_sync(0xffffffffu, s.begin < upto)) - 1;
+            const uint32_t each = static_cast<uint32_t>(__shfl_sync(0xffffffffu, units, who));
+            const uint32_t rem = static_cast<uint32_t>(s.begin - __shfl_sync(0xffffffffu, upto - mine, who));
+            it.b = who;
+            it.head = static_cast<int>(rem / each);
+            it.q0 = __shfl_sync(0xffffffffu, r.q0, who);
+            it.ql = __shfl_sync(0xffffffffu, r.ql, who);
+            it.kv = __shfl_sync(0xffffffffu, r.kv, who);
+            it.tiles = row_tiles(p, it.ql);
+            find_tile(p, it, static_cast<int>(rem - it.head * each), s.begin);
+            fill_tile(p, it);
+        }
+        __syncthreads();
+        return s;
+    }
     const int chunk = (p.b.batch + NT - 1) / NT;     // requests of a thread, in order
     long long mine = 0, last = 0;
     Request r{0, 0, 0, false};
@@ -136,24 +226,10 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
             r = load_request(p.b, b, p.page_log2);
             if (r.bad && cta == 0) atomicOr(status, kAttnBadBatch);
         }
-        // a request of many row tiles is summed by the whole warp
-        const bool many = row_tiles(p, r.ql) > 4;
-        last = many ? 0 : tile_units(p, r.ql, r.kv, 0, 1);
-        for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
-            const int who = __ffs(left) - 1;
-            long long s = tile_units(p, __shfl_sync(0xffffffffu, r.ql, who), __shfl_sync(0xffffffffu, r.kv, who), lane, 32);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == who) last = s;
-        }
+        last = request_units(p, r);
         mine += last * p.hkv;
     }
-    long long upto = mine;                           // inclusive prefix within the warp
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
+    const long long upto = prefix_sum(mine);
     if (lane == 31) sm.warp_sum[warp] = upto;
     __syncthreads();
     long long before = 0, total = 0;
@@ -162,14 +238,7 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
         if (w < warp) before += sm.warp_sum[w];
         total += sm.warp_sum[w];
     }
-    if (total >= 1ll << 31) {                        // units are counted in 32 bits: the call is not done
-        if (cta == 0 && tid == 0) atomicOr(status, kAttnTooLong);
-        total = 0;
-    }
-    Share s;
-    s.per = max((static_cast<uint32_t>(total) + ctas - 1) / ctas, 1u);
-    s.begin = static_cast<int>(min(static_cast<long long>(cta) * s.per, total));
-    s.end = static_cast<int>(min(s.begin + static_cast<long long>(s.per), total));
+    const Share s = share_of(total, cta, ctas, status);
     before += upto - mine;
     if (s.begin < s.end && before <= s.begin && s.begin < before + mine) {
         // this thread's requests hold the first unit: find which
@@ -202,35 +271,10 @@ __device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int c
     it.kv = sm.kv;
     it.tiles = row_tiles(p, it.ql);
     if (warp == 0) {
-        // the row tile: a scan over 32 tiles at a time
-        int rem = sm.rem;
-#pragma unroll 1
-        for (int base = 0;; base += 32) {
-            it.tile = base + lane;
-            it.n = 0;
-            if (it.tile < it.tiles) fill_tile(p, it);
-            int pre = it.n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, pre, o);
-                if (lane >= o) pre += v;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, pre > rem);
-            if (past) {
-                if (lane == __ffs(past) - 1) {
-                    sm.tile = it.tile;
-                    sm.u = s.begin - (rem - (pre - it.n));
-                }
-                break;
-            }
-            if (base + 32 >= it.tiles) {             // cannot be: the sums said otherwise
-                if (lane == 0) {
-                    sm.tile = it.tiles - 1;
-                    sm.u = s.begin;
-                }
-                break;
-            }
-            rem -= __shfl_sync(0xffffffffu, pre, 31);
+        find_tile(p, it, sm.rem, s.begin);
+        if (lane == 0) {
+            sm.tile = it.tile;
+            sm.u = it.u;
         }
     }
     __syncthreads();

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = tok < a.tokens && t <= it.t1, valid = active && mine;
             const int lim = mine ? it.kv - it.ql + t : -1;             // last key that the row sees
             const int lim_lo = a.p.window > 0 ? lim - a.p.window : -1; // keys up to this one are out of the window
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, f0 = 1.f, f1 = 0.f;
             if (it.hi > 0 && (active || joins)) {
                 // keys that every row of this row tile sees
                 const int own = it.kv - it.ql, tb = min(ta + a.tokens - 1, it.t1);
@@ -328,27 +328,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (me == 0) {
                         const float2 v = s_ml[row];
                         const float top = fmaxf(m, v.x), ref = top == -INFINITY ? 0.f : top;
-                        const float f0 = ex2((m - ref) * c), f1 = ex2((v.x - ref) * c);
-#pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
-                            uint32_t x[16], y[16];
-                            tmem_ld16(tO + 16 * q, x);
-                            tmem_ld16(tO + 128 + 16 * q, y);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
-                            tmem_st16(tO + 16 * q, x);
-                        }
-                        tmem_wait_st();
+                        f0 = ex2((m - ref) * c);
+                        f1 = ex2((v.x - ref) * c);
                         m = top;
                         l = l * f0 + v.y * f1;
                     }
-                    tc_fence_before();
-                    bar_softmax();                       // the second buffer has been read
-                    tc_fence_after();
                 }
             }
+            const bool rows_here = __any_sync(0xffffffffu, valid);     // in this warp
+            auto outputs = [&](int q, float *o) {                      // 32 columns, of both buffers where they join
+                tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(o));
+                if (joins) {
+                    float y[32];
+                    tmem_ld32(tO + 128 + 32 * q, reinterpret_cast<uint32_t *>(y));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + y[e] * f1;
+                } else {
+                    tmem_wait_ld();
+                }
+            };
+            auto end_item = [&] {
+                tc_fence_before();
+                if (joins) bar_softmax();                // the second buffer has been read
+                tc_fence_after();
+            };
             // ------------------------------------------ output, or a piece for the workspace
             uint16_t *dst = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                             (it.head * static_cast<int>(a.p.group.d) + head_in) * D;
@@ -361,24 +365,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    pack2<BF>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
             };
             if (part.j0 == 0 && part.j1 == it.n) {
-                if (active) {
+                if (active && rows_here) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         float o[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                        if (it.hi > 0) {
-                            tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(o));
-                            tmem_wait_ld();
-                        }
+                        if (it.hi > 0) outputs(q, o);
                         if (l == 0.f)                    // a row that sees nothing
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = 0.f;
                         if (valid) store(o, inv, q);
                     }
-                    tc_fence_before();
                 }
+                end_item();
                 continue;
             }
             const int me_cta = blockIdx.x;
@@ -397,20 +398,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool last = false;
             if (few) {
                 if (threadIdx.x == 0) {
-                    const int there = *reinterpret_cast<volatile int *>(a.tickets + c0);
-                    __threadfence();
-                    *last_flag = there == c1 - c0;
+                    *last_flag = pieces_counted(a.tickets + c0) == c1 - c0;
                 }
                 bar_softmax();
                 last = *reinterpret_cast<volatile int *>(last_flag);
             }
             if (!last) {
-                if (active) {
-#pragma unroll
+                if (active && rows_here) {
+#pragma unroll 1
                     for (int q = 0; q < D / 32; ++q) {
                         float o[32];
-                        tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(o));
-                        tmem_wait_ld();
+                        outputs(q, o);
                         if (valid)                       // the other rows are not anybody's
 #pragma unroll
                             for (int v = 0; v < 8; ++v)
@@ -457,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (last) {
                 // the pieces in the order of their CTAs, this one's from tensor memory
                 if (threadIdx.x == 0) a.tickets[c0] = 0;
-                if (active) {
-                    float top = m;
+                if (active && rows_here) {
+                    float top = m, sum = 0.f;
+#pragma unroll 4
                     for (int k = c0; k <= c1; ++k)
                         if (k != me_cta && valid) top = fmaxf(top, __ldcg(ml(k)).x);
                     const float ref = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f;
+#pragma unroll 4
                     for (int k = c0; k <= c1; ++k) {
                         const float2 v = k == me_cta || !valid ? make_float2(m, l) : __ldcg(ml(k));
                         sum += v.y * ex2((v.x - ref) * c);
@@ -477,16 +476,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = c0; k <= c1; ++k) {
                             float x[32], f;
                             if (k == me_cta) {
-                                tmem_ld32(tO + 32 * q, reinterpret_cast<uint32_t *>(x));
-                                tmem_wait_ld();
+                                outputs(q, x);
                                 f = ex2((m - ref) * c);
                             } else {
+                                const float2 v = valid ? __ldcg(ml(k)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-                                for (int v = 0; v < 8; ++v) {
-                                    const float4 y = valid ? __ldcg(columns(k, q) + v * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-                                    x[4 * v] = y.x, x[4 * v + 1] = y.y, x[4 * v + 2] = y.z, x[4 * v + 3] = y.w;
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 y = valid ? __ldcg(columns(k, q) + e * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    x[4 * e] = y.x, x[4 * e + 1] = y.y, x[4 * e + 2] = y.z, x[4 * e + 3] = y.w;
                                 }
-                                f = valid ? ex2((__ldcg(ml(k)).x - ref) * c) : 0.f;
+                                f = valid ? ex2((v.x - ref) * c) : 0.f;
                                 __syncwarp();
                             }
 #pragma unroll
@@ -496,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            tc_fence_before();
+            end_item();
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");

@@ -56,6 +56,12 @@ __device__ __forceinline__ int count_piece(int *ticket) {
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
     return before;
 }
+// Pieces counted so far; what they hold may be read.
+__device__ __forceinline__ int pieces_counted(const int *ticket) {
+    int n;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(n) : "l"(ticket) : "memory");
+    return n;
+}
 
 // The pages of one key tile, as a loader warp holds them: lane i has page i.
 struct TilePages {
