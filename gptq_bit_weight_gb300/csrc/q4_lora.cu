@@ -67,28 +67,45 @@ __global__ void lora_set_kernel(uint16_t *a, uint16_t *b, LoraSlot *slot, const 
     }
 }
 
-constexpr int kRows = 64;            // rows of a call's chunk that one CTA looks over
 constexpr int kWarps = 8;
 constexpr int kCluster = 8;          // CTAs that split K, at most
+constexpr int kRows = 64;            // rows of a class that one unit of the first launch takes
 
-// The rows of chunk [m0, m0 + 64), by adapter.  An adapter in use is a class,
+// The rows of a chunk of up to R, by adapter.  An adapter in use is a class,
 // in the order of its first row; the rows without one are a class as well.
+template <int R>
 struct Classes {
-    int slot[kRows], rank[kRows];    // of each class; rank padded to 16, 0: no adapter
-    int first[kRows + 1];            // its first place in `row`
-    int units[kRows + 1];            // units of work of earlier classes
-    int row[kRows];                  // chunk-relative rows, class after class
+    int slot[R], rank[R];            // of each class; rank padded to 16, 0: no adapter
+    int first[R + 1];                // its first place in `row`
+    int units[R + 1];                // units of work of earlier classes
+    int row[R];                      // chunk-relative rows, class after class
     int n;
-    __align__(16) int s_slot[kRows]; // while it is built
-    int s_lead[2], s_count[kRows], s_units[kRows];
 };
-// Called by the whole CTA.  work(rows, rank): the units of a class.
+// While they are found: the first rows' bits, and more.
+template <int R>
+struct Scratch {
+    static constexpr int kMaxSlots = 4096;
+    uint32_t lead[R / 32];
+    __align__(4) uint8_t in[R / 32][R];      // of each warp's 32 rows those of a class
+    uint16_t before[R / 32][R];              // rows of a class in earlier warps
+    int2 sum[R / 32];
+    int first[kMaxSlots + 1];                // first row of a slot (of none: at 0)
+};
+template <>
+struct Scratch<64> {
+    uint32_t lead[2];
+    __align__(16) int slot[64];
+    int count[64], units[64];
+};
+// Called by the whole CTA.  work(rows, rank): the units of a class.  A chunk
+// of 64 compares all its rows with one another.
 template <class Work>
-__device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &c, int m0, Classes &k, Work work) {
+__device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &c, int m0, Classes<64> &k,
+                                             Scratch<64> &z, Work work) {
     const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
     int slot = -2, rank = 0;                             // -2: no row, -1: no adapter
-    if (i < kRows) {
-        if (m0 + i < c.M) {
+    if (i < 64) {
+        if (i < c.chunk && m0 + i < c.M) {
             slot = c.row_slot[m0 + i];
             if (slot >= v.slots) {
                 atomicOr(v.status, kLoraBadSlot);
@@ -96,41 +113,41 @@ __device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &
             }
             slot = max(slot, -1);
         }
-        k.s_slot[i] = slot;
-        k.s_count[i] = k.s_units[i] = 0;
+        z.slot[i] = slot;
+        z.count[i] = z.units[i] = 0;
         if (slot >= 0) rank = ceil16(v.slot[slot].rank);
     }
     __syncthreads();
     uint32_t same[2] = {0, 0};                           // the rows of the same slot
     int lead = 0;
-    if (i < kRows) {
+    if (i < 64) {
 #pragma unroll
-        for (int j = 0; j < kRows / 4; ++j) {
-            const int4 o = reinterpret_cast<const int4 *>(k.s_slot)[j];
+        for (int j = 0; j < 64 / 4; ++j) {
+            const int4 o = reinterpret_cast<const int4 *>(z.slot)[j];
             same[j / 8] |= (o.x == slot ? 1u : 0u) << (4 * j & 31) | (o.y == slot ? 2u : 0u) << (4 * j & 31) |
                            (o.z == slot ? 4u : 0u) << (4 * j & 31) | (o.w == slot ? 8u : 0u) << (4 * j & 31);
         }
         lead = same[0] ? __ffs(same[0]) - 1 : 31 + __ffs(same[1]);
         const unsigned leads = __ballot_sync(0xffffffffu, slot != -2 && lead == i);
-        if (lane == 0) k.s_lead[warp] = leads;
+        if (lane == 0) z.lead[warp] = leads;
     }
     __syncthreads();
     auto below = [](uint32_t m, int n) { return __popc(n >= 32 ? m : m & ((1u << n) - 1)); };
     auto earlier = [&](const auto *m, int n) { return below(m[0], n) + (n > 32 ? below(m[1], n - 32) : 0); };
     int id = 0;
-    if (i < kRows && slot != -2) {
-        id = earlier(k.s_lead, lead);
+    if (i < 64 && slot != -2) {
+        id = earlier(z.lead, lead);
         if (lead == i) {
             const int count = __popc(same[0]) + __popc(same[1]);
             k.slot[id] = slot;
             k.rank[id] = rank;
-            k.s_count[id] = count;
-            k.s_units[id] = work(count, rank);
+            z.count[id] = count;
+            z.units[id] = work(count, rank);
         }
     }
     __syncthreads();
-    if (i < kRows) {                                     // prefix sums, by either warp for itself
-        int rows[2] = {k.s_count[lane], k.s_count[lane + 32]}, units[2] = {k.s_units[lane], k.s_units[lane + 32]};
+    if (i < 64) {                                     // prefix sums, by either warp for itself
+        int rows[2] = {z.count[lane], z.count[lane + 32]}, units[2] = {z.units[lane], z.units[lane + 32]};
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
@@ -151,19 +168,108 @@ __device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &
             }
         if (i == 0) {
             k.first[0] = k.units[0] = 0;
-            k.n = __popc(k.s_lead[0]) + __popc(k.s_lead[1]);
+            k.n = __popc(z.lead[0]) + __popc(z.lead[1]);
         }
         // the row's place: the rows of the classes before its own, and its own class's before it
         const int upto[2] = {__shfl_sync(0xffffffffu, rows[0], id & 31), __shfl_sync(0xffffffffu, rows[1], id & 31)};
-        if (slot != -2) k.row[upto[id >> 5] - k.s_count[id] + earlier(same, i)] = i;
+        if (slot != -2) k.row[upto[id >> 5] - z.count[id] + earlier(same, i)] = i;
     }
     __syncthreads();
 }
+// The same for larger chunks, by way of a table of the slots.
+template <int R, class Work>
+__device__ __forceinline__ void find_classes(const LoraView &v, const LoraCall &c, int m0, Classes<R> &k,
+                                             Scratch<R> &z, Work work) {
+    constexpr int W = R / 32;
+    static_assert(R <= 32 * kWarps, "a thread for each row");
+    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+    int slot = -2, rank = 0;                             // -2: no row, -1: no adapter
+    if (i < c.chunk && m0 + i < c.M) {
+        slot = c.row_slot[m0 + i];
+        if (slot >= v.slots) {
+            atomicOr(v.status, kLoraBadSlot);
+            slot = -1;
+        }
+        slot = max(slot, -1);
+        if (slot >= 0) rank = ceil16(v.slot[slot].rank);
+    }
+    for (int j = i; j <= v.slots; j += blockDim.x) z.first[j] = R;
+    for (int j = i; j < W * R / 4; j += blockDim.x) reinterpret_cast<uint32_t *>(&z.in[0][0])[j] = 0;
+    __syncthreads();
+    uint32_t same = 0;                                   // the warp's rows of the same slot
+    bool head = false;
+    if (i < R) {
+        same = __match_any_sync(0xffffffffu, slot);
+        head = slot != -2 && lane == __ffs(same) - 1;
+        if (head) atomicMin(z.first + slot + 1, i);        // the first row of a slot: any order gives the same
+    }
+    __syncthreads();
+    const int lead = slot != -2 ? z.first[slot + 1] : -1;
+    if (i < R) {
+        const unsigned leads = __ballot_sync(0xffffffffu, lead == i);
+        if (lane == 0) z.lead[warp] = leads;
+    }
+    __syncthreads();
+    auto earlier = [](const uint32_t (&m)[W], int n) {   // bits below bit n
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            sum += __popc(n >= 32 * (w + 1) ? m[w] : n > 32 * w ? m[w] & ((1u << (n - 32 * w)) - 1) : 0);
+        return sum;
+    };
+    const int n = earlier(z.lead, R), id = slot != -2 ? earlier(z.lead, lead) : 0;
+    if (head) z.in[warp][id] = static_cast<uint8_t>(__popc(same));
+    if (lead == i) {
+        k.slot[id] = slot;
+        k.rank[id] = rank;
+    }
+    __syncthreads();
+    int rows = 0, units = 0;                             // prefix sums over the classes
+    if (i < R) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            z.before[w][i] = static_cast<uint16_t>(rows);
+            rows += z.in[w][i];
+        }
+        units = i < n ? work(rows, k.rank[i]) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, rows, o), y = __shfl_up_sync(0xffffffffu, units, o);
+            if (lane >= o) {
+                rows += x;
+                units += y;
+            }
+        }
+        if (lane == 31) z.sum[warp] = make_int2(rows, units);
+    }
+    __syncthreads();
+    if (i < R) {
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w) {
+            const int2 o = z.sum[w];
+            rows += w < warp ? o.x : 0;
+            units += w < warp ? o.y : 0;
+        }
+        k.first[i + 1] = rows;
+        k.units[i + 1] = units;
+        if (i == 0) {
+            k.first[0] = k.units[0] = 0;
+            k.n = n;
+        }
+    }
+    __syncthreads();
+    // the row's place: behind the rows of the classes before its own, and its own class's before it
+    if (i < R && slot != -2)
+        k.row[k.first[id] + z.before[warp][id] + __popc(same & ((1u << lane) - 1))] = i;
+    __syncthreads();
+}
 // The class of a unit, by a whole warp.
-__device__ __forceinline__ int class_of(const Classes &k, int unit) {
-    const int lane = threadIdx.x & 31;
-    return __popc(__ballot_sync(0xffffffffu, k.units[lane + 1] <= unit)) +
-           __popc(__ballot_sync(0xffffffffu, k.units[lane + 33] <= unit));
+template <int R>
+__device__ __forceinline__ int class_of(const Classes<R> &k, int unit) {
+    int id = 0;
+#pragma unroll
+    for (int w = 0; w < R / 32; ++w) id += __popc(__ballot_sync(0xffffffffu, k.units[32 * w + (threadIdx.x & 31) + 1] <= unit));
+    return id;
 }
 
 template <bool BF>
@@ -243,24 +349,27 @@ __device__ __forceinline__ float load_of(const float *p, int rank) {
     return x;
 }
 
-// Grid: (clusters over the chunk's (class, block of 16 ranks) units x CTAs of
-// a cluster along K, chunks of 64 rows).  Few: at most 16 rows in all, for
-// fewer registers.
-template <bool BF, bool Few>
+// Grid: (clusters over the chunk's (class, 64 of its rows, block of 16 ranks)
+// units x CTAs of a cluster along K, chunks of R rows).  Few: at most 16 rows
+// in all, for fewer registers.
+template <bool BF, bool Few, int R>
 __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v, LoraCall c, int ck) {
-    __shared__ Classes k;
+    __shared__ Classes<R> k;
     __shared__ __align__(16) float red[kRows / 8 * kWarps * 128];
     __shared__ __align__(16) float sum[kRows / 8 * 128];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int part = blockIdx.x % ck, warp = threadIdx.x >> 5, m0 = blockIdx.y * kRows;
-    find_classes(v, c, m0, k, [](int, int rank) { return rank / 16; });
+    const int part = blockIdx.x % ck, warp = threadIdx.x >> 5, m0 = blockIdx.y * c.chunk;
+    static_assert(sizeof(Scratch<R>) <= sizeof(red), "in the same place");
+    find_classes(v, c, m0, k, *reinterpret_cast<Scratch<R> *>(red),
+                 [](int rows, int rank) { return (rows + kRows - 1) / kRows * (rank / 16); });
     c.x += m0 * c.xs;
     v.t += static_cast<size_t>(m0) * v.rpad;
     // every CTA of a cluster takes the same way through this loop
     for (int unit = blockIdx.x / ck; unit < k.units[k.n]; unit += gridDim.x / ck) {
-        const int id = class_of(k, unit), slot = k.slot[id], rank = k.rank[id], n = k.first[id + 1] - k.first[id];
-        const int r0 = 16 * (unit - k.units[id]), nt = (n + 7) / 8;
-        const int *s_rows = k.row + k.first[id];
+        const int id = class_of(k, unit), slot = k.slot[id], rank = k.rank[id];
+        const int group = (unit - k.units[id]) / (rank / 16), r0 = 16 * (unit - k.units[id]) - group * rank;
+        const int n = min(k.first[id + 1] - k.first[id] - group * kRows, kRows), nt = (n + 7) / 8;
+        const int *s_rows = k.row + k.first[id] + group * kRows;
         const uint16_t *a = v.a + static_cast<size_t>(slot) * v.rpad * ceil64(v.K) + static_cast<size_t>(r0) * 64;
         const int first = part * kWarps + warp, step = ck * kWarps, rg = rank / 8;
         float4 *mine = reinterpret_cast<float4 *>(red) + 32 * warp;
@@ -304,7 +413,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v,
 struct Run {
     int nb;                  // column blocks of a group of 16 rows
     int64_t u, end;          // the warp's units
-    __device__ Run(const Classes &k, int N) : nb((N + 31) / 32) {
+    template <int R>
+    __device__ Run(const Classes<R> &k, int N) : nb((N + 31) / 32) {
         const int warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + (threadIdx.x >> 5);
         const int64_t units = static_cast<int64_t>(k.units[k.n]) * nb;
         u = units * me / warps;
@@ -312,7 +422,8 @@ struct Run {
     }
 };
 // B and y of the warp's units into L2.
-__device__ __forceinline__ void prefetch_units(const LoraView &v, const LoraCall &c, const Classes &k, const Run &run) {
+template <int R>
+__device__ __forceinline__ void prefetch_units(const LoraView &v, const LoraCall &c, const Classes<R> &k, const Run &run) {
     const int lane = threadIdx.x & 31, nb = run.nb;
     auto prefetch = [](const uint16_t *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); };
     for (int64_t w = run.u; w < run.end;) {
@@ -331,8 +442,8 @@ __device__ __forceinline__ void prefetch_units(const LoraView &v, const LoraCall
     }
 }
 // t: [row][pitch] in global memory, written by another launch, or in shared memory.
-template <bool BF, bool Shared>
-__device__ __forceinline__ void expand_units(const LoraView &v, const LoraCall &c, const Classes &k, const Run &run,
+template <bool BF, bool Shared, int R>
+__device__ __forceinline__ void expand_units(const LoraView &v, const LoraCall &c, const Classes<R> &k, const Run &run,
                                              const float *t, int pitch) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, nb = run.nb;
     auto load4 = [](const float4 *p) {
@@ -449,11 +560,12 @@ __device__ __forceinline__ void expand_units(const LoraView &v, const LoraCall &
     }
 }
 
-template <bool BF>
+template <bool BF, int R>
 __global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v, LoraCall c) {
-    __shared__ Classes k;
-    const int m0 = blockIdx.y * kRows;
-    find_classes(v, c, m0, k, [](int rows, int) { return (rows + 15) / 16; });
+    __shared__ Classes<R> k;
+    const int m0 = blockIdx.y * c.chunk;
+    __shared__ Scratch<R> scratch;
+    find_classes(v, c, m0, k, scratch, [](int rows, int) { return (rows + 15) / 16; });
     c.y += m0 * c.ys;
     c.out += m0 * c.os;
     const Run run(k, v.N);
@@ -475,7 +587,7 @@ constexpr int kOneRank = 256;
 constexpr int64_t kOneValues = 1 << 19;      // of A
 template <bool BF>
 __global__ void __launch_bounds__(32 * kWarps, 2) lora_one_kernel(LoraView v, LoraCall c) {
-    __shared__ Classes k;
+    __shared__ Classes<32> k;
     __shared__ __align__(16) float part[kOneRank / 16 * 128];                // [16 ranks, part of K][128]
     __shared__ __align__(16) float t[kOneRank];
     const int warp = threadIdx.x >> 5, cta = blockIdx.x % kOneCtas;
@@ -488,7 +600,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_one_kernel(LoraView v, Lo
     LoraSlot info{0, 0.f, 1};
     if (slot >= 0) info = v.slot[slot];
     const int rank = ceil16(info.rank);
-    if (threadIdx.x <= kRows) k.units[threadIdx.x] = threadIdx.x > 0;        // one class, of one row
+    if (threadIdx.x <= 32) k.units[threadIdx.x] = threadIdx.x > 0;           // one class, of one row
     if (threadIdx.x == 0) {
         k.n = 1;
         k.slot[0] = slot;
@@ -567,29 +679,28 @@ cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlo
     return cudaGetLastError();
 }
 
-cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
-    if (c.M == 1 && v.rpad <= kOneRank && static_cast<int64_t>(v.rpad) * v.K <= kOneValues) {
-        const int clusters = std::min((v.N + 32 * kWarps * kOneCtas - 1) / (32 * kWarps * kOneCtas), kOneClusters);
-        *launches += 1;
-        return start(bf16 ? lora_one_kernel<true> : lora_one_kernel<false>, dim3(clusters * kOneCtas), 32 * kWarps, 0,
-                     kOneCtas, false, st, v, c);
-    }
-    const int chunks_all = (c.M + kRows - 1) / kRows;
-    for (int c0 = 0; c0 < chunks_all; c0 += 65535) {     // chunks are the grid's y dimension
+// The two launches for chunks of R rows (the grid's y dimension); the chunks of
+// 256 share the rows equally, as one is most of a call.
+template <int R>
+cudaError_t launch_chunks(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
+    const int chunks_all = (c.M + R - 1) / R;
+    const int each = R == 64 ? R : (c.M + chunks_all - 1) / chunks_all;
+    for (int c0 = 0; c0 < chunks_all; c0 += 65535) {
         LoraCall d = c;
         LoraView w = v;
-        const int64_t m0 = static_cast<int64_t>(c0) * kRows;
+        const int64_t m0 = static_cast<int64_t>(c0) * each;
         const int chunks = std::min(chunks_all - c0, 65535);
-        d.M = static_cast<int>(std::min<int64_t>(c.M - m0, static_cast<int64_t>(chunks) * kRows));
+        d.M = static_cast<int>(std::min<int64_t>(c.M - m0, static_cast<int64_t>(chunks) * each));
+        d.chunk = each;
         d.x += m0 * c.xs;
         d.y += m0 * c.ys;
         d.out += m0 * c.os;
         d.row_slot += m0;
         w.t += m0 * v.rpad;
-        const int rows = std::min(d.M, kRows);
-        // (class, 16 ranks) units that one chunk can hold, and two CTAs for each SM over them; K is split over a
-        // cluster where the units alone are fewer
-        const int units = std::min(rows, v.slots) * (v.rpad / 16);
+        const int rows = std::min(d.M, each);
+        // units that one chunk can hold, and two CTAs for each SM over them; K is split over a cluster where the units
+        // alone are fewer
+        const int units = (std::min(rows, v.slots) + (rows - 1) / kRows) * (v.rpad / 16);
         int ck = kCluster;
         while (ck > 1 && (static_cast<int64_t>(units) * chunks * ck > 2 * 304 || v.K / ck < 512)) ck /= 2;
         const int gx = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, 304 / (static_cast<int64_t>(ck) * chunks))));
@@ -598,15 +709,30 @@ cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cud
         const int64_t most = static_cast<int64_t>(groups) * ((v.N + 31) / 32);
         const int ex = static_cast<int>(std::min<int64_t>((most + kWarps - 1) / kWarps, std::max(1, 304 / chunks)));
         const dim3 gs(gx * ck, chunks), ge(ex, chunks);
-        const bool few = rows <= 16;
-        auto shrink = bf16 ? (few ? lora_shrink_kernel<true, true> : lora_shrink_kernel<true, false>)
-                           : (few ? lora_shrink_kernel<false, true> : lora_shrink_kernel<false, false>);
+        auto shrink = bf16 ? lora_shrink_kernel<true, false, R> : lora_shrink_kernel<false, false, R>;
+        if constexpr (R == 64)
+            if (rows <= 16) shrink = bf16 ? lora_shrink_kernel<true, true, R> : lora_shrink_kernel<false, true, R>;
         cudaError_t e = start(shrink, gs, 32 * kWarps, 0, ck, false, st, w, d, ck);
-        if (!e) e = start(bf16 ? lora_expand_kernel<true> : lora_expand_kernel<false>, ge, 32 * kWarps, 0, 1, true, st, w, d);
+        if (!e) e = start(bf16 ? lora_expand_kernel<true, R> : lora_expand_kernel<false, R>, ge, 32 * kWarps, 0, 1, true, st, w, d);
         if (e) return e;
         *launches += 2;
     }
     return cudaSuccess;
+}
+
+cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
+    if (c.M == 1 && v.rpad <= kOneRank && static_cast<int64_t>(v.rpad) * v.K <= kOneValues) {
+        const int clusters = std::min((v.N + 32 * kWarps * kOneCtas - 1) / (32 * kWarps * kOneCtas), kOneClusters);
+        *launches += 1;
+        return start(bf16 ? lora_one_kernel<true> : lora_one_kernel<false>, dim3(clusters * kOneCtas), 32 * kWarps, 0,
+                     kOneCtas, false, st, v, c);
+    }
+    // Chunks of 256 read an adapter that their rows share once, but sort and sum them more slowly than chunks of 64.
+    // Where those could read more than 96 MB again: 256 rows over 32 adapters of up to 64 ranks, 8192 x 28672, 44 us
+    // instead of 101; 256 rows in 4 runs 32 instead of 37.  Where not: 100 rows over 32 adapters of up to 32
+    // ranks, 8192 x 10240, 20 us by 256, 17 by 64; 200 rows over 8 of 16, 4096 x 4096, 13.4 and 11.8.
+    const int64_t again = static_cast<int64_t>((c.M - 1) / 64) * std::min(64, v.slots) * v.rpad * (v.K + v.N) * 2;
+    return again > 96 << 20 ? launch_chunks<256>(v, c, bf16, st, launches) : launch_chunks<64>(v, c, bf16, st, launches);
 }
 
 }  // namespace q4

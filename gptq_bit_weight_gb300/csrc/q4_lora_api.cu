@@ -178,7 +178,7 @@ int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int3
                          static_cast<long long>(out_stride), static_cast<long long>(y_stride));
     if (int r = ensure_rows(h, static_cast<size_t>(M), stream, false)) return r;
     const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
-                         static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M};
+                         static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M, M};
     // Tiles of 128 rows from 321 rows on, except for the highest ranks, which do not fit them.  Measured at 8192 x
     // 28672, rank 64: 128 rows of one adapter 19 us by chunks of 64 rows, 20 by tiles; 256 rows of 4 runs 36 and 27, but
     // 256 rows that mix 32 adapters 102 and 214 (a tile holds 176 ranks at a time); 320 rows of 20 runs at 8192 x 10240

@@ -48,6 +48,7 @@ struct LoraCall {
     const int32_t *row_slot;
     int64_t xs, ys, os;
     int M;
+    int chunk;                   // rows that a CTA of the few-row kernels looks over
 };
 
 cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,

@@ -90,6 +90,14 @@ CASES = [  # (M, K, N, ranks, rows: "one", "mixed", "runs")
     (1, 4096, 512, [256], "one"),            # and of a larger one: two
     (4, 1000, 1288, [16] * 10, "mixed"),
     (16, 4096, 512, [33, 16, 64], "mixed"),
+    (256, 512, 392, [16, 5, 64, 33] * 8, "mixed"),
+    (255, 1024, 264, [48], "one"),
+    (256, 1024, 8200, [16, 5, 64, 33] * 6, "mixed"),   # one chunk of many adapters
+    (290, 8192, 2056, [64, 8, 33, 16] * 5, "runs"),    # two; more rows of an adapter than a unit takes
+    (133, 2048, 14344, [64] * 64, "mixed"),
+    (320, 328, 520, [16, 40, 64], "runs"),
+    (70, 64, 64, [8] * 70, "mixed"),
+    (700, 256, 264, [200, 16, 256], "mixed"),          # ranks too high for the tiles
 ]
 
 
