@@ -5,14 +5,15 @@
 // the first runs (programmatic dependent launch) and waits for t only.
 //
 // Here: the adapters' private layout, and the kernels for few rows (single
-// tokens, decode steps).  A call looks at chunks of 64 rows and sorts them by
-// adapter.  First launch: a unit is 16 ranks of an adapter for all its rows in
-// the chunk, K split over a CTA's warps and, where units are few, a cluster;
-// second: 32 columns for 16 rows.  Weights go straight into mma.sync fragments
+// tokens, decode steps; and the tiles of a larger call that mix too many
+// adapters).  A call looks at chunks of 64 to 256 rows and sorts them by
+// adapter.  First launch: a unit is 16 ranks of an adapter for up to 64 of its
+// rows in the chunk, K split over a CTA's warps and, where units are few, a
+// cluster; second: 32 columns for 16 rows.  Weights go straight into mma.sync fragments
 // with 16-byte loads, A once, B once for every 16 rows.
 //
 // Bound by latency: 64 rows over 32 adapters of up to 64 ranks, 8192 x 10240,
-// take 18.5 us where the bytes would take 6.2.  The first launch is done after
+// take 19.4 us where the bytes would take 6.2.  The first launch is done after
 // 7.4 (2 to find the rows' adapters, 3 for its loads, 2 to join its sums); the
 // second's CTAs find registers as the first's end, and have 4 to 5 units a
 // warp at about 1 us, a load from L2 and its products.  Tried and slower: B
@@ -349,60 +350,101 @@ __device__ __forceinline__ float load_of(const float *p, int rank) {
     return x;
 }
 
+// The chunks that a CTA (or a cluster, `me` of `all`) looks at, and its place
+// among those that share one: the chunk of its blockIdx.y, or every so many of
+// the marked ones.
+template <int R>
+struct Chunks {
+    int step, at, marked;    // in the order of the marked ones; of them all
+    int me, all;             // of those that share a chunk
+    __device__ __forceinline__ Chunks(const LoraCall &c, int me_, int all_) : step(1), at(0), marked(1), me(me_), all(all_) {
+        if constexpr (R > 64)
+            if (c.marks) {
+                marked = 0;
+                for (int base = 0; base < count(c); base += 32) marked += __popc(marks(c, base));
+                step = max(min(marked, all_), 1);
+                at = me_ % step;
+                me = me_ / step;
+                all = (all_ - at + step - 1) / step;
+            }
+    }
+    __device__ __forceinline__ bool more() const { return at < marked; }
+    __device__ __forceinline__ void next() { at += step; }
+    __device__ __forceinline__ int chunk(const LoraCall &c) const {
+        if constexpr (R > 64)
+            if (c.marks) {
+                int left = at, base = 0;
+                unsigned b = marks(c, 0);
+                for (int n; (n = __popc(b)) <= left; left -= n) b = marks(c, base += 32);
+                return base + static_cast<int>(__fns(b, 0, left + 1));
+            }
+        return blockIdx.y;
+    }
+    static __device__ __forceinline__ int count(const LoraCall &c) { return (c.M - 1) / c.chunk + 1; }
+    static __device__ __forceinline__ unsigned marks(const LoraCall &c, int base) {
+        const int i = base + (threadIdx.x & 31);
+        return __ballot_sync(0xffffffffu, i < count(c) && c.marks[i]);
+    }
+};
+
 // Grid: (clusters over the chunk's (class, 64 of its rows, block of 16 ranks)
 // units x CTAs of a cluster along K, chunks of R rows).  Few: at most 16 rows
 // in all, for fewer registers.
 template <bool BF, bool Few, int R>
-__global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v, LoraCall c, int ck) {
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_shrink_kernel(LoraView v, LoraCall call, int ck) {
     __shared__ Classes<R> k;
     __shared__ __align__(16) float red[kRows / 8 * kWarps * 128];
     __shared__ __align__(16) float sum[kRows / 8 * 128];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int part = blockIdx.x % ck, warp = threadIdx.x >> 5, m0 = blockIdx.y * c.chunk;
-    static_assert(sizeof(Scratch<R>) <= sizeof(red), "in the same place");
-    find_classes(v, c, m0, k, *reinterpret_cast<Scratch<R> *>(red),
-                 [](int rows, int rank) { return (rows + kRows - 1) / kRows * (rank / 16); });
-    c.x += m0 * c.xs;
-    v.t += static_cast<size_t>(m0) * v.rpad;
-    // every CTA of a cluster takes the same way through this loop
-    for (int unit = blockIdx.x / ck; unit < k.units[k.n]; unit += gridDim.x / ck) {
-        const int id = class_of(k, unit), slot = k.slot[id], rank = k.rank[id];
-        const int group = (unit - k.units[id]) / (rank / 16), r0 = 16 * (unit - k.units[id]) - group * rank;
-        const int n = min(k.first[id + 1] - k.first[id] - group * kRows, kRows), nt = (n + 7) / 8;
-        const int *s_rows = k.row + k.first[id] + group * kRows;
-        const uint16_t *a = v.a + static_cast<size_t>(slot) * v.rpad * ceil64(v.K) + static_cast<size_t>(r0) * 64;
-        const int first = part * kWarps + warp, step = ck * kWarps, rg = rank / 8;
-        float4 *mine = reinterpret_cast<float4 *>(red) + 32 * warp;
-        if (nt == 1) shrink_rows<BF, 1>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
-        else if (Few || nt == 2) shrink_rows<BF, 2>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
-        else if (nt <= 4) shrink_rows<BF, 4>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
-        else shrink_rows<BF, 8>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
-        __syncthreads();
-        // the warps' parts of K in order, then the cluster's
-        for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[(e >> 7) * kWarps * 128 + w * 128 + (e & 127)];
-            sum[e] = s;
-        }
-        if (ck > 1) cluster_sync();
-        else __syncthreads();
-        if (part == 0) {
-            const LoraSlot info = v.slot[slot];
+    const int part = blockIdx.x % ck, warp = threadIdx.x >> 5;
+    for (Chunks<R> chunks(call, blockIdx.x / ck, gridDim.x / ck); chunks.more(); chunks.next()) {
+        LoraCall c = call;
+        const int m0 = chunks.chunk(c) * c.chunk;
+        static_assert(sizeof(Scratch<R>) <= sizeof(red), "in the same place");
+        find_classes(v, c, m0, k, *reinterpret_cast<Scratch<R> *>(red),
+                     [](int rows, int rank) { return (rows + kRows - 1) / kRows * (rank / 16); });
+        c.x += m0 * c.xs;
+        float *t = v.t + static_cast<size_t>(m0) * v.rpad;
+        // every CTA of a cluster takes the same way through this loop
+        for (int unit = chunks.me; unit < k.units[k.n]; unit += chunks.all) {
+            const int id = class_of(k, unit), slot = k.slot[id], rank = k.rank[id];
+            const int group = (unit - k.units[id]) / (rank / 16), r0 = 16 * (unit - k.units[id]) - group * rank;
+            const int n = min(k.first[id + 1] - k.first[id] - group * kRows, kRows), nt = (n + 7) / 8;
+            const int *s_rows = k.row + k.first[id] + group * kRows;
+            const uint16_t *a = v.a + static_cast<size_t>(slot) * v.rpad * ceil64(v.K) + static_cast<size_t>(r0) * 64;
+            const int first = part * kWarps + warp, step = ck * kWarps, rg = rank / 8;
+            float4 *mine = reinterpret_cast<float4 *>(red) + 32 * warp;
+            if (nt == 1) shrink_rows<BF, 1>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+            else if (Few || nt == 2) shrink_rows<BF, 2>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+            else if (nt <= 4) shrink_rows<BF, 4>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+            else shrink_rows<BF, 8>(v, c, a, rg, s_rows, n, first, step, mine, 32 * kWarps);
+            __syncthreads();
+            // the warps' parts of K in order, then the cluster's
             for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
-                float x[kCluster], s = 0.f;              // on their way together, added in order
+                float s = 0.f;
 #pragma unroll
-                for (int p = 0; p < kCluster; ++p) x[p] = p < ck ? load_of(sum + e, p) : 0.f;
-#pragma unroll
-                for (int p = 0; p < kCluster; ++p) s += x[p];
-                const int lane = e >> 2 & 31, row = (e >> 7) * 8 + 2 * (lane & 3) + (e & 1);
-                const int r = r0 + (lane >> 2) + 8 * (e >> 1 & 1);
-                // a rank of the padding would be NaN in a row of x with an infinity
-                if (row < n) v.t[static_cast<size_t>(s_rows[row]) * v.rpad + r] = r < info.rank ? s * info.scale : 0.f;
+                for (int w = 0; w < kWarps; ++w) s += red[(e >> 7) * kWarps * 128 + w * 128 + (e & 127)];
+                sum[e] = s;
             }
+            if (ck > 1) cluster_sync();
+            else __syncthreads();
+            if (part == 0) {
+                const LoraSlot info = v.slot[slot];
+                for (int e = threadIdx.x; e < nt * 128; e += blockDim.x) {
+                    float x[kCluster], s = 0.f;              // on their way together, added in order
+#pragma unroll
+                    for (int p = 0; p < kCluster; ++p) x[p] = p < ck ? load_of(sum + e, p) : 0.f;
+#pragma unroll
+                    for (int p = 0; p < kCluster; ++p) s += x[p];
+                    const int lane = e >> 2 & 31, row = (e >> 7) * 8 + 2 * (lane & 3) + (e & 1);
+                    const int r = r0 + (lane >> 2) + 8 * (e >> 1 & 1);
+                    // a rank of the padding would be NaN in a row of x with an infinity
+                    if (row < n) t[static_cast<size_t>(s_rows[row]) * v.rpad + r] = r < info.rank ? s * info.scale : 0.f;
+                }
+            }
+            if (ck > 1) cluster_sync();                      // nobody goes on while its sums are read
+            else __syncthreads();
         }
-        if (ck > 1) cluster_sync();                      // nobody goes on while its sums are read
-        else __syncthreads();
     }
 }
 
@@ -414,8 +456,8 @@ struct Run {
     int nb;                  // column blocks of a group of 16 rows
     int64_t u, end;          // the warp's units
     template <int R>
-    __device__ Run(const Classes<R> &k, int N) : nb((N + 31) / 32) {
-        const int warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    __device__ Run(const Classes<R> &k, int N, int cta, int ctas) : nb((N + 31) / 32) {
+        const int warps = ctas * kWarps, me = cta * kWarps + (threadIdx.x >> 5);
         const int64_t units = static_cast<int64_t>(k.units[k.n]) * nb;
         u = units * me / warps;
         end = units * (me + 1) / warps;
@@ -561,17 +603,22 @@ __device__ __forceinline__ void expand_units(const LoraView &v, const LoraCall &
 }
 
 template <bool BF, int R>
-__global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v, LoraCall c) {
+__global__ void __launch_bounds__(32 * kWarps, 2) lora_expand_kernel(LoraView v, LoraCall call) {
     __shared__ Classes<R> k;
-    const int m0 = blockIdx.y * c.chunk;
     __shared__ Scratch<R> scratch;
-    find_classes(v, c, m0, k, scratch, [](int rows, int) { return (rows + 15) / 16; });
-    c.y += m0 * c.ys;
-    c.out += m0 * c.os;
-    const Run run(k, v.N);
-    prefetch_units(v, c, k, run);                        // while the first launch runs
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    expand_units<BF, false>(v, c, k, run, v.t + static_cast<size_t>(m0) * v.rpad, v.rpad);
+    for (Chunks<R> chunks(call, blockIdx.x, gridDim.x); chunks.more(); chunks.next()) {
+        LoraCall c = call;
+        const int m0 = chunks.chunk(c) * c.chunk;
+        find_classes(v, c, m0, k, scratch, [](int rows, int) { return (rows + 15) / 16; });
+        c.y += m0 * c.ys;
+        c.out += m0 * c.os;
+        const Run run(k, v.N, chunks.me, chunks.all);
+        prefetch_units(v, c, k, run);                    // while the first launch runs
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        expand_units<BF, false>(v, c, k, run, v.t + static_cast<size_t>(m0) * v.rpad, v.rpad);
+        __syncthreads();                                 // the classes have been read
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // without a chunk, too
 }
 
 // Both products in one launch, for a single row whose adapter has few values:
@@ -609,7 +656,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) lora_one_kernel(LoraView v, Lo
         k.first[1] = 1;
     }
     __syncthreads();
-    const Run run(k, v.N);
+    const Run run(k, v.N, blockIdx.x, gridDim.x);
     prefetch_units(v, c, k, run);
     const int units = rank / 16, split = max(1, kWarps / max(units, 1));     // warps of 16 ranks along K
     for (int job = warp; job < units * split; job += kWarps)
@@ -679,8 +726,32 @@ cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlo
     return cudaGetLastError();
 }
 
-// The two launches for chunks of R rows (the grid's y dimension); the chunks of
-// 256 share the rows equally, as one is most of a call.
+// The two launches.
+template <int R>
+cudaError_t launch_pair(const LoraView &v, const LoraCall &c, int chunks, bool bf16, cudaStream_t st, int *launches) {
+    const int rows = std::min(c.M, c.chunk);
+    // units that one chunk can hold, and two CTAs for each SM over them; K is split over a cluster where the units
+    // alone are fewer
+    const int units = (std::min(rows, v.slots) + (rows - 1) / kRows) * (v.rpad / 16);
+    int ck = kCluster;
+    while (ck > 1 && (static_cast<int64_t>(units) * chunks * ck > 2 * 304 || v.K / ck < 512)) ck /= 2;
+    if (c.marks) ck = 2;                                 // how many chunks are marked is not known here
+    const int gx = static_cast<int>(std::min<int64_t>(c.marks ? 304 : units, std::max<int64_t>(1, 304 / (static_cast<int64_t>(ck) * chunks))));
+    // two CTAs for each SM, as long as every warp has a unit
+    const int groups = (rows + 15) / 16 + std::min(rows, v.slots + 1);
+    const int64_t most = static_cast<int64_t>(groups) * ((v.N + 31) / 32);
+    const int ex = static_cast<int>(std::min<int64_t>((most + kWarps - 1) / kWarps, std::max(1, 304 / chunks)));
+    const dim3 gs(gx * ck, chunks), ge(ex, chunks);
+    auto shrink = bf16 ? lora_shrink_kernel<true, false, R> : lora_shrink_kernel<false, false, R>;
+    if constexpr (R == 64)
+        if (rows <= 16) shrink = bf16 ? lora_shrink_kernel<true, true, R> : lora_shrink_kernel<false, true, R>;
+    cudaError_t e = start(shrink, gs, 32 * kWarps, 0, ck, false, st, v, c, ck);
+    if (!e) e = start(bf16 ? lora_expand_kernel<true, R> : lora_expand_kernel<false, R>, ge, 32 * kWarps, 0, 1, true, st, v, c);
+    if (!e) *launches += 2;
+    return e;
+}
+// For chunks of R rows (the grid's y dimension); the chunks of 256 share the
+// rows equally, as one is most of a call.
 template <int R>
 cudaError_t launch_chunks(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
     const int chunks_all = (c.M + R - 1) / R;
@@ -697,25 +768,7 @@ cudaError_t launch_chunks(const LoraView &v, const LoraCall &c, bool bf16, cudaS
         d.out += m0 * c.os;
         d.row_slot += m0;
         w.t += m0 * v.rpad;
-        const int rows = std::min(d.M, each);
-        // units that one chunk can hold, and two CTAs for each SM over them; K is split over a cluster where the units
-        // alone are fewer
-        const int units = (std::min(rows, v.slots) + (rows - 1) / kRows) * (v.rpad / 16);
-        int ck = kCluster;
-        while (ck > 1 && (static_cast<int64_t>(units) * chunks * ck > 2 * 304 || v.K / ck < 512)) ck /= 2;
-        const int gx = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, 304 / (static_cast<int64_t>(ck) * chunks))));
-        // two CTAs for each SM, as long as every warp has a unit
-        const int groups = (rows + 15) / 16 + std::min(rows, v.slots + 1);
-        const int64_t most = static_cast<int64_t>(groups) * ((v.N + 31) / 32);
-        const int ex = static_cast<int>(std::min<int64_t>((most + kWarps - 1) / kWarps, std::max(1, 304 / chunks)));
-        const dim3 gs(gx * ck, chunks), ge(ex, chunks);
-        auto shrink = bf16 ? lora_shrink_kernel<true, false, R> : lora_shrink_kernel<false, false, R>;
-        if constexpr (R == 64)
-            if (rows <= 16) shrink = bf16 ? lora_shrink_kernel<true, true, R> : lora_shrink_kernel<false, true, R>;
-        cudaError_t e = start(shrink, gs, 32 * kWarps, 0, ck, false, st, w, d, ck);
-        if (!e) e = start(bf16 ? lora_expand_kernel<true, R> : lora_expand_kernel<false, R>, ge, 32 * kWarps, 0, 1, true, st, w, d);
-        if (e) return e;
-        *launches += 2;
+        if (cudaError_t e = launch_pair<R>(w, d, chunks, bf16, st, launches)) return e;
     }
     return cudaSuccess;
 }
@@ -733,6 +786,10 @@ cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cud
     // ranks, 8192 x 10240, 20 us by 256, 17 by 64; 200 rows over 8 of 16, 4096 x 4096, 13.4 and 11.8.
     const int64_t again = static_cast<int64_t>((c.M - 1) / 64) * std::min(64, v.slots) * v.rpad * (v.K + v.N) * 2;
     return again > 96 << 20 ? launch_chunks<256>(v, c, bf16, st, launches) : launch_chunks<64>(v, c, bf16, st, launches);
+}
+
+cudaError_t launch_lora_marked(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches) {
+    return launch_pair<256>(v, c, 1, bf16, st, launches);
 }
 
 }  // namespace q4

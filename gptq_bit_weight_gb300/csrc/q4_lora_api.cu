@@ -64,7 +64,7 @@ int ensure_rows(gptq_q4_lora_s *h, size_t rows, cudaStream_t s, bool sync_alloc)
         h->t_rows = 0;
     }
     void *p = nullptr;
-    const size_t bytes = rows * (q4::ceil16(h->max_rank) + 1) * sizeof(float);
+    const size_t bytes = rows * (q4::ceil16(h->max_rank) + 2) * sizeof(float);
     if (cudaError_t e = sync_alloc ? cudaMalloc(&p, bytes) : cudaMallocAsync(&p, bytes, s))
         return api_cuda_fail(e, "allocating the adapter workspace");
     h->t = static_cast<float *>(p);
@@ -178,17 +178,17 @@ int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int3
                          static_cast<long long>(out_stride), static_cast<long long>(y_stride));
     if (int r = ensure_rows(h, static_cast<size_t>(M), stream, false)) return r;
     const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
-                         static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M, M};
-    // Tiles of 128 rows from 321 rows on, except for the highest ranks, which do not fit them.  Measured at 8192 x
-    // 28672, rank 64: 128 rows of one adapter 19 us by chunks of 64 rows, 20 by tiles; 256 rows of 4 runs 36 and 27, but
-    // 256 rows that mix 32 adapters 102 and 214 (a tile holds 176 ranks at a time); 320 rows of 20 runs at 8192 x 10240
-    // 18 and 24; 643 rows of 6 runs at 28672 x 8192 166 and 42; 1024 rows 96 and 37.
+                         static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M, M, nullptr};
+    // Tiles of 128 rows from 321 rows on, except for the highest ranks, which do not fit them.  Measured at rank 64:
+    // 8192 x 28672, 128 rows of one adapter 19 us by chunks, 20 by tiles; 256 rows of 4 runs 32 and 27; 1024 rows 96
+    // and 37; 643 rows of 6 runs at 28672 x 8192 166 and 42.  8192 x 10240, rows that mix 32 adapters: 400 rows 36 and
+    // 66, 800 rows 59 and 100; in 6 runs 31 and 25, 65 and 31.
     const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
     const q4::LoraTcPlan plan = q4::plan_lora_tc(view(h), M, h->sms);
-    int launches = 2;
+    int launches = 0;
     cudaError_t e;
-    if (M > 320 && plan.ok) e = q4::launch_lora_tc(view(h), c, plan, h->sms, bf16, stream);
-    else launches = 0, e = q4::launch_lora_add(view(h), c, bf16, stream, &launches);
+    if (M > 320 && plan.ok) e = q4::launch_lora_tc(view(h), c, plan, h->sms, bf16, stream, &launches);
+    else e = q4::launch_lora_add(view(h), c, bf16, stream, &launches);
     if (e) return api_cuda_fail(e, "adapter launch");
     q4::api_count_launches(launches);
     return api_set_status(GPTQ_Q4_OK, nullptr);

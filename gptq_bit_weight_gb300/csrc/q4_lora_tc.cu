@@ -18,12 +18,14 @@
 //           buffers; y tiles are loaded, added to, rounded in place and
 //           stored by TMA
 //
-// Adapters that a tile cannot hold at once (over kCap ranks in the second
-// launch), and adapters with an infinity or NaN, which must not meet another
-// row's zero, get passes of their own over the tile's output, each of which
-// changes only the rows that use them.
+// A tile whose adapters have more than kCap ranks in all (single tokens of many
+// requests) is left to the kernels of few rows, which run behind over the tiles
+// that the first launch marks (2.5 us where none is; 800 rows that mix 32
+// adapters, 8192 x 10240: 100 us instead of 260 by passes).  Adapters with an infinity or NaN, which must
+// not meet another row's zero, get passes of their own over the tile's output,
+// each of which changes only the rows that use them.
 //
-// 4099 rows of 6 runs, 8192 x 28672, rank 64, fp16: 112 us, 4.5 TB/s of the
+// 4099 rows of 6 runs, 8192 x 28672, rank 64, fp16: 115 us, 4.4 TB/s of the
 // bytes that the call cannot do without (74 us at the copy rate): the first
 // launch 15 of them (x is 67 MB), the second 1.43 us for a job of 128 x 128
 // outputs on each SM, at which y, out and B (512 B a column) move at 6.9 TB/s
@@ -57,7 +59,7 @@ constexpr int kShrinkCap = 176;      // of the first
 
 // The adapters of a tile's rows.
 struct TileInfo {
-    int n, passes;
+    int n, passes, marked;
     int slot[kTile], rank[kTile];    // of each class; rank padded to 16
     int pass[kTile], off[kTile];     // its pass, and its first rank there
     int cls[kTile];                  // of each row; -1: none
@@ -107,7 +109,7 @@ __device__ void build_info(const LoraView &v, const LoraCall &c, int m0, int cap
     __syncthreads();
     if (i == 0) {
         const int n = __popc(k.leads[0]) + __popc(k.leads[1]) + __popc(k.leads[2]) + __popc(k.leads[3]);
-        int pass = 0, off = 0;
+        int pass = 0, off = 0, ranks = 0;
         bool alone = false;
         for (int j = 0; j < n; ++j) {
             const bool own = solo && !k.s_id[j];
@@ -119,9 +121,12 @@ __device__ void build_info(const LoraView &v, const LoraCall &c, int m0, int cap
             k.pass[j] = pass;
             k.off[j] = off;
             off += k.rank[j];
+            ranks += k.rank[j];
         }
-        k.n = n;
-        k.passes = n ? pass + 1 : 0;
+        // a tile whose adapters have too many ranks is left to the kernels of few rows
+        k.marked = ranks > kCap;
+        k.n = k.marked ? 0 : n;
+        k.passes = k.n ? pass + 1 : 0;
     }
     __syncthreads();
 }
@@ -165,14 +170,14 @@ __host__ __device__ constexpr int shrink_stages(int rpad) {
     return n < kShrinkMaxStages ? n : kShrinkMaxStages;
 }
 
-// Grid: (parts of K, row tiles), the parts of a tile in one cluster: each sums
+// Grid: parts of K x row tiles, the parts of a tile in one cluster: each sums
 // its share of the tile's rows over the parts, in their order, and splits
 // scale times the sum into its two 16-bit parts.
 // t16 [rows][2][rpad]: high and low parts; up [rows]: what they have been divided by.
 template <bool BF>
 __global__ void __launch_bounds__(kShrinkThreads, 1)
     shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, LoraView v, LoraCall c, uint16_t *t16, float *up,
-                     int blocks_each, int S) {
+                     int blocks_each, int parts, int S) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sb = smem_raw + (base - raw);
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 16 * kShrinkMaxStages + 16);
     TileInfo &k = *reinterpret_cast<TileInfo *>(misc + 256);
     const int warp = threadIdx.x >> 5;
-    const int m0 = blockIdx.y * kTile;
+    const int part = blockIdx.x % parts, tile = blockIdx.x / parts, m0 = tile * kTile;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmX) : "memory");
@@ -202,8 +207,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     tc_fence_before();
     build_info(v, c, m0, kShrinkCap, false, k);                      // synchronizes
     tc_fence_after();
+    if (part == 0 && threadIdx.x == 0) c.marks[tile] = k.marked;
     const uint32_t tmem = *tmem_slot;
-    const int kb0 = blockIdx.x * blocks_each, kb1 = min(kb0 + blocks_each, (v.K + 63) / 64);
+    const int kb0 = part * blocks_each, kb1 = min(kb0 + blocks_each, (v.K + 63) / 64);
     bool alive = true;
     if (warp == 4) {
         int seq = 0;
@@ -291,10 +297,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     };
     cluster_sync();
     // rows part, part + parts, ..: a warp holds a row, a lane two of each 64 ranks
-    const int parts = gridDim.x, lane = threadIdx.x & 31;
-    for (int row = blockIdx.x + parts * warp; row < kTile; row += parts * (kShrinkThreads / 32)) {
+    const int lane = threadIdx.x & 31;
+    for (int row = part + parts * warp; row < kTile; row += parts * (kShrinkThreads / 32)) {
         const int mine = k.cls[row];
-        if (mine < 0) continue;
+        if (mine < 0 || k.marked) continue;
         const int rank = k.rank[mine];
         const LoraSlot info = v.slot[k.slot[mine]];
         float2 x[3];                                     // kShrinkCap ranks
@@ -586,6 +592,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms) {
     LoraTcPlan p;
     p.ok = v.rpad <= kCap && v.rpad <= kShrinkCap;
+    p.marks = std::min(std::min(M, kTile), v.slots) * v.rpad > kCap;
     p.tiles = (M + kTile - 1) / kTile;
     const int blocks = (v.K + 63) / 64;
     // parts of K: as many CTAs as fill the GPU once, at least four blocks of 64 each
@@ -596,7 +603,7 @@ LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms) {
 }
 
 cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, int sms, bool bf16,
-                           cudaStream_t st) {
+                           cudaStream_t st, int *launches) {
     CUtensorMap tx, ty, to;
     const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;        // 16-bit values either way
     cudaError_t e = encode_2d(&tx, dt, c.x, v.K, c.M, c.xs * 2, 64, kTile, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -616,20 +623,25 @@ cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPla
     attr.val.clusterDim.x = p.parts;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.parts, p.tiles);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.parts) * p.tiles);
     cfg.blockDim = dim3(kShrinkThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, shrink, tx, v, c, t16, up, p.blocks_each, S))) return e;
+    LoraCall marked = c;
+    marked.chunk = kTile;
+    marked.marks = reinterpret_cast<int *>(up + c.M);
+    if ((e = cudaLaunchKernelEx(&cfg, shrink, tx, v, marked, t16, up, p.blocks_each, p.parts, S))) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(sms, static_cast<int64_t>(p.tiles) * ((v.N + kTile - 1) / kTile))));
     cfg.blockDim = dim3(kExpandThreads);
     cfg.dynamicSmemBytes = kExpandSmem;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, expand, ty, to, v, c, static_cast<const uint16_t *>(t16), static_cast<const float *>(up));
+    e = cudaLaunchKernelEx(&cfg, expand, ty, to, v, c, static_cast<const uint16_t *>(t16), static_cast<const float *>(up));
+    if (!e) *launches += 2;
+    return e || !p.marks ? e : launch_lora_marked(v, marked, bf16, st, launches);
 }
 
 }  // namespace q4

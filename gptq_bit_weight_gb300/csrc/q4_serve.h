@@ -38,7 +38,7 @@ struct LoraView {
     const uint16_t *a;           // [slots][rpad * ceil64(K)], layout in q4_lora.cu
     const uint16_t *b;           // [slots][rpad * N]
     const LoraSlot *slot;        // [slots]
-    float *t;                    // [rows][rpad] fp32: scale * x . A^T; and room for one more each row
+    float *t;                    // [rows][rpad] fp32: scale * x . A^T; and room for two more each row
     int *status;
 };
 
@@ -49,20 +49,23 @@ struct LoraCall {
     int64_t xs, ys, os;
     int M;
     int chunk;                   // rows that a CTA of the few-row kernels looks over
+    int *marks;                  // [chunks] or NULL: only the chunks that are marked
 };
 
 cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,
                             const uint16_t *src_b, int rank, float scale, bool bf16, cudaStream_t st);
 // few rows, and ranks over 128 (q4_lora.cu)
 cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
-// many rows (q4_lora_tc.cu)
+// the marked chunks of c.chunk rows
+cudaError_t launch_lora_marked(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
+// many rows (q4_lora_tc.cu); marks the tiles of 128 rows whose adapters have too many ranks, which it leaves out
 struct LoraTcPlan {
-    bool ok;
+    bool ok, marks;              // whether there can be marked tiles
     int tiles, parts, blocks_each;
 };
 LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms);
 cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPlan &p, int sms, bool bf16,
-                           cudaStream_t st);
+                           cudaStream_t st, int *launches);
 
 // The step's requests and one layer's cache, as the kernels read them.
 struct AttnBatch {

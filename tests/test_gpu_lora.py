@@ -98,6 +98,8 @@ CASES = [  # (M, K, N, ranks, rows: "one", "mixed", "runs")
     (320, 328, 520, [16, 40, 64], "runs"),
     (70, 64, 64, [8] * 70, "mixed"),
     (700, 256, 264, [200, 16, 256], "mixed"),          # ranks too high for the tiles
+    (700, 264, 520, [64, 16, 33] * 8, "mixed"),        # each tile has too many adapters
+    (9000, 64, 72, [64, 16, 33] * 8, "mixed"),         # more tiles than a warp looks at together
 ]
 
 
@@ -134,6 +136,28 @@ def test_matches_definition(q4, M, K, N, ranks, kind, dtype):
     assert torch.equal(out.cpu()[none], y[none])         # a row without an adapter is y itself
     pool.add(xd, rd, yd, out=yd)
     assert torch.equal(yd, out)                          # in place: the same
+    pool.device_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+def test_a_prompt_beside_single_tokens(q4, dtype):
+    """Tiles of one adapter and tiles of many in one call, the rows of both kinds in one tile among them."""
+    K, N, M = 520, 1032, 1700
+    g = torch.Generator().manual_seed(15)
+    ads = adapters(g, [64, 40, 16, 64] * 6, K, N, dtype)
+    rows = torch.full((M,), 3, dtype=torch.int32)
+    rows[200:500] = torch.randint(-1, 24, (300,), generator=g, dtype=torch.int32)
+    rows[1300:] = torch.randint(-1, 24, (400,), generator=g, dtype=torch.int32)
+    x, y = torch.randn(M, K, generator=g).to(dtype), torch.randn(M, N, generator=g).to(dtype)
+    pool = pool_of(q4, ads, K, N, 24, 64, dtype)
+    ref, tol = reference(x, y, rows, ads, K)
+    xd, yd, rd = x.to(DEV), y.to(DEV), rows.to(DEV)
+    out = pool.add(xd, rd, yd)
+    check(out, ref, tol, "out of place")
+    assert torch.equal(out, pool.add(xd, rd, yd))
+    assert torch.equal(out.cpu()[rows < 0], y[rows < 0])
+    pool.add(xd, rd, yd, out=yd)
+    assert torch.equal(yd, out)
     pool.device_error()
 
 
