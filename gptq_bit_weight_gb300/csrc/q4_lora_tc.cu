@@ -19,13 +19,13 @@
 //           stored by TMA
 //
 // A tile whose adapters have more than kCap ranks in all (single tokens of many
-// requests) is left to the kernels of few rows, which run behind over the tiles
-// that the first launch marks (2.5 us where none is; 800 rows that mix 32
-// adapters, 8192 x 10240: 100 us instead of 260 by passes).  Adapters with an infinity or NaN, which must
-// not meet another row's zero, get passes of their own over the tile's output,
-// each of which changes only the rows that use them.
+// requests) takes passes over its output, each of which changes only the rows
+// that use its adapters; where a pool could ask for many, such tiles are left
+// to the kernels of few rows, which run behind over the tiles that the first
+// launch marks.  Adapters with an infinity or NaN, which must not meet another
+// row's zero, get passes of their own.
 //
-// 4099 rows of 6 runs, 8192 x 28672, rank 64, fp16: 115 us, 4.4 TB/s of the
+// 4099 rows of 6 runs, 8192 x 28672, rank 64, fp16: 112 us, 4.5 TB/s of the
 // bytes that the call cannot do without (74 us at the copy rate): the first
 // launch 15 of them (x is 67 MB), the second 1.43 us for a job of 128 x 128
 // outputs on each SM, at which y, out and B (512 B a column) move at 6.9 TB/s
@@ -123,8 +123,7 @@ __device__ void build_info(const LoraView &v, const LoraCall &c, int m0, int cap
             off += k.rank[j];
             ranks += k.rank[j];
         }
-        // a tile whose adapters have too many ranks is left to the kernels of few rows
-        k.marked = ranks > kCap;
+        k.marked = c.marks && ranks > kCap;              // left to the kernels of few rows
         k.n = k.marked ? 0 : n;
         k.passes = k.n ? pass + 1 : 0;
     }
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     tc_fence_before();
     build_info(v, c, m0, kShrinkCap, false, k);                      // synchronizes
     tc_fence_after();
-    if (part == 0 && threadIdx.x == 0) c.marks[tile] = k.marked;
+    if (c.marks && part == 0 && threadIdx.x == 0) c.marks[tile] = k.marked;
     const uint32_t tmem = *tmem_slot;
     const int kb0 = part * blocks_each, kb1 = min(kb0 + blocks_each, (v.K + 63) / 64);
     bool alive = true;
@@ -592,7 +591,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms) {
     LoraTcPlan p;
     p.ok = v.rpad <= kCap && v.rpad <= kShrinkCap;
-    p.marks = std::min(std::min(M, kTile), v.slots) * v.rpad > kCap;
+    // Passes over a tile's output while there can be three at most.  8 adapters of 64 ranks, 8192 x 10240: 800 rows in 6
+    // runs 26 us, 29 with marked tiles; rows that mix them 72 and 55.  32 adapters: 27 and 30, 260 and 100.
+    p.marks = std::min(kTile, v.slots) * v.rpad > 512;
     p.tiles = (M + kTile - 1) / kTile;
     const int blocks = (v.K + 63) / 64;
     // parts of K: as many CTAs as fill the GPU once, at least four blocks of 64 each
@@ -631,7 +632,7 @@ cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPla
     cfg.numAttrs = 1;
     LoraCall marked = c;
     marked.chunk = kTile;
-    marked.marks = reinterpret_cast<int *>(up + c.M);
+    marked.marks = p.marks ? reinterpret_cast<int *>(up + c.M) : nullptr;
     if ((e = cudaLaunchKernelEx(&cfg, shrink, tx, v, marked, t16, up, p.blocks_each, p.parts, S))) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(sms, static_cast<int64_t>(p.tiles) * ((v.N + kTile - 1) / kTile))));
     cfg.blockDim = dim3(kExpandThreads);
@@ -639,7 +640,7 @@ cudaError_t launch_lora_tc(const LoraView &v, const LoraCall &c, const LoraTcPla
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, expand, ty, to, v, c, static_cast<const uint16_t *>(t16), static_cast<const float *>(up));
+    e = cudaLaunchKernelEx(&cfg, expand, ty, to, v, marked, static_cast<const uint16_t *>(t16), static_cast<const float *>(up));
     if (!e) *launches += 2;
     return e || !p.marks ? e : launch_lora_marked(v, marked, bf16, st, launches);
 }
