@@ -257,8 +257,8 @@ int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const g
                            scale, window, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
     // More query rows for each key/value head than the streaming kernel's row tile has: the tensor-core kernel
     // (which takes its maximum before scaling, so a positive scale).  Measured at 64 heads over 8, contexts of up
-    // to 4096: 32 requests of 2 tokens (16 rows) 54 us streaming, 71 on tcgen05; of 4 tokens, streaming with row
-    // tiles of 32 rows 134, tcgen05 72; one request of 4 tokens 25 and 19.
+    // to 4096: 32 requests of 2 tokens (16 rows) 45 us streaming, 53 on tcgen05, one such request 12 and 15; 32 of 4
+    // tokens, streaming with row tiles of 32 rows 134, tcgen05 54; one request of 4 tokens 25 and 17.
     const bool chunk = static_cast<int64_t>(batch->max_q) * s.group > 16 && scale > 0.f;
     if (cudaError_t e = (chunk ? q4::launch_attend_tc : q4::launch_attend_stream)(
             s, batch_view(batch), cache_view(cache), a, h->dtype == GPTQ_Q4_DTYPE_BF16, stream))

@@ -3,7 +3,7 @@
 // memory and the products run on mma.sync in tiles of 16 query rows (token x
 // query head of the group): bound by reading the cache, not by the tensor
 // cores.  64 requests of up to 8192 tokens, 64 heads over 8: 131 us, 6.2 TB/s;
-// two of 131071 and about 100000: 103 us, 6.3 TB/s; one of 777, 32 heads: 12
+// two of 131071 and about 100000: 103 us, 6.3 TB/s; one of 777, 32 heads: 11
 // us, latency (lengths, page table, keys, the join of the pieces).
 //
 //   scores s = scale log2(e) q . k in fp32; running maximum m and sum l,

@@ -24,14 +24,14 @@
 // Two row tiles, because one alone leaves the tensor cores idle during its
 // softmax; 184 registers for the softmax threads (a row of 128 scores each) and
 // 136 for the others add up to the launch's 384 x 168 (with 208 and 88 the
-// loaders and the issuer spill: 32 requests of 4 tokens 58 us instead of 54.5).  4096 tokens over 16384,
-// 64 heads over 8 of 128: 1120 to 1150 us, 1.7 PFLOP/s, what the tensor cores
-// sustain under the power limit; 512 over 8192: 98 us (1.36 PFLOP/s: start,
-// last wave and the join of the pieces); 384 together with 47 single tokens of
-// others: 111 us, units of single tokens bound by the ring of loads (1.3 us a
-// tile).  Heads of 64, 4096 over 16384, 32 over 8: 463 us, bound by the softmax
-// warps' own chain (with columns of their own for the weights, so that the next
-// scores never wait for the second product: 503).
+// loaders and the issuer spill: 32 requests of 4 tokens 58 us instead of 54.5).
+// 4096 tokens over 16384, 64 heads over 8 of 128: 1120 us, 1.7 PFLOP/s, what the
+// tensor cores sustain under the power limit; 512 over 8192: 98 us (1.36
+// PFLOP/s: start, last wave and the join of the pieces); 384 together with 47
+// single tokens of others: 111 us (a key tile is 1.8 us with two row tiles, 1.3
+// with one).  Heads of 64, 4096 over 16384, 32 over 8: 463 us, bound by the
+// softmax warps' own chain (with columns of their own for the weights, so that
+// the next scores never wait for the second product: 503).
 // Every wait is bounded; a wait that runs out sets a status bit and its role
 // goes on without waiting.
 #include <cuda.h>
