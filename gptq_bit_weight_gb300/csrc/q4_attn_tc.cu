@@ -60,6 +60,7 @@ struct Cfg {
     static constexpr int kQ = 128 * D * 2;       // of one row tile's queries
     static constexpr int kMisc = 2048;
     static constexpr int kRoom = (232448 - 1024 - 2 * kQ - kMisc) / kHalf;
+    // what fits, 5 at D = 128; at D = 64 no more than 8 (12: 62.5 us for the window of 1024 instead of 59.4)
     static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
     static constexpr int kSmem = 2 * kQ + kStages * kHalf + kMisc + 1024;
     static constexpr int kPiece = 2 * 128 * (D + 2);   // floats of a piece in the workspace
