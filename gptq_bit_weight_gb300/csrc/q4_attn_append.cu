@@ -58,9 +58,11 @@ __global__ void __launch_bounds__(kThreads)
             if (req < b.batch && b.cu_q[req] <= t) {
                 const Request r = load_request(b, req, s.page_log2);
                 const int idx = r.kv - r.ql + (t - r.q0);
-                int bad = r.bad ? kAttnBadBatch : 0;
-                if (idx < 0 || idx >= r.kv) {
-                    bad |= kAttnBadBatch;
+                int bad = 0;
+                // A length that had to be cut says nothing of where the token belongs: its index in the cut context
+                // is another token's, and a table's padding may be another request's page.
+                if (r.bad || idx < 0 || idx >= r.kv) {
+                    bad = kAttnBadBatch;
                 } else {
                     const int page = b.table[req * b.table_stride + (idx >> s.page_log2)];
                     k.pos = a.positions ? a.positions[t] : idx;

@@ -506,7 +506,7 @@ typedef struct {
  * The arrays are read on the GPU when the call runs.  A length or page index
  * outside its range is cut to it (no access leaves the caller's arrays),
  * makes that request's results meaningless, and is reported by
- * gptq_q4_attn_device_error. */
+ * gptq_q4_attn_device_error; nothing is written to the cache for it. */
 typedef struct {
     const int32_t *cu_q, *kv_len, *table;
     int64_t table_stride;
@@ -566,9 +566,11 @@ int gptq_q4_attn_set_rope(gptq_q4_attn h, int rotary_dim, int interleaved, const
  *              rotated queries; may be qkv itself (same stride), else must not overlap it
  * 16-byte aligned, strides multiples of 8.  Rotation in fp32, rounded once.
  * Rows that no request owns are left alone.  A token whose index is negative
- * or past the table (kv_len < q_len, say), or whose position is outside
- * 0 .. max_pos - 1, is not written anywhere and is reported by
- * gptq_q4_attn_device_error.  Errors: INVALID_ARGUMENT, CUDA_ERROR. */
+ * (kv_len < q_len, say), whose position is outside 0 .. max_pos - 1 or whose
+ * page index is outside the cache is not written anywhere, nor is any token of
+ * a request with a length outside its range (a kv_len past the table, say);
+ * gptq_q4_attn_device_error reports either.  Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED (batch > 4096), CUDA_ERROR. */
 int gptq_q4_attn_append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const gptq_q4_cache *cache,
                         const gptq_q4_batch *batch, const int32_t *positions, void *q_out, int64_t q_stride,
                         cudaStream_t stream);

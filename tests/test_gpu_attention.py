@@ -442,6 +442,47 @@ def test_append_out_of_range_is_reported_and_not_written(q4):
         assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
 
 
+@pytest.mark.parametrize("what", ["one_past", "long", "huge", "chunk", "cu_past", "cu_back"])
+def test_a_request_past_its_limits_writes_nothing(q4, what):
+    """A request that overruns its table, whose last entries are padding on another request's page, or whose rows are
+    out of range: neither its pages nor anybody's change, and the other request is served."""
+    Hq, Hkv, D, page, dtype = 2, 1, 64, 8, torch.float16
+    step = Step(q4, [(4, 16), (2, 21)], Hkv, D, page, dtype, seed=13)
+    assert step.table.shape == (2, 3)
+    step.table[0, 2] = step.table[1, 0]                   # the first request's padding
+    cu, kv, table = (t.clone() for t in (*step.batch.tensors[:2], step.table.to(DEV)))
+    good = 0 if what == "cu_past" else 1
+    if what == "one_past":                               # 24 tokens fit the table
+        kv[0] = 25
+    if what == "long":
+        kv[0] = 1000
+    if what == "huge":
+        kv[0] = 2 ** 31 - 1
+    if what == "chunk":                                  # its first new tokens would fit, its last would not
+        kv[0] = 26
+    if what == "cu_past":
+        cu[2] = 1000
+    if what == "cu_back":                                # the first request's rows begin before the step's
+        cu[0] = -7
+    x = torch.randn(6, 4 * D, generator=torch.Generator().manual_seed(12)).to(dtype)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    cache = q4.PagedCache(step.k.to(DEV), step.v.to(DEV))
+    q = torch.zeros(6, Hq, D, dtype=dtype, device=DEV)
+    att.append(x.to(DEV), cache, q4.PagedBatch(cu, kv, table, tokens=6), q_out=q)
+    want_k, want_v, want_q = step.k.clone(), step.v.clone(), torch.zeros(6, Hq, D, dtype=dtype)
+    heads = x.view(6, 4, D)
+    ql, n = step.lens[good]
+    for t in range(ql):
+        i, row = n - ql + t, step.cu[good] + t
+        p = int(step.table[good, i // page])
+        want_k[p, :, i % page], want_v[p, :, i % page], want_q[row] = heads[row, 2:3], heads[row, 3:4], heads[row, :2]
+    for got, want in ((cache.k, want_k), (cache.v, want_v), (q, want_q)):
+        assert torch.equal(torch.nan_to_num(got.cpu(), nan=99.0), torch.nan_to_num(want, nan=99.0))
+    with pytest.raises(q4.GPTQ4Error) as e:
+        att.device_error()
+    assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
+
+
 def test_decode_loop_matches_one_prompt(q4):
     """Appending and attending token by token, or in uneven chunks, gives what one prompt gives."""
     Hq, Hkv, D, page, dtype, n = 8, 2, 128, 16, torch.bfloat16, 200
