@@ -253,8 +253,10 @@ int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const g
                          "row strides (q %lld, out %lld) must be multiples of 8, at least %lld and below 2^39",
                          static_cast<long long>(q_stride), static_cast<long long>(out_stride),
                          static_cast<long long>(row));
+    // Contexts end at 2^30 tokens, so a longer window hides nothing; differences with a shorter one fit 32 bits.
+    const int seen = window < 1 << 30 ? window : 0;
     const q4::AttendCall a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), q_stride, out_stride,
-                           scale, window, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
+                           scale, seen, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
     // More query rows for each key/value head than the streaming kernel's row tile has: the tensor-core kernel
     // (which takes its maximum before scaling, so a positive scale).  Measured at 64 heads over 8, contexts of up
     // to 4096: 32 requests of 2 tokens (16 rows) 45 us streaming, 53 on tcgen05, one such request 12 and 15; 32 of 4

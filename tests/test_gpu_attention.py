@@ -181,6 +181,21 @@ def test_window(q4, shape, window, dtype, max_q):
     att.device_error()
 
 
+@pytest.mark.parametrize("max_q", [1, 100000])
+@pytest.mark.parametrize("window", [2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_window_longer_than_any_context(q4, D, window, max_q):
+    """The largest windows hide nothing, for requests with more new tokens than context among them (their first rows
+    have negative indexes, of which a window is subtracted)."""
+    Hq, Hkv, page, dtype = 4, 2, 16, torch.bfloat16
+    step = Step(q4, [(10, 5), (5, 2), (1, 300), (160, 20), (40, 0), (3, 200)], Hkv, D, page, dtype, seed=14)
+    q = torch.randn(step.tokens, Hq, D, generator=torch.Generator().manual_seed(13)).to(dtype)
+    ref, tol = attention_reference(step, q, D ** -0.5, 0)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    check(att.attend(q.to(DEV), step.cache, step.make_batch(q4, max_q), window=window), ref, tol, f"window {window}")
+    att.device_error()
+
+
 @pytest.mark.parametrize("lens", [[(1, 400), (1, 70)], [(140, 400), (1, 70)]], ids=["tokens", "chunk"])
 def test_strided_rows_scale_and_stream(q4, lens):
     """q as columns of wider rows, out as columns of wider rows, keys and values side by side in a
