@@ -152,7 +152,7 @@ __device__ __forceinline__ Request load_request(const AttnBatch &b, int i, int p
     const long long cap = min(static_cast<long long>(b.width) << page_log2, 1ll << 30);
     Request r;
     r.q0 = min(max(a, 0), b.tokens);
-    r.ql = max(min(e, b.tokens) - r.q0, 0);
+    r.ql = max(min(e, b.tokens), r.q0) - r.q0;           // (any cu_q: the difference stays within the rows)
     r.kv = static_cast<int>(min(static_cast<long long>(max(n, 0)), cap));
     r.bad = r.q0 != a || r.q0 + r.ql != e || r.kv != n;
     return r;

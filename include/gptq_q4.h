@@ -506,7 +506,8 @@ typedef struct {
  * The arrays are read on the GPU when the call runs.  A length or page index
  * outside its range is cut to it (no access leaves the caller's arrays),
  * makes that request's results meaningless, and is reported by
- * gptq_q4_attn_device_error; nothing is written to the cache for it. */
+ * gptq_q4_attn_device_error (by an append, if the request holds a row);
+ * nothing is written to the cache for it. */
 typedef struct {
     const int32_t *cu_q, *kv_len, *table;
     int64_t table_stride;

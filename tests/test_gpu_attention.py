@@ -310,6 +310,38 @@ def test_lengths_and_pages_out_of_range_are_reported(q4, max_q):
 
 
 @pytest.mark.parametrize("max_q", [1, 100000])
+def test_any_row_ranges_are_cut_to_the_rows(q4, max_q):
+    """Row ranges at the ends of 32 bits: reported, nothing is written outside the rows, and nothing is appended."""
+    Hq, Hkv, D, page, dtype = 2, 1, 64, 8, torch.float16
+    low, high = -2 ** 31, 2 ** 31 - 1
+    step = Step(q4, [(3, 20), (2, 9)], Hkv, D, page, dtype, seed=15)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    x = torch.randn(step.tokens, 4 * D, generator=torch.Generator().manual_seed(14)).to(dtype).to(DEV)
+    for cu in ([0, 3, low], [0, low, low], [2, low, high], [low, high, low], [high, low, 3], [0, high, 5], [low, low, low]):
+        batch = q4.PagedBatch(torch.tensor(cu, dtype=torch.int32, device=DEV), *step.batch.tensors[1:],
+                              tokens=step.tokens, max_q=max_q)
+        room = torch.full((step.tokens + 64, Hq * D), 7.0, dtype=dtype, device=DEV)
+        att.attend(x[:, :Hq * D], step.cache, batch, out=room[32:32 + step.tokens])
+        assert (room[:32] == 7).all() and (room[32 + step.tokens:] == 7).all()
+        with pytest.raises(q4.GPTQ4Error) as e:
+            att.device_error()
+        assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
+        cache = q4.PagedCache(step.k.to(DEV), step.v.to(DEV))
+        att.append(x, cache, batch, q_out=room[32:32 + step.tokens])
+        if cu == [0, 3, low]:                             # the first request's range is right
+            p, o = int(step.table[0, 2]), slice(1, 4)
+            cache.k[p, :, o] = cache.v[p, :, o] = float("nan")
+            step.k[p, :, o] = step.v[p, :, o] = float("nan")
+        assert torch.equal(torch.nan_to_num(cache.k.cpu(), nan=99.0), torch.nan_to_num(step.k, nan=99.0))
+        assert torch.equal(torch.nan_to_num(cache.v.cpu(), nan=99.0), torch.nan_to_num(step.v, nan=99.0))
+        assert (room[:32] == 7).all() and (room[32 + step.tokens:] == 7).all()
+        try:
+            att.device_error()
+        except q4.GPTQ4Error as e:                        # if the range held a row
+            assert e.status == q4.GPTQ_Q4_DEVICE_FAULT
+
+
+@pytest.mark.parametrize("max_q", [1, 100000])
 def test_more_work_than_a_call_counts_is_reported_and_not_done(q4, max_q):
     """2^31 tiles of work, from lengths alone: nothing is read or written."""
     heads, D, page = 128, 64, 1024
