@@ -1026,6 +1026,46 @@ HandleView api_view(const gptq_q4_s *h) { return view(h); }
 void api_count_launches(int n) { g_launches += static_cast<uint64_t>(n); }
 int api_check_device_ptr(const void *p, int dev, const char *name) { return check_device_ptr(p, dev, name); }
 int api_check_device_sm103(int *dev_out) { return check_device_sm103(dev_out); }
+bool api_retire(Retired &old, void *p) {
+    if (!p) return true;
+    Retired::Node *n = new (std::nothrow) Retired::Node{p, old.head};
+    if (n) old.head = n;
+    return n != nullptr;
+}
+void api_free_retired(Retired &old) {
+    while (Retired::Node *n = old.head) {
+        cudaFree(n->p);
+        old.head = n->next;
+        delete n;
+    }
+}
+cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync) {
+    // A stream-ordered allocation on a capturing stream would belong to the graph, and calls outside it would use
+    // memory that is there only while the graph runs: an ordinary allocation serves both.
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (!sync)
+        if (cudaError_t e = cudaStreamIsCapturing(s, &capture)) return e;
+    const bool captured = capture != cudaStreamCaptureStatusNone;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (captured) cudaThreadExchangeStreamCaptureMode(&mode);
+    void *p = nullptr;
+    auto allocate = [&](size_t n) { return sync || captured ? cudaMalloc(&p, n) : cudaMallocAsync(&p, n, s); };
+    size_t size = sync ? need : std::max(need, 2 * *bytes);
+    cudaError_t e = allocate(size);
+    if (e && size > need) {
+        cudaGetLastError();
+        e = allocate(size = need);
+    }
+    if (!e && !api_retire(old, *buf)) {
+        sync || captured ? cudaFree(p) : cudaFreeAsync(p, s);
+        e = cudaErrorMemoryAllocation;
+    }
+    if (captured) cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e) return e;
+    *buf = p;
+    *bytes = size;
+    return cudaSuccess;
+}
 int api_failf(int code, const char *fmt, ...) {
     t_status = code;
     va_list ap;

@@ -6,6 +6,17 @@
 #include "../../include/gptq_q4.h"
 #include "q4_internal.cuh"
 
+namespace q4 {
+// Device buffers that a handle has replaced.  A captured graph holds the
+// addresses that its calls were given, so they stay until the handle is freed.
+struct Retired {
+    struct Node {
+        void *p;
+        Node *next;
+    } *head = nullptr;
+};
+}  // namespace q4
+
 struct gptq_q4_s {
     int device = -1;
     int K = 0, N = 0, groupsize = 0, geff = 0, G = 0;   // K, geff: rows and rows per group of the private layout
@@ -45,6 +56,13 @@ int api_cuda_fail(cudaError_t e, const char *what);
 int api_check_matmul_args(gptq_q4_handle h, const void *x, int M, const void *out);
 HandleView api_view(const gptq_q4_s *h);
 void api_count_launches(int n);
+// Puts a buffer of at least `need` bytes in the place of *buf (*bytes large), which is retired; the contents are not
+// kept.  sync: exactly `need`, at once; else by stream order, and twice the old size where there is room, so that
+// the retired ones add up to no more than the present one.  On an error nothing has changed.
+cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync);
+// Keeps p until the handle is freed; false if there is no host memory for that.
+bool api_retire(Retired &old, void *p);
+void api_free_retired(Retired &old);
 int api_check_device_ptr(const void *p, int dev, const char *name);
 int api_check_device_sm103(int *dev_out);
 int api_failf(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));

@@ -15,8 +15,9 @@ struct gptq_q4_lora_s {
     uint16_t *a = nullptr, *b = nullptr;
     q4::LoraSlot *slot = nullptr;
     int *status = nullptr;
-    float *t = nullptr;
-    size_t t_rows = 0;
+    void *t = nullptr;           // workspace of t_bytes
+    size_t t_bytes = 0;
+    q4::Retired retired;
     int sms = 0;
 };
 
@@ -47,28 +48,21 @@ void release(gptq_q4_lora_s *h) {
     cudaFree(h->slot);
     cudaFree(h->status);
     cudaFree(h->t);
+    q4::api_free_retired(h->retired);
     if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
 
 q4::LoraView view(const gptq_q4_lora_s *h) {
-    return q4::LoraView{h->K, h->N, h->slots, q4::ceil16(h->max_rank), h->a, h->b, h->slot, h->t, h->status};
+    return q4::LoraView{h->K, h->N, h->slots, q4::ceil16(h->max_rank), h->a, h->b, h->slot,
+                        static_cast<float *>(h->t), h->status};
 }
 
 int ensure_rows(gptq_q4_lora_s *h, size_t rows, cudaStream_t s, bool sync_alloc) {
-    if (rows <= h->t_rows) return GPTQ_Q4_OK;
-    if (h->t) {
-        if (cudaError_t e = sync_alloc ? cudaFree(h->t) : cudaFreeAsync(h->t, s))
-            return api_cuda_fail(e, "freeing the adapter workspace");
-        h->t = nullptr;
-        h->t_rows = 0;
-    }
-    void *p = nullptr;
-    const size_t bytes = rows * (q4::ceil16(h->max_rank) + 2) * sizeof(float);
-    if (cudaError_t e = sync_alloc ? cudaMalloc(&p, bytes) : cudaMallocAsync(&p, bytes, s))
+    const size_t need = rows * (q4::ceil16(h->max_rank) + 2) * sizeof(float);
+    if (need <= h->t_bytes) return GPTQ_Q4_OK;
+    if (cudaError_t e = q4::api_replace(h->retired, &h->t, &h->t_bytes, need, s, sync_alloc))
         return api_cuda_fail(e, "allocating the adapter workspace");
-    h->t = static_cast<float *>(p);
-    h->t_rows = rows;
     return GPTQ_Q4_OK;
 }
 

@@ -450,9 +450,12 @@ gptq_q4_lora gptq_q4_lora_make(int K, int N, int slots, int max_rank, int dtype)
 int gptq_q4_lora_set(gptq_q4_lora h, int slot, const void *a, const void *b, int rank, float scale,
                      cudaStream_t stream);
 
-/* Size the workspace for calls with up to max_m rows (a later call with more
- * rows grows it on its stream).  Synchronizes.  Errors: INVALID_ARGUMENT,
- * OUT_OF_MEMORY. */
+/* Size the workspace for calls with up to max_m rows.  A later call with more
+ * rows replaces it by a larger one, by stream order (on a capturing stream by
+ * an ordinary allocation, which is no part of the graph).  A workspace that was
+ * replaced stays allocated until the pool is freed, so a graph captured before
+ * goes on running; the replaced ones of such calls add up to no more than the
+ * present one.  Synchronizes.  Errors: INVALID_ARGUMENT, OUT_OF_MEMORY. */
 int gptq_q4_lora_reserve(gptq_q4_lora h, int max_m);
 
 /* out = y + the adapters' part, as above.

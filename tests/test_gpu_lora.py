@@ -312,6 +312,77 @@ def test_beside_the_quantised_projection(q4):
     check(pool.add(x.to(DEV), rows.to(DEV), y), ref, tol, "beside the projection")
 
 
+def captured(f):
+    """f() captured into a graph, after one call outside it."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        f()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            f()
+    torch.cuda.synchronize()
+    return graph
+
+
+@pytest.mark.parametrize("M", [3, 40])
+@pytest.mark.parametrize("grow", ["call", "reserve"])
+def test_a_captured_step_outlives_a_larger_call(q4, M, grow):
+    """A step captured at few rows, then calls that need larger workspaces: the graph goes on giving its result, and
+    writes nothing into memory that others have been given since."""
+    K, N, dtype = 264, 520, torch.bfloat16
+    g = torch.Generator().manual_seed(16)
+    ads = adapters(g, [256, 40, 16], K, N, dtype)
+    pool = pool_of(q4, ads, K, N, 3, 256, dtype)
+    x, y = torch.randn(2000, K, generator=g).to(dtype), torch.randn(2000, N, generator=g).to(dtype)
+    rows = row_slots(g, 2000, 3, "mixed")
+    ref, tol = reference(x, y, rows, ads, K)
+    xd, yd, rd = x.to(DEV), y.to(DEV), rows.to(DEV)
+    out = torch.empty(M, N, dtype=dtype, device=DEV)
+    graph = captured(lambda: pool.add(xd[:M], rd[:M], yd[:M], out=out))
+    if grow == "reserve":
+        pool.reserve(700)
+        pool.reserve(2000)
+    for m in (65, 300, 700, 2000):
+        check(pool.add(xd[:m], rd[:m], yd[:m]), ref[:m], tol[:m], f"{m} rows")
+    others = [torch.full((n,), 77, dtype=torch.int8, device=DEV) for n in [1 << 16] * 40 + [1 << 21] * 4]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, ref[:M], tol[:M], "replayed")
+    assert all((o == 77).all() for o in others)
+    pool.device_error()
+
+
+@pytest.mark.parametrize("M", [200, 900])
+def test_a_workspace_grown_while_capturing(q4, M):
+    """The captured call is the first that needs the larger workspace; calls outside the graph use it too, before and
+    after the graph has gone."""
+    K, N, dtype = 264, 520, torch.float16
+    g = torch.Generator().manual_seed(17)
+    ads = adapters(g, [64, 40, 16], K, N, dtype)
+    pool = pool_of(q4, ads, K, N, 3, 64, dtype)
+    x, y = torch.randn(M, K, generator=g).to(dtype), torch.randn(M, N, generator=g).to(dtype)
+    rows = row_slots(g, M, 3, "mixed")
+    ref, tol = reference(x, y, rows, ads, K)
+    xd, yd, rd = x.to(DEV), y.to(DEV), rows.to(DEV)
+    out, side, graph = torch.empty_like(yd), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        pool.add(xd, rd, yd, out=out)
+    check(pool.add(xd, rd, yd), ref, tol, "before a replay")
+    graph.replay()
+    check(out, ref, tol, "replayed")
+    del graph
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    check(pool.add(xd, rd, yd), ref, tol, "after the graph")
+    pool.device_error()
+
+
 def test_refusals(q4):
     bad = q4.GPTQ_Q4_INVALID_ARGUMENT
 
