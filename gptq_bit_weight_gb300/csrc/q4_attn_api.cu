@@ -16,6 +16,7 @@ struct gptq_q4_attn_s {
     q4::AttnShape shape{};
     int rot = 0, interleaved = 0, max_pos = 0;
     float2 *rope = nullptr;
+    q4::Retired retired;
     int *status = nullptr;
     float *ws = nullptr;
     int *tickets = nullptr;
@@ -79,6 +80,7 @@ void release(gptq_q4_attn_s *h) {
     if (h->device >= 0) cudaSetDevice(h->device);
     cudaDeviceSynchronize();
     cudaFree(h->rope);
+    q4::api_free_retired(h->retired);
     cudaFree(h->status);
     cudaFree(h->ws);
     cudaFree(h->tickets);
@@ -185,20 +187,27 @@ int gptq_q4_attn_set_rope(gptq_q4_attn h, int rotary_dim, int interleaved, const
     for (int i = 0; i < rotary_dim / 2; ++i)
         if (!std::isfinite(inv_freq[i])) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "inv_freq[%d] is not finite", i);
     if (cudaError_t e = cudaDeviceSynchronize()) return api_cuda_fail(e, "set_rope");
-    void *table = nullptr;
+    // A captured append holds the table's address, so the table is written anew only where all else that such a call
+    // holds stays true, and otherwise kept beside the next one.
+    const bool same = h->rope && rotary_dim == h->rot && max_pos == h->max_pos && (interleaved != 0) == (h->interleaved != 0);
+    void *table = same ? h->rope : nullptr;
     if (rotary_dim) {
         const size_t bytes = static_cast<size_t>(max_pos) * (rotary_dim / 2) * sizeof(float2);
-        if (cudaError_t e = cudaMalloc(&table, bytes)) return api_cuda_fail(e, "allocating the rotary table");
+        if (!same)
+            if (cudaError_t e = cudaMalloc(&table, bytes)) return api_cuda_fail(e, "allocating the rotary table");
         cudaError_t e = q4::launch_rope_table(static_cast<float2 *>(table), inv_freq, length_scale, rotary_dim / 2,
                                               max_pos, nullptr);
         if (!e) e = cudaDeviceSynchronize();
         if (e) {
-            cudaFree(table);
+            if (!same) cudaFree(table);
             return api_cuda_fail(e, "building the rotary table");
         }
         q4::api_count_launches(1);
     }
-    cudaFree(h->rope);
+    if (!same && !q4::api_retire(h->retired, h->rope)) {
+        cudaFree(table);
+        return api_failf(GPTQ_Q4_OUT_OF_MEMORY, "host allocation for the rotary table failed");
+    }
     h->rope = static_cast<float2 *>(table);
     h->rot = rotary_dim;
     h->interleaved = interleaved ? 1 : 0;

@@ -557,8 +557,11 @@ int gptq_q4_rope_freqs(int rotary_dim, double base, int kind, double factor, dou
  * Builds a table of fp32 cosines and sines for positions 0 .. max_pos - 1
  * (angles in fp64), 4 * max_pos * rotary_dim bytes.  rotary_dim: even, at most
  * head_dim, a multiple of 16; 0 turns rotation off again (the state of a new
- * handle).  Synchronizes.  Errors: INVALID_ARGUMENT, OUT_OF_MEMORY,
- * CUDA_ERROR. */
+ * handle).  The table of the same rotary_dim, interleaved and max_pos is
+ * written anew in its place, and a graph captured before turns by the new
+ * angles; any other table stays allocated until the handle is freed, and such
+ * a graph goes on with it.  Synchronizes.  Errors: INVALID_ARGUMENT,
+ * OUT_OF_MEMORY, CUDA_ERROR. */
 int gptq_q4_attn_set_rope(gptq_q4_attn h, int rotary_dim, int interleaved, const double *inv_freq,
                           double length_scale, int max_pos);
 

@@ -489,6 +489,57 @@ def test_append_out_of_range_is_reported_and_not_written(q4):
         assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
 
 
+def test_a_captured_append_outlives_its_rotary_table(q4):
+    """set_rope after a capture: another table leaves the graph its own, which nobody else is given; the same sizes
+    change the angles of the graph as well."""
+    Hq, Hkv, D, page, dtype = 4, 2, 128, 16, torch.float16
+    step = Step(q4, [(3, 40), (1, 700)], Hkv, D, page, dtype, seed=16)
+    x = torch.randn(step.tokens, Hq + 2 * Hkv, D, generator=torch.Generator().manual_seed(15)).to(dtype)
+    xd = x.view(step.tokens, -1).to(DEV)
+    pos = torch.tensor([37, 38, 39, 699])
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+
+    def right(q, rot, base, interleaved, what):
+        ref, tol = rotate_reference(x[:, :Hq], pos, q4.gptq_q4_rope_freqs(rot, base, 0)[0], 1.0, interleaved, dtype)
+        assert ((q.double().cpu() - ref).abs() <= tol).all(), what
+
+    att.set_rope(128, 1000)
+    q = torch.empty(step.tokens, Hq, D, dtype=dtype, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        att.append(xd, step.cache, step.batch, q_out=q)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            att.append(xd, step.cache, step.batch, q_out=q)
+    torch.cuda.synchronize()
+    others = []
+    for rot, base, interleaved, max_pos in ((128, 10000.0, True, 1000), (64, 500.0, False, 1000), (64, 900.0, False, 1000),
+                                            (128, 500000.0, False, 4000), (0, 1.0, False, 0)):
+        att.set_rope(rot, max_pos, base=base, interleaved=interleaved)
+        others += [torch.full((n,), 77, dtype=torch.int8, device=DEV) for n in [512000] * 6 + [1 << 21] * 2]
+        if rot:
+            right(att.append(xd, step.cache, step.batch), rot, base, interleaved, (rot, base))
+        else:
+            assert torch.equal(att.append(xd, step.cache, step.batch).cpu(), x[:, :Hq])
+        q.fill_(float("nan"))
+        graph.replay()
+        right(q, 128, 10000.0, False, "replayed")
+    assert all((o == 77).all() for o in others)
+    att.device_error()
+
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    att.set_rope(128, 1000)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        att.append(xd, step.cache, step.batch, q_out=q)
+    att.set_rope(128, 1000, base=300.0)
+    graph.replay()
+    right(q, 128, 300.0, False, "written anew")
+    att.device_error()
+
+
 @pytest.mark.parametrize("what", ["one_past", "long", "huge", "chunk", "cu_past", "cu_back"])
 def test_a_request_past_its_limits_writes_nothing(q4, what):
     """A request that overruns its table, whose last entries are padding on another request's page, or whose rows are
