@@ -126,6 +126,7 @@ void release(gptq_q4_s *h) {
     cudaFree(h->temp_state);
     cudaFree(h->rowscale);
     cudaFree(h->part);
+    q4::api_free_retired(h->retired);
     if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
@@ -158,96 +159,41 @@ int check_handle(gptq_q4_handle h) {
     return GPTQ_Q4_OK;
 }
 
-// Grow the split-K workspace / tickets (stream-ordered when a stream is given).
-int ensure_decode_work(gptq_q4_s *h, size_t ws_floats, int n_tickets, cudaStream_t s, bool sync_alloc) {
-    if (ws_floats > h->ws_floats) {
-        if (h->ws) {
-            if (sync_alloc) cudaFree(h->ws);
-            else Q4_CUDA(cudaFreeAsync(h->ws, s), "cudaFreeAsync(workspace)");
-            h->device_bytes -= h->ws_floats * sizeof(float);
-            h->ws = nullptr;
-            h->ws_floats = 0;
-        }
-        void *v = nullptr;
-        cudaError_t e = sync_alloc ? cudaMalloc(&v, ws_floats * sizeof(float))
-                                   : cudaMallocAsync(&v, ws_floats * sizeof(float), s);
-        if (e != cudaSuccess) return cuda_fail(e, "allocating split-K workspace");
-        h->ws = static_cast<float *>(v);
-        h->ws_floats = ws_floats;
-        h->device_bytes += ws_floats * sizeof(float);
-    }
-    if (n_tickets > h->n_tickets) {
-        if (h->tickets) {
-            if (sync_alloc) cudaFree(h->tickets);
-            else Q4_CUDA(cudaFreeAsync(h->tickets, s), "cudaFreeAsync(tickets)");
-            h->device_bytes -= static_cast<size_t>(h->n_tickets) * sizeof(int);
-            h->tickets = nullptr;
-            h->n_tickets = 0;
-        }
-        void *v = nullptr;
-        cudaError_t e = sync_alloc ? cudaMalloc(&v, n_tickets * sizeof(int))
-                                   : cudaMallocAsync(&v, n_tickets * sizeof(int), s);
-        if (e != cudaSuccess) return cuda_fail(e, "allocating split-K tickets");
-        h->tickets = static_cast<int *>(v);
-        h->n_tickets = n_tickets;
-        h->device_bytes += static_cast<size_t>(n_tickets) * sizeof(int);
-        if (sync_alloc) Q4_CUDA(cudaMemset(h->tickets, 0, n_tickets * sizeof(int)), "cudaMemset(tickets)");
-        else Q4_CUDA(cudaMemsetAsync(h->tickets, 0, n_tickets * sizeof(int), s), "cudaMemsetAsync(tickets)");
-    }
+// Grow a work buffer (stream-ordered when a stream is given); the one before stays until the handle is freed.
+template <typename T>
+int ensure_buffer(gptq_q4_s *h, T **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync_alloc, const char *what,
+                  bool zero = false) {
+    if (need <= *bytes) return GPTQ_Q4_OK;
+    void *p = *buf;
+    if (cudaError_t e = q4::api_replace(h->retired, &p, bytes, need, s, sync_alloc, zero)) return cuda_fail(e, what);
+    *buf = static_cast<T *>(p);
+    h->device_bytes += *bytes;
     return GPTQ_Q4_OK;
 }
 
+// The split-K workspace and tickets (zero between calls).
+int ensure_decode_work(gptq_q4_s *h, size_t ws_floats, int n_tickets, cudaStream_t s, bool sync_alloc) {
+    if (int r = ensure_buffer(h, &h->ws, &h->ws_bytes, ws_floats * sizeof(float), s, sync_alloc,
+                              "allocating split-K workspace"))
+        return r;
+    return ensure_buffer(h, &h->tickets, &h->tickets_bytes, static_cast<size_t>(n_tickets) * sizeof(int), s, sync_alloc,
+                         "allocating split-K tickets", true);
+}
+
 int ensure_temp_state(gptq_q4_s *h, int M, cudaStream_t s, bool sync_alloc) {
-    const size_t need = static_cast<size_t>(M) * h->K;
-    if ((h->act_bf16 || h->act_f32) && static_cast<size_t>(M) > h->rowscale_elems) {
-        if (h->rowscale) {
-            if (sync_alloc) cudaFree(h->rowscale);
-            else Q4_CUDA(cudaFreeAsync(h->rowscale, s), "cudaFreeAsync(rowscale)");
-            h->device_bytes -= h->rowscale_elems * sizeof(float);
-            h->rowscale = nullptr;
-            h->rowscale_elems = 0;
-        }
-        void *v = nullptr;
-        cudaError_t e = sync_alloc ? cudaMalloc(&v, M * sizeof(float)) : cudaMallocAsync(&v, M * sizeof(float), s);
-        if (e != cudaSuccess) return cuda_fail(e, "allocating row scales");
-        h->rowscale = static_cast<float *>(v);
-        h->rowscale_elems = static_cast<size_t>(M);
-        h->device_bytes += M * sizeof(float);
-    }
-    if (!(h->act_order || h->act_bf16 || h->act_f32) || need <= h->temp_state_elems) return GPTQ_Q4_OK;
-    if (h->temp_state) {
-        if (sync_alloc) cudaFree(h->temp_state);
-        else Q4_CUDA(cudaFreeAsync(h->temp_state, s), "cudaFreeAsync(temp_state)");
-        h->device_bytes -= h->temp_state_elems * 2;
-        h->temp_state = nullptr;
-        h->temp_state_elems = 0;
-    }
-    void *v = nullptr;
-    cudaError_t e = sync_alloc ? cudaMalloc(&v, need * 2) : cudaMallocAsync(&v, need * 2, s);
-    if (e != cudaSuccess) return cuda_fail(e, "allocating temp_state");
-    h->temp_state = static_cast<uint16_t *>(v);
-    h->temp_state_elems = need;
-    h->device_bytes += need * 2;
-    return GPTQ_Q4_OK;
+    if (!(h->act_order || h->act_bf16 || h->act_f32)) return GPTQ_Q4_OK;
+    if (h->act_bf16 || h->act_f32)
+        if (int r = ensure_buffer(h, &h->rowscale, &h->rowscale_bytes, static_cast<size_t>(M) * sizeof(float), s,
+                                  sync_alloc, "allocating row scales"))
+            return r;
+    return ensure_buffer(h, &h->temp_state, &h->temp_state_bytes, static_cast<size_t>(M) * h->K * 2, s, sync_alloc,
+                         "allocating temp_state");
 }
 
 // fp32 activations: room for the raw fp32 sums of 2M rows
 int ensure_part(gptq_q4_s *h, size_t elems, cudaStream_t s, bool sync_alloc) {
-    if (elems <= h->part_elems) return GPTQ_Q4_OK;
-    if (h->part) {
-        if (sync_alloc) cudaFree(h->part);
-        else Q4_CUDA(cudaFreeAsync(h->part, s), "cudaFreeAsync(partial rows)");
-        h->device_bytes -= h->part_elems * sizeof(float);
-        h->part = nullptr;
-        h->part_elems = 0;
-    }
-    void *v = nullptr;
-    cudaError_t e = sync_alloc ? cudaMalloc(&v, elems * sizeof(float)) : cudaMallocAsync(&v, elems * sizeof(float), s);
-    if (e != cudaSuccess) return cuda_fail(e, "allocating the fp32 partial rows");
-    h->part = static_cast<float *>(v);
-    h->part_elems = elems;
-    h->device_bytes += elems * sizeof(float);
-    return GPTQ_Q4_OK;
+    return ensure_buffer(h, &h->part, &h->part_bytes, elems * sizeof(float), s, sync_alloc,
+                         "allocating the fp32 partial rows");
 }
 
 int decode_max_ws_rows() { return 16; }
@@ -686,7 +632,8 @@ static int run_path(gptq_q4_handle h, const q4::HandleView &v, const uint16_t *x
         case Kern::Reg: {
             const q4::DecodePlan p = q4::plan_decode(M, h->K, h->N, h->geff);
             if (int r = ensure_decode_work(h, p.ws_floats, p.n_tickets, stream, false)) return r;
-            q4::DecodeWork w{h->ws, h->ws_floats, h->tickets, h->n_tickets};
+            q4::DecodeWork w{h->ws, h->ws_bytes / sizeof(float), h->tickets,
+                             static_cast<int>(h->tickets_bytes / sizeof(int))};
             Q4_CUDA(q4::launch_decode(v, p, w, xin, M, out, stream), "decode launch");
             break;
         }
@@ -1039,7 +986,7 @@ void api_free_retired(Retired &old) {
         delete n;
     }
 }
-cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync) {
+cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync, bool zero) {
     // A stream-ordered allocation on a capturing stream would belong to the graph, and calls outside it would use
     // memory that is there only while the graph runs: an ordinary allocation serves both.
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
@@ -1055,6 +1002,14 @@ cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cu
     if (e && size > need) {
         cudaGetLastError();
         e = allocate(size = need);
+    }
+    if (!e && zero) {
+        cudaStream_t own = nullptr;                  // a capturing stream would clear it at every replay, and not now
+        if (captured) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+        if (!e) e = sync ? cudaMemset(p, 0, size) : cudaMemsetAsync(p, 0, size, captured ? own : s);
+        if (!e && captured) e = cudaStreamSynchronize(own);
+        if (own) cudaStreamDestroy(own);
+        if (e) sync || captured ? cudaFree(p) : cudaFreeAsync(p, s);
     }
     if (!e && !api_retire(old, *buf)) {
         sync || captured ? cudaFree(p) : cudaFreeAsync(p, s);

@@ -30,11 +30,11 @@ struct gptq_q4_s {
     uint16_t *bias = nullptr;
     int *status = nullptr;
     float *ws = nullptr;
-    size_t ws_floats = 0;
+    size_t ws_bytes = 0;
     int *tickets = nullptr;
-    int n_tickets = 0;
+    size_t tickets_bytes = 0;
     uint16_t *temp_state = nullptr;
-    size_t temp_state_elems = 0;
+    size_t temp_state_bytes = 0;
     int path = GPTQ_Q4_PATH_AUTO;
     int prefill_min_m = 0;
     int zero_offset = 1;    // GPTQ_Q4_FORMAT_GPTQ: effective zero = stored + 1
@@ -43,10 +43,11 @@ struct gptq_q4_s {
     int act_bf16 = 0;       // x and out are bf16 (GPTQ_Q4_DTYPE_BF16)
     int act_f32 = 0;        // x and out are fp32 (GPTQ_Q4_DTYPE_FP32)
     float *rowscale = nullptr;  // bf16 / fp32: 2^e per row of the current call
-    size_t rowscale_elems = 0;
+    size_t rowscale_bytes = 0;
     float *part = nullptr;      // fp32: the raw sums of the hi and lo rows, [2M][N]
-    size_t part_elems = 0;
-    size_t device_bytes = 0;
+    size_t part_bytes = 0;
+    q4::Retired retired;        // replaced ones of these work buffers
+    size_t device_bytes = 0;    // the replaced ones among them
 };
 
 namespace q4 {
@@ -58,8 +59,9 @@ HandleView api_view(const gptq_q4_s *h);
 void api_count_launches(int n);
 // Puts a buffer of at least `need` bytes in the place of *buf (*bytes large), which is retired; the contents are not
 // kept.  sync: exactly `need`, at once; else by stream order, and twice the old size where there is room, so that
-// the retired ones add up to no more than the present one.  On an error nothing has changed.
-cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync);
+// the retired ones add up to no more than the present one.  zero: filled with zeros.  On an error nothing has changed.
+cudaError_t api_replace(Retired &old, void **buf, size_t *bytes, size_t need, cudaStream_t s, bool sync,
+                        bool zero = false);
 // Keeps p until the handle is freed; false if there is no host memory for that.
 bool api_retire(Retired &old, void *p);
 void api_free_retired(Retired &old);

@@ -51,6 +51,11 @@
  *     gptq_q4_device_error, which synchronize as stated.
  *   - A handle may be used from one stream at a time (its workspaces are
  *     reused by every call).  Distinct handles are independent.
+ *   - A work buffer that a call outgrows is replaced by one of at least twice
+ *     its size (where there is room), by stream order; on a capturing stream by
+ *     an ordinary allocation, which is no part of the graph.  The replaced ones
+ *     stay allocated until the handle is freed, so that graphs captured before
+ *     go on running; they add up to no more than the present buffer.
  */
 #ifndef GPTQ_Q4_H
 #define GPTQ_Q4_H
@@ -146,7 +151,8 @@ int gptq_q4_set_bias(gptq_q4_handle h, const uint16_t *bias);
  * act-order activation buffer temp_state [max_m][K] fp16 and the split-K
  * partial sums.  The counterpart of the Lorax page's create_exllama_buffers
  * (max_total_tokens).  A later gptq_q4_matmul with more rows grows the buffers
- * itself (stream-ordered allocation on the caller's stream); calling this
+ * itself (stream-ordered allocation on the caller's stream; the smaller ones
+ * stay until the handle is freed); calling this
  * first keeps allocation out of gptq_q4_matmul.  Synchronizes the device.
  * Errors: INVALID_ARGUMENT (NULL handle, max_m < 0), OUT_OF_MEMORY. */
 int gptq_q4_reserve(gptq_q4_handle h, int max_m);
