@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto store = [&](int n, int h, float x, float y, float inv) {
             const int r = g + 8 * h;
             if (r >= rows) return;
+            if (inv == 0.f) x = y = 0.f;                     // a row that sees nothing, beside whatever the values hold
             const int rr = r_first + r, t = a.p.group(rr);
             *reinterpret_cast<uint32_t *>(a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                                           (it.head * group + rr - t * group) * D + 8 * n + 2 * t4) =

@@ -492,6 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) acc[e] += x[e] * f;
                         }
+                        // a row that sees nothing, beside whatever the values hold (no such row is in an item of few
+                        // rows that is cut: the last of them sees fewer keys than there are rows)
+                        if (sum == 0.f)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
                         if (valid) store(acc, inv, q);
                     }
                 }

@@ -245,6 +245,30 @@ def test_rising_and_extreme_scores(q4, lens, dtype):
     att.device_error()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("max_q", [1, 100000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_see_nothing_beside_values_without_number(q4, D, max_q, bad):
+    """More new tokens than context, and no number in a value that only the later ones see: the first ones' outputs
+    are zeros, in items of one CTA and in those that two share (of 300 tokens, at two key tiles a CTA)."""
+    Hq, Hkv, page, dtype = 4, 4, 16, torch.bfloat16
+    lens = [(9, 4), (300, 290), (1510, 1500), (70, 66), (4, 4)]
+    step = Step(q4, lens, Hkv, D, page, dtype, seed=17)
+    for b, at in ((0, 3), (1, 4), (1, 200), (1, 289), (2, 4), (2, 1499), (3, 60)):
+        step.cache.v[int(step.table[b, at // page]), :, at % page] = bad
+    q = torch.randn(step.tokens, Hq, D, generator=torch.Generator().manual_seed(16)).to(dtype)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    out = att.attend(q.to(DEV), step.cache, step.make_batch(q4, max_q)).cpu()
+    for b, (ql, kv) in enumerate(lens):
+        rows = out[step.cu[b]:step.cu[b] + ql]
+        assert (rows[:ql - kv] == 0).all(), b                # they see nothing
+        if b == 4:
+            assert torch.isfinite(rows).all()                # another request's values are not its own
+        else:
+            assert not torch.isfinite(rows[-1]).any(), b
+    att.device_error()
+
+
 @pytest.mark.parametrize("max_q", [1, 100000])
 def test_cache_past_32_bit_offsets(q4, max_q):
     """Pages that begin more than 2^32 bytes into the cache."""
