@@ -31,12 +31,26 @@ _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _add = _lib.gptq_q4_lora_add
 
 
-def _rows(t, what: str, width: int, dtype, device):
-    """`t` as rows of `width` elements, dense within a row: (tensor [rows, width], row stride)."""
+def _flat(t, what: str, width: int, written: bool):
+    """`t`, not of two dimensions, as [rows, width]; a copy only where it is not written to."""
+    n, at = 1, t.dim()
+    while at and n < width:                              # the last dimensions that make up a row
+        at -= 1
+        n *= t.shape[at]
+    if n != width and not (t.dim() == 1 and n % width == 0):
+        _refuse(f"{what} {tuple(t.shape)} does not end in rows of {width} elements")
+    flat = t.reshape(-1, width)
+    if written and flat.data_ptr() != t.data_ptr():
+        _refuse(f"{what} {tuple(t.shape)} cannot be viewed as rows")
+    return flat
+
+
+def _rows(t, what: str, width: int, dtype, device, written: bool = False):
+    """`t` as rows of `width` elements, dense within a row: (tensor [rows, width], rows, row stride)."""
     if t.dtype != dtype or t.device != device:
         _refuse(f"{what} is {t.dtype} on {t.device}: {dtype} on {device} is wanted")
     if t.dim() != 2:
-        t = t.reshape(-1, width) if t.dim() else t.reshape(1, -1)
+        t = _flat(t, what, width, written)
     rows, have = t.shape
     stride, inner = t.stride()
     if have != width:
@@ -86,10 +100,8 @@ class LoraPool:
             out = torch.empty(y.shape, dtype=dtype, device=device)
             at, mo, os_ = out.data_ptr(), my, self.N
         else:
-            o2, mo, os_ = _rows(out, "out", self.N, dtype, device)
+            o2, mo, os_ = _rows(out, "out", self.N, dtype, device, written=True)
             at = o2.data_ptr()
-            if at != out.data_ptr():
-                _refuse("out cannot be viewed as rows")
         if my != M or mo != M or row_slot.numel() != M:
             _refuse(f"x has {M} rows, y {my}, out {mo}, row_slot {row_slot.numel()}")
         if row_slot.dtype != torch.int32 or row_slot.device != device or not row_slot.is_contiguous():

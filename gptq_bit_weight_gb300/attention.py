@@ -108,7 +108,7 @@ class PagedAttention:
             q_out = torch.empty((rows, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
             q, q_rows, qs = q_out, rows, self._q_width
         else:
-            q, q_rows, qs = self._token_rows(q_out, "q_out")
+            q, q_rows, qs = self._token_rows(q_out, "q_out", written=True)
         if rows != batch.tokens or q_rows != batch.tokens:
             _refuse(f"qkv has {rows} rows and q_out {q_rows}, the batch {batch.tokens} tokens")
         if positions is not None and (positions.dtype != torch.int32 or positions.device != self.device or
@@ -128,17 +128,17 @@ class PagedAttention:
             out = torch.empty((rows, self.q_heads, self.head_dim), dtype=self.dtype, device=self.device)
             o, o_rows, os_ = out, rows, self._q_width
         else:
-            o, o_rows, os_ = self._token_rows(out, "out")
+            o, o_rows, os_ = self._token_rows(out, "out", written=True)
         if rows != batch.tokens or o_rows != batch.tokens:
             _refuse(f"q has {rows} rows and out {o_rows}, the batch {batch.tokens} tokens")
         _check(_attend(self.handle, x.data_ptr(), xs, cache.ref, batch.ref, self._scale if scale is None else scale,
                        window, o.data_ptr(), os_, _stream(self.device.index)))
         return out
 
-    def _token_rows(self, t, what: str):
+    def _token_rows(self, t, what: str, written: bool = False):
         """[tokens, q_heads, head_dim] (a view of wider rows allowed) or [tokens, q_heads * head_dim]."""
         if t.dim() != 3:
-            return _rows(t, what, self._q_width, self.dtype, self.device)
+            return _rows(t, what, self._q_width, self.dtype, self.device, written)
         rows, heads, width = t.shape
         stride, s1, s2 = t.stride()
         if heads != self.q_heads or width != self.head_dim or s1 != width or s2 != 1:

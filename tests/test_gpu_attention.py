@@ -634,6 +634,36 @@ def test_decode_loop_matches_one_prompt(q4):
     att.device_error()
 
 
+def test_results_go_where_they_were_asked_for(q4):
+    """Outputs of more dimensions are written in place, or refused where their rows do not lie in a row each (they
+    were computed into a copy); inputs of any layout are taken, but not other shapes with as many elements."""
+    Hq, Hkv, D, page, dtype = 4, 2, 64, 16, torch.float16
+    step = Step(q4, [(2, 30), (4, 9)], Hkv, D, page, dtype, seed=18)
+    qkv = torch.randn(6, (Hq + 2 * Hkv) * D, generator=torch.Generator().manual_seed(17)).to(dtype).to(DEV)
+    q = qkv[:, :Hq * D].reshape(6, Hq, D)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    att.append(qkv, step.cache, step.batch)
+    want = att.attend(q, step.cache, step.batch)
+    for shape in ((2, 3, Hq, D), (1, 6, Hq * D // 2, 2), (6, Hq * D)):
+        out = torch.full(shape, float("nan"), dtype=dtype, device=DEV)
+        assert att.attend(q, step.cache, step.batch, out=out) is out and torch.equal(out.view_as(want), want)
+        out.fill_(float("nan"))
+        assert att.append(qkv, step.cache, step.batch, q_out=out) is out and torch.equal(out.view_as(q), q)
+    apart = torch.zeros(3, 2, Hq, D, dtype=dtype, device=DEV).transpose(0, 1)       # rows in another order
+    assert torch.equal(att.attend(apart.copy_(q.view(2, 3, Hq, D)), step.cache, step.batch), want)
+    for f in (lambda: att.attend(q, step.cache, step.batch, out=apart),
+              lambda: att.append(qkv, step.cache, step.batch, q_out=apart),
+              lambda: att.attend(q.view(6, 1, 2 * Hq, D // 2).transpose(2, 3), step.cache, step.batch, out=apart)):
+        with pytest.raises(q4.GPTQ4Error) as e:
+            f()
+        assert e.value.status == q4.GPTQ_Q4_INVALID_ARGUMENT
+    for shape in ((3, 2, Hq * D // 3), (12, 1, Hq * D // 2 + 1), (7, 3, 5, 2)):
+        with pytest.raises(q4.GPTQ4Error) as e:
+            att.append(torch.zeros(shape, dtype=dtype, device=DEV), step.cache, step.batch)
+        assert e.value.status == q4.GPTQ_Q4_INVALID_ARGUMENT
+    att.device_error()
+
+
 def test_refusals(q4):
     bad, no = q4.GPTQ_Q4_INVALID_ARGUMENT, q4.GPTQ_Q4_UNSUPPORTED
 

@@ -312,6 +312,31 @@ def test_beside_the_quantised_projection(q4):
     check(pool.add(x.to(DEV), rows.to(DEV), y), ref, tol, "beside the projection")
 
 
+def test_shapes_of_more_dimensions(q4):
+    """x [.., K] and y [.., N] of any leading dimensions; another shape with as many elements is refused, not read as
+    other rows."""
+    K, N, dtype = 64, 96, torch.float16
+    g = torch.Generator().manual_seed(18)
+    ads = adapters(g, [8], K, N, dtype)
+    pool = pool_of(q4, ads, K, N, 1, 8, dtype)
+    x, y = torch.randn(6, K, generator=g).to(dtype).to(DEV), torch.randn(6, N, generator=g).to(dtype).to(DEV)
+    rows = torch.zeros(6, dtype=torch.int32, device=DEV)
+    want = pool.add(x, rows, y)
+    got = pool.add(x.view(2, 3, K), rows, y.view(3, 1, 2, N))
+    assert got.shape == (3, 1, 2, N) and torch.equal(got.view(6, N), want)
+    assert torch.equal(pool.add(x.view(6, 8, 8), rows, y.view(6, 4, 24)).view(6, N), want)     # heads of a row
+    assert torch.equal(pool.add(x[0], rows[:1], y[0]), want[0])
+    assert torch.equal(pool.add(x.view(-1), rows, y), want)
+    apart = y.view(2, 3, N).transpose(0, 1).contiguous().transpose(0, 1)                       # rows in another order
+    assert torch.equal(pool.add(x, rows, apart).view(6, N), want)
+    for args in ((x.view(3, 4, K // 2), rows, y), (x.view(3, 2, 2, K // 2), rows[:4], y), (x, rows, y.view(2, 6, N // 2)),
+                 (x[:5].reshape(-1)[:-1], rows[:5], y[:5]), (x, rows, y, apart)):
+        with pytest.raises(q4.GPTQ4Error) as e:
+            pool.add(*args)
+        assert e.value.status == q4.GPTQ_Q4_INVALID_ARGUMENT
+    pool.device_error()
+
+
 def captured(f):
     """f() captured into a graph, after one call outside it."""
     side = torch.cuda.Stream()
