@@ -54,8 +54,10 @@ int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache *c, const gptq_q4_ba
     if (b->batch > kMaxBatch)
         return api_failf(GPTQ_Q4_UNSUPPORTED, "batch=%d: at most %d requests in a call", b->batch, kMaxBatch);
     if (b->batch == 0 || b->tokens == 0) return GPTQ_Q4_OK;
-    if (!b->cu_q || !b->kv_len || !b->table || !aligned4(b->cu_q) || !aligned4(b->kv_len) || !aligned4(b->table))
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "cu_q, kv_len and table must be 4-byte aligned and not NULL");
+    if (!b->cu_q || !b->kv_len || (b->width && !b->table) || !aligned4(b->cu_q) || !aligned4(b->kv_len) ||
+        !aligned4(b->table))
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "cu_q, kv_len and (unless its width is 0) table must be 4-byte aligned and not NULL");
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "the cache's k and v must be 16-byte aligned and not NULL");
     const int64_t page = static_cast<int64_t>(h->shape.hkv) * h->shape.page * h->shape.d;

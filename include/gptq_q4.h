@@ -510,6 +510,7 @@ typedef struct {
  *   kv_len device int32 [batch], each 0 .. width * page_size, at most 2^30
  *   table  device int32 [batch][width], table_stride elements from row to row;
  *          only entries of pages that a call reads or writes have to be valid
+ *          (NULL if width is 0: contexts without a token)
  *   max_q  no request has more new tokens (a larger number is allowed and
  *          changes no result, only which kernel runs)
  * The arrays are read on the GPU when the call runs.  A length or page index

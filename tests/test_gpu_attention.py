@@ -634,6 +634,28 @@ def test_decode_loop_matches_one_prompt(q4):
     att.device_error()
 
 
+@pytest.mark.parametrize("max_q", [1, 100000])
+def test_contexts_without_a_page(q4, max_q):
+    """A table of no columns: no row sees anything, and a token has no place to go."""
+    Hq, Hkv, D, page, dtype = 4, 2, 64, 16, torch.float16
+    i32 = torch.int32
+    k = torch.full((2, Hkv, page, D), float("nan"), dtype=dtype, device=DEV)
+    cache = q4.PagedCache(k, k.clone())
+    batch = q4.PagedBatch(torch.tensor([0, 5, 5, 6], dtype=i32, device=DEV), torch.zeros(3, dtype=i32, device=DEV),
+                          torch.empty(3, 0, dtype=i32, device=DEV), tokens=7, max_q=max_q)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    out = torch.full((7, Hq, D), 5.0, dtype=dtype, device=DEV)
+    att.attend(torch.ones_like(out), cache, batch, out=out)
+    assert (out[:6] == 0).all() and (out[6] == 5).all()
+    att.device_error()
+    q = torch.full_like(out, 5.0)
+    att.append(torch.ones(7, (Hq + 2 * Hkv) * D, dtype=dtype, device=DEV), cache, batch, q_out=q)
+    assert (q == 5).all() and torch.isnan(cache.k).all() and torch.isnan(cache.v).all()
+    with pytest.raises(q4.GPTQ4Error) as e:
+        att.device_error()
+    assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
+
+
 def test_results_go_where_they_were_asked_for(q4):
     """Outputs of more dimensions are written in place, or refused where their rows do not lie in a row each (they
     were computed into a copy); inputs of any layout are taken, but not other shapes with as many elements."""
