@@ -28,12 +28,18 @@ class PagedCache:
     def __init__(self, k, v):
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or not k.is_cuda:
             _refuse("k and v must be CUDA tensors [pages, kv_heads, page_size, head_dim] of one shape and type")
-        inner = (k.shape[2] * k.shape[3], k.shape[3], 1)
-        if k.stride()[1:] != inner or v.stride()[1:] != inner or k.stride(0) != v.stride(0):
-            _refuse("k and v must be dense within a page, with one stride from page to page")
+        pages, heads, page, width = k.shape
+        strides = []
+        for t in (k, v):                     # a dimension of one has no stride of its own
+            s = t.stride()
+            if s[3] != 1 or s[2] != width or (heads > 1 and s[1] != page * width):
+                _refuse("k and v must be dense within a page")
+            strides.append(s[0] if pages > 1 else heads * page * width)
+        if strides[0] != strides[1]:
+            _refuse("k and v must have one stride from page to page")
         self.k, self.v = k, v
         self.kind = (k.dtype, k.device, *k.shape[1:])
-        self.struct = gptq_q4_cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.stride(0))
+        self.struct = gptq_q4_cache(k.data_ptr(), v.data_ptr(), pages, strides[0])
         self.ref = ctypes.byref(self.struct)
 
 
@@ -45,7 +51,8 @@ class PagedBatch:
 
     def __init__(self, cu_q, kv_len, table, tokens: int, max_q: int | None = None):
         for t, what in ((cu_q, "cu_q"), (kv_len, "kv_len"), (table, "table")):
-            if t.dtype != torch.int32 or not t.is_cuda or t.device != cu_q.device or (t.numel() and t.stride(-1) != 1):
+            if t.dtype != torch.int32 or not t.is_cuda or t.device != cu_q.device or \
+                    (t.dim() and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1):
                 _refuse(f"{what} must be int32 on the GPU, dense in its last dimension")
         batch = kv_len.numel()
         if cu_q.dim() != 1 or kv_len.dim() != 1 or cu_q.numel() != batch + 1 or table.dim() != 2 or \
@@ -141,7 +148,7 @@ class PagedAttention:
             return _rows(t, what, self._q_width, self.dtype, self.device, written)
         rows, heads, width = t.shape
         stride, s1, s2 = t.stride()
-        if heads != self.q_heads or width != self.head_dim or s1 != width or s2 != 1:
+        if heads != self.q_heads or width != self.head_dim or (s1 != width and heads > 1) or s2 != 1:
             _refuse(f"{what} {tuple(t.shape)} must be [tokens, {self.q_heads}, {self.head_dim}], dense in a token")
         if t.dtype != self.dtype or t.device != self.device:
             _refuse(f"{what} is {t.dtype} on {t.device}: {self.dtype} on {self.device} is wanted")

@@ -634,6 +634,39 @@ def test_decode_loop_matches_one_prompt(q4):
     att.device_error()
 
 
+def test_dimensions_of_one_have_any_stride(q4):
+    """One head, one page or one request, cut out of tensors that give such a dimension another stride."""
+    D, page, dtype = 64, 16, torch.float16
+    g = torch.Generator().manual_seed(19)
+    i32 = torch.int32
+    new = lambda *s: torch.randn(*s, generator=g).to(dtype).to(DEV)                    # noqa: E731
+    att = q4.PagedAttention(1, 1, D, page, dtype=dtype)
+    one, lens = torch.tensor([0, 3], dtype=i32, device=DEV), torch.tensor([[13, 1], [9, 1]], dtype=i32, device=DEV)
+    q, k, v = new(1, 3, D), new(1, page, 1, D), new(1, page, 1, D)
+    dense = q4.PagedCache(k.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous())
+    table = torch.zeros(1, 1, dtype=i32, device=DEV)
+    want = att.attend(q[0][:, None].contiguous(), dense, q4.PagedBatch(one, lens[0, :1].contiguous(), table, 3))
+    # one key/value head between the tokens and their elements; one page, of keys and values that lie apart
+    caches = [q4.PagedCache(k.transpose(1, 2), v.transpose(1, 2)),
+              q4.PagedCache(k.transpose(1, 2).as_strided((1, 1, page, D), (8, D, D, 1)),
+                            torch.stack([v, v], 1)[:, 1].transpose(1, 2))]
+    # one query head; a request's length out of a column, its table's only column out of a row
+    batches = [q4.PagedBatch(one, lens[:1, 0], table.expand(7, 1)[:1], 3),
+               q4.PagedBatch(one, lens.t()[:1, 0], torch.zeros(1, 9, dtype=i32, device=DEV).t()[:1], 3)]
+    for cache in caches:
+        for batch in batches:
+            assert torch.equal(att.attend(q.transpose(0, 1), cache, batch), want)
+    out = torch.zeros(1, 3, D, dtype=dtype, device=DEV)
+    att.attend(q.transpose(0, 1), caches[0], batches[0], out=out.transpose(0, 1))
+    assert torch.equal(out[0], want[:, 0])
+    two = new(3, 2, page, D)
+    for a, b in ((two[:, :, :, :32], two[:, :, :, :32]), (two[:, :, ::2], two[:, :, ::2]), (two[::2], two[:2]),
+                 (two.transpose(0, 1), two.transpose(0, 1))):
+        with pytest.raises(q4.GPTQ4Error):
+            q4.PagedCache(a, b)
+    att.device_error()
+
+
 @pytest.mark.parametrize("max_q", [1, 100000])
 def test_contexts_without_a_page(q4, max_q):
     """A table of no columns: no row sees anything, and a token has no place to go."""
