@@ -591,8 +591,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 LoraTcPlan plan_lora_tc(const LoraView &v, int M, int sms) {
     LoraTcPlan p;
     p.ok = v.rpad <= kCap && v.rpad <= kShrinkCap;
-    // Passes over a tile's output while there can be three at most.  8 adapters of 64 ranks, 8192 x 10240: 800 rows in 6
-    // runs 26 us, 29 with marked tiles; rows that mix them 72 and 55.  32 adapters: 27 and 30, 260 and 100.
+    // Passes over a tile's output where it can hold few adapters: five passes at most (adapters of 96 ranks, one to a
+    // pass; four of 64 ranks), and one more for each adapter with an infinity or NaN in B.  Marked tiles are the
+    // faster way where rows do mix the adapters, and slower where they come in runs, which only the GPU knows.  8
+    // adapters of 64 ranks, 8192 x 10240: 800 rows in 6 runs 26 us, 29 with marked tiles; rows that mix them 72 and 55.
+    // 32 adapters: 27 and 30, 260 and 100.
     p.marks = std::min(kTile, v.slots) * v.rpad > 512;
     p.tiles = (M + kTile - 1) / kTile;
     const int blocks = (v.K + 63) / 64;

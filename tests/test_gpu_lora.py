@@ -161,6 +161,36 @@ def test_a_prompt_beside_single_tokens(q4, dtype):
     pool.device_error()
 
 
+@pytest.mark.parametrize("ranks", [[96] * 5, [64] * 8, [112, 97, 100, 128], [176, 161], [16] * 32, [48] * 10],
+                         ids=lambda r: f"{len(r)}x{max(r)}")
+def test_tiles_that_take_passes(q4, ranks):
+    """Rows of a pool that is served by passes over a tile's output mix all its adapters; then some of those have no
+    number in B, which takes a pass for each."""
+    K, N, M, dtype = 264, 392, 700, torch.float16
+    assert len(ranks) * ((max(ranks) + 15) // 16 * 16) <= 512
+    g = torch.Generator().manual_seed(19)
+    ads = adapters(g, ranks, K, N, dtype)
+    rows = torch.randint(-1, len(ranks), (M,), generator=g, dtype=torch.int32)
+    x, y = torch.randn(M, K, generator=g).to(dtype), torch.randn(M, N, generator=g).to(dtype)
+    ref, tol = reference(x, y, rows, ads, K)
+    xd, yd, rd = x.to(DEV), y.to(DEV), rows.to(DEV)
+    pool = pool_of(q4, ads, K, N, len(ranks), max(ranks), dtype)
+    out = pool.add(xd, rd, yd)
+    check(out, ref, tol, "mixed")
+    assert torch.equal(pool.add(xd, rd, yd, out=yd.clone()), out)
+    broken = list(range(0, len(ranks), 2))
+    for s in broken:
+        ads[s][1][5, 1] = float("nan")
+        pool.set(s, ads[s][0].to(DEV), ads[s][1].to(DEV), ads[s][2])
+    out = pool.add(xd, rd, yd).cpu()
+    whole = ~torch.isin(rows, torch.tensor(broken, dtype=torch.int32))
+    check(out[whole], ref[whole], tol[whole], "beside broken adapters")
+    fine = torch.arange(N) != 5
+    check(out[:, fine], ref[:, fine], tol[:, fine], "their other columns")
+    assert torch.isnan(out[~whole][:, 5]).all()
+    pool.device_error()
+
+
 @pytest.mark.parametrize("M", [2, 40, 300])
 def test_strided_columns_of_a_fused_projection(q4, M):
     """One part of a fused projection: columns of a wider y, x a view of wider rows, on a side stream."""
