@@ -602,8 +602,11 @@ int gptq_q4_attn_append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, con
  * rounded once.  Rows that no request owns are left alone.  The order of the
  * sums depends on the lengths of the whole batch, not on timing: the same
  * call gives the same bits.  A NaN or infinity in a key reaches the rows that
- * see it; one in a value may reach earlier new tokens of the same chunk too
- * (their weight for it is 0, and 0 times it is NaN).  A call of more than 2^31
+ * see it.  One in a value reaches those, and may reach new tokens of the same
+ * request that do not see it but share a tile with one that does (256 rows of
+ * a key/value head, a row being a token for one query head): earlier ones of
+ * the chunk and, with a window, later ones (their weight for it is 0, and 0
+ * times it is NaN).  A call of more than 2^31
  * tiles of work (a prompt of over a million tokens at once) is not done and
  * reported by gptq_q4_attn_device_error.  Errors: INVALID_ARGUMENT (NULL, sizes, strides,
  * alignment, scale not finite, window < 0), UNSUPPORTED (batch > 4096),

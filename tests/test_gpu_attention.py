@@ -269,6 +269,27 @@ def test_rows_that_see_nothing_beside_values_without_number(q4, D, max_q, bad):
     att.device_error()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("max_q,tile", [(1, 16), (100000, 256)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_without_number_stay_in_their_tiles(q4, D, max_q, tile, window, bad):
+    """A NaN or infinity in one value: rows that see it have no number, rows of other tiles (tokens, at one query head
+    for each key/value head) and of other requests and heads are right."""
+    Hq, Hkv, page, dtype, at = 2, 2, 16, torch.float16, 300
+    step = Step(q4, [(600, 600), (9, 500)], Hkv, D, page, dtype, seed=20)
+    q = torch.randn(step.tokens, Hq, D, generator=torch.Generator().manual_seed(18)).to(dtype)
+    ref, tol = attention_reference(step, q, D ** -0.5, window)
+    step.cache.v[int(step.table[0, at // page]), 1, at % page] = bad
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    out = att.attend(q.to(DEV), step.cache, step.make_batch(q4, max_q), window=window).cpu()
+    end = at + window if window else 600                  # the first row that no longer sees it
+    assert not torch.isfinite(out[at:end, 1]).any()
+    ref[at // tile * tile:min(-(-end // tile) * tile, 600), 1] = float("nan")       # no claim for the rest of the tiles
+    check(out, ref, tol, f"beside {bad}")
+    att.device_error()
+
+
 @pytest.mark.parametrize("max_q", [1, 100000])
 def test_cache_past_32_bit_offsets(q4, max_q):
     """Pages that begin more than 2^32 bytes into the cache."""
