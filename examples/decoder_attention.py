@@ -45,7 +45,7 @@ class DecoderAttention:
         self.attention.set_rope(head_dim, max_pos, base=500000.0, scaling="bands", factor=8.0, original=8192)
 
     def reserve(self, rows):
-        """Size every workspace for steps of up to `rows` tokens (needed before a graph is captured)."""
+        """Size every workspace for steps of up to `rows` tokens, so that no step allocates."""
         for part in (self.qkv, self.o, self.qkv_adapters, self.o_adapters):
             part.reserve(rows)
 

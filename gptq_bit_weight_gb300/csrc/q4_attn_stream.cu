@@ -9,6 +9,10 @@
 //   scores s = scale log2(e) q . k in fp32; running maximum m and sum l,
 //   p = 2^(s - m) rounded to 16 bits for its product with v (l sums the
 //   unrounded ones), o = sum p v in fp32; o / l rounded once.
+//   One 16-bit part of p, as in the kernel for chunks, where a second would cost:
+//   either kernel rounds alike.  The result's error against 64 bits is 1.04 to
+//   1.08 times that of rounding the exact result (relative, bf16 1.7e-3, fp16
+//   2.2e-4).
 //
 // One CTA per SM.  Warps 8 and 9 load key tiles of 128 tokens by TMA, keys and
 // values, one box for each page and 64 columns, into a ring of half-stages

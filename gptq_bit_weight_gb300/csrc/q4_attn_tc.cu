@@ -7,6 +7,10 @@
 //   once.  m is the maximum of the row's first key tile, and is raised to a
 //   later tile's only when that is more than 2^8 away: any m gives the same
 //   result as long as p fits 16 bits, so most tiles rescale no output.
+//   The tensor cores take 16-bit operands: p in two parts would be half as much
+//   again of the whole work.  In one, the result's error against 64 bits is 1.4
+//   times that of rounding the exact result (relative, 512 tokens over 8192:
+//   bf16 2.3e-3 and 1.7e-3; 384 over 4096, fp16: 2.8e-4 and 2.1e-4).
 //
 // One CTA per SM works on two tiles of up to 128 rows at a time (row = token x
 // query head of the group, so the heads that share a key/value head share its
@@ -23,15 +27,19 @@
 //                   at the edges: such slots hold anything, and 0 x NaN is NaN
 // Two row tiles, because one alone leaves the tensor cores idle during its
 // softmax; 184 registers for the softmax threads (a row of 128 scores each) and
-// 136 for the others add up to the launch's 384 x 168 (with 208 and 88 the
-// loaders and the issuer spill: 32 requests of 4 tokens 58 us instead of 54.5).
+// 136 for the others add up to the launch's 384 x 168.  The compiler keeps to
+// 168 for all roles: the softmax's loop over key tiles spills (456 bytes of
+// stores and 520 of loads; without the loop there are none), whatever the split
+// leaves it; with 208 and 88 the other roles spill as well (604 and 648; 32
+// requests of 4 tokens 58 us instead of 54.5).
 // 4096 tokens over 16384, 64 heads over 8 of 128: 1120 us, 1.7 PFLOP/s, what the
 // tensor cores sustain under the power limit; 512 over 8192: 98 us (1.36
 // PFLOP/s: start, last wave and the join of the pieces); 384 together with 47
 // single tokens of others: 111 us (a key tile is 1.8 us with two row tiles, 1.3
 // with one).  Heads of 64, 4096 over 16384, 32 over 8: 463 us, bound by the
-// softmax warps' own chain (with columns of their own for the weights, so that
-// the next scores never wait for the second product: 503).
+// softmax warps' own chain as it is compiled, spills among it (with columns of
+// their own for the weights, so that the next scores never wait for the second
+// product: 503).
 // Every wait is bounded; a wait that runs out sets a status bit and its role
 // goes on without waiting.
 #include <cuda.h>

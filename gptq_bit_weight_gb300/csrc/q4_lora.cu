@@ -16,7 +16,9 @@
 // take 19.4 us where the bytes would take 6.2.  The first launch is done after
 // 7.4 (2 to find the rows' adapters, 3 for its loads, 2 to join its sums); the
 // second's CTAs find registers as the first's end, and have 4 to 5 units a
-// warp at about 1 us, a load from L2 and its products.  Tried and slower: B
+// warp at about 1 us, a load from L2 and its products, one unit after the other.
+// At two CTAs for each SM, 128 registers, both spill (the first 52 to 60 bytes
+// of stores, its form for 16 rows none; the second 60 to 72).  Tried and slower: B
 // copied ahead through shared memory (24 us: the copies' instructions cost more
 // than the loads), one CTA for each SM in the first launch (20.6), B prefetched
 // by the first launch (20.8).  A single row of a small adapter is one launch

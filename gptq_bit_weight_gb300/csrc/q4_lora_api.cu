@@ -173,10 +173,12 @@ int gptq_q4_lora_add(gptq_q4_lora h, const void *x, int64_t x_stride, const int3
     if (int r = ensure_rows(h, static_cast<size_t>(M), stream, false)) return r;
     const q4::LoraCall c{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(y),
                          static_cast<uint16_t *>(out), row_slot, x_stride, y_stride, out_stride, M, M, nullptr};
-    // Tiles of 128 rows from 321 rows on, except for the highest ranks, which do not fit them.  Measured at rank 64:
-    // 8192 x 28672, 128 rows of one adapter 19 us by chunks, 20 by tiles; 256 rows of 4 runs 32 and 27; 1024 rows 96
-    // and 37; 643 rows of 6 runs at 28672 x 8192 166 and 42.  8192 x 10240, rows that mix 32 adapters: 400 rows 36 and
-    // 66, 800 rows 59 and 100; in 6 runs 31 and 25, 65 and 31.
+    // Tiles of 128 rows from 321 rows on, for pools whose adapters fit a tile's pass (up to 176 ranks).  Only the GPU
+    // knows how the rows lie: this many are taken to be prompts, whose rows come in runs, and rows that do mix their
+    // adapters lose by it.  Measured at rank 64, by chunks and by tiles: 8192 x 28672, 128 rows of one adapter 19 us and
+    // 20, 256 rows of 4 runs 32 and 27 (below the limit, as rows that mix are the rule there); 1024 rows 96 and 37; 643
+    // rows of 6 runs at 28672 x 8192 166 and 42; 8192 x 10240 in 6 runs, 400 rows 31 and 25, 800 rows 65 and 31; rows
+    // that mix 32 adapters, 400 rows 36 and 66, 800 rows 59 and 100.
     const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
     const q4::LoraTcPlan plan = q4::plan_lora_tc(view(h), M, h->sms);
     int launches = 0;

@@ -20,20 +20,21 @@
 //
 // A tile whose adapters have more than kCap ranks in all (single tokens of many
 // requests) takes passes over its output, each of which changes only the rows
-// that use its adapters; where a pool could ask for many, such tiles are left
-// to the kernels of few rows, which run behind over the tiles that the first
-// launch marks.  Adapters with an infinity or NaN, which must not meet another
-// row's zero, get passes of their own.
+// that use its adapters; where a tile can hold more than 512 ranks, such tiles
+// are left to the kernels of few rows, which run behind over the tiles that the
+// first launch marks (the second has copied their y to out by then).  Adapters
+// with an infinity or NaN, which must not meet another row's zero, get passes
+// of their own.
 //
 // 4099 rows of 6 runs, 8192 x 28672, rank 64, fp16: 112 us, 4.5 TB/s of the
 // bytes that the call cannot do without (74 us at the copy rate): the first
 // launch 15 of them (x is 67 MB), the second 1.43 us for a job of 128 x 128
-// outputs on each SM, at which y, out and B (512 B a column) move at 6.9 TB/s
-// between the SMs and L2.  The tensor cores are 5 % busy.  Sizes: 128 x 128
-// jobs in two tensor memory buffers keep loads, products and stores of three
-// jobs in flight; four y stages and two B stages are what shared memory holds.
-// Every wait is bounded; one that runs out sets a status bit, and its role
-// goes on without waiting.
+// outputs on each SM.  There y and out move at 5.1 TB/s, and L2 serves 9.4 TB/s
+// in all, B for each row tile among it; what that path could do at most is not
+// measured.  The tensor cores are 5 % busy.  Sizes: 128 x 128 jobs in two tensor
+// memory buffers keep loads, products and stores of three jobs in flight; four y
+// stages and two B stages are what shared memory holds.  Every wait is bounded;
+// one that runs out sets a status bit, and its role goes on without waiting.
 #include <cuda.h>
 
 #include <algorithm>

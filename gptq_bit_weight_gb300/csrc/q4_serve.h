@@ -54,7 +54,7 @@ struct LoraCall {
 
 cudaError_t launch_lora_set(const LoraView &v, uint16_t *a, uint16_t *b, LoraSlot *slot, int s, const uint16_t *src_a,
                             const uint16_t *src_b, int rank, float scale, bool bf16, cudaStream_t st);
-// few rows, and ranks over 128 (q4_lora.cu)
+// few rows, and ranks over 176 (q4_lora.cu)
 cudaError_t launch_lora_add(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
 // the marked chunks of c.chunk rows
 cudaError_t launch_lora_marked(const LoraView &v, const LoraCall &c, bool bf16, cudaStream_t st, int *launches);
