@@ -119,7 +119,7 @@ void release(gptq_q4_s *h) {
     cudaFree(h->zeros);
     cudaFree(h->perm);
     cudaFree(h->inv8);
-    cudaFree(h->bias);
+    cudaFree(h->bias_store);
     cudaFree(h->status);
     cudaFree(h->ws);
     cudaFree(h->tickets);
@@ -540,18 +540,17 @@ gptq_q4_handle gptq_q4_make_fused(int parts, const int32_t *const *qweight, cons
 
 int gptq_q4_set_bias(gptq_q4_handle h, const uint16_t *bias) {
     if (int r = check_handle(h)) return r;
-    if (!bias) {
+    if (!bias) {                     // the store stays: a captured call may add from it
         cudaDeviceSynchronize();
-        cudaFree(h->bias);
-        if (h->bias) h->device_bytes -= static_cast<size_t>(h->N) * 2;
         h->bias = nullptr;
         return ok();
     }
     if (int r = check_device_ptr(bias, h->device, "bias")) return r;
     if (!aligned(bias, 2)) return set_status(GPTQ_Q4_INVALID_ARGUMENT, "misaligned bias");
-    if (!h->bias && dev_alloc(&h->bias, static_cast<size_t>(h->N), h, "allocating bias")) return t_status;
-    Q4_CUDA(cudaMemcpy(h->bias, bias, static_cast<size_t>(h->N) * 2, cudaMemcpyDeviceToDevice), "copying bias");
+    if (!h->bias_store && dev_alloc(&h->bias_store, static_cast<size_t>(h->N), h, "allocating bias")) return t_status;
+    Q4_CUDA(cudaMemcpy(h->bias_store, bias, static_cast<size_t>(h->N) * 2, cudaMemcpyDeviceToDevice), "copying bias");
     Q4_CUDA(cudaDeviceSynchronize(), "set_bias");
+    h->bias = h->bias_store;
     return ok();
 }
 

@@ -27,7 +27,8 @@ struct gptq_q4_s {
     uint32_t *zeros = nullptr;
     int32_t *perm = nullptr;
     int32_t *inv8 = nullptr;    // 8-bit: private row of each split row (2 Kx entries)
-    uint16_t *bias = nullptr;
+    uint16_t *bias = nullptr;   // bias_store, or NULL without a bias
+    uint16_t *bias_store = nullptr;
     int *status = nullptr;
     float *ws = nullptr;
     size_t ws_bytes = 0;

@@ -144,6 +144,8 @@ gptq_q4_handle gptq_q4_make(const int32_t *qweight, const int32_t *qzeros,
  * handle.  Bias is added to the fp32 accumulator before the single rounding
  * to fp16 ("Inference Backends", "Numeric epilogues and input gradients").
  * Enqueued on the legacy default stream and synchronized before returning.
+ * The handle keeps one copy until it is freed: a graph captured with a bias
+ * goes on adding it, or another that is attached later.
  * Errors: INVALID_ARGUMENT (NULL handle), OUT_OF_MEMORY, CUDA_ERROR. */
 int gptq_q4_set_bias(gptq_q4_handle h, const uint16_t *bias);
 

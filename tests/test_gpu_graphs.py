@@ -102,3 +102,29 @@ def test_buffers_grown_while_capturing(q4, case):
     for m in (mat, other):
         m.device_error()
         m.close()
+
+
+def test_a_captured_step_outlives_its_bias(q4):
+    """Detached, the bias stays with the graph and with nobody else; another one, attached later, is the graph's too."""
+    K, N, M = 1024, 448, 3
+    mat = make(q4, K, N, 128, False, torch.float16, q4.GPTQ_Q4_PATH_AUTO)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(3)).half().to(DEV)
+    want = mat(x).clone()
+    y, side, graph = torch.empty_like(want), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        y.copy_(mat(x))
+    q4.gptq_q4_set_bias(mat.handle, None)
+    others = [torch.full((1024,), 77, dtype=torch.int8, device=DEV) for _ in range(4000)]
+    plain = mat(x)
+    assert not torch.equal(plain, want)
+    graph.replay()
+    assert torch.equal(y, want)
+    other = torch.randn(N, generator=torch.Generator().manual_seed(4)).half().to(DEV)
+    q4.gptq_q4_set_bias(mat.handle, other.data_ptr())
+    want = mat(x)
+    graph.replay()
+    assert torch.equal(y, want) and not torch.equal(want, plain)
+    assert all((o == 77).all() for o in others[::97])
+    mat.device_error()
+    mat.close()
