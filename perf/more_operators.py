@@ -248,6 +248,7 @@ def prepare(case, seed):
         if case["op"] in ("fork", "compact"):
             s["pool"] = q4.PagePool([q4.PagedCache4(s["kv4"][i], case["D"], case["group"], dt) if case["bits"] == 4
                                      else q4.PagedCache(s["k"][i], s["v"][i]) for i in range(case["layers"])])
+            s["dropped"] = s["child"].long()
             return s
         att = q4.PagedAttention(case["Hq"], case["Hkv"], case["D"], case["page"], dtype=dt)
         if case["op"] == "append4":
@@ -383,7 +384,7 @@ def run(state):
         return state["attention"].attend(state["q"], state["cache"], state["batch"], window=c["window"], sinks=c["sinks"])
     caches = {"cache_" + n: t for n, t in _caches(state).items()}
     if op == "fork":
-        state["kv"].index_fill_(0, state["child"], 0)
+        state["kv"].index_fill_(0, state["dropped"], 0)
         free, _ = state["pool"].free(state["table"], state["kv"])
         state["pool"].fork(state["table"], state["kv"], state["parent"], state["child"], free[: c["forks"]])
         return {"table": state["table"], "kv": state["kv"], "free": free} | caches
