@@ -58,6 +58,10 @@ EXPORTED = [
     "gptq_q4_lora_free",
     "gptq_q4_attn_make", "gptq_q4_rope_freqs", "gptq_q4_attn_set_rope", "gptq_q4_attn_append", "gptq_q4_attn_attend",
     "gptq_q4_attn_device_error", "gptq_q4_attn_free",
+    "gptq_q4_attn_attend_sinks", "gptq_q4_attn_read", "gptq_q4_attn_append4", "gptq_q4_attn_attend4",
+    "gptq_q4_attn_read4",
+    "gptq_q4_pages_make", "gptq_q4_pages_free_list", "gptq_q4_pages_fork", "gptq_q4_pages_copy",
+    "gptq_q4_pages_compact", "gptq_q4_pages_device_error", "gptq_q4_pages_free",
 ]
 
 _P = ctypes.c_void_p
@@ -75,6 +79,21 @@ class gptq_q4_batch(ctypes.Structure):
     """The requests of one step (see include/gptq_q4.h)."""
     _fields_ = [("cu_q", _P), ("kv_len", _P), ("table", _P), ("table_stride", _L),
                 ("width", _I), ("batch", _I), ("tokens", _I), ("max_q", _I)]
+
+
+class gptq_q4_cache4(ctypes.Structure):
+    """One layer's keys and values in 4 bits (see include/gptq_q4.h)."""
+    _fields_ = [("kv", _P), ("pages", _I), ("page_stride", _L), ("group", _I)]
+
+
+class gptq_q4_buffer(ctypes.Structure):
+    """A buffer with a part of every page (see include/gptq_q4.h)."""
+    _fields_ = [("data", _P), ("bytes", _L), ("stride", _L)]
+
+
+class gptq_q4_rows(ctypes.Structure):
+    """The rows of a page table (see include/gptq_q4.h)."""
+    _fields_ = [("table", _P), ("kv_len", _P), ("table_stride", _L), ("width", _I), ("batch", _I)]
 
 
 
@@ -123,6 +142,18 @@ _sig("gptq_q4_attn_append", _I, _P, _P, _L, _P, _P, _P, _P, _L, _P)
 _sig("gptq_q4_attn_attend", _I, _P, _P, _L, _P, _P, ctypes.c_float, _I, _P, _L, _P)
 _sig("gptq_q4_attn_device_error", _I, _P)
 _sig("gptq_q4_attn_free", None, _P)
+_sig("gptq_q4_attn_attend_sinks", _I, _P, _P, _L, _P, _P, ctypes.c_float, _I, _I, _P, _L, _P)
+_sig("gptq_q4_attn_read", _I, _P, _P, _P, _P, _L, _P, _L, _P)
+_sig("gptq_q4_attn_append4", _I, _P, _P, _L, _P, _P, _P, _P, _L, _P)
+_sig("gptq_q4_attn_attend4", _I, _P, _P, _L, _P, _P, ctypes.c_float, _I, _I, _P, _L, _P)
+_sig("gptq_q4_attn_read4", _I, _P, _P, _P, _P, _L, _P, _L, _P)
+_sig("gptq_q4_pages_make", _P, _P, _I, _I, _I)
+_sig("gptq_q4_pages_free_list", _I, _P, _P, _I, _I, _P, _P, _P)
+_sig("gptq_q4_pages_fork", _I, _P, _P, _P, _P, _P, _I, _P)
+_sig("gptq_q4_pages_copy", _I, _P, _P, _P, _I, _P)
+_sig("gptq_q4_pages_compact", _I, _P, _P, _I, _I, _P, _L, _P, _P)
+_sig("gptq_q4_pages_device_error", _I, _P)
+_sig("gptq_q4_pages_free", None, _P)
 
 GPTQ_Q4_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -369,6 +400,71 @@ def gptq_q4_attn_free(h: int | None) -> None:
         _lib.gptq_q4_attn_free(h)
 
 
+def gptq_q4_attn_attend_sinks(h: int, q: int, q_stride: int, cache: gptq_q4_cache, batch: gptq_q4_batch, scale: float,
+                              window: int, sinks: int, out: int, out_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_attend_sinks(h, q, q_stride, ctypes.byref(cache), ctypes.byref(batch), scale, window,
+                                                 sinks, out, out_stride, stream))
+
+
+def gptq_q4_attn_read(h: int, cache: gptq_q4_cache, batch: gptq_q4_batch, k_out: int, k_stride: int, v_out: int,
+                      v_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_read(h, ctypes.byref(cache), ctypes.byref(batch), k_out, k_stride, v_out, v_stride,
+                                         stream))
+
+
+def gptq_q4_attn_append4(h: int, qkv: int, qkv_stride: int, cache: gptq_q4_cache4, batch: gptq_q4_batch,
+                         positions: int | None, q_out: int, q_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_append4(h, qkv, qkv_stride, ctypes.byref(cache), ctypes.byref(batch), positions,
+                                            q_out, q_stride, stream))
+
+
+def gptq_q4_attn_attend4(h: int, q: int, q_stride: int, cache: gptq_q4_cache4, batch: gptq_q4_batch, scale: float,
+                         window: int, sinks: int, out: int, out_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_attend4(h, q, q_stride, ctypes.byref(cache), ctypes.byref(batch), scale, window,
+                                            sinks, out, out_stride, stream))
+
+
+def gptq_q4_attn_read4(h: int, cache: gptq_q4_cache4, batch: gptq_q4_batch, k_out: int, k_stride: int, v_out: int,
+                       v_stride: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_attn_read4(h, ctypes.byref(cache), ctypes.byref(batch), k_out, k_stride, v_out, v_stride,
+                                          stream))
+
+
+def gptq_q4_pages_make(buffers, pages: int, page_size: int) -> int:
+    """buffers: a sequence of gptq_q4_buffer."""
+    buffers = list(buffers)
+    h = _lib.gptq_q4_pages_make((gptq_q4_buffer * len(buffers))(*buffers), len(buffers), pages, page_size)
+    if not h:
+        raise GPTQ4Error(gptq_q4_last_status(), gptq_q4_last_error())
+    return h
+
+
+def gptq_q4_pages_free_list(h: int, rows: gptq_q4_rows, window: int, sinks: int, ids: int, count: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_pages_free_list(h, ctypes.byref(rows), window, sinks, ids, count, stream))
+
+
+def gptq_q4_pages_fork(h: int, rows: gptq_q4_rows, parent: int, child: int, fresh: int, n: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_pages_fork(h, ctypes.byref(rows), parent, child, fresh, n, stream))
+
+
+def gptq_q4_pages_copy(h: int, src: int, dst: int, n: int, stream: int) -> int:
+    return _check(_lib.gptq_q4_pages_copy(h, src, dst, n, stream))
+
+
+def gptq_q4_pages_compact(h: int, rows: gptq_q4_rows, window: int, sinks: int, table_out: int, out_stride: int, count: int,
+                          stream: int) -> int:
+    return _check(_lib.gptq_q4_pages_compact(h, ctypes.byref(rows), window, sinks, table_out, out_stride, count, stream))
+
+
+def gptq_q4_pages_device_error(h: int) -> int:
+    return _check(_lib.gptq_q4_pages_device_error(h))
+
+
+def gptq_q4_pages_free(h: int | None) -> None:
+    if h:
+        _lib.gptq_q4_pages_free(h)
+
+
 # --------------------------------------------------------- torch marshalling
 
 class Q4Matrix:
@@ -515,7 +611,8 @@ def gemm_f16(a, b, bias=None):
 
 
 # The operators around the projection; their modules need torch when imported.
-_LAZY = {"LoraPool": "adapters", "PagedAttention": "attention", "PagedBatch": "attention", "PagedCache": "attention"}
+_LAZY = {"LoraPool": "adapters", "PagedAttention": "attention", "PagedBatch": "attention", "PagedCache": "attention",
+         "PagedCache4": "attention", "PagePool": "pages"}
 
 
 def __getattr__(name):

@@ -6,7 +6,9 @@
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 
+#include "q4_cache4.cuh"
 #include "q4_handle.h"
 #include "q4_serve.h"
 
@@ -44,7 +46,9 @@ int check(gptq_q4_attn h) {
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool aligned4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
-int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache *c, const gptq_q4_batch *b) {
+bool empty(const gptq_q4_batch *b) { return b->batch == 0 || b->tokens == 0; }
+
+int check_batch(const void *c, const gptq_q4_batch *b) {
     if (!c || !b) return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "cache and batch must not be NULL");
     if (b->batch < 0 || b->tokens < 0 || b->width < 0 || b->max_q < 0 || b->table_stride < b->width)
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
@@ -53,11 +57,17 @@ int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache *c, const gptq_q4_ba
                          b->batch, b->tokens, b->width, b->max_q, static_cast<long long>(b->table_stride));
     if (b->batch > kMaxBatch)
         return api_failf(GPTQ_Q4_UNSUPPORTED, "batch=%d: at most %d requests in a call", b->batch, kMaxBatch);
-    if (b->batch == 0 || b->tokens == 0) return GPTQ_Q4_OK;
+    if (empty(b)) return GPTQ_Q4_OK;
     if (!b->cu_q || !b->kv_len || (b->width && !b->table) || !aligned4(b->cu_q) || !aligned4(b->kv_len) ||
         !aligned4(b->table))
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
                          "cu_q, kv_len and (unless its width is 0) table must be 4-byte aligned and not NULL");
+    return GPTQ_Q4_OK;
+}
+
+int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache *c, const gptq_q4_batch *b) {
+    if (int r = check_batch(c, b)) return r;
+    if (empty(b)) return GPTQ_Q4_OK;
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
         return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "the cache's k and v must be 16-byte aligned and not NULL");
     const int64_t page = static_cast<int64_t>(h->shape.hkv) * h->shape.page * h->shape.d;
@@ -68,11 +78,30 @@ int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache *c, const gptq_q4_ba
     return GPTQ_Q4_OK;
 }
 
+int check_step(const gptq_q4_attn_s *h, const gptq_q4_cache4 *c, const gptq_q4_batch *b) {
+    if (int r = check_batch(c, b)) return r;
+    if (empty(b)) return GPTQ_Q4_OK;
+    if (c->group != 32 && c->group != 64)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "group=%d must be 32 or 64", c->group);
+    if (!c->kv || !aligned16(c->kv))
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "the cache's kv must be 16-byte aligned and not NULL");
+    const int64_t page = static_cast<int64_t>(h->shape.hkv) * h->shape.page *
+                         q4::record_bytes(h->shape.d, c->group == 32 ? 5 : 6);
+    if (c->pages < 1 || c->page_stride < page || c->page_stride % 16 || c->page_stride >= int64_t{1} << 39)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "pages=%d must be positive and page_stride=%lld a multiple of 16, at least %lld and below 2^39",
+                         c->pages, static_cast<long long>(c->page_stride), static_cast<long long>(page));
+    return GPTQ_Q4_OK;
+}
+
 q4::AttnBatch batch_view(const gptq_q4_batch *b) {
     return q4::AttnBatch{b->cu_q, b->kv_len, b->table, b->table_stride, b->width, b->batch, b->tokens};
 }
 q4::AttnCache cache_view(const gptq_q4_cache *c) {
     return q4::AttnCache{static_cast<uint16_t *>(c->k), static_cast<uint16_t *>(c->v), c->pages, c->page_stride};
+}
+q4::Cache4 cache_view(const gptq_q4_cache4 *c) {
+    return q4::Cache4{static_cast<uint8_t *>(c->kv), c->pages, c->page_stride, c->group == 32 ? 5 : 6};
 }
 
 void release(gptq_q4_attn_s *h) {
@@ -88,6 +117,108 @@ void release(gptq_q4_attn_s *h) {
     cudaFree(h->tickets);
     if (cur >= 0) cudaSetDevice(cur);
     delete h;
+}
+
+// For either cache.
+template <class Cache>
+int append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const Cache *cache, const gptq_q4_batch *batch,
+           const int32_t *positions, void *q_out, int64_t q_stride, cudaStream_t stream) {
+    if (int r = check(h)) return r;
+    if (int r = check_step(h, cache, batch)) return r;
+    if (empty(batch)) return api_set_status(GPTQ_Q4_OK, nullptr);
+    const q4::AttnShape &s = h->shape;
+    if (!qkv || !q_out || !aligned16(qkv) || !aligned16(q_out) || !aligned4(positions))
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "qkv and q_out must be 16-byte aligned and not NULL, positions 4-byte aligned");
+    const int64_t row = static_cast<int64_t>(s.hq + 2 * s.hkv) * s.d, qrow = static_cast<int64_t>(s.hq) * s.d;
+    if (qkv_stride < row || qkv_stride % 8 || q_stride < qrow || q_stride % 8)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "row strides (qkv %lld, q %lld) must be multiples of 8 and at least %lld and %lld",
+                         static_cast<long long>(qkv_stride), static_cast<long long>(q_stride),
+                         static_cast<long long>(row), static_cast<long long>(qrow));
+    if (q_out == qkv && q_stride != qkv_stride)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "q_out is qkv but their row strides differ (%lld and %lld)",
+                         static_cast<long long>(q_stride), static_cast<long long>(qkv_stride));
+    const q4::AppendCall a{static_cast<const uint16_t *>(qkv), static_cast<uint16_t *>(q_out), qkv_stride, q_stride,
+                           positions, h->rope, h->rot, h->interleaved, h->max_pos, h->status};
+    cudaError_t e;
+    if constexpr (std::is_same_v<Cache, gptq_q4_cache>)
+        e = q4::launch_attn_append(s, batch_view(batch), cache_view(cache), a, h->dtype == GPTQ_Q4_DTYPE_BF16, stream);
+    else
+        e = q4::launch_attn_append4(s, batch_view(batch), cache_view(cache), a, h->dtype == GPTQ_Q4_DTYPE_BF16, stream);
+    if (e) return api_cuda_fail(e, "append launch");
+    q4::api_count_launches(1);
+    return api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+template <class Cache>
+int read(gptq_q4_attn h, const Cache *cache, const gptq_q4_batch *batch, void *k_out, int64_t k_stride, void *v_out,
+         int64_t v_stride, cudaStream_t stream) {
+    if (int r = check(h)) return r;
+    if (int r = check_step(h, cache, batch)) return r;
+    if (empty(batch)) return api_set_status(GPTQ_Q4_OK, nullptr);
+    const q4::AttnShape &s = h->shape;
+    const int64_t row = static_cast<int64_t>(s.hkv) * s.d;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || k_stride < row || k_stride % 8 || v_stride < row ||
+        v_stride % 8)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "k_out and v_out must be 16-byte aligned and not NULL, their row strides (%lld and %lld) "
+                         "multiples of 8 and at least %lld",
+                         static_cast<long long>(k_stride), static_cast<long long>(v_stride), static_cast<long long>(row));
+    const auto view = cache_view(cache);
+    const q4::AttnCache *wide = nullptr;
+    const q4::Cache4 *four = nullptr;
+    if constexpr (std::is_same_v<Cache, gptq_q4_cache>) wide = &view;
+    else four = &view;
+    if (cudaError_t e = q4::launch_attn_read(s, batch_view(batch), wide, four, static_cast<uint16_t *>(k_out), k_stride,
+                                             static_cast<uint16_t *>(v_out), v_stride, h->dtype == GPTQ_Q4_DTYPE_BF16,
+                                             h->status, stream))
+        return api_cuda_fail(e, "read launch");
+    q4::api_count_launches(1);
+    return api_set_status(GPTQ_Q4_OK, nullptr);
+}
+
+template <class Cache>
+int attend(gptq_q4_attn h, const void *q, int64_t q_stride, const Cache *cache, const gptq_q4_batch *batch, float scale,
+           int window, int sinks, void *out, int64_t out_stride, cudaStream_t stream) {
+    if (int r = check(h)) return r;
+    if (int r = check_step(h, cache, batch)) return r;
+    if (!std::isfinite(scale) || window < 0 || sinks < 0)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "scale=%g must be finite, window=%d and sinks=%d not negative",
+                         static_cast<double>(scale), window, sinks);
+    if (empty(batch)) return api_set_status(GPTQ_Q4_OK, nullptr);
+    const q4::AttnShape &s = h->shape;
+    if (!q || !out || !aligned16(q) || !aligned16(out))
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "q and out must be 16-byte aligned and not NULL");
+    const int64_t row = static_cast<int64_t>(s.hq) * s.d;
+    if (q_stride < row || q_stride % 8 || out_stride < row || out_stride % 8 ||
+        q_stride >= int64_t{1} << 39)
+        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
+                         "row strides (q %lld, out %lld) must be multiples of 8, at least %lld and below 2^39",
+                         static_cast<long long>(q_stride), static_cast<long long>(out_stride),
+                         static_cast<long long>(row));
+    // Contexts end at 2^30 tokens, so a longer window hides nothing; differences with a shorter one fit 32 bits.
+    const int seen = window < 1 << 30 ? window : 0;
+    const q4::AttendCall a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), q_stride, out_stride,
+                           scale, seen, seen ? std::min(sinks, 1 << 30) : 0, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
+    // More query rows for each key/value head than the streaming kernel's row tile has: the tensor-core kernel
+    // (which takes its maximum before scaling, so a positive scale).  Measured at 64 heads over 8, contexts of up
+    // to 4096: 32 requests of 2 tokens (16 rows) 45 us streaming, 53 on tcgen05, one such request 12 and 15; 32 of 4
+    // tokens, streaming with row tiles of 32 rows 134, tcgen05 54; one request of 4 tokens 25 and 17.
+    const bool chunk = static_cast<int64_t>(batch->max_q) * s.group > 16 && scale > 0.f;
+    const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
+    cudaError_t e;
+    if constexpr (std::is_same_v<Cache, gptq_q4_cache>) {
+        const q4::AttnCache view = cache_view(cache);
+        if (a.sinks) e = q4::launch_attend_any(s, batch_view(batch), &view, nullptr, a, bf16, stream);
+        else e = (chunk ? q4::launch_attend_tc : q4::launch_attend_stream)(s, batch_view(batch), view, a, bf16, stream);
+    } else {
+        const q4::Cache4 view = cache_view(cache);
+        e = q4::launch_attend_any(s, batch_view(batch), nullptr, &view, a, bf16, stream);
+    }
+    if (e) return api_cuda_fail(e, "attention launch");
+    q4::api_count_launches(1);
+    return api_set_status(GPTQ_Q4_OK, nullptr);
 }
 
 }  // namespace
@@ -220,64 +351,41 @@ int gptq_q4_attn_set_rope(gptq_q4_attn h, int rotary_dim, int interleaved, const
 int gptq_q4_attn_append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const gptq_q4_cache *cache,
                         const gptq_q4_batch *batch, const int32_t *positions, void *q_out, int64_t q_stride,
                         cudaStream_t stream) {
-    if (int r = check(h)) return r;
-    if (int r = check_step(h, cache, batch)) return r;
-    if (batch->batch == 0 || batch->tokens == 0) return api_set_status(GPTQ_Q4_OK, nullptr);
-    const q4::AttnShape &s = h->shape;
-    if (!qkv || !q_out || !aligned16(qkv) || !aligned16(q_out) || !aligned4(positions))
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
-                         "qkv and q_out must be 16-byte aligned and not NULL, positions 4-byte aligned");
-    const int64_t row = static_cast<int64_t>(s.hq + 2 * s.hkv) * s.d, qrow = static_cast<int64_t>(s.hq) * s.d;
-    if (qkv_stride < row || qkv_stride % 8 || q_stride < qrow || q_stride % 8)
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
-                         "row strides (qkv %lld, q %lld) must be multiples of 8 and at least %lld and %lld",
-                         static_cast<long long>(qkv_stride), static_cast<long long>(q_stride),
-                         static_cast<long long>(row), static_cast<long long>(qrow));
-    if (q_out == qkv && q_stride != qkv_stride)
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "q_out is qkv but their row strides differ (%lld and %lld)",
-                         static_cast<long long>(q_stride), static_cast<long long>(qkv_stride));
-    const q4::AppendCall a{static_cast<const uint16_t *>(qkv), static_cast<uint16_t *>(q_out), qkv_stride, q_stride,
-                           positions, h->rope, h->rot, h->interleaved, h->max_pos, h->status};
-    if (cudaError_t e = q4::launch_attn_append(s, batch_view(batch), cache_view(cache), a,
-                                               h->dtype == GPTQ_Q4_DTYPE_BF16, stream))
-        return api_cuda_fail(e, "append launch");
-    q4::api_count_launches(1);
-    return api_set_status(GPTQ_Q4_OK, nullptr);
+    return append(h, qkv, qkv_stride, cache, batch, positions, q_out, q_stride, stream);
+}
+
+int gptq_q4_attn_append4(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const gptq_q4_cache4 *cache,
+                         const gptq_q4_batch *batch, const int32_t *positions, void *q_out, int64_t q_stride,
+                         cudaStream_t stream) {
+    return append(h, qkv, qkv_stride, cache, batch, positions, q_out, q_stride, stream);
+}
+
+int gptq_q4_attn_read(gptq_q4_attn h, const gptq_q4_cache *cache, const gptq_q4_batch *batch, void *k_out,
+                      int64_t k_stride, void *v_out, int64_t v_stride, cudaStream_t stream) {
+    return read(h, cache, batch, k_out, k_stride, v_out, v_stride, stream);
+}
+
+int gptq_q4_attn_read4(gptq_q4_attn h, const gptq_q4_cache4 *cache, const gptq_q4_batch *batch, void *k_out,
+                       int64_t k_stride, void *v_out, int64_t v_stride, cudaStream_t stream) {
+    return read(h, cache, batch, k_out, k_stride, v_out, v_stride, stream);
 }
 
 int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache *cache,
                         const gptq_q4_batch *batch, float scale, int window, void *out, int64_t out_stride,
                         cudaStream_t stream) {
-    if (int r = check(h)) return r;
-    if (int r = check_step(h, cache, batch)) return r;
-    if (!std::isfinite(scale) || window < 0)
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "scale=%g must be finite and window=%d not negative",
-                         static_cast<double>(scale), window);
-    if (batch->batch == 0 || batch->tokens == 0) return api_set_status(GPTQ_Q4_OK, nullptr);
-    const q4::AttnShape &s = h->shape;
-    if (!q || !out || !aligned16(q) || !aligned16(out))
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT, "q and out must be 16-byte aligned and not NULL");
-    const int64_t row = static_cast<int64_t>(s.hq) * s.d;
-    if (q_stride < row || q_stride % 8 || out_stride < row || out_stride % 8 ||
-        q_stride >= int64_t{1} << 39)
-        return api_failf(GPTQ_Q4_INVALID_ARGUMENT,
-                         "row strides (q %lld, out %lld) must be multiples of 8, at least %lld and below 2^39",
-                         static_cast<long long>(q_stride), static_cast<long long>(out_stride),
-                         static_cast<long long>(row));
-    // Contexts end at 2^30 tokens, so a longer window hides nothing; differences with a shorter one fit 32 bits.
-    const int seen = window < 1 << 30 ? window : 0;
-    const q4::AttendCall a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), q_stride, out_stride,
-                           scale, seen, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
-    // More query rows for each key/value head than the streaming kernel's row tile has: the tensor-core kernel
-    // (which takes its maximum before scaling, so a positive scale).  Measured at 64 heads over 8, contexts of up
-    // to 4096: 32 requests of 2 tokens (16 rows) 45 us streaming, 53 on tcgen05, one such request 12 and 15; 32 of 4
-    // tokens, streaming with row tiles of 32 rows 134, tcgen05 54; one request of 4 tokens 25 and 17.
-    const bool chunk = static_cast<int64_t>(batch->max_q) * s.group > 16 && scale > 0.f;
-    if (cudaError_t e = (chunk ? q4::launch_attend_tc : q4::launch_attend_stream)(
-            s, batch_view(batch), cache_view(cache), a, h->dtype == GPTQ_Q4_DTYPE_BF16, stream))
-        return api_cuda_fail(e, "attention launch");
-    q4::api_count_launches(1);
-    return api_set_status(GPTQ_Q4_OK, nullptr);
+    return attend(h, q, q_stride, cache, batch, scale, window, 0, out, out_stride, stream);
+}
+
+int gptq_q4_attn_attend_sinks(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache *cache,
+                              const gptq_q4_batch *batch, float scale, int window, int sinks, void *out,
+                              int64_t out_stride, cudaStream_t stream) {
+    return attend(h, q, q_stride, cache, batch, scale, window, sinks, out, out_stride, stream);
+}
+
+int gptq_q4_attn_attend4(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache4 *cache,
+                         const gptq_q4_batch *batch, float scale, int window, int sinks, void *out,
+                         int64_t out_stride, cudaStream_t stream) {
+    return attend(h, q, q_stride, cache, batch, scale, window, sinks, out, out_stride, stream);
 }
 
 int gptq_q4_attn_device_error(gptq_q4_attn h) {

@@ -10,7 +10,7 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "q4_serve.h"
+#include "q4_attn_rows.cuh"
 
 namespace q4 {
 namespace {
@@ -32,13 +32,6 @@ __global__ void rope_table_kernel(float2 *table, Freqs f, double scale, int half
 }
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;        // of one CTA: one warp looks each of them up
-
-struct Token {
-    int64_t dst;      // element offset of (page, head 0, token) in the cache; -1: no request or out of range
-    int pos;          // rotary position
-};
-
 // Work item: 16 elements of one head of one token, as two 16-byte vectors:
 // both halves of eight pairs (i, i + rot / 2), or eight interleaved pairs, or
 // 16 elements past the rotated part.
@@ -49,31 +42,8 @@ __global__ void __launch_bounds__(kThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * tokens_per_cta, nt = min(tokens_per_cta, b.tokens - t0);
     if (warp < nt) {
-        const int t = t0 + warp;
-        int before = 0;                                  // requests that end at or before t
-        for (int i = lane; i < b.batch; i += 32) before += b.cu_q[i + 1] <= t;
-        const int req = __reduce_add_sync(0xffffffffu, before);
-        if (lane == 0) {
-            Token k{-1, 0};
-            if (req < b.batch && b.cu_q[req] <= t) {
-                const Request r = load_request(b, req, s.page_log2);
-                const int idx = r.kv - r.ql + (t - r.q0);
-                int bad = 0;
-                // A length that had to be cut says nothing of where the token belongs: its index in the cut context
-                // is another token's, and a table's padding may be another request's page.
-                if (r.bad || idx < 0 || idx >= r.kv) {
-                    bad = kAttnBadBatch;
-                } else {
-                    const int page = b.table[req * b.table_stride + (idx >> s.page_log2)];
-                    k.pos = a.positions ? a.positions[t] : idx;
-                    if (page < 0 || page >= c.pages) bad |= kAttnBadPage;
-                    else if (a.rope && (k.pos < 0 || k.pos >= a.max_pos)) bad |= kAttnBadPosition;
-                    else k.dst = page * c.page_stride + static_cast<int64_t>(idx & (s.page - 1)) * s.d;
-                }
-                if (bad) atomicOr(a.status, bad);
-            }
-            tok[warp] = k;
-        }
+        const Token k = find_token(b, s, c.pages, t0 + warp, a.positions, a.rope ? a.max_pos : 0, a.status);
+        if (lane == 0) tok[warp] = k;
     }
     __syncthreads();
     const int per_head = s.d / 16, heads = s.hq + 2 * s.hkv, per_token = heads * per_head;
@@ -81,7 +51,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int w = threadIdx.x; w < nt * per_token; w += kThreads) {
         const int ti = w / per_token, u = w - ti * per_token, head = u / per_head, item = u - head * per_head;
         const Token k = tok[ti];
-        if (k.dst < 0) continue;
+        if (k.page < 0) continue;
         const int64_t t = t0 + ti;
         const bool turn = item < turned && head < s.hq + s.hkv;
         int e0 = 16 * item, e1 = e0 + 8;                 // first elements of the two vectors
@@ -115,7 +85,7 @@ __global__ void __launch_bounds__(kThreads)
         } else {
             const bool key = head < s.hq + s.hkv;
             const int h = head - s.hq - (key ? 0 : s.hkv);
-            dst = (key ? c.k : c.v) + k.dst + static_cast<int64_t>(h) * s.page * s.d;
+            dst = (key ? c.k : c.v) + k.page * c.page_stride + static_cast<int64_t>(h * s.page + k.slot) * s.d;
         }
         *reinterpret_cast<uint4 *>(dst + e0) = v0;
         *reinterpret_cast<uint4 *>(dst + e1) = v1;

@@ -1,0 +1,230 @@
+// Rotary positions and the append to a paged cache held in 4 bits, and reading
+// tokens back out of either cache as 16-bit values.
+//
+// Appending is one pass over the fused projection's output, as for the 16-bit
+// cache (q4_attn_append.cu): queries are rotated and written; keys are rotated
+// and rounded to 16 bits, then keys and values are quantised by groups of 32 or
+// 64 elements: m = least, s = (greatest - m) / 15 rounded to 16 bits, c = round
+// to even of (x - m) / s.
+//   A code changes where (x - m) / s passes a half, so what goes in has to be the
+//   same number wherever it is computed: the rotation carries the errors of its
+//   two products and of their sum (fma and two-sum), so that its fp32 result is
+//   the exact one rounded once; and a code is found from an approximate quotient,
+//   then set right by the sign of x - m - (k + 1/2) s, one exact fma.
+// A work item has 16 elements of a head.  A key's pairs (i, i + rot / 2) come from
+// two places, so the rotated elements go through shared memory, after which an
+// item holds 16 neighbours and a group is 2 or 4 lanes.
+#include <algorithm>
+#include <cstdint>
+
+#include "q4_attn_rows.cuh"
+#include "q4_cache4.cuh"
+
+namespace q4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// x y - u v, rounded once: the products' errors and the sum's are added back.
+__device__ __forceinline__ float cross(float x, float y, float u, float v) {
+    const float p = __fmul_rn(x, y), q = __fmul_rn(u, v);
+    const float ep = __fmaf_rn(x, y, -p), eq = __fmaf_rn(u, v, -q);
+    const float s = __fsub_rn(p, q), b = __fsub_rn(s, p);
+    const float es = __fsub_rn(__fsub_rn(p, __fsub_rn(s, b)), __fadd_rn(q, b));
+    const float r = __fadd_rn(s, __fadd_rn(es, __fsub_rn(ep, eq)));
+    return fabsf(s) < INFINITY ? r : s;                  // of infinities there are no errors
+}
+
+// Sixteen 16-bit values in two vectors -> their codes; s and m of the group (`lanes` lanes).
+template <bool BF>
+__device__ __forceinline__ uint2 quantise(const uint4 &v0, const uint4 &v1, int lanes, unsigned mask, uint32_t &sm) {
+    float x[16], lo = INFINITY, hi = -INFINITY, odd = 0.f;
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = unpack2<BF>(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+        lo = fminf(lo, fminf(f.x, f.y));
+        hi = fmaxf(hi, fmaxf(f.x, f.y));
+        odd += f.x * 0.f + f.y * 0.f;                    // NaN if either is no finite number
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
+        odd += __shfl_xor_sync(mask, odd, o);
+    }
+    const float span = __fadd_rn(__fsub_rn(hi, lo), odd);
+    if (!(span < INFINITY)) {
+        const float nan = __int_as_float(0x7fffffff);
+        sm = pack2<BF>(nan, nan);
+        return make_uint2(0, 0);
+    }
+    sm = pack2<BF>(__fdiv_rn(span, 15.f), lo);
+    const float step = unpack2<BF>(sm).x, up = step < 1e-30f ? 0x1p64f : 1.f;      // 1 / s stays in range
+    const float s = step * up, inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float d = __fsub_rn(x[e], lo) * up, k = fminf(floorf(d * inv), 15.f);
+        const float past = __fmaf_rn(-(k + 0.5f), s, d);                 // of the half after k
+        const int n = static_cast<int>(k);
+        const int code = s > 0.f ? min(n + (past > 0.f || (past == 0.f && (n & 1))), 15) : 0;
+        c[e >> 3] |= static_cast<uint32_t>(code) << (4 * ((e & 7) >> 1) + 16 * (e & 1));
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+template <bool BF>
+__global__ void __launch_bounds__(kThreads)
+    append4_kernel(AttnShape s, AttnBatch b, Cache4 c, AppendCall a, int tokens_per_cta) {
+    __shared__ Token tok[kMaxTokens];
+    __shared__ uint4 turned_rows[2 * kThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * tokens_per_cta, nt = min(tokens_per_cta, b.tokens - t0);
+    if (warp < nt) {
+        const Token k = find_token(b, s, c.pages, t0 + warp, a.positions, a.rope ? a.max_pos : 0, a.status);
+        if (lane == 0) tok[warp] = k;
+    }
+    __syncthreads();
+    const int per_head = s.d / 16, heads = s.hq + 2 * s.hkv, per_token = heads * per_head;       // 4 or 8 lanes a head
+    const int half = a.rot / 2, turned = a.rope ? a.rot / 16 : 0;
+    const int record = record_bytes(s.d, c.group_log2), group_lanes = 1 << (c.group_log2 - 4);
+    const unsigned mask = ((1u << per_head) - 1) << (lane & ~(per_head - 1));                    // the head's lanes
+    uint4 *row = turned_rows + 2 * (threadIdx.x & ~(per_head - 1));                              // the head's elements
+    for (int w = threadIdx.x; w < nt * per_token; w += kThreads) {
+        const int ti = w / per_token, u = w - ti * per_token, head = u / per_head, item = u - head * per_head;
+        const Token k = tok[ti];
+        if (k.page < 0) continue;
+        const int64_t t = t0 + ti;
+        const bool query = head < s.hq, key = !query && head < s.hq + s.hkv;
+        const bool turn = item < turned && (query || key);
+        int e0 = 16 * item, e1 = e0 + 8;                 // first elements of the two vectors
+        if (turn && !a.interleaved) {
+            e0 = 8 * item;
+            e1 = e0 + half;
+        }
+        const uint16_t *src = a.qkv + t * a.qkv_stride + head * s.d;
+        uint4 v0 = *reinterpret_cast<const uint4 *>(src + e0), v1 = *reinterpret_cast<const uint4 *>(src + e1);
+        if (turn) {
+            const float4 *cs = reinterpret_cast<const float4 *>(a.rope + static_cast<int64_t>(k.pos) * half + 8 * item);
+            uint32_t *p = reinterpret_cast<uint32_t *>(&v0), *q = reinterpret_cast<uint32_t *>(&v1);
+            auto rotate = [&](float x, float y, float co, float si) {
+                return make_float2(cross(x, co, y, si), cross(y, co, -x, si));
+            };
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {                // pairs 2e and 2e + 1 of the item's eight
+                const float4 r = cs[e];                  // cos, sin, cos, sin
+                if (a.interleaved) {
+                    uint32_t *x = e < 2 ? p + 2 * e : q + 2 * (e - 2);
+                    const float2 m = unpack2<BF>(x[0]), n = unpack2<BF>(x[1]);
+                    const float2 f = rotate(m.x, m.y, r.x, r.y), g = rotate(n.x, n.y, r.z, r.w);
+                    x[0] = pack2<BF>(f.x, f.y);
+                    x[1] = pack2<BF>(g.x, g.y);
+                } else {
+                    const float2 m = unpack2<BF>(p[e]), n = unpack2<BF>(q[e]);
+                    const float2 f = rotate(m.x, n.x, r.x, r.y), g = rotate(m.y, n.y, r.z, r.w);
+                    p[e] = pack2<BF>(f.x, g.x);
+                    q[e] = pack2<BF>(f.y, g.y);
+                }
+            }
+        }
+        if (query) {
+            uint16_t *dst = a.q_out + t * a.q_stride + head * s.d;
+            *reinterpret_cast<uint4 *>(dst + e0) = v0;
+            *reinterpret_cast<uint4 *>(dst + e1) = v1;
+            continue;
+        }
+        if (key) {
+            row[e0 / 8] = v0;
+            row[e1 / 8] = v1;
+            __syncwarp(mask);
+            v0 = row[2 * item];
+            v1 = row[2 * item + 1];
+            __syncwarp(mask);
+        }
+        uint32_t sm;
+        const uint2 codes = quantise<BF>(v0, v1, group_lanes, mask, sm);
+        const int h = head - s.hq - (key ? 0 : s.hkv);
+        uint8_t *dst = c.kv + k.page * c.page_stride + static_cast<int64_t>(h * s.page + k.slot) * record;
+        *reinterpret_cast<uint2 *>(dst + (key ? 0 : s.d / 2) + 8 * item) = codes;
+        if (item % group_lanes == 0)
+            *reinterpret_cast<uint32_t *>(dst + s.d + (key ? 0 : 4 * s.d >> c.group_log2) + 4 * (item / group_lanes)) = sm;
+    }
+}
+
+struct ReadOut {
+    uint16_t *k, *v;
+    int64_t k_stride, v_stride;
+    int *status;
+};
+
+// Work item: 16 elements of one head's key and value.
+template <bool BF, bool FOUR>
+__global__ void __launch_bounds__(kThreads)
+    read_kernel(AttnShape s, AttnBatch b, AttnCache c, Cache4 c4, ReadOut o, int tokens_per_cta) {
+    __shared__ Token tok[kMaxTokens];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * tokens_per_cta, nt = min(tokens_per_cta, b.tokens - t0);
+    if (warp < nt) {
+        const Token k = find_token(b, s, FOUR ? c4.pages : c.pages, t0 + warp, nullptr, 0, o.status);
+        if (lane == 0) tok[warp] = k;
+    }
+    __syncthreads();
+    const int per_head = s.d / 16, per_token = s.hkv * per_head;
+    for (int w = threadIdx.x; w < nt * per_token; w += kThreads) {
+        const int ti = w / per_token, u = w - ti * per_token, head = u / per_head, item = u - head * per_head;
+        const Token k = tok[ti];
+        if (k.page < 0) continue;
+        const int64_t t = t0 + ti, slot = static_cast<int64_t>(head) * s.page + k.slot;
+        uint4 out[4];
+        if constexpr (FOUR) {
+            const uint8_t *src = c4.kv + k.page * c4.page_stride + slot * record_bytes(s.d, c4.group_log2);
+            const uint2 kc = *reinterpret_cast<const uint2 *>(src + 8 * item);
+            const uint2 vc = *reinterpret_cast<const uint2 *>(src + s.d / 2 + 8 * item);
+            const uint32_t *params = reinterpret_cast<const uint32_t *>(src + s.d);
+            const int g = item >> (c4.group_log2 - 4);
+            const uint32_t kp = params[g], vp = params[(s.d >> c4.group_log2) + g];
+            out[0] = values_of<BF>(kc.x, both_low(kp), both_high(kp));
+            out[1] = values_of<BF>(kc.y, both_low(kp), both_high(kp));
+            out[2] = values_of<BF>(vc.x, both_low(vp), both_high(vp));
+            out[3] = values_of<BF>(vc.y, both_low(vp), both_high(vp));
+        } else {
+            const int64_t at = k.page * c.page_stride + slot * s.d + 16 * item;
+            out[0] = *reinterpret_cast<const uint4 *>(c.k + at);
+            out[1] = *reinterpret_cast<const uint4 *>(c.k + at + 8);
+            out[2] = *reinterpret_cast<const uint4 *>(c.v + at);
+            out[3] = *reinterpret_cast<const uint4 *>(c.v + at + 8);
+        }
+        uint4 *kd = reinterpret_cast<uint4 *>(o.k + t * o.k_stride + head * s.d + 16 * item);
+        uint4 *vd = reinterpret_cast<uint4 *>(o.v + t * o.v_stride + head * s.d + 16 * item);
+        kd[0] = out[0];
+        kd[1] = out[1];
+        vd[0] = out[2];
+        vd[1] = out[3];
+    }
+}
+
+// Tokens of a CTA: one until the GPU is full, then up to eight.
+int tokens_each(int tokens) { return std::max(1, std::min(kMaxTokens, tokens / 1216)); }
+
+}  // namespace
+
+cudaError_t launch_attn_append4(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AppendCall &a, bool bf16,
+                                cudaStream_t st) {
+    const int per = tokens_each(b.tokens), grid = (b.tokens + per - 1) / per;
+    if (bf16) append4_kernel<true><<<grid, kThreads, 0, st>>>(s, b, c, a, per);
+    else append4_kernel<false><<<grid, kThreads, 0, st>>>(s, b, c, a, per);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_read(const AttnShape &s, const AttnBatch &b, const AttnCache *c, const Cache4 *c4, uint16_t *k,
+                             int64_t k_stride, uint16_t *v, int64_t v_stride, bool bf16, int *status, cudaStream_t st) {
+    const ReadOut o{k, v, k_stride, v_stride, status};
+    const int per = tokens_each(b.tokens), grid = (b.tokens + per - 1) / per;
+    auto kernel = !c4 ? read_kernel<false, false> : bf16 ? read_kernel<true, true> : read_kernel<false, true>;
+    kernel<<<grid, kThreads, 0, st>>>(s, b, c ? *c : AttnCache{}, c4 ? *c4 : Cache4{}, o, per);
+    return cudaGetLastError();
+}
+
+}  // namespace q4

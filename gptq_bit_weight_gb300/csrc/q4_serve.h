@@ -96,12 +96,21 @@ cudaError_t launch_rope_table(float2 *table, const double *inv_freq, double leng
 cudaError_t launch_attn_append(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AppendCall &a,
                                bool bf16, cudaStream_t st);
 
+// A cache of 4 bits (q4_cache4.cuh).
+struct Cache4;
+cudaError_t launch_attn_append4(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AppendCall &a, bool bf16,
+                                cudaStream_t st);
+// The step's new tokens out of either cache (the other one is NULL).
+cudaError_t launch_attn_read(const AttnShape &s, const AttnBatch &b, const AttnCache *c, const Cache4 *c4, uint16_t *k,
+                             int64_t k_stride, uint16_t *v, int64_t v_stride, bool bf16, int *status, cudaStream_t st);
+
 struct AttendCall {
     const uint16_t *q;
     uint16_t *out;
     int64_t q_stride, out_stride;
     float scale;
     int window;
+    int sinks;                   // first tokens seen besides the window; 0 without one
     int max_q;
     int *status;
     float *ws;                   // pieces of cut items
@@ -116,6 +125,8 @@ cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const A
 size_t attend_tc_ws_bytes(int ctas);
 cudaError_t launch_attend_tc(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
                              cudaStream_t st);
+cudaError_t launch_attend_any(const AttnShape &s, const AttnBatch &b, const AttnCache *c, const Cache4 *c4,
+                              const AttendCall &a, bool bf16, cudaStream_t st);
 // Tensor map of the queries [tokens][heads][d]: boxes of 64 columns, a
 // group's heads and `rows` tokens.
 cudaError_t encode_queries(CUtensorMap *map, const void *ptr, const AttnShape &s, int64_t stride, int tokens,

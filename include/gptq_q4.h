@@ -617,9 +617,147 @@ int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const g
                         const gptq_q4_batch *batch, float scale, int window, void *out, int64_t out_stride,
                         cudaStream_t stream);
 
+/* gptq_q4_attn_attend with the first `sinks` tokens of each context visible
+ * besides the window: token j <= i is seen if j > i - window or j < sinks.
+ * Pages that hold neither a token below `sinks` nor one of a window are not
+ * read, and their table entries may be anything.  sinks = 0, or window = 0
+ * (all tokens are visible), is gptq_q4_attn_attend.  The sums, and their
+ * order, may differ from that call's where sinks > 0 adds no token (a context
+ * within its window).  Errors: as gptq_q4_attn_attend, and INVALID_ARGUMENT for
+ * sinks < 0. */
+int gptq_q4_attn_attend_sinks(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache *cache,
+                              const gptq_q4_batch *batch, float scale, int window, int sinks, void *out,
+                              int64_t out_stride, cudaStream_t stream);
+
+/* What the cache holds for the step's new tokens:
+ *   k_out, v_out  device [tokens][kv_heads * head_dim], row strides k_stride,
+ *                 v_stride; 16-byte aligned, strides multiples of 8, not overlapping
+ * (a batch whose requests have q_len = kv_len reads whole contexts).  Rows
+ * that no request owns are left alone, as are those of a token whose index or
+ * page index, or whose request's length, is outside its range;
+ * gptq_q4_attn_device_error reports those.  Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED (batch > 4096), CUDA_ERROR. */
+int gptq_q4_attn_read(gptq_q4_attn h, const gptq_q4_cache *cache, const gptq_q4_batch *batch, void *k_out,
+                      int64_t k_stride, void *v_out, int64_t v_stride, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache held in 4 bits, for the same handle and batch.
+ *
+ * Keys and values of one layer, a record of bytes for each token and head:
+ *   kv  device uint8 [pages][kv_heads][page_size][record], 16-byte aligned;
+ *       page_stride bytes from page to page (at least kv_heads * page_size *
+ *       record, a multiple of 16);  record = head_dim + 8 * head_dim / group
+ * A record holds, in this order,
+ *   head_dim / 2 bytes     codes of the key: eight to a 32-bit word, code e of
+ *                          a word's eight at bit 4 (e / 2) + 16 (e % 2)
+ *   head_dim / 2 bytes     codes of the value
+ *   4 * head_dim / group   for each group of the key its step s and least value m
+ *   4 * head_dim / group   for each group of the value
+ * with s and m of the handle's 16-bit type and groups of 32 or 64 elements.
+ * Code c stands for m + s * c, rounded to the handle's type. */
+typedef struct {
+    void *kv;
+    int pages;
+    int64_t page_stride;
+    int group;
+} gptq_q4_cache4;
+
+/* gptq_q4_attn_append into a cache of 4 bits.  Keys are rotated and rounded to
+ * the handle's type (in enough precision that the rounding is of the exact
+ * products' sum) and values taken as they are; then for each group
+ *   m = the least element,  s = (greatest - m) / 15 rounded to the type,
+ *   c = (x - m) / s rounded to the nearest (ties to even), at most 15;  0 where s is 0.
+ * A group with an infinity or NaN, or whose span is past fp32, reads as NaN throughout. */
+int gptq_q4_attn_append4(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const gptq_q4_cache4 *cache,
+                         const gptq_q4_batch *batch, const int32_t *positions, void *q_out, int64_t q_stride,
+                         cudaStream_t stream);
+
+/* gptq_q4_attn_attend_sinks and gptq_q4_attn_read over a cache of 4 bits: over
+ * the values that its codes stand for. */
+int gptq_q4_attn_attend4(gptq_q4_attn h, const void *q, int64_t q_stride, const gptq_q4_cache4 *cache,
+                         const gptq_q4_batch *batch, float scale, int window, int sinks, void *out,
+                         int64_t out_stride, cudaStream_t stream);
+int gptq_q4_attn_read4(gptq_q4_attn h, const gptq_q4_cache4 *cache, const gptq_q4_batch *batch, void *k_out,
+                       int64_t k_stride, void *v_out, int64_t v_stride, cudaStream_t stream);
+
 /* As gptq_q4_device_error and gptq_q4_free, for an attention handle. */
 int gptq_q4_attn_device_error(gptq_q4_attn h);
 void gptq_q4_attn_free(gptq_q4_attn h);
+
+/* ------------------------------------------------------------------------
+ * The pages of a cache: which are free, forks that share them, copies, and
+ * moving those in use together.
+ *
+ * A handle serves the caches of all layers, which share tables and page
+ * numbers.  No counts are kept: a page is in use if the table, up to the
+ * lengths, names it, however often (requests may share pages), and with a
+ * window only if it holds one of the last `window` tokens or of the first
+ * `sinks`.  (A step of n new tokens reads window - 1 + n tokens back from the
+ * length after it; give a window that covers the next step's.)  Entries that
+ * are needed but negative are no page and are passed over, ones past the last
+ * page are and are reported by gptq_q4_pages_device_error.
+ *
+ * The handle has a workspace: one stream at a time.  It does not own the
+ * buffers, which have to outlive it. */
+typedef struct gptq_q4_pages_s *gptq_q4_pages;
+
+/* One buffer with `bytes` of each page (k, v or kv of a layer's cache), page
+ * p at data + p * stride; 16-byte aligned, bytes and stride multiples of 16. */
+typedef struct {
+    void *data;
+    int64_t bytes, stride;
+} gptq_q4_buffer;
+
+/* The table's rows, as in gptq_q4_batch. */
+typedef struct {
+    int32_t *table, *kv_len;
+    int64_t table_stride;
+    int width, batch;
+} gptq_q4_rows;
+
+/* buffers: host, n of them (0: only the numbers are managed); pages at most
+ * 2^22; page_size positive.  Device memory: about 12 bytes a page.
+ * Synchronizes.  NULL on error: INVALID_ARGUMENT, UNSUPPORTED (device not
+ * sm_103), OUT_OF_MEMORY, CUDA_ERROR. */
+gptq_q4_pages gptq_q4_pages_make(const gptq_q4_buffer *buffers, int n, int pages, int page_size);
+
+/* The pages that are not in use: ids, device int32 [pages], ascending, then
+ * -1; count, device int32 [1].  Errors: INVALID_ARGUMENT, CUDA_ERROR. */
+int gptq_q4_pages_free_list(gptq_q4_pages h, const gptq_q4_rows *rows, int window, int sinks, int32_t *ids,
+                            int32_t *count, cudaStream_t stream);
+
+/* Rows child[i] become copies of rows parent[i], i < n: the entries up to the
+ * parent's length (-1 past them) and the length.  A page that the parent has
+ * filled in part is not shared: its contents go to page fresh[i] in every
+ * buffer, and the child's entry is fresh[i] (not read where the length is a
+ * multiple of page_size).  A negative parent or child, or parent = child, is
+ * no fork.  Left out, and reported by gptq_q4_pages_device_error: a fork whose
+ * row numbers, parent's length or pages are outside their range, whose child
+ * is the parent of another or the child of an earlier one, or whose fresh page
+ * is that of an earlier one.  fresh pages have to be free.  parent, child, fresh:
+ * device int32 [n], n at most 4096.  Errors: INVALID_ARGUMENT, UNSUPPORTED (n),
+ * CUDA_ERROR. */
+int gptq_q4_pages_fork(gptq_q4_pages h, const gptq_q4_rows *rows, const int32_t *parent, const int32_t *child,
+                       const int32_t *fresh, int n, cudaStream_t stream);
+
+/* Contents of pages src[i] to pages dst[i], i < n, in every buffer; a negative
+ * number is no copy, one past the last page neither and is reported.  No page
+ * may be a destination twice, or a destination and a source.  src, dst: device
+ * int32 [n].  Errors: INVALID_ARGUMENT, CUDA_ERROR. */
+int gptq_q4_pages_copy(gptq_q4_pages h, const int32_t *src, const int32_t *dst, int n, cudaStream_t stream);
+
+/* Moves the pages in use together: with n of them, those numbered n and up go,
+ * in ascending order, to the numbers below n that are not in use, ascending,
+ * in every buffer; the others stay.  table_out (row stride out_stride; the
+ * table itself if equal) gets the new numbers of the entries in use, -1
+ * elsewhere; count, device int32 [1], gets n.  Pages from n on are free
+ * afterwards.  Errors: INVALID_ARGUMENT, CUDA_ERROR. */
+int gptq_q4_pages_compact(gptq_q4_pages h, const gptq_q4_rows *rows, int window, int sinks, int32_t *table_out,
+                          int64_t out_stride, int32_t *count, cudaStream_t stream);
+
+/* As gptq_q4_device_error and gptq_q4_free. */
+int gptq_q4_pages_device_error(gptq_q4_pages h);
+void gptq_q4_pages_free(gptq_q4_pages h);
 
 /* Status and message of the last call made on this host thread.
  * "Inference Backends", "Hardware, dependency, and format requirements":
