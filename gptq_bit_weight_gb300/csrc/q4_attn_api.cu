@@ -214,7 +214,12 @@ int attend(gptq_q4_attn h, const void *q, int64_t q_stride, const Cache *cache, 
         else e = (chunk ? q4::launch_attend_tc : q4::launch_attend_stream)(s, batch_view(batch), view, a, bf16, stream);
     } else {
         const q4::Cache4 view = cache_view(cache);
-        e = q4::launch_attend_any(s, batch_view(batch), nullptr, &view, a, bf16, stream);
+        const int64_t rows = static_cast<int64_t>(batch->max_q) * s.group;
+        if (rows <= 32)
+            e = (rows <= 8 ? q4::launch_attend_stream4_8 : rows <= 16 ? q4::launch_attend_stream4_16 : q4::launch_attend_stream4_32)(
+                s, batch_view(batch), view, a, bf16, stream);
+        else
+            e = q4::launch_attend_any(s, batch_view(batch), nullptr, &view, a, bf16, stream);
     }
     if (e) return api_cuda_fail(e, "attention launch");
     q4::api_count_launches(1);
@@ -258,8 +263,8 @@ gptq_q4_attn gptq_q4_attn_make(int q_heads, int kv_heads, int head_dim, int page
     if (!e) e = cudaMemset(h->status, 0, sizeof(int));
     h->ctas = q4::device_sm_count();
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->ws), std::max(q4::attend_stream_ws_bytes(h->ctas), q4::attend_tc_ws_bytes(h->ctas)));
-    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->tickets), h->ctas * sizeof(int));
-    if (!e) e = cudaMemset(h->tickets, 0, h->ctas * sizeof(int));
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->tickets), 2 * h->ctas * sizeof(int));
+    if (!e) e = cudaMemset(h->tickets, 0, 2 * h->ctas * sizeof(int));
     if (!e) e = cudaDeviceSynchronize();
     if (e) {
         api_cuda_fail(e, "allocating the attention handle");
@@ -395,7 +400,7 @@ int gptq_q4_attn_device_error(gptq_q4_attn h) {
     if (!e) e = cudaMemcpy(&flag, h->status, sizeof(int), cudaMemcpyDeviceToHost);
     if (!e && flag) e = cudaMemset(h->status, 0, sizeof(int));
     // a kernel that gave up may have left pieces uncounted
-    if (!e && (flag & q4::kAttnTimeout)) e = cudaMemset(h->tickets, 0, h->ctas * sizeof(int));
+    if (!e && (flag & q4::kAttnTimeout)) e = cudaMemset(h->tickets, 0, 2 * h->ctas * sizeof(int));
     if (e) return api_cuda_fail(e, "reading the attention handle's status word");
     if (flag)
         return api_failf(GPTQ_Q4_DEVICE_FAULT, "attention kernels reported status 0x%x:%s%s%s%s%s", flag,

@@ -26,14 +26,18 @@ struct FastDiv {
     }
 };
 
-struct SchedParams {
+template <bool SINKS>
+struct SchedParamsT {
+    static constexpr bool kSinks = SINKS;
     AttnBatch b;
     int hkv, page_log2, window;
     int kt_log2;      // log2 of the tokens of a key tile
     FastDiv group;    // query heads of a key/value head
     int step_log2;    // log2 of the rows of a row tile, or -1:
     FastDiv tokens;   // tokens of a row tile, where tiles hold whole tokens
+    int sinks;        // if kSinks: first tokens that are visible besides the window
 };
+using SchedParams = SchedParamsT<false>;
 
 struct Item {
     int b, head, tile, tiles;
@@ -41,16 +45,36 @@ struct Item {
     int t0, t1;      // first and last token of the row tile
     int lo, hi;      // keys [lo, hi) that some row of the tile sees; hi <= 0: none
     int first, n;    // key tiles
+    int near;        // if kSinks: of these, tiles of first tokens; the others are `first` tiles further on
     int u;           // the item's first unit
 };
+// The key tile that unit j of an item is.
+template <class P>
+__device__ __forceinline__ int key_tile(const P &, const Item &it, int j) {
+    if constexpr (P::kSinks) return j < it.near ? j : it.first + j;
+    else return it.first + j;
+}
+// Whether some row of the item sees a key of [key, key + n), or all of these are seen or of no harm.
+template <class P>
+__device__ __forceinline__ bool sees_some(const P &p, const Item &it, int key, int n) {
+    if constexpr (P::kSinks) return key < it.hi && (key + n > it.lo || key < p.sinks);
+    else return key < it.hi && key + n > it.lo;
+}
+template <class P>
+__device__ __forceinline__ bool sees_all(const P &p, const Item &it, int key, int n) {
+    if constexpr (P::kSinks) return key + n <= it.hi && (key >= it.lo || key + n <= p.sinks);
+    else return key + n <= it.hi && key >= it.lo;
+}
 
-__device__ __forceinline__ int row_tiles(const SchedParams &p, int ql) {
+template <class P>
+__device__ __forceinline__ int row_tiles(const P &p, int ql) {
     if (p.step_log2 < 0) return p.tokens(ql + static_cast<int>(p.tokens.d) - 1);
     return (ql * static_cast<int>(p.group.d) + (1 << p.step_log2) - 1) >> p.step_log2;
 }
 
 // The tokens, keys and key tiles of row tile `it.tile`.
-__device__ __forceinline__ void fill_tile(const SchedParams &p, Item &it) {
+template <class P>
+__device__ __forceinline__ void fill_tile(const P &p, Item &it) {
     if (p.step_log2 < 0) {
         it.t0 = it.tile * static_cast<int>(p.tokens.d);
         it.t1 = min(it.t0 + static_cast<int>(p.tokens.d), it.ql) - 1;
@@ -65,10 +89,17 @@ __device__ __forceinline__ void fill_tile(const SchedParams &p, Item &it) {
     it.first = it.lo >> p.kt_log2;
     const int kt = 1 << p.kt_log2;
     it.n = it.hi > 0 ? ((it.hi + kt - 1) >> p.kt_log2) - it.first : 1;
+    if constexpr (P::kSinks) {
+        // tiles of first tokens, as far as the window's do not hold them anyway
+        it.near = it.hi > 0 ? min((p.sinks + kt - 1) >> p.kt_log2, it.first) : 0;
+        it.first -= it.near;
+        it.n += it.near;
+    }
 }
 
 // Units of row tiles i0, i0 + stride, .. of a request with ql tokens and a context of kv.
-__device__ __forceinline__ long long tile_units(const SchedParams &p, int ql, int kv, int i0, int stride) {
+template <class P>
+__device__ __forceinline__ long long tile_units(const P &p, int ql, int kv, int i0, int stride) {
     Item it;
     it.ql = ql;
     it.kv = kv;
@@ -82,7 +113,8 @@ __device__ __forceinline__ long long tile_units(const SchedParams &p, int ql, in
     return sum;
 }
 
-__device__ __forceinline__ void load_item_request(const SchedParams &p, Item &it) {
+template <class P>
+__device__ __forceinline__ void load_item_request(const P &p, Item &it) {
     const Request r = load_request(p.b, it.b, p.page_log2);
     it.q0 = r.q0;
     it.ql = r.ql;
@@ -91,7 +123,8 @@ __device__ __forceinline__ void load_item_request(const SchedParams &p, Item &it
 }
 
 // Step to the next item; false after the last.
-__device__ __forceinline__ bool next_item(const SchedParams &p, Item &it) {
+template <class P>
+__device__ __forceinline__ bool next_item(const P &p, Item &it) {
     it.u += it.n;
     if (++it.tile == it.tiles) {
         it.tile = 0;
@@ -121,7 +154,8 @@ struct SchedSmem {
 };
 
 // Units of a lane's request (or of none: ql 0), by a whole warp.
-__device__ __forceinline__ long long request_units(const SchedParams &p, const Request &r) {
+template <class P>
+__device__ __forceinline__ long long request_units(const P &p, const Request &r) {
     // a request of many row tiles is summed by all lanes
     const bool many = row_tiles(p, r.ql) > 4;
     long long units = many ? 0 : tile_units(p, r.ql, r.kv, 0, 1);
@@ -157,7 +191,8 @@ __device__ __forceinline__ Share share_of(long long total, int cta, int ctas, in
 }
 // The row tile of it's request and head that holds unit `rem` of theirs, by a
 // whole warp; `at` is that unit's number.  Sets it.tile and it.u.
-__device__ __forceinline__ void find_tile(const SchedParams &p, Item &it, int rem, int at) {
+template <class P>
+__device__ __forceinline__ void find_tile(const P &p, Item &it, int rem, int at) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int base = 0;; base += 32) {
@@ -190,8 +225,8 @@ __device__ __forceinline__ void find_tile(const SchedParams &p, Item &it, int re
 // threads of the CTA, which it synchronizes; `sm` must not be in use before or
 // within the call.  A call of up to 32 requests is short, and this is at its
 // head: every warp works its share out for itself.
-template <int NT>
-__device__ Share sched_share(const SchedParams &p, SchedSmem &sm, int cta, int ctas, int *status, Item &it) {
+template <int NT, class P>
+__device__ Share sched_share(const P &p, SchedSmem &sm, int cta, int ctas, int *status, Item &it) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.b.batch <= 32) {
         Request r{0, 0, 0, false};

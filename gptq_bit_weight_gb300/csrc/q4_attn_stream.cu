@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int j0 = max(sh.begin - it.u, 0);
             const int j1 = min(sh.end - it.u, it.n);
             const PageWalk walk(a.p, it, a.c.pages);
-            TilePages next = walk.tile(it, j0, bad);
+            TilePages next = walk.tile(a.p, it, j0, bad);
             for (int j = j0; j < j1; ++j, seq += 2) {
                 const TilePages t = next;
-                if (j + 1 < j1) next = walk.tile(it, j + 1, bad);            // on its way while this one waits
+                if (j + 1 < j1) next = walk.tile(a.p, it, j + 1, bad);            // on its way while this one waits
                 const int s = seq % S;
                 if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
                 if (!alive) break;

@@ -535,10 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++items;
                 }
                 const PageWalk walk(a.p, it, a.c.pages);
-                TilePages next = walk.tile(it, part.j0, bad);
+                TilePages next = walk.tile(a.p, it, part.j0, bad);
                 for (int j = part.j0; j < part.j1; ++j, seq += 2) {
                     const TilePages t = next;
-                    if (j + 1 < part.j1) next = walk.tile(it, j + 1, bad);       // on its way while this one waits
+                    if (j + 1 < part.j1) next = walk.tile(a.p, it, j + 1, bad);       // on its way while this one waits
                     const int s = seq % S, key_t = (it.first + j) << kKtLog2;
                     if (seq >= S) alive = wait_all(alive, empty(s), ((seq / S) & 1) ^ 1);
                     if (!alive) break;

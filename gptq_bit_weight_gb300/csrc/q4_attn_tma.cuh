@@ -73,15 +73,17 @@ struct PageWalk {
     const int32_t *table;
     int page_log2, box_log2, pages;      // tokens of a page and of a box (at most a tile's), pages of the cache
 
-    __device__ PageWalk(const SchedParams &p, const Item &it, int cache_pages)
+    template <class P>
+    __device__ PageWalk(const P &p, const Item &it, int cache_pages)
         : table(p.b.table + it.b * p.b.table_stride),
           page_log2(p.page_log2),
           box_log2(min(p.page_log2, kKtLog2)),
           pages(cache_pages) {}
-    // Tile j (counted from it.first); a page index outside the cache becomes page 0 and sets `bad`.
-    __device__ __forceinline__ TilePages tile(const Item &it, int j, int &bad) const {
-        const int lane = threadIdx.x & 31, key_t = (it.first + j) << kKtLog2, key = key_t + (lane << box_log2);
-        const bool mine = lane < (kKt >> box_log2) && key < it.hi && key + (1 << box_log2) > it.lo;
+    // The item's unit j; a page index outside the cache becomes page 0 and sets `bad`.
+    template <class P>
+    __device__ __forceinline__ TilePages tile(const P &p, const Item &it, int j, int &bad) const {
+        const int lane = threadIdx.x & 31, key_t = key_tile(p, it, j) << kKtLog2, key = key_t + (lane << box_log2);
+        const bool mine = lane < (kKt >> box_log2) && sees_some(p, it, key, 1 << box_log2);
         TilePages t;
         t.page = mine ? table[key >> page_log2] : 0;
         if (t.page < 0 || t.page >= pages) {

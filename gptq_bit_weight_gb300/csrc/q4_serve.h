@@ -114,7 +114,7 @@ struct AttendCall {
     int max_q;
     int *status;
     float *ws;                   // pieces of cut items
-    int *tickets;                // [ctas], zero between calls
+    int *tickets;                // [2 * ctas], zero between calls
     int ctas;                    // one for each SM
 };
 // few rows for each key/value head (q4_attn_stream.cu)
@@ -125,6 +125,13 @@ cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const A
 size_t attend_tc_ws_bytes(int ctas);
 cudaError_t launch_attend_tc(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
                              cudaStream_t st);
+// few rows over a cache of 4 bits, in row tiles of 8, 16 and 32 (q4_attn_stream4*.cu); pieces as launch_attend_tc's
+cudaError_t launch_attend_stream4_8(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
+                                    bool bf16, cudaStream_t st);
+cudaError_t launch_attend_stream4_16(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
+                                     bool bf16, cudaStream_t st);
+cudaError_t launch_attend_stream4_32(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
+                                     bool bf16, cudaStream_t st);
 cudaError_t launch_attend_any(const AttnShape &s, const AttnBatch &b, const AttnCache *c, const Cache4 *c4,
                               const AttendCall &a, bool bf16, cudaStream_t st);
 // Tensor map of the queries [tokens][heads][d]: boxes of 64 columns, a
