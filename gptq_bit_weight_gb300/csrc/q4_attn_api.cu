@@ -263,8 +263,8 @@ gptq_q4_attn gptq_q4_attn_make(int q_heads, int kv_heads, int head_dim, int page
     if (!e) e = cudaMemset(h->status, 0, sizeof(int));
     h->ctas = q4::device_sm_count();
     if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->ws), std::max(q4::attend_stream_ws_bytes(h->ctas), q4::attend_tc_ws_bytes(h->ctas)));
-    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->tickets), 2 * h->ctas * sizeof(int));
-    if (!e) e = cudaMemset(h->tickets, 0, 2 * h->ctas * sizeof(int));
+    if (!e) e = cudaMalloc(reinterpret_cast<void **>(&h->tickets), 4 * h->ctas * sizeof(int));
+    if (!e) e = cudaMemset(h->tickets, 0, 4 * h->ctas * sizeof(int));
     if (!e) e = cudaDeviceSynchronize();
     if (e) {
         api_cuda_fail(e, "allocating the attention handle");
@@ -400,7 +400,7 @@ int gptq_q4_attn_device_error(gptq_q4_attn h) {
     if (!e) e = cudaMemcpy(&flag, h->status, sizeof(int), cudaMemcpyDeviceToHost);
     if (!e && flag) e = cudaMemset(h->status, 0, sizeof(int));
     // a kernel that gave up may have left pieces uncounted
-    if (!e && (flag & q4::kAttnTimeout)) e = cudaMemset(h->tickets, 0, 2 * h->ctas * sizeof(int));
+    if (!e && (flag & q4::kAttnTimeout)) e = cudaMemset(h->tickets, 0, 4 * h->ctas * sizeof(int));
     if (e) return api_cuda_fail(e, "reading the attention handle's status word");
     if (flag)
         return api_failf(GPTQ_Q4_DEVICE_FAULT, "attention kernels reported status 0x%x:%s%s%s%s%s", flag,

@@ -152,6 +152,12 @@ struct SchedSmem {
     int b, head, tile, q0, ql, kv;
     int rem, u;
 };
+// Of team_share: where each team's first unit is.
+template <int TEAMS>
+struct TeamSchedSmem {
+    long long warp_sum[32];
+    int b[TEAMS], head[TEAMS], rem[TEAMS], q0[TEAMS], ql[TEAMS], kv[TEAMS];
+};
 
 // Units of a lane's request (or of none: ql 0), by a whole warp.
 template <class P>
@@ -219,6 +225,104 @@ __device__ __forceinline__ void find_tile(const P &p, Item &it, int rem, int at)
         }
         rem -= __shfl_sync(0xffffffffu, pre, 31);
     }
+}
+
+// The share `cta` of a call of up to 32 requests and, if it has units, its
+// first item, by a whole warp for itself.
+template <class P>
+__device__ __forceinline__ Share warp_share(const P &p, int cta, int ctas, int *status, Item &it) {
+    const int lane = threadIdx.x & 31;
+    Request r{0, 0, 0, false};
+    if (lane < p.b.batch) r = load_request(p.b, lane, p.page_log2);
+    if (r.bad && cta == 0) atomicOr(status, kAttnBadBatch);
+    const long long units = request_units(p, r), mine = units * p.hkv, upto = prefix_sum(mine);
+    const Share s = share_of(__shfl_sync(0xffffffffu, upto, 31), cta, ctas, status);
+    if (s.begin < s.end) {
+        const int who = __ffs(__ballot_sync(0xffffffffu, s.begin < upto)) - 1;
+        const uint32_t each = static_cast<uint32_t>(__shfl_sync(0xffffffffu, units, who));
+        const uint32_t rem = static_cast<uint32_t>(s.begin - __shfl_sync(0xffffffffu, upto - mine, who));
+        it.b = who;
+        it.head = static_cast<int>(rem / each);
+        it.q0 = __shfl_sync(0xffffffffu, r.q0, who);
+        it.ql = __shfl_sync(0xffffffffu, r.ql, who);
+        it.kv = __shfl_sync(0xffffffffu, r.kv, who);
+        it.tiles = row_tiles(p, it.ql);
+        find_tile(p, it, static_cast<int>(rem - it.head * each), s.begin);
+        fill_tile(p, it);
+    }
+    return s;
+}
+
+// The shares of a CTA's teams, one each, of TEAMS * ctas in all; a warp gets
+// that of `team`.  Called by all NT threads of the CTA, which it synchronizes.
+template <int NT, int TEAMS, class P>
+__device__ Share team_share(const P &p, TeamSchedSmem<TEAMS> &sm, int team, int cta, int ctas, int *status, Item &it) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mine_cta = cta * TEAMS + team, all = ctas * TEAMS;
+    if (p.b.batch <= 32) {
+        const Share s = warp_share(p, mine_cta, all, status, it);
+        __syncthreads();
+        return s;
+    }
+    const int chunk = (p.b.batch + NT - 1) / NT;     // requests of a thread, in order
+    long long mine = 0, last = 0;
+    Request r{0, 0, 0, false};
+#pragma unroll 1
+    for (int i = 0; i < chunk; ++i) {
+        const int b = tid * chunk + i;
+        r = Request{0, 0, 0, false};
+        if (b < p.b.batch) {
+            r = load_request(p.b, b, p.page_log2);
+            if (r.bad && cta == 0) atomicOr(status, kAttnBadBatch);
+        }
+        last = request_units(p, r);
+        mine += last * p.hkv;
+    }
+    const long long upto = prefix_sum(mine);
+    if (lane == 31) sm.warp_sum[warp] = upto;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll 1
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sm.warp_sum[w];
+        total += sm.warp_sum[w];
+    }
+    before += upto - mine;
+#pragma unroll 1
+    for (int t = 0; t < TEAMS; ++t) {
+        const Share s = share_of(total, cta * TEAMS + t, all, status);
+        if (!(s.begin < s.end && before <= s.begin && s.begin < before + mine)) continue;
+        // this thread's requests hold the first unit: find which
+        uint32_t rem = static_cast<uint32_t>(s.begin - before), units = static_cast<uint32_t>(last);
+        Request q = r;
+        int b = tid * chunk;
+#pragma unroll 1
+        for (;; ++b) {
+            if (chunk > 1) {
+                q = load_request(p.b, b, p.page_log2);
+                units = static_cast<uint32_t>(tile_units(p, q.ql, q.kv, 0, 1));
+            }
+            if (rem < units * p.hkv) break;
+            rem -= units * p.hkv;
+        }
+        sm.b[t] = b;
+        sm.head[t] = static_cast<int>(rem / units);
+        sm.rem[t] = static_cast<int>(rem - sm.head[t] * units);
+        sm.q0[t] = q.q0;
+        sm.ql[t] = q.ql;
+        sm.kv[t] = q.kv;
+    }
+    __syncthreads();
+    const Share s = share_of(total, mine_cta, all, status);
+    if (s.begin >= s.end) return s;
+    it.b = sm.b[team];
+    it.head = sm.head[team];
+    it.q0 = sm.q0[team];
+    it.ql = sm.ql[team];
+    it.kv = sm.kv[team];
+    it.tiles = row_tiles(p, it.ql);
+    find_tile(p, it, sm.rem[team], s.begin);
+    fill_tile(p, it);
+    return s;
 }
 
 // This CTA's share and, if it has one, its first item.  Called by all NT

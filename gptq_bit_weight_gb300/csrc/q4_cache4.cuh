@@ -38,7 +38,12 @@ __device__ __forceinline__ uint32_t sub_2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ uint32_t both_low(uint32_t v) { return __byte_perm(v, v, 0x1010); }     // (low, low) halves
 __device__ __forceinline__ uint32_t both_high(uint32_t v) { return __byte_perm(v, v, 0x3232); }
-__device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask, uint32_t bits) { return (v & mask) | bits; }
+// (v & mask) | bits in one instruction (from C++ it becomes two, each with a constant of its own).
+__device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+    return d;
+}
 
 // Codes 2 i and 2 i + 1 of a word, i = 0 .. 3, as 16-bit numbers 0 .. 15.
 template <bool BF>

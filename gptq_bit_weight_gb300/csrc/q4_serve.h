@@ -114,7 +114,7 @@ struct AttendCall {
     int max_q;
     int *status;
     float *ws;                   // pieces of cut items
-    int *tickets;                // [2 * ctas], zero between calls
+    int *tickets;                // [4 * ctas], zero between calls
     int ctas;                    // one for each SM
 };
 // few rows for each key/value head (q4_attn_stream.cu)
