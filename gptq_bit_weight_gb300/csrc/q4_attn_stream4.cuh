@@ -306,38 +306,76 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                 lim_lo[n][e] = window > 0 ? lim[n][e] - window : -1;
             }
         }
-        // One tile: its scores against the rows' references, weights, sums.  edge: some token is hidden from some row
-        // (in a few instructions beside the rest: a copy of the code for it ran cold, 5 us where a tile takes 1).
-        auto tile = [&](const uint8_t *stage, int key0, bool edge) {
-            float s[kBlocks][NT][4];                     // token key_row (+ 8 from e = 2 on), row 8 n + 2 t4 + (e & 1)
+        // The products of two tiles go together, a tile's values and the next one's keys: neither waits for the other.
+        // Scores of a tile: token key_row (+ 8 from e = 2 on, + 16 b), row 8 n + 2 t4 + (e & 1).
+        float s[kBlocks][NT][4];
+        uint32_t pb[kBlocks][NT][2];
+        auto keys = [&](const uint8_t *stage, int b) {
+            const uint8_t *r0 = stage + k_at + 16 * b * R, *r1 = r0 + 8 * R;
+            uint32_t w0[WORDS], w1[WORDS];
+            if constexpr (WORDS == 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(r0 + k_codes), y = *reinterpret_cast<const uint4 *>(r1 + k_codes);
+                w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+                w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(r0 + k_codes), y = *reinterpret_cast<const uint2 *>(r1 + k_codes);
+                w0[0] = x.x, w0[1] = x.y;
+                w1[0] = y.x, w1[1] = y.y;
+            }
+            const uint32_t p0 = *reinterpret_cast<const uint32_t *>(r0 + k_param), p1 = *reinterpret_cast<const uint32_t *>(r1 + k_param);
+            const uint32_t s0 = both_low(p0), m0 = both_high(p0), s1 = both_low(p1), m1 = both_high(p1);
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const uint8_t *r0 = stage + k_at + 16 * b * R, *r1 = r0 + 8 * R;
-                uint32_t w0[WORDS], w1[WORDS];
-                if constexpr (WORDS == 4) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(r0 + k_codes), y = *reinterpret_cast<const uint4 *>(r1 + k_codes);
-                    w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
-                    w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(r0 + k_codes), y = *reinterpret_cast<const uint2 *>(r1 + k_codes);
-                    w0[0] = x.x, w0[1] = x.y;
-                    w1[0] = y.x, w1[1] = y.y;
-                }
-                const uint32_t p0 = *reinterpret_cast<const uint32_t *>(r0 + k_param), p1 = *reinterpret_cast<const uint32_t *>(r1 + k_param);
-                const uint32_t s0 = both_low(p0), m0 = both_high(p0), s1 = both_low(p1), m1 = both_high(p1);
+            for (int n = 0; n < NT; ++n) s[b][n][0] = s[b][n][1] = s[b][n][2] = s[b][n][3] = 0.f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[b][n][0] = s[b][n][1] = s[b][n][2] = s[b][n][3] = 0.f;
+            for (int w = 0; w < WORDS; ++w) {
+                const uint4 x = values_of<BF>(w0[w], s0, m0), y = values_of<BF>(w1[w], s1, m1);
 #pragma unroll
-                for (int w = 0; w < WORDS; ++w) {
-                    const uint4 x = values_of<BF>(w0[w], s0, m0), y = values_of<BF>(w1[w], s1, m1);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 q = NT == 1 ? qr[w] : qf[(n * WORDS + w) * 32 + lane];
-                        mma16816<BF>(s[b][n], x.x, y.x, x.y, y.y, q.x, q.y);
-                        mma16816<BF>(s[b][n], x.z, y.z, x.w, y.w, q.z, q.w);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 q = NT == 1 ? qr[w] : qf[(n * WORDS + w) * 32 + lane];
+                    mma16816<BF>(s[b][n], x.x, y.x, x.y, y.y, q.x, q.y);
+                    mma16816<BF>(s[b][n], x.z, y.z, x.w, y.w, q.z, q.w);
                 }
             }
+        };
+        auto values = [&](const uint8_t *stage, int b) {
+            const uint8_t *ra = stage + va_at + 16 * b * R, *rb = stage + vb_at + 16 * b * R;
+            uint32_t wa[2][OCT], wb[2][OCT], sv[2], mv[2];              // tokens 2 t4 and 2 t4 + 1, and 8 further on
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (OCT == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(ra + 8 * h * R + v_codes);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(rb + 8 * h * R + v_codes);
+                    wa[h][0] = x.x, wa[h][1] = x.y;
+                    wb[h][0] = y.x, wb[h][1] = y.y;
+                } else {
+                    wa[h][0] = *reinterpret_cast<const uint32_t *>(ra + 8 * h * R + v_codes);
+                    wb[h][0] = *reinterpret_cast<const uint32_t *>(rb + 8 * h * R + v_codes);
+                }
+                const uint32_t pa = *reinterpret_cast<const uint32_t *>(ra + 8 * h * R + v_param);
+                const uint32_t pc = *reinterpret_cast<const uint32_t *>(rb + 8 * h * R + v_param);
+                sv[h] = __byte_perm(pa, pc, 0x5410);
+                mv[h] = __byte_perm(pa, pc, 0x7632);
+            }
+#pragma unroll
+            for (int w = 0; w < OCT; ++w) {
+                uint32_t x[2][2][4];                                   // [tokens][even, odd elements][4]
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    codes_of<BF>(__byte_perm(wa[h][w], wb[h][w], 0x5410), x[h][0]);
+                    codes_of<BF>(__byte_perm(wa[h][w], wb[h][w], 0x7632), x[h][1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = fma_2<BF>(x[0][0][i], sv[0], mv[0]), a1 = fma_2<BF>(x[0][1][i], sv[0], mv[0]);
+                    const uint32_t a2 = fma_2<BF>(x[1][0][i], sv[1], mv[1]), a3 = fma_2<BF>(x[1][1][i], sv[1], mv[1]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816<BF>(o[n][4 * w + i], a0, a1, a2, a3, pb[b][n][0], pb[b][n][1]);
+                }
+            }
+        };
+        // Scores to weights.  edge: some token is hidden from some row (a few instructions beside the rest: a copy of the
+        // code for such tiles ran cold, 5 us where a tile takes 1).
+        auto weights = [&](uint8_t *stage, int key0, bool edge) {
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -354,6 +392,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                             const int key = key0 + key_row - key_first + 16 * b + (e & 2) * 4;
                             if (key > lim[n][e & 1] || (key <= lim_lo[n][e & 1] && key >= sinks)) s[b][n][e] = -INFINITY;
                         }
+                // slots past the visible tokens hold anything: their values must not meet a weight of 0
+                if (!sees_some(a.p, it, key0 + lane, 1)) {
+                    uint32_t *params = reinterpret_cast<uint32_t *>(stage + (key_first + lane) * R + vParams);
+#pragma unroll
+                    for (int i = 0; i < D >> GL; ++i) params[i] = 0;
+                }
+                fence_proxy_async();                     // before the next copy to the stage
+                __syncwarp();
             }
             float top = -INFINITY;                       // the most that a score is above its row's reference
 #pragma unroll
@@ -389,8 +435,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                 }
             }
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                uint32_t pb[NT][2];
+            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
@@ -398,64 +443,45 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                     for (int e = 0; e < 4; ++e) p[e] = ex2(s[b][n][e] - ref[n][e & 1]);
                     l[n][0] += p[0] + p[2];
                     l[n][1] += p[1] + p[3];
-                    pb[n][0] = transpose8(pack2<BF>(p[0], p[1]));
-                    pb[n][1] = transpose8(pack2<BF>(p[2], p[3]));
+                    pb[b][n][0] = transpose8(pack2<BF>(p[0], p[1]));
+                    pb[b][n][1] = transpose8(pack2<BF>(p[2], p[3]));
                 }
-                const uint8_t *ra = stage + va_at + 16 * b * R, *rb = stage + vb_at + 16 * b * R;
-                uint32_t wa[2][OCT], wb[2][OCT], sv[2], mv[2];          // tokens 2 t4 and 2 t4 + 1, and 8 further on
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (OCT == 2) {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(ra + 8 * h * R + v_codes);
-                        const uint2 y = *reinterpret_cast<const uint2 *>(rb + 8 * h * R + v_codes);
-                        wa[h][0] = x.x, wa[h][1] = x.y;
-                        wb[h][0] = y.x, wb[h][1] = y.y;
-                    } else {
-                        wa[h][0] = *reinterpret_cast<const uint32_t *>(ra + 8 * h * R + v_codes);
-                        wb[h][0] = *reinterpret_cast<const uint32_t *>(rb + 8 * h * R + v_codes);
-                    }
-                    uint32_t pa = *reinterpret_cast<const uint32_t *>(ra + 8 * h * R + v_param);
-                    uint32_t pc = *reinterpret_cast<const uint32_t *>(rb + 8 * h * R + v_param);
-                    if (edge) {
-                        // slots past the visible keys hold anything: their values must not meet a weight of 0
-                        const int ka = key0 + val_row0 - key_first + 16 * b + 8 * h, kb = ka + val_row1 - val_row0;
-                        if (!sees_some(a.p, it, ka, 1)) pa = 0;
-                        if (!sees_some(a.p, it, kb, 1)) pc = 0;
-                    }
-                    sv[h] = __byte_perm(pa, pc, 0x5410);
-                    mv[h] = __byte_perm(pa, pc, 0x7632);
-                }
-#pragma unroll
-                for (int w = 0; w < OCT; ++w) {
-                    uint32_t x[2][2][4];                               // [tokens][even, odd elements][4]
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        codes_of<BF>(__byte_perm(wa[h][w], wb[h][w], 0x5410), x[h][0]);
-                        codes_of<BF>(__byte_perm(wa[h][w], wb[h][w], 0x7632), x[h][1]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = fma_2<BF>(x[0][0][i], sv[0], mv[0]), a1 = fma_2<BF>(x[0][1][i], sv[0], mv[0]);
-                        const uint32_t a2 = fma_2<BF>(x[1][0][i], sv[1], mv[1]), a3 = fma_2<BF>(x[1][1][i], sv[1], mv[1]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816<BF>(o[n][4 * w + i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                    }
-                }
-            }
         };
         const int tiles = it.hi > 0 ? j1 - j0 : 0;
-        for (int j = j0; j < j0 + tiles; ++j) {
-            const int key_t = key_tile(a.p, it, j) << kKtLog2, key0 = key_t + key_first;       // the warp's first token
-            const int at = first_stage + stage;
-            alive = wait_all(alive, full(at), phase);
-            // tiles without a hidden token: all but the last and those at the window's ends
-            const bool edge = key_t + kKt - 1 > lim_min || (window > 0 && key_t <= lim_max - window && key_t + kKt > sinks);
-            if (!edge || sees_some(a.p, it, key0, kKeys)) tile(sb + at * C::kStage, key0, edge);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty(at));
+        auto next_stage = [&] {
             if (++stage == ST) {
                 stage = 0;
                 phase ^= 1;
+            }
+        };
+        if (tiles) {
+            int at = first_stage + stage;
+            alive = wait_all(alive, full(at), phase);
+            next_stage();
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) keys(sb + at * C::kStage, b);
+#pragma unroll 1
+            for (int j = j0; j < j0 + tiles; ++j) {
+                const int key_t = key_tile(a.p, it, j) << kKtLog2;
+                // tiles without a hidden token: all but the last and those at the window's ends
+                const bool edge = key_t + kKt - 1 > lim_min || (window > 0 && key_t <= lim_max - window && key_t + kKt > sinks);
+                uint8_t *here = sb + at * C::kStage;
+                weights(here, key_t + key_first, edge);
+                const bool more_tiles = j + 1 < j0 + tiles;
+                const int now = at;
+                if (more_tiles) {                        // (past the last tile its own keys go through once more, for nothing)
+                    at = first_stage + stage;
+                    alive = wait_all(alive, full(at), phase);
+                    next_stage();
+                }
+                const uint8_t *there = sb + at * C::kStage;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    values(here, b);
+                    keys(there, b);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(now));
             }
         }
         // ---------------------------------------- the warps' parts of the keys, added in a fixed order
@@ -573,7 +599,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         // The pieces' weights first, all at once, then their fragments, eight pieces at a time; in the order of the CTAs.
         const int pieces = c1 - c0 + 1;
         float4 *factors = reinterpret_cast<float4 *>(slots + team * (kWarps / 2) * C::kSlot);     // [n][t4]: (m, m, l, l) of all
-        float *weights = reinterpret_cast<float *>(factors + 4 * NT);                             // [32 pieces][n][t4][2]
+        float *lifts = reinterpret_cast<float *>(factors + 4 * NT);                             // [32 pieces][n][t4][2]
         if (warp == team * kWarps) {
             // lane: piece lane / 4 of eight, row pair t4
             for (int n = 0; n < NT; ++n) {
@@ -602,8 +628,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             for (int i = threadIdx.x % (32 * kWarps); i < here * 4 * NT; i += 32 * kWarps) {
                 const int c = i / (4 * NT), row = i - c * 4 * NT;
                 const float4 v = __ldcg(piece(c0 + cc + c) + NT * MT * 32 + row), all = factors[row];
-                weights[2 * i] = ex2(v.x - ref_of(all.x));
-                weights[2 * i + 1] = ex2(v.y - ref_of(all.y));
+                lifts[2 * i] = ex2(v.x - ref_of(all.x));
+                lifts[2 * i + 1] = ex2(v.y - ref_of(all.y));
             }
             bar_team(team);
 #pragma unroll
@@ -617,7 +643,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         if (c + k >= here) continue;
-                        const float2 w = *reinterpret_cast<const float2 *>(weights + 2 * ((c + k) * 4 * NT + 4 * n + t4));
+                        const float2 w = *reinterpret_cast<const float2 *>(lifts + 2 * ((c + k) * 4 * NT + 4 * n + t4));
                         acc[u].x += x[k].x * w.x;
                         acc[u].y += x[k].y * w.y;
                         acc[u].z += x[k].z * w.x;
