@@ -209,17 +209,16 @@ int attend(gptq_q4_attn h, const void *q, int64_t q_stride, const Cache *cache, 
     const bool bf16 = h->dtype == GPTQ_Q4_DTYPE_BF16;
     cudaError_t e;
     if constexpr (std::is_same_v<Cache, gptq_q4_cache>) {
-        const q4::AttnCache view = cache_view(cache);
-        if (a.sinks) e = q4::launch_attend_any(s, batch_view(batch), &view, nullptr, a, bf16, stream);
-        else e = (chunk ? q4::launch_attend_tc : q4::launch_attend_stream)(s, batch_view(batch), view, a, bf16, stream);
+        const auto tc = a.sinks ? q4::launch_attend_tc_sinks : q4::launch_attend_tc;
+        const auto stream_kv = a.sinks ? q4::launch_attend_stream_sinks : q4::launch_attend_stream;
+        e = (chunk ? tc : stream_kv)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
     } else {
-        const q4::Cache4 view = cache_view(cache);
         const int64_t rows = static_cast<int64_t>(batch->max_q) * s.group;
-        if (rows <= 32)
-            e = (rows <= 8 ? q4::launch_attend_stream4_8 : rows <= 16 ? q4::launch_attend_stream4_16 : q4::launch_attend_stream4_32)(
-                s, batch_view(batch), view, a, bf16, stream);
-        else
-            e = q4::launch_attend_any(s, batch_view(batch), nullptr, &view, a, bf16, stream);
+        const auto tc = s.d == 64 ? q4::launch_attend_tc4_64 : q4::launch_attend_tc4_128;
+        const auto stream_kv = rows <= 8    ? q4::launch_attend_stream4_8
+                               : rows <= 16 ? q4::launch_attend_stream4_16
+                                            : q4::launch_attend_stream4_32;
+        e = (rows > 32 && scale > 0.f ? tc : stream_kv)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
     }
     if (e) return api_cuda_fail(e, "attention launch");
     q4::api_count_launches(1);

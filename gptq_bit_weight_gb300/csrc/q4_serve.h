@@ -132,8 +132,16 @@ cudaError_t launch_attend_stream4_16(const AttnShape &s, const AttnBatch &b, con
                                      bool bf16, cudaStream_t st);
 cudaError_t launch_attend_stream4_32(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
                                      bool bf16, cudaStream_t st);
-cudaError_t launch_attend_any(const AttnShape &s, const AttnBatch &b, const AttnCache *c, const Cache4 *c4,
-                              const AttendCall &a, bool bf16, cudaStream_t st);
+// chunks over a cache of 4 bits; scale > 0
+cudaError_t launch_attend_tc4_64(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
+                                 cudaStream_t st);
+cudaError_t launch_attend_tc4_128(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
+                                  cudaStream_t st);
+// with a window and first tokens that stay visible
+cudaError_t launch_attend_stream_sinks(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a,
+                                       bool bf16, cudaStream_t st);
+cudaError_t launch_attend_tc_sinks(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a,
+                                   bool bf16, cudaStream_t st);
 // Tensor map of the queries [tokens][heads][d]: boxes of 64 columns, a
 // group's heads and `rows` tokens.
 cudaError_t encode_queries(CUtensorMap *map, const void *ptr, const AttnShape &s, int64_t stride, int tokens,
