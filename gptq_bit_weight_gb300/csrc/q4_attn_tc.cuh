@@ -46,6 +46,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 #include <type_traits>
 
@@ -64,16 +65,20 @@ constexpr int kKeys = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kCleaner = kSo
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
 
-template <int D_>
+// GL: 0 for the 16-bit cache, else log2 of the groups of a cache of 4 bits.
+template <int D_, int GL_ = 0>
 struct Cfg {
-    static constexpr int D = D_;
+    static constexpr int D = D_, GL = GL_;
     static constexpr int kHalf = kKt * D * 2;    // bytes of a half-stage: keys or values of a tile
     static constexpr int kQ = 128 * D * 2;       // of one row tile's queries
     static constexpr int kMisc = 2048;
-    static constexpr int kRoom = (232448 - 1024 - 2 * kQ - kMisc) / kHalf;
+    static constexpr int kRecord = GL ? record_bytes(D, GL) : 0;
+    static constexpr int kRaw = 64 * kRecord;    // the records of half a tile
+    static constexpr int kRawStages = 3;
+    static constexpr int kRoom = (232448 - 1024 - 2 * kQ - kRawStages * kRaw - kMisc) / kHalf;
     // what fits, 5 at D = 128; at D = 64 no more than 8 (12: 62.5 us for the window of 1024 instead of 59.4)
     static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
-    static constexpr int kSmem = 2 * kQ + kStages * kHalf + kMisc + 1024;
+    static constexpr int kSmem = 2 * kQ + kStages * kHalf + kRawStages * kRaw + kMisc + 1024;
     static constexpr int kPiece = 2 * 128 * (D + 2);   // floats of a piece in the workspace
 };
 
@@ -186,41 +191,34 @@ struct Part {
           two(it.t1 >= it.t0 + tokens) {}
 };
 
-// A token's codes and parameters of its key or value, on their way to a tile: GL the groups' log2.
-template <int D, int GL>
-struct Row4 {
-    static constexpr int kWords = D / 8, kGroups = D >> GL, R = record_bytes(D, GL);
-    uint32_t w[kWords], p[kGroups];
-    bool seen;
-    __device__ __forceinline__ void load(const uint8_t *r, bool value) {
-        const uint8_t *codes = r + (value ? D / 2 : 0), *params = r + D + (value ? 4 * kGroups : 0);
-        if constexpr (R % 16 == 0) {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 4) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(codes + 4 * i));
-                w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
-            }
+// The values of 32 tokens, one of each lane, from their records to rows of a tile [D / 64][128][64], swizzled; zeros
+// where `seen` is not set.  A loop, and one for all warps that decode: unrolled for a warp's blocks it was 17 KB beside
+// the softmax's code and ran at 7 cycles an instruction (1024 tokens over 16384: 968 us).
+template <bool BF, class C>
+__device__ __forceinline__ void decode_rows(const uint8_t *record, bool value, bool seen, uint8_t *tile, int row) {
+    constexpr int D = C::D, GL = C::GL;
+    const uint8_t *codes = record + (value ? D / 2 : 0), *params = record + D + (value ? 4 * (D >> GL) : 0);
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {                   // 32 elements, in one group
+        uint32_t w[4];
+        if constexpr (C::kRecord % 16 == 0) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(codes + 16 * q);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
         } else {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 2) {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(codes + 4 * i));
-                w[i] = x.x, w[i + 1] = x.y;
-            }
+            const uint2 x = *reinterpret_cast<const uint2 *>(codes + 16 * q), y = *reinterpret_cast<const uint2 *>(codes + 16 * q + 8);
+            w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
         }
+        uint32_t p = *reinterpret_cast<const uint32_t *>(params + 4 * (32 * q >> GL));
+        if (!seen) p = 0;
+        const uint32_t s2 = both_low(p), m2 = both_high(p);
+        uint8_t *dst = tile + (q >> 1) * (kKt * 128) + row * 128;
+        uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) p[i] = __ldg(reinterpret_cast<const uint32_t *>(params) + i);
-    }
-    // The row's values to row `row` of a tile [D / 64][128][64], swizzled; zeros if no row sees the token.
-    template <bool BF>
-    __device__ __forceinline__ void store(uint8_t *tile, int row) const {
+        for (int i = 0; i < 4; ++i) v[i] = values_of<BF>(w[i], s2, m2);
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            uint4 v = values_of<BF>(w[i], both_low(p[8 * i >> GL]), both_high(p[8 * i >> GL]));
-            if (!seen) v = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(tile + (i >> 3) * (kKt * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v;
-        }
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(dst + (((4 * (q & 1) + i) ^ (row & 7)) << 4)) = v[i];
     }
-};
+}
 
 // FOUR: 0 for the 16-bit cache, else log2 of the groups of a cache of 4 bits.
 template <bool BF, class C, bool SINKS, int FOUR>
@@ -231,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sb = smem_raw + (base - raw);
-    const uint32_t ring = base + 2 * C::kQ, bars = ring + S * C::kHalf;
-    uint8_t *misc = sb + 2 * C::kQ + S * C::kHalf;
+    const uint32_t ring = base + 2 * C::kQ, raws = ring + S * C::kHalf, bars = raws + C::kRawStages * C::kRaw;
+    uint8_t *misc = sb + 2 * C::kQ + S * C::kHalf + C::kRawStages * C::kRaw;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (S + s); };
     auto tail = [&](int s) { return bars + 8u * (2 * S + s); };
@@ -240,11 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto s_full = [&](int i) { return q_full + 24 + 8u * i; };
     auto p_ready = [&](int i) { return q_full + 40 + 8u * i; };
     auto pv_done = [&](int i) { return q_full + 56 + 8u * i; };
+    auto raw_full = [&](int s) { return q_full + 72 + 8u * s; };
+    auto raw_empty = [&](int s) { return q_full + 72 + 8u * (C::kRawStages + s); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
     int *last_flags = reinterpret_cast<int *>(misc + 1016);             // of the first and the last item
     SchedSmem &sched = *reinterpret_cast<SchedSmem *>(misc + 520);
     float2 *s_ml = reinterpret_cast<float2 *>(misc + 1024);             // [128]: (m, l) of the second buffer
-    static_assert(8 * (3 * S + 13) <= 512 && 520 + sizeof(SchedSmem) <= 1016, "misc region");
+    static_assert(8 * (3 * S + 9 + 2 * C::kRawStages) <= 512 && 520 + sizeof(SchedSmem) <= 1016, "misc region");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!FOUR)
             for (const CUtensorMap *map : {&tmK, &tmV}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), FOUR ? 2 : 1);
+            mbar_init(full(s), FOUR ? 4 : 1);
             mbar_init(empty(s), 1);
             mbar_init(tail(s), 1);
         }
@@ -263,6 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(s_full(i), 1);
             mbar_init(p_ready(i), 4);
             mbar_init(pv_done(i), 1);
+        }
+        for (int i = 0; FOUR && i < C::kRawStages; ++i) {
+            mbar_init(raw_full(i), 1);
+            mbar_init(raw_empty(i), 3);
         }
         mbar_init_fence();
     }
@@ -605,37 +609,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (FOUR && warp != kIssuer) {
             if constexpr (FOUR) {
-                // Each lane decodes a token of each of the warp's blocks of 32: three of the keys', three of the values', and
-                // the last one of both.  A block's records of the next tile are on their way while this tile's are decoded.
-                using Row = Row4<D, FOUR>;
+                // Records of half a tile come by bulk copies, issued by the first of the three warps; each decodes some of
+                // its blocks of 32 tokens: keys 0 and 1, values 0 and 1; the second half's the same.
+                constexpr int RS = C::kRawStages, R = C::kRecord;
                 const int q_bytes = a.tokens * a.p.group.d * D * 2;
+                const int me = warp == kKeys ? 0 : warp == kCleaner ? 1 : 2;
+                const int box_log2 = min(a.p.page_log2, 6), boxes = 64 >> box_log2, bytes = R << box_log2;
                 int seq = 0, items = 0, bad = 0;
-                const bool both = warp == kCleaner, values = warp == kValues;
+                int got = 0, sent = 0;                   // halves decoded, and on their way, so far
                 for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
                     if (it.hi <= 0) continue;
                     const Part part(it, sh, a.tokens);
+                    const int halves = 2 * (part.j1 - part.j0), before = got;
                     const int32_t *table = a.p.b.table + it.b * a.p.b.table_stride;
-                    auto fetch = [&](Row &r, int j, int block, bool value) {
-                        const int key = (key_tile(a.p, it, j) << kKtLog2) + 32 * block + lane;
-                        r.seen = sees_some(a.p, it, key, 1);
-                        if (!r.seen) return;
-                        int page = __ldg(table + (key >> a.p.page_log2));
-                        if (page < 0 || page >= a.c.pages) {
+                    const uint8_t *head = a.c.kv + static_cast<int64_t>(it.head << a.p.page_log2) * R;
+                    auto first_key = [&](int h) { return (key_tile(a.p, it, part.j0 + (h >> 1)) << kKtLog2) + 64 * (h & 1); };
+                    // lane i has the page of box i; INT_MIN: no row sees it
+                    auto entry = [&](int h) {
+                        const int key = first_key(h) + (lane << box_log2);
+                        return h < halves && lane < boxes && sees_some(a.p, it, key, 1 << box_log2) ? __ldg(table + (key >> a.p.page_log2)) : INT_MIN;
+                    };
+                    int next = me == 0 ? entry(0) : 0;
+                    auto send = [&](int h) {
+                        int page = next;
+                        next = entry(h + 1);
+                        const int st = sent % RS;
+                        if (sent >= RS) alive = wait_all(alive, raw_empty(st), ((sent / RS) & 1) ^ 1);
+                        if (!alive) return;
+                        const unsigned wanted = __ballot_sync(0xffffffffu, page != INT_MIN);
+                        if (page != INT_MIN && (page < 0 || page >= a.c.pages)) {
                             bad = kAttnBadPage;
                             page = 0;
                         }
-                        r.load(a.c.kv + page * a.c.page_stride +
-                                   static_cast<int64_t>((it.head << a.p.page_log2) + (key & ((1 << a.p.page_log2) - 1))) * Row::R,
-                               value);
+                        __syncwarp();
+                        const int row = first_key(h) & ((1 << a.p.page_log2) - 1) & ~((1 << box_log2) - 1);
+                        if (elect_one()) mbar_arrive_expect_tx(raw_full(st), __popc(wanted) * bytes);
+#pragma unroll 1
+                        for (int i = 0; i < boxes; ++i) {
+                            const int pg = __shfl_sync(0xffffffffu, page, i);
+                            if ((wanted >> i & 1) && elect_one())
+                                bulk_load(raws + st * C::kRaw + i * bytes, head + pg * a.c.page_stride + row * R, bytes, raw_full(st));
+                            __syncwarp();
+                        }
+                        ++sent;
                     };
-                    Row r[3];
-                    if (both) {
-                        fetch(r[0], part.j0, 3, false);
-                        fetch(r[1], part.j0, 3, true);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 3; ++i) fetch(r[i], part.j0, i, values);
-                    }
+                    if (me == 0)
+                        for (int h = 0; h < min(RS - 1, halves) && alive; ++h) send(h);
                     if (warp == kKeys) {
                         if (items) alive = wait_all(alive, q_empty, (items - 1) & 1);
                         if (!alive) break;
@@ -649,39 +668,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         ++items;
                     }
-                    for (int j = part.j0; j < part.j1 && alive; ++j, seq += 2) {
-                        const bool next = j + 1 < part.j1;
-                        auto wait_for = [&](int q) {
+                    for (int h = 0; h < halves && alive; ++h, ++got) {
+                        if (me == 0 && sent - before < halves) send(sent - before);
+                        const int st = got % RS, key0 = first_key(h);
+                        alive = wait_all(alive, raw_full(st), (got / RS) & 1);
+                        const uint8_t *raw = sb + 2 * C::kQ + S * C::kHalf + st * C::kRaw;
+#pragma unroll 1
+                        for (int u = 0; u < 4 && alive; ++u) {
+                            // blocks K0 K1 V0 V1 and K2 K3 V2 V3 to warps 1 2 2 0 and 0 1 1 2
+                            if (((h & 1 ? 0x2110 : 0x0221) >> (4 * u) & 15) != me) continue;
+                            const int q = seq + 2 * (h >> 1) + (u >> 1), part_row = 32 * (u & 1) + lane;
                             if (q >= S) alive = wait_all(alive, empty(q % S), ((q / S) & 1) ^ 1);
-                        };
-                        auto hand_over = [&](int q) {
+                            if (!alive) break;
+                            decode_rows<BF, C>(raw + part_row * R, u >> 1, sees_some(a.p, it, key0 + part_row, 1),
+                                               sb + 2 * C::kQ + q % S * C::kHalf, 64 * (h & 1) + part_row);
                             fence_proxy_async();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(full(q % S));
-                        };
-                        if (both) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                wait_for(seq + i);
-                                if (!alive) break;
-                                r[i].template store<BF>(sb + 2 * C::kQ + (seq + i) % S * C::kHalf, 96 + lane);
-                                if (next) fetch(r[i], j + 1, 3, i);
-                                hand_over(seq + i);
-                            }
-                        } else {
-                            wait_for(seq + values);
-                            if (!alive) break;
-#pragma unroll
-                            for (int i = 0; i < 3; ++i) {
-                                r[i].template store<BF>(sb + 2 * C::kQ + (seq + values) % S * C::kHalf, 32 * i + lane);
-                                if (next) fetch(r[i], j + 1, i, values);
-                            }
-                            hand_over(seq + values);
                         }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(raw_empty(st));
                     }
+                    seq += halves;
                 }
                 if (bad) atomicOr(a.status, bad);
-                if (!alive && items) wait_bounded(q_full, (items - 1) & 1);      // the queries' copy in flight
+                if (!alive && me == 0) {
+                    // let the copies in flight land before the CTA can exit
+                    if (items) wait_bounded(q_full, (items - 1) & 1);
+                    for (int i = sent - 1; i >= 0 && i >= sent - RS; --i) wait_bounded(raw_full(i % RS), (i / RS) & 1);
+                }
             }
         } else if (warp == kIssuer) {
             if (elect_one()) {
