@@ -192,13 +192,13 @@ struct Part {
 };
 
 // The values of 32 tokens, one of each lane, from their records to rows of a tile [D / 64][128][64], swizzled; zeros
-// where `seen` is not set.  A loop, and one for all warps that decode: unrolled for a warp's blocks it was 17 KB beside
-// the softmax's code and ran at 7 cycles an instruction (1024 tokens over 16384: 968 us).
+// where `seen` is not set.  One copy of the code for all warps that decode: unrolled for a warp's blocks it was 17 KB
+// beside the softmax's code and ran at 7 cycles an instruction (1024 tokens over 16384: 968 us).
 template <bool BF, class C>
 __device__ __forceinline__ void decode_rows(const uint8_t *record, bool value, bool seen, uint8_t *tile, int row) {
     constexpr int D = C::D, GL = C::GL;
     const uint8_t *codes = record + (value ? D / 2 : 0), *params = record + D + (value ? 4 * (D >> GL) : 0);
-#pragma unroll 1
+#pragma unroll
     for (int q = 0; q < D / 32; ++q) {                   // 32 elements, in one group
         uint32_t w[4];
         if constexpr (C::kRecord % 16 == 0) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!FOUR)
             for (const CUtensorMap *map : {&tmK, &tmV}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), FOUR ? 4 : 1);
+            mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
             mbar_init(tail(s), 1);
         }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; FOUR && i < C::kRawStages; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_empty(i), 3);
+            mbar_init(raw_empty(i), 2);
         }
         mbar_init_fence();
     }
@@ -609,33 +609,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (FOUR && warp != kIssuer) {
             if constexpr (FOUR) {
-                // Records of half a tile come by bulk copies, issued by the first of the three warps; each decodes some of
-                // its blocks of 32 tokens: keys 0 and 1, values 0 and 1; the second half's the same.
+                // Records of half a tile come by bulk copies, issued by one of the three warps; the others decode them, one
+                // the keys and one the values.
                 constexpr int RS = C::kRawStages, R = C::kRecord;
-                const int q_bytes = a.tokens * a.p.group.d * D * 2;
-                const int me = warp == kKeys ? 0 : warp == kCleaner ? 1 : 2;
                 const int box_log2 = min(a.p.page_log2, 6), boxes = 64 >> box_log2, bytes = R << box_log2;
-                int seq = 0, items = 0, bad = 0;
-                int got = 0, sent = 0;                   // halves decoded, and on their way, so far
+                const bool values = warp == kValues;
+                const int q_bytes = a.tokens * a.p.group.d * D * 2;
+                int items = 0, bad = 0, half = 0, tile = 0;          // half tiles and tiles so far
                 for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
                     if (it.hi <= 0) continue;
                     const Part part(it, sh, a.tokens);
-                    const int halves = 2 * (part.j1 - part.j0), before = got;
+                    const int halves = 2 * (part.j1 - part.j0);
+                    auto first_key = [&](int h) { return (key_tile(a.p, it, part.j0 + (h >> 1)) << kKtLog2) + 64 * (h & 1); };
+                    if (warp != kKeys) {
+                        for (int h = 0; h < halves; ++h, ++half) {
+                            const int st = half % RS, slot = 2 * (tile + (h >> 1)) + values;
+                            alive = wait_all(alive, raw_full(st), (half / RS) & 1);
+                            if (!(h & 1) && slot >= S) alive = wait_all(alive, empty(slot % S), ((slot / S) & 1) ^ 1);
+                            if (!alive) break;
+                            const uint8_t *raw = sb + 2 * C::kQ + S * C::kHalf + st * C::kRaw;
+#pragma unroll 1
+                            for (int row = lane; row < 64; row += 32)
+                                decode_rows<BF, C>(raw + row * R, values, sees_some(a.p, it, first_key(h) + row, 1),
+                                                   sb + 2 * C::kQ + slot % S * C::kHalf, 64 * (h & 1) + row);
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive(raw_empty(st));
+                                if (h & 1) mbar_arrive(full(slot % S));
+                            }
+                        }
+                        tile += halves >> 1;
+                        continue;
+                    }
                     const int32_t *table = a.p.b.table + it.b * a.p.b.table_stride;
                     const uint8_t *head = a.c.kv + static_cast<int64_t>(it.head << a.p.page_log2) * R;
-                    auto first_key = [&](int h) { return (key_tile(a.p, it, part.j0 + (h >> 1)) << kKtLog2) + 64 * (h & 1); };
                     // lane i has the page of box i; INT_MIN: no row sees it
                     auto entry = [&](int h) {
                         const int key = first_key(h) + (lane << box_log2);
                         return h < halves && lane < boxes && sees_some(a.p, it, key, 1 << box_log2) ? __ldg(table + (key >> a.p.page_log2)) : INT_MIN;
                     };
-                    int next = me == 0 ? entry(0) : 0;
-                    auto send = [&](int h) {
+                    int next = entry(0);
+                    if (items) alive = wait_all(alive, q_empty, (items - 1) & 1);
+                    if (!alive) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(q_full, part.two ? 2 * q_bytes : q_bytes);
+                        for (int i = 0; i < (part.two ? 2 : 1); ++i)
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_3d(base + i * C::kQ + h * (128 * 128), &tmQ, q_full, 64 * h, it.head * a.p.group.d,
+                                            it.q0 + it.t0 + i * a.tokens);
+                    }
+                    __syncwarp();
+                    ++items;
+                    for (int h = 0; h < halves; ++h, ++half) {
                         int page = next;
                         next = entry(h + 1);
-                        const int st = sent % RS;
-                        if (sent >= RS) alive = wait_all(alive, raw_empty(st), ((sent / RS) & 1) ^ 1);
-                        if (!alive) return;
+                        const int st = half % RS;
+                        if (half >= RS) alive = wait_all(alive, raw_empty(st), ((half / RS) & 1) ^ 1);
+                        if (!alive) break;
                         const unsigned wanted = __ballot_sync(0xffffffffu, page != INT_MIN);
                         if (page != INT_MIN && (page < 0 || page >= a.c.pages)) {
                             bad = kAttnBadPage;
@@ -643,59 +674,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         __syncwarp();
                         const int row = first_key(h) & ((1 << a.p.page_log2) - 1) & ~((1 << box_log2) - 1);
-                        if (elect_one()) mbar_arrive_expect_tx(raw_full(st), __popc(wanted) * bytes);
+                        const uint32_t dst = raws + st * C::kRaw, bar = raw_full(st);
+                        const uint8_t *src = head + row * R;
+                        if (elect_one()) mbar_arrive_expect_tx(bar, __popc(wanted) * bytes);
 #pragma unroll 1
-                        for (int i = 0; i < boxes; ++i) {
-                            const int pg = __shfl_sync(0xffffffffu, page, i);
-                            if ((wanted >> i & 1) && elect_one())
-                                bulk_load(raws + st * C::kRaw + i * bytes, head + pg * a.c.page_stride + row * R, bytes, raw_full(st));
+                        for (int i0 = 0; i0 < boxes; i0 += 4) {
+                            int pg[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) pg[i] = __shfl_sync(0xffffffffu, page, i0 + i);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (wanted >> (i0 + i) & 1) bulk_load(dst + (i0 + i) * bytes, src + pg[i] * a.c.page_stride, bytes, bar);
+                            }
                             __syncwarp();
                         }
-                        ++sent;
-                    };
-                    if (me == 0)
-                        for (int h = 0; h < min(RS - 1, halves) && alive; ++h) send(h);
-                    if (warp == kKeys) {
-                        if (items) alive = wait_all(alive, q_empty, (items - 1) & 1);
-                        if (!alive) break;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(q_full, part.two ? 2 * q_bytes : q_bytes);
-                            for (int i = 0; i < (part.two ? 2 : 1); ++i)
-                                for (int h = 0; h < D / 64; ++h)
-                                    tma_load_3d(base + i * C::kQ + h * (128 * 128), &tmQ, q_full, 64 * h, it.head * a.p.group.d,
-                                                it.q0 + it.t0 + i * a.tokens);
-                        }
-                        __syncwarp();
-                        ++items;
                     }
-                    for (int h = 0; h < halves && alive; ++h, ++got) {
-                        if (me == 0 && sent - before < halves) send(sent - before);
-                        const int st = got % RS, key0 = first_key(h);
-                        alive = wait_all(alive, raw_full(st), (got / RS) & 1);
-                        const uint8_t *raw = sb + 2 * C::kQ + S * C::kHalf + st * C::kRaw;
-#pragma unroll 1
-                        for (int u = 0; u < 4 && alive; ++u) {
-                            // blocks K0 K1 V0 V1 and K2 K3 V2 V3 to warps 1 2 2 0 and 0 1 1 2
-                            if (((h & 1 ? 0x2110 : 0x0221) >> (4 * u) & 15) != me) continue;
-                            const int q = seq + 2 * (h >> 1) + (u >> 1), part_row = 32 * (u & 1) + lane;
-                            if (q >= S) alive = wait_all(alive, empty(q % S), ((q / S) & 1) ^ 1);
-                            if (!alive) break;
-                            decode_rows<BF, C>(raw + part_row * R, u >> 1, sees_some(a.p, it, key0 + part_row, 1),
-                                               sb + 2 * C::kQ + q % S * C::kHalf, 64 * (h & 1) + part_row);
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(full(q % S));
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(raw_empty(st));
-                    }
-                    seq += halves;
                 }
                 if (bad) atomicOr(a.status, bad);
-                if (!alive && me == 0) {
+                if (!alive && warp == kKeys) {
                     // let the copies in flight land before the CTA can exit
                     if (items) wait_bounded(q_full, (items - 1) & 1);
-                    for (int i = sent - 1; i >= 0 && i >= sent - RS; --i) wait_bounded(raw_full(i % RS), (i / RS) & 1);
+                    for (int i = half - 1; i >= 0 && i >= half - RS; --i) wait_bounded(raw_full(i % RS), (i / RS) & 1);
                 }
             }
         } else if (warp == kIssuer) {
