@@ -60,8 +60,11 @@ namespace {
 using namespace tc;
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kKeys = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kCleaner = kSoftmaxWarps + 2, kValues = kSoftmaxWarps + 3;
+// Of the kernel for the 4-bit cache: decoders, one on each of the SM's partitions (the launch has whole groups of four
+// warps; the last two have nothing to do).
+constexpr int kDecoders = kSoftmaxWarps + 2;
+constexpr int threads_of(int four) { return 32 * (kSoftmaxWarps + (four ? 8 : 4)); }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
 
@@ -222,7 +225,7 @@ __device__ __forceinline__ void decode_rows(const uint8_t *record, bool value, b
 
 // FOUR: 0 for the 16-bit cache, else log2 of the groups of a cache of 4 bits.
 template <bool BF, class C, bool SINKS, int FOUR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(FOUR), 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, Args<SINKS, FOUR != 0> a) {
     constexpr int D = C::D, S = C::kStages;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!FOUR)
             for (const CUtensorMap *map : {&tmK, &tmV}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), 1);
+            mbar_init(full(s), FOUR ? 2 : 1);
             mbar_init(empty(s), 1);
             mbar_init(tail(s), 1);
         }
@@ -266,19 +269,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; FOUR && i < C::kRawStages; ++i) {
             mbar_init(raw_full(i), 1);
-            mbar_init(raw_empty(i), 2);
+            mbar_init(raw_empty(i), 4);
         }
         mbar_init_fence();
     }
     if (warp == kIssuer) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tc_fence_before();
     Item it;
-    const Share sh = sched_share<kThreads>(a.p, sched, blockIdx.x, gridDim.x, a.status, it);   // synchronizes
+    const Share sh = sched_share<threads_of(FOUR)>(a.p, sched, blockIdx.x, gridDim.x, a.status, it);   // synchronizes
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     bool alive = true;
     const bool work = sh.begin < sh.end;
-    // 168 registers a thread at launch: 256 x 184 + 128 x 136 = 384 x 168
+    // 168 registers a thread at launch: 256 x 184 + 128 x 136 = 384 x 168; or 128: 256 x 184 + 256 x 72 = 512 x 128
     if (warp < kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---------------------------------------------- softmax: a thread holds a row
@@ -562,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             end_item();
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
+        if constexpr (FOUR) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
         if (!work) {
         } else if (!FOUR && (warp == kKeys || warp == kValues)) {
             if constexpr (!FOUR) {
@@ -607,13 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             }
-        } else if (FOUR && warp != kIssuer) {
+        } else if (FOUR && warp != kIssuer && warp < kDecoders + 4) {
             if constexpr (FOUR) {
-                // Records of half a tile come by bulk copies, issued by one of the three warps; the others decode them, one
-                // the keys and one the values.
+                // Records of half a tile come by bulk copies, issued by one warp; four decode a block of 32 tokens each, two
+                // the keys and two the values.
                 constexpr int RS = C::kRawStages, R = C::kRecord;
                 const int box_log2 = min(a.p.page_log2, 6), boxes = 64 >> box_log2, bytes = R << box_log2;
-                const bool values = warp == kValues;
+                const bool values = warp >= kDecoders + 2;
+                const int row = 32 * ((warp - kDecoders) & 1) + lane;
                 const int q_bytes = a.tokens * a.p.group.d * D * 2;
                 int items = 0, bad = 0, half = 0, tile = 0;          // half tiles and tiles so far
                 for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
@@ -628,10 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!(h & 1) && slot >= S) alive = wait_all(alive, empty(slot % S), ((slot / S) & 1) ^ 1);
                             if (!alive) break;
                             const uint8_t *raw = sb + 2 * C::kQ + S * C::kHalf + st * C::kRaw;
-#pragma unroll 1
-                            for (int row = lane; row < 64; row += 32)
-                                decode_rows<BF, C>(raw + row * R, values, sees_some(a.p, it, first_key(h) + row, 1),
-                                                   sb + 2 * C::kQ + slot % S * C::kHalf, 64 * (h & 1) + row);
+                            decode_rows<BF, C>(raw + row * R, values, sees_some(a.p, it, first_key(h) + row, 1),
+                                               sb + 2 * C::kQ + slot % S * C::kHalf, 64 * (h & 1) + row);
                             fence_proxy_async();
                             __syncwarp();
                             if (lane == 0) {
@@ -673,9 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             page = 0;
                         }
                         __syncwarp();
-                        const int row = first_key(h) & ((1 << a.p.page_log2) - 1) & ~((1 << box_log2) - 1);
+                        const int slot = first_key(h) & ((1 << a.p.page_log2) - 1) & ~((1 << box_log2) - 1);
                         const uint32_t dst = raws + st * C::kRaw, bar = raw_full(st);
-                        const uint8_t *src = head + row * R;
+                        const uint8_t *src = head + slot * R;
                         if (elect_one()) mbar_arrive_expect_tx(bar, __popc(wanted) * bytes);
 #pragma unroll 1
                         for (int i0 = 0; i0 < boxes; i0 += 4) {
@@ -813,7 +816,7 @@ cudaError_t launch(const AttnShape &s, const AttnBatch &b, const Cache &c, const
         c, a.out, a.out_stride, a.scale * 1.4426950408889634f, tokens, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_tc_kernel<true, C, SINKS, FOUR> : attend_tc_kernel<false, C, SINKS, FOUR>;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem))) return e;
-    kernel<<<a.ctas, kThreads, C::kSmem, st>>>(tq, tk, tv, args);
+    kernel<<<a.ctas, threads_of(FOUR), C::kSmem, st>>>(tq, tk, tv, args);
     return cudaGetLastError();
 }
 
