@@ -215,10 +215,8 @@ int attend(gptq_q4_attn h, const void *q, int64_t q_stride, const Cache *cache, 
     } else {
         const int64_t rows = static_cast<int64_t>(batch->max_q) * s.group;
         const auto tc = s.d == 64 ? q4::launch_attend_tc4_64 : q4::launch_attend_tc4_128;
-        const auto stream_kv = rows <= 8    ? q4::launch_attend_stream4_8
-                               : rows <= 16 ? q4::launch_attend_stream4_16
-                                            : q4::launch_attend_stream4_32;
-        e = (rows > 32 && scale > 0.f ? tc : stream_kv)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
+        const auto stream_kv = rows <= 8 ? q4::launch_attend_stream4_8 : q4::launch_attend_stream4_16;
+        e = (chunk ? tc : stream_kv)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
     }
     if (e) return api_cuda_fail(e, "attention launch");
     q4::api_count_launches(1);

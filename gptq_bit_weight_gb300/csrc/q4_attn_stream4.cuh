@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
 template <class C>
 cudaError_t launch(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
                    cudaStream_t st) {
-    constexpr int rows_log2 = C::NT == 1 ? 3 : C::NT == 2 ? 4 : 5;
+    constexpr int rows_log2 = C::NT == 1 ? 3 : 4;
     Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), rows_log2, FastDiv(1), a.sinks},
               c, a.q, a.out, a.q_stride, a.out_stride, a.scale * 1.4426950408889634f, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_stream4_kernel<true, C> : attend_stream4_kernel<false, C>;

@@ -61,9 +61,9 @@ using namespace tc;
 
 constexpr int kSoftmaxWarps = 8;
 constexpr int kKeys = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1, kCleaner = kSoftmaxWarps + 2, kValues = kSoftmaxWarps + 3;
-// Of the kernel for the 4-bit cache: decoders, one on each of the SM's partitions (the launch has whole groups of four
-// warps; the last two have nothing to do).
-constexpr int kDecoders = kSoftmaxWarps + 2;
+// Of the kernel for the 4-bit cache: the first of its decoders, which are all warps but the softmax's, the loader and the
+// issuer.
+constexpr int kDecoder = kSoftmaxWarps + 2, kDecoders = 6;
 constexpr int threads_of(int four) { return 32 * (kSoftmaxWarps + (four ? 8 : 4)); }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(threads_of(FOUR), 1)
         if constexpr (!FOUR)
             for (const CUtensorMap *map : {&tmK, &tmV}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), FOUR ? 2 : 1);
+            mbar_init(full(s), FOUR ? 4 : 1);
             mbar_init(empty(s), 1);
             mbar_init(tail(s), 1);
         }
@@ -611,15 +611,16 @@ __global__ void __launch_bounds__(threads_of(FOUR), 1)
                 }
             }
             }
-        } else if (FOUR && warp != kIssuer && warp < kDecoders + 4) {
+        } else if (FOUR && warp != kIssuer) {
             if constexpr (FOUR) {
-                // Records of half a tile come by bulk copies, issued by one warp; four decode a block of 32 tokens each, two
-                // the keys and two the values.
+                // Records of half a tile come by bulk copies, issued by one warp.  A half has four blocks, two of 32 keys and
+                // two of 32 values, which go to the decoders in turn.  (A decoder has a block in two of three halves, so it
+                // sees the same two of the three raw stages at every turn of theirs.)
                 constexpr int RS = C::kRawStages, R = C::kRecord;
                 const int box_log2 = min(a.p.page_log2, 6), boxes = 64 >> box_log2, bytes = R << box_log2;
-                const bool values = warp >= kDecoders + 2;
-                const int row = 32 * ((warp - kDecoders) & 1) + lane;
+                static_assert(RS == 3 && kDecoders == 6, "who sees which stage");
                 const int q_bytes = a.tokens * a.p.group.d * D * 2;
+                int block = warp - kDecoder;                         // the decoder's next one
                 int items = 0, bad = 0, half = 0, tile = 0;          // half tiles and tiles so far
                 for (bool more = true; more && it.u < sh.end && alive; more = next_item(a.p, it)) {
                     if (it.hi <= 0) continue;
@@ -627,21 +628,24 @@ __global__ void __launch_bounds__(threads_of(FOUR), 1)
                     const int halves = 2 * (part.j1 - part.j0);
                     auto first_key = [&](int h) { return (key_tile(a.p, it, part.j0 + (h >> 1)) << kKtLog2) + 64 * (h & 1); };
                     if (warp != kKeys) {
-                        for (int h = 0; h < halves; ++h, ++half) {
-                            const int st = half % RS, slot = 2 * (tile + (h >> 1)) + values;
-                            alive = wait_all(alive, raw_full(st), (half / RS) & 1);
-                            if (!(h & 1) && slot >= S) alive = wait_all(alive, empty(slot % S), ((slot / S) & 1) ^ 1);
+                        for (; block < 4 * (half + halves); block += kDecoders) {
+                            const int h = (block >> 2) - half, st = (block >> 2) % RS;
+                            const bool value = block & 2;
+                            const int row = 32 * (block & 1) + lane, slot = 2 * (tile + (h >> 1)) + value;
+                            alive = wait_all(alive, raw_full(st), ((block >> 2) / RS) & 1);
+                            if (slot >= S) alive = wait_all(alive, empty(slot % S), ((slot / S) & 1) ^ 1);
                             if (!alive) break;
                             const uint8_t *raw = sb + 2 * C::kQ + S * C::kHalf + st * C::kRaw;
-                            decode_rows<BF, C>(raw + row * R, values, sees_some(a.p, it, first_key(h) + row, 1),
+                            decode_rows<BF, C>(raw + row * R, value, sees_some(a.p, it, first_key(h) + row, 1),
                                                sb + 2 * C::kQ + slot % S * C::kHalf, 64 * (h & 1) + row);
                             fence_proxy_async();
                             __syncwarp();
                             if (lane == 0) {
                                 mbar_arrive(raw_empty(st));
-                                if (h & 1) mbar_arrive(full(slot % S));
+                                mbar_arrive(full(slot % S));
                             }
                         }
+                        half += halves;
                         tile += halves >> 1;
                         continue;
                     }

@@ -125,12 +125,10 @@ cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const A
 size_t attend_tc_ws_bytes(int ctas);
 cudaError_t launch_attend_tc(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
                              cudaStream_t st);
-// few rows over a cache of 4 bits, in row tiles of 8, 16 and 32 (q4_attn_stream4*.cu); pieces as launch_attend_tc's
+// few rows over a cache of 4 bits, in row tiles of 8 and 16 (q4_attn_stream4*.cu); pieces as launch_attend_tc's
 cudaError_t launch_attend_stream4_8(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
                                     bool bf16, cudaStream_t st);
 cudaError_t launch_attend_stream4_16(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
-                                     bool bf16, cudaStream_t st);
-cudaError_t launch_attend_stream4_32(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
                                      bool bf16, cudaStream_t st);
 // chunks over a cache of 4 bits; scale > 0
 cudaError_t launch_attend_tc4_64(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
