@@ -9,8 +9,8 @@
 //   A code changes where (x - m) / s passes a half, so what goes in has to be the
 //   same number wherever it is computed: the rotation carries the errors of its
 //   two products and of their sum (fma and two-sum), so that its fp32 result is
-//   the exact one rounded once; and a code is found from an approximate quotient,
-//   then set right by the sign of x - m - (k + 1/2) s, one exact fma.
+//   the exact one rounded once; and the quotient is corrected by its remainder,
+//   one exact fma.
 // A work item has 16 elements of a head.  A key's pairs (i, i + rot / 2) come from
 // two places, so the rotated elements go through shared memory, after which an
 // item holds 16 neighbours and a group is 2 or 4 lanes.
@@ -35,38 +35,97 @@ __device__ __forceinline__ float cross(float x, float y, float u, float v) {
     return fabsf(s) < INFINITY ? r : s;                  // of infinities there are no errors
 }
 
+template <bool BF>
+__device__ __forceinline__ uint32_t min_2(uint32_t a, uint32_t b) {          // NaN if either is
+    uint32_t d;
+    if constexpr (BF) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// x / 15, rounded once, for x >= 1e-30: the product with the rounded reciprocal, corrected by its remainder.
+__device__ __forceinline__ float fifteenth(float x) {
+    const float r = 1.f / 15.f, q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, 15.f, x), r, q);
+}
+
 // Sixteen 16-bit values in two vectors -> their codes; s and m of the group (`lanes` lanes).
 template <bool BF>
 __device__ __forceinline__ uint2 quantise(const uint4 &v0, const uint4 &v1, int lanes, unsigned mask, uint32_t &sm) {
-    float x[16], lo = INFINITY, hi = -INFINITY, odd = 0.f;
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t least = w[0], most = w[0] ^ 0x80008000u;                // of the negated values
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 f = unpack2<BF>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-        lo = fminf(lo, fminf(f.x, f.y));
-        hi = fmaxf(hi, fmaxf(f.x, f.y));
-        odd += f.x * 0.f + f.y * 0.f;                    // NaN if either is no finite number
+    for (int i = 1; i < 8; ++i) {
+        least = min_2<BF>(least, w[i]);
+        most = min_2<BF>(most, w[i] ^ 0x80008000u);
     }
-    for (int o = 1; o < lanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-        odd += __shfl_xor_sync(mask, odd, o);
-    }
-    const float span = __fadd_rn(__fsub_rn(hi, lo), odd);
+    uint32_t ends = min_2<BF>(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));     // (least, -greatest)
+    for (int o = 1; o < lanes; o <<= 1) ends = min_2<BF>(ends, __shfl_xor_sync(mask, ends, o));
+    const float lo = unpack2<BF>(ends).x, span = __fsub_rn(-unpack2<BF>(ends).y, lo);
     if (!(span < INFINITY)) {
         const float nan = __int_as_float(0x7fffffff);
         sm = pack2<BF>(nan, nan);
         return make_uint2(0, 0);
     }
-    sm = pack2<BF>(__fdiv_rn(span, 15.f), lo);
-    const float step = unpack2<BF>(sm).x, up = step < 1e-30f ? 0x1p64f : 1.f;      // 1 / s stays in range
-    const float s = step * up, inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
-    uint32_t c[2] = {0, 0};
+    const bool small = span < 1e-30f;
+    sm = pack2<BF>(small ? __fdiv_rn(span, 15.f) : fifteenth(span), lo);
+    const float step = unpack2<BF>(sm).x, by = __fdividef(1.f, step);
+    // d / s to its last bit, the approximate quotient corrected by its remainder, so that a half is a half (in bf16 every
+    // other warp has one); to the nearest by adding 1.5 2^23.  Four codes of a half word add up in fp32 as digits of base
+    // 16.
+    constexpr float kRound = 12582912.f;
+    const uint64_t least2 = pair(-lo, -lo), by2 = pair(by, by), step2 = pair(-step, -step), round2 = pair(kRound, kRound);
+    const uint64_t back2 = pair(-kRound, -kRound), base2 = pair(16.f, 16.f), whole2 = pair(8388608.f, 8388608.f);
+    uint32_t c[2];
+    float last = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint64_t sum = 0;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const float2 f = unpack2<BF>(w[4 * h + i]);
+            const uint64_t d = add2(pair(f.x, f.y), least2), near = fma2(d, by2, 0);
+            const uint64_t q = add2(add2(fma2(fma2(near, step2, d), by2, near), round2), back2);
+            const float2 k = unpair(q);
+            last = max3(last, k.x, k.y);
+            sum = fma2(sum, base2, q);
+        }
+        const float2 digits = unpair(add2(sum, whole2));
+        c[h] = __byte_perm(__float_as_uint(digits.x), __float_as_uint(digits.y), 0x5410);
+    }
+    if (!small && step > 0.f && last <= 15.f) return make_uint2(c[0], c[1]);
+    // values past the last code (of a step that is a multiple of the type's least number), the smallest steps and none
+    const float up = small ? 0x1p64f : 1.f, s = step * up, inv = s > 0.f ? __fdividef(1.f, s) : 0.f;   // 1 / s in range
+    c[0] = c[1] = 0;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        const float d = __fsub_rn(x[e], lo) * up, k = fminf(floorf(d * inv), 15.f);
+        const float2 f = unpack2<BF>(w[e >> 1]);
+        const float d = __fsub_rn(e & 1 ? f.y : f.x, lo) * up, k = fminf(floorf(d * inv), 15.f);
         const float past = __fmaf_rn(-(k + 0.5f), s, d);                 // of the half after k
         const int n = static_cast<int>(k);
         const int code = s > 0.f ? min(n + (past > 0.f || (past == 0.f && (n & 1))), 15) : 0;
@@ -76,7 +135,7 @@ __device__ __forceinline__ uint2 quantise(const uint4 &v0, const uint4 &v1, int 
 }
 
 template <bool BF>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     append4_kernel(AttnShape s, AttnBatch b, Cache4 c, AppendCall a, int tokens_per_cta) {
     __shared__ Token tok[kMaxTokens];
     __shared__ uint4 turned_rows[2 * kThreads];
@@ -87,16 +146,14 @@ __global__ void __launch_bounds__(kThreads)
         if (lane == 0) tok[warp] = k;
     }
     __syncthreads();
-    const int per_head = s.d / 16, heads = s.hq + 2 * s.hkv, per_token = heads * per_head;       // 4 or 8 lanes a head
+    const int head_log2 = s.d == 64 ? 2 : 3, per_head = 1 << head_log2, per_token = (s.hq + 2 * s.hkv) << head_log2;
     const int half = a.rot / 2, turned = a.rope ? a.rot / 16 : 0;
     const int record = record_bytes(s.d, c.group_log2), group_lanes = 1 << (c.group_log2 - 4);
     const unsigned mask = ((1u << per_head) - 1) << (lane & ~(per_head - 1));                    // the head's lanes
     uint4 *row = turned_rows + 2 * (threadIdx.x & ~(per_head - 1));                              // the head's elements
-    for (int w = threadIdx.x; w < nt * per_token; w += kThreads) {
-        const int ti = w / per_token, u = w - ti * per_token, head = u / per_head, item = u - head * per_head;
-        const Token k = tok[ti];
-        if (k.page < 0) continue;
-        const int64_t t = t0 + ti;
+    // a thread has the same place in every token
+    for (int u = threadIdx.x; u < per_token; u += kThreads) {
+        const int head = u >> head_log2, item = u & (per_head - 1);
         const bool query = head < s.hq, key = !query && head < s.hq + s.hkv;
         const bool turn = item < turned && (query || key);
         int e0 = 16 * item, e1 = e0 + 8;                 // first elements of the two vectors
@@ -104,52 +161,64 @@ __global__ void __launch_bounds__(kThreads)
             e0 = 8 * item;
             e1 = e0 + half;
         }
-        const uint16_t *src = a.qkv + t * a.qkv_stride + head * s.d;
-        uint4 v0 = *reinterpret_cast<const uint4 *>(src + e0), v1 = *reinterpret_cast<const uint4 *>(src + e1);
-        if (turn) {
-            const float4 *cs = reinterpret_cast<const float4 *>(a.rope + static_cast<int64_t>(k.pos) * half + 8 * item);
-            uint32_t *p = reinterpret_cast<uint32_t *>(&v0), *q = reinterpret_cast<uint32_t *>(&v1);
-            auto rotate = [&](float x, float y, float co, float si) {
-                return make_float2(cross(x, co, y, si), cross(y, co, -x, si));
-            };
+        const uint16_t *src = a.qkv + static_cast<int64_t>(t0) * a.qkv_stride + head * s.d;
+        uint4 n0 = *reinterpret_cast<const uint4 *>(src + e0), n1 = *reinterpret_cast<const uint4 *>(src + e1);
+        for (int ti = 0; ti < nt; ++ti) {
+            const Token k = tok[ti];
+            uint4 v0 = n0, v1 = n1;
+            src += a.qkv_stride;
+            if (ti + 1 < nt) {                           // the next token's, while this one's are worked on
+                n0 = *reinterpret_cast<const uint4 *>(src + e0);
+                n1 = *reinterpret_cast<const uint4 *>(src + e1);
+            }
+            if (k.page < 0) continue;
+            const int64_t t = t0 + ti;
+            if (turn) {
+                const float4 *cs = reinterpret_cast<const float4 *>(a.rope + static_cast<int64_t>(k.pos) * half + 8 * item);
+                uint32_t *p = reinterpret_cast<uint32_t *>(&v0), *q = reinterpret_cast<uint32_t *>(&v1);
+                // queries are rounded once, whatever the last bit of the fp32 sum; keys go through a border
+                auto rotate = [&](float x, float y, float co, float si) {
+                    return key ? make_float2(cross(x, co, y, si), cross(y, co, -x, si)) : make_float2(x * co - y * si, y * co + x * si);
+                };
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {                // pairs 2e and 2e + 1 of the item's eight
-                const float4 r = cs[e];                  // cos, sin, cos, sin
-                if (a.interleaved) {
-                    uint32_t *x = e < 2 ? p + 2 * e : q + 2 * (e - 2);
-                    const float2 m = unpack2<BF>(x[0]), n = unpack2<BF>(x[1]);
-                    const float2 f = rotate(m.x, m.y, r.x, r.y), g = rotate(n.x, n.y, r.z, r.w);
-                    x[0] = pack2<BF>(f.x, f.y);
-                    x[1] = pack2<BF>(g.x, g.y);
-                } else {
-                    const float2 m = unpack2<BF>(p[e]), n = unpack2<BF>(q[e]);
-                    const float2 f = rotate(m.x, n.x, r.x, r.y), g = rotate(m.y, n.y, r.z, r.w);
-                    p[e] = pack2<BF>(f.x, g.x);
-                    q[e] = pack2<BF>(f.y, g.y);
+                for (int e = 0; e < 4; ++e) {            // pairs 2e and 2e + 1 of the item's eight
+                    const float4 r = cs[e];              // cos, sin, cos, sin
+                    if (a.interleaved) {
+                        uint32_t *x = e < 2 ? p + 2 * e : q + 2 * (e - 2);
+                        const float2 m = unpack2<BF>(x[0]), n = unpack2<BF>(x[1]);
+                        const float2 f = rotate(m.x, m.y, r.x, r.y), g = rotate(n.x, n.y, r.z, r.w);
+                        x[0] = pack2<BF>(f.x, f.y);
+                        x[1] = pack2<BF>(g.x, g.y);
+                    } else {
+                        const float2 m = unpack2<BF>(p[e]), n = unpack2<BF>(q[e]);
+                        const float2 f = rotate(m.x, n.x, r.x, r.y), g = rotate(m.y, n.y, r.z, r.w);
+                        p[e] = pack2<BF>(f.x, g.x);
+                        q[e] = pack2<BF>(f.y, g.y);
+                    }
                 }
             }
+            if (query) {
+                uint16_t *dst = a.q_out + t * a.q_stride + head * s.d;
+                *reinterpret_cast<uint4 *>(dst + e0) = v0;
+                *reinterpret_cast<uint4 *>(dst + e1) = v1;
+                continue;
+            }
+            if (key && turned && !a.interleaved) {       // to sixteen neighbours
+                row[e0 / 8] = v0;
+                row[e1 / 8] = v1;
+                __syncwarp(mask);
+                v0 = row[2 * item];
+                v1 = row[2 * item + 1];
+                __syncwarp(mask);
+            }
+            uint32_t sm;
+            const uint2 codes = quantise<BF>(v0, v1, group_lanes, mask, sm);
+            const int h = head - s.hq - (key ? 0 : s.hkv);
+            uint8_t *dst = c.kv + k.page * c.page_stride + static_cast<int64_t>(h * s.page + k.slot) * record;
+            *reinterpret_cast<uint2 *>(dst + (key ? 0 : s.d / 2) + 8 * item) = codes;
+            if (item % group_lanes == 0)
+                *reinterpret_cast<uint32_t *>(dst + s.d + (key ? 0 : 4 * s.d >> c.group_log2) + 4 * (item / group_lanes)) = sm;
         }
-        if (query) {
-            uint16_t *dst = a.q_out + t * a.q_stride + head * s.d;
-            *reinterpret_cast<uint4 *>(dst + e0) = v0;
-            *reinterpret_cast<uint4 *>(dst + e1) = v1;
-            continue;
-        }
-        if (key) {
-            row[e0 / 8] = v0;
-            row[e1 / 8] = v1;
-            __syncwarp(mask);
-            v0 = row[2 * item];
-            v1 = row[2 * item + 1];
-            __syncwarp(mask);
-        }
-        uint32_t sm;
-        const uint2 codes = quantise<BF>(v0, v1, group_lanes, mask, sm);
-        const int h = head - s.hq - (key ? 0 : s.hkv);
-        uint8_t *dst = c.kv + k.page * c.page_stride + static_cast<int64_t>(h * s.page + k.slot) * record;
-        *reinterpret_cast<uint2 *>(dst + (key ? 0 : s.d / 2) + 8 * item) = codes;
-        if (item % group_lanes == 0)
-            *reinterpret_cast<uint32_t *>(dst + s.d + (key ? 0 : 4 * s.d >> c.group_log2) + 4 * (item / group_lanes)) = sm;
     }
 }
 
@@ -205,14 +274,14 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Tokens of a CTA: one until the GPU is full, then up to eight.
-int tokens_each(int tokens) { return std::max(1, std::min(kMaxTokens, tokens / 1216)); }
+// Tokens of a CTA: one until the GPU is full, then up to `most`.
+int tokens_each(int tokens, int most) { return std::max(1, std::min(most, tokens / 1216)); }
 
 }  // namespace
 
 cudaError_t launch_attn_append4(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AppendCall &a, bool bf16,
                                 cudaStream_t st) {
-    const int per = tokens_each(b.tokens), grid = (b.tokens + per - 1) / per;
+    const int per = tokens_each(b.tokens, 4), grid = (b.tokens + per - 1) / per;
     if (bf16) append4_kernel<true><<<grid, kThreads, 0, st>>>(s, b, c, a, per);
     else append4_kernel<false><<<grid, kThreads, 0, st>>>(s, b, c, a, per);
     return cudaGetLastError();
@@ -221,7 +290,7 @@ cudaError_t launch_attn_append4(const AttnShape &s, const AttnBatch &b, const Ca
 cudaError_t launch_attn_read(const AttnShape &s, const AttnBatch &b, const AttnCache *c, const Cache4 *c4, uint16_t *k,
                              int64_t k_stride, uint16_t *v, int64_t v_stride, bool bf16, int *status, cudaStream_t st) {
     const ReadOut o{k, v, k_stride, v_stride, status};
-    const int per = tokens_each(b.tokens), grid = (b.tokens + per - 1) / per;
+    const int per = tokens_each(b.tokens, kMaxTokens), grid = (b.tokens + per - 1) / per;
     auto kernel = !c4 ? read_kernel<false, false> : bf16 ? read_kernel<true, true> : read_kernel<false, true>;
     kernel<<<grid, kThreads, 0, st>>>(s, b, c ? *c : AttnCache{}, c4 ? *c4 : Cache4{}, o, per);
     return cudaGetLastError();
