@@ -170,19 +170,25 @@ class PagedAttention:
         [tokens, kv_heads, head_dim] of the handle's type; of a PagedCache4 the
         values that its codes stand for."""
         self._check(cache, batch)
-        shape = (batch.tokens, self.kv_heads, self.head_dim)
-        outs, args = [], []
-        for t, what in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is None:
-                t = torch.empty(shape, dtype=self.dtype, device=self.device)
-            o, rows, stride = self._token_rows(t, what, self.kv_heads, written=True)
-            if rows != batch.tokens:
-                _refuse(f"{what} has {rows} rows, the batch {batch.tokens} tokens")
-            outs.append(t)
-            args += [o.data_ptr(), stride]
+        if k_out is None and v_out is None:
+            k_out = torch.empty((batch.tokens, self.kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
+            outs = k_out, torch.empty_like(k_out)
+            width = self.kv_heads * self.head_dim
+            args = k_out.data_ptr(), width, outs[1].data_ptr(), width
+        else:
+            outs, args = [], []
+            for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+                if t is None:
+                    t = torch.empty((batch.tokens, self.kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
+                o, rows, stride = self._token_rows(t, what, self.kv_heads, written=True)
+                if rows != batch.tokens:
+                    _refuse(f"{what} has {rows} rows, the batch {batch.tokens} tokens")
+                outs.append(t)
+                args += [o.data_ptr(), stride]
+            outs = tuple(outs)
         call = _read4 if type(cache.struct) is gptq_q4_cache4 else _read
         _check(call(self.handle, cache.ref, batch.ref, *args, _stream(self.device.index)))
-        return tuple(outs)
+        return outs
 
     def attend(self, q, cache, batch: PagedBatch, scale: float | None = None, window: int = 0, out=None, sinks: int = 0):
         """Attention of the new tokens' queries q [tokens, q_heads, head_dim]

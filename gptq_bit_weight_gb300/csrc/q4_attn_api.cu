@@ -213,10 +213,8 @@ int attend(gptq_q4_attn h, const void *q, int64_t q_stride, const Cache *cache, 
         const auto stream_kv = a.sinks ? q4::launch_attend_stream_sinks : q4::launch_attend_stream;
         e = (chunk ? tc : stream_kv)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
     } else {
-        const int64_t rows = static_cast<int64_t>(batch->max_q) * s.group;
         const auto tc = s.d == 64 ? q4::launch_attend_tc4_64 : q4::launch_attend_tc4_128;
-        const auto stream_kv = rows <= 8 ? q4::launch_attend_stream4_8 : q4::launch_attend_stream4_16;
-        e = (chunk ? tc : stream_kv)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
+        e = (chunk ? tc : q4::launch_attend_stream4)(s, batch_view(batch), cache_view(cache), a, bf16, stream);
     }
     if (e) return api_cuda_fail(e, "attention launch");
     q4::api_count_launches(1);

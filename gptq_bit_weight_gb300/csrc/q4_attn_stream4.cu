@@ -29,7 +29,6 @@
 //   Three CTAs of one team each took as long as the slowest: some had finished
 // after 29 us and others after 67.  Teams that shared the items of a CTA met
 // too often: 88 us for 64 ragged requests.
-#pragma once
 #include <climits>
 
 #include "q4_attn_tma.cuh"
@@ -43,18 +42,18 @@ using namespace tc;
 
 constexpr int kWarps = 4;                       // of a team, and a loader
 constexpr int kKeys = kKt / kWarps;             // tokens of a warp in a tile
+constexpr int kRows = 8, kRowsLog2 = 3;         // rows of a row tile: the columns of an MMA
 constexpr int kBlocks = kKeys / 16;             // of 16 tokens, the rows of an MMA
 
-template <int D_, int GL_, int NT_, int TEAMS_>
+template <int D_, int GL_>
 struct Cfg {
-    static constexpr int D = D_, GL = GL_, NT = NT_, kTeams = TEAMS_;
+    static constexpr int D = D_, GL = GL_, kTeams = 3;
     static constexpr int kThreads = 32 * (kWarps + 1) * kTeams;
     static constexpr int kRecord = record_bytes(D, GL);
-    static constexpr int kRows = 8 * NT;                        // rows of a row tile
     static constexpr int MT = D / 16;                           // MMAs along the value's elements
     static constexpr int kStage = kKt * kRecord;
-    static constexpr int kQ = NT * (D / 32) * 32 * 16;          // query fragments, double-buffered for each team
-    static constexpr int kSlot = NT * MT * 32 * 16 + NT * 4 * 16;      // a warp's part: fragments, (m, m, l, l)
+    static constexpr int kQ = (D / 32) * 32 * 16;               // query fragments, double-buffered for each team
+    static constexpr int kSlot = MT * 32 * 16 + 4 * 16;      // a warp's part: fragments, (m, m, l, l)
     static constexpr int kMisc = 1536;
     static constexpr int kFixed = kTeams * (2 * kQ + kWarps / 2 * kSlot) + kMisc + 128;
     static constexpr int kRoom = (232448 - 1024 - kFixed) / kStage;
@@ -130,17 +129,44 @@ __device__ __forceinline__ int token_of(int r) {
     else return (r & 1) << 2 | r >> 1;
 }
 
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 constexpr float kRescale = 8.f;                  // log2 of the growth that p may have
 
 template <bool BF, class C>
 __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) {
-    constexpr int D = C::D, NT = C::NT, MT = C::MT, S = C::kStages, T = C::kTeams, R = C::kRecord, GL = C::GL;
+    constexpr int D = C::D, MT = C::MT, S = C::kStages, T = C::kTeams, R = C::kRecord, GL = C::GL;
     constexpr int WORDS = D / 32;                // words of a key's codes in a thread
     constexpr int OCT = D / 64;                  // words of a value's codes
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 127u) & ~127u;
     uint8_t *sb = smem_raw + (base - raw);
-    uint4 *sq = reinterpret_cast<uint4 *>(sb + S * C::kStage);                            // [T][2][NT][WORDS][32]
+    uint4 *sq = reinterpret_cast<uint4 *>(sb + S * C::kStage);                            // [T][2][WORDS][32]
     uint8_t *slots = sb + S * C::kStage + 2 * T * C::kQ;                                  // [T][kWarps / 2]
     uint8_t *misc = slots + T * (kWarps / 2) * C::kSlot;
     const uint32_t bar0 = smem_u32(misc);
@@ -151,7 +177,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
     int *flags = reinterpret_cast<int *>(misc + 8 * (2 * S + 4 * T));                     // [T]
     Handed *items = reinterpret_cast<Handed *>(misc + 320);                               // [T][2]
     TeamSchedSmem<T> &sched = *reinterpret_cast<TeamSchedSmem<T> *>(misc + 1024);
-    static_assert((4 * NT * 16 + 32 * 4 * NT * 8) <= kWarps / 2 * C::kSlot && S >= 2 * T && S % T == 0 && 8 * (2 * S + 4 * T) + 4 * T <= 320 && 320 + 2 * T * sizeof(Handed) <= 1024 &&
+    static_assert(4 * 16 + 32 * 4 * 8 <= kWarps / 2 * C::kSlot && S >= 2 * T && S % T == 0 && 8 * (2 * S + 4 * T) + 4 * T <= 320 && 320 + 2 * T * sizeof(Handed) <= 1024 &&
                       1024 + sizeof(TeamSchedSmem<T>) <= C::kMisc,
                   "shared memory");
 
@@ -183,27 +209,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         const int g = lane >> 2, t4 = lane & 3, group = a.p.group.d;
         bool more = true;
         for (int k = 0;; ++k) {
-            // the item and its query fragments to the team: row 8 n + g, a quarter of its elements
+            // the item and its query fragments to the team: row g, a quarter of its elements
             more = more && it.u < sh.end;
-            const int buf = k & 1, r_first = it.tile * C::kRows, rows = more ? it.ql * group - r_first : 0;
-            uint4 q[NT * WORDS];
+            const int buf = k & 1, rr = it.tile * kRows + g, t = a.p.group(rr);
+            const bool row = more && rr < it.ql * group;
+            const uint16_t *src = a.q + static_cast<int64_t>(it.q0 + t) * a.q_stride + (it.head * group + rr - t * group) * D + D / 4 * t4;
+            uint4 q[WORDS];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int r = 8 * n + g, rr = r_first + r, t = a.p.group(rr);
-                const uint16_t *src = a.q + static_cast<int64_t>(it.q0 + t) * a.q_stride + (it.head * group + rr - t * group) * D + D / 4 * t4;
-#pragma unroll
-                for (int w = 0; w < WORDS; ++w)
-                    q[n * WORDS + w] = r < rows ? *reinterpret_cast<const uint4 *>(src + 8 * w) : make_uint4(0, 0, 0, 0);
-            }
-            if (k >= 2) alive = wait_all(alive, taken(team, buf), ((k >> 1) & 1) ^ 1);
-            if (!alive) break;
-#pragma unroll
-            for (int f = 0; f < NT * WORDS; ++f) sq[((2 * team + buf) * NT * WORDS + f) * 32 + lane] = q[f];
-            if (lane == 0) items[2 * team + buf] = Handed{it, more};
-            __syncwarp();
-            if (lane == 0) mbar_arrive(handed(team, buf));
-            if (!more) break;
-            const int j0 = max(sh.begin - it.u, 0), j1 = it.hi > 0 ? min(sh.end - it.u, it.n) : j0;
+            for (int w = 0; w < WORDS; ++w) q[w] = row ? *reinterpret_cast<const uint4 *>(src + 8 * w) : make_uint4(0, 0, 0, 0);
+            const int j0 = max(sh.begin - it.u, 0), j1 = more && it.hi > 0 ? min(sh.end - it.u, it.n) : j0;
             const PageWalk walk(a.p, it, a.c.pages);
             const int boxes = kKt >> walk.box_log2, bytes = R << walk.box_log2;
             const uint8_t *head = a.c.kv + static_cast<int64_t>(it.head << a.p.page_log2) * R;
@@ -213,6 +227,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                 return lane < boxes && sees_some(a.p, it, key, 1 << walk.box_log2) ? __ldg(walk.table + (key >> walk.page_log2)) : INT_MIN;
             };
             int next = j0 < j1 ? entry(j0) : INT_MIN;
+            if (k >= 2) alive = wait_all(alive, taken(team, buf), ((k >> 1) & 1) ^ 1);
+            if (!alive) break;
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) sq[((2 * team + buf) * WORDS + w) * 32 + lane] = q[w];
+            if (lane == 0) items[2 * team + buf] = Handed{it, more};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(handed(team, buf));
+            if (!more) break;
             for (int j = j0; j < j1; ++j) {
                 int page = next;
                 if (j + 1 < j1) next = entry(j + 1);
@@ -283,33 +305,28 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         if (!alive || !items[2 * team + buf].more) break;
         it = items[2 * team + buf].it;
         const int j0 = max(sh.begin - it.u, 0), j1 = min(sh.end - it.u, it.n);
-        const int r_first = it.tile * C::kRows, rows = it.ql * group - r_first;    // of this tile: min(rows, kRows)
-        const uint4 *qf = sq + (2 * team + buf) * NT * WORDS * 32;
+        const int r_first = it.tile * kRows, rows = it.ql * group - r_first;    // of this tile: min(rows, kRows)
         uint4 qr[WORDS];
-        if constexpr (NT == 1)
 #pragma unroll
-            for (int w = 0; w < WORDS; ++w) qr[w] = qf[w * 32 + lane];
-        // m: greatest score so far; ref: what exponents are taken against, m as it was when it last moved, 0 for -inf
-        float o[NT][MT][4], m[NT][2], ref[NT][2], l[NT][2];
-        int lim[NT][2], lim_lo[NT][2];                                 // last key that a row sees; last one before its window
-        bool fresh = true;                                             // some row has seen no key
+        for (int w = 0; w < WORDS; ++w) qr[w] = sq[((2 * team + buf) * WORDS + w) * 32 + lane];
+        // of the thread's two rows: what exponents are taken against, the sum of its tokens' weights, whether a token was seen
+        float o[MT][4] = {}, ref[2] = {0.f, 0.f};
+        uint64_t l2 = 0;
+        bool unseen[2] = {true, true};
         const int own = it.kv - it.ql, lim_min = own + it.t0, lim_max = own + it.t1, window = a.p.window, sinks = a.p.sinks;
+        int lim[2], lim_lo[2];                                         // last token that a row sees; last one before its window
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[n][e] = -INFINITY;
-                ref[n][e] = l[n][e] = 0.f;
-                lim[n][e] = own + min(a.p.group(r_first + 8 * n + 2 * t4 + e), it.t1);
-                lim_lo[n][e] = window > 0 ? lim[n][e] - window : -1;
-            }
+        for (int e = 0; e < 2; ++e) {
+            lim[e] = own + min(a.p.group(r_first + 2 * t4 + e), it.t1);
+            lim_lo[e] = window > 0 ? lim[e] - window : -1;
         }
+        // tiles without a hidden token: neither the last ones, nor at the windows' ends, nor of the first tokens
+        const int plain_hi = (max(lim_min + 1, 0) >> kKtLog2) - it.first;
+        const int plain_lo = max(it.near, window > 0 && lim_max >= window ? ((lim_max - window) >> kKtLog2) + 1 - it.first : 0);
         // The products of two tiles go together, a tile's values and the next one's keys: neither waits for the other.
-        // Scores of a tile: token key_row (+ 8 from e = 2 on, + 16 b), row 8 n + 2 t4 + (e & 1).
-        float s[kBlocks][NT][4];
-        uint32_t pb[kBlocks][NT][2];
+        // Scores of a tile: token key_row (+ 8 from e = 2 on, + 16 b), row 2 t4 + (e & 1).
+        float s[kBlocks][4];
+        uint32_t pb[kBlocks][2];
         auto keys = [&](const uint8_t *stage, int b) {
             const uint8_t *r0 = stage + k_at + 16 * b * R, *r1 = r0 + 8 * R;
             uint32_t w0[WORDS], w1[WORDS];
@@ -324,17 +341,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             }
             const uint32_t p0 = *reinterpret_cast<const uint32_t *>(r0 + k_param), p1 = *reinterpret_cast<const uint32_t *>(r1 + k_param);
             const uint32_t s0 = both_low(p0), m0 = both_high(p0), s1 = both_low(p1), m1 = both_high(p1);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) s[b][n][0] = s[b][n][1] = s[b][n][2] = s[b][n][3] = 0.f;
+            s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) {
                 const uint4 x = values_of<BF>(w0[w], s0, m0), y = values_of<BF>(w1[w], s1, m1);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 q = NT == 1 ? qr[w] : qf[(n * WORDS + w) * 32 + lane];
-                    mma16816<BF>(s[b][n], x.x, y.x, x.y, y.y, q.x, q.y);
-                    mma16816<BF>(s[b][n], x.z, y.z, x.w, y.w, q.z, q.w);
-                }
+                mma16816<BF>(s[b], x.x, y.x, x.y, y.y, qr[w].x, qr[w].y);
+                mma16816<BF>(s[b], x.z, y.z, x.w, y.w, qr[w].z, qr[w].w);
             }
         };
         auto values = [&](const uint8_t *stage, int b) {
@@ -368,30 +380,31 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t a0 = fma_2<BF>(x[0][0][i], sv[0], mv[0]), a1 = fma_2<BF>(x[0][1][i], sv[0], mv[0]);
                     const uint32_t a2 = fma_2<BF>(x[1][0][i], sv[1], mv[1]), a3 = fma_2<BF>(x[1][1][i], sv[1], mv[1]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16816<BF>(o[n][4 * w + i], a0, a1, a2, a3, pb[b][n][0], pb[b][n][1]);
+                    mma16816<BF>(o[4 * w + i], a0, a1, a2, a3, pb[b][0], pb[b][1]);
                 }
             }
         };
         // Scores to weights.  edge: some token is hidden from some row (a few instructions beside the rest: a copy of the
         // code for such tiles ran cold, 5 us where a tile takes 1).
         auto weights = [&](uint8_t *stage, int key0, bool edge) {
+            const uint64_t scale2 = pair(a.scale, a.scale), ref2 = pair(-ref[0], -ref[1]);
+            float x[kBlocks][4];                         // exponents
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[b][n][e] *= a.scale;
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 v = unpair(fma2(pair(s[b][e], s[b][e + 1]), scale2, ref2));
+                    x[b][e] = v.x;
+                    x[b][e + 1] = v.y;
+                }
             if (edge) {
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + key_row - key_first + 16 * b + (e & 2) * 4;
-                            if (key > lim[n][e & 1] || (key <= lim_lo[n][e & 1] && key >= sinks)) s[b][n][e] = -INFINITY;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + key_row - key_first + 16 * b + (e & 2) * 4;
+                        if (key > lim[e & 1] || (key <= lim_lo[e & 1] && key >= sinks)) x[b][e] = -INFINITY;
+                    }
                 // slots past the visible tokens hold anything: their values must not meet a weight of 0
                 if (!sees_some(a.p, it, key0 + lane, 1)) {
                     uint32_t *params = reinterpret_cast<uint32_t *>(stage + (key_first + lane) * R + vParams);
@@ -401,51 +414,44 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                 fence_proxy_async();                     // before the next copy to the stage
                 __syncwarp();
             }
-            float top = -INFINITY;                       // the most that a score is above its row's reference
+            float top = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+            for (int b = 0; b < kBlocks; ++b) top = max3(max3(top, x[b][0], x[b][1]), x[b][2], x[b][3]);
+            if (__any_sync(0xffffffffu, top > kRescale || unseen[0] || unseen[1])) {
+                float keep[2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int c = 0; c < 2; ++c) {
+                    float high = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top = fmaxf(top, s[b][n][e] - ref[n][e & 1]);
-            if (__any_sync(0xffffffffu, top > kRescale || fresh)) {
-                fresh = false;
+                    for (int b = 0; b < kBlocks; ++b) high = max3(high, x[b][c], x[b][c + 2]);
+                    high = max_g(high);
+                    // to the greatest so far; a row's first token sets it, up or down
+                    const float up = high == -INFINITY ? 0.f : unseen[c] ? high : fmaxf(high, 0.f);
+                    keep[c] = unseen[c] ? 1.f : ex2(-up);
+                    unseen[c] = unseen[c] && high == -INFINITY;
+                    ref[c] += up;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float keep[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float high = m[n][c];
-#pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) high = fmaxf(high, fmaxf(s[b][n][c], s[b][n][c + 2]));
-                        high = max_g(high);
-                        ref[n][c] = ref_of(high);
-                        keep[c] = ex2(m[n][c] - ref[n][c]);
-                        m[n][c] = high;
-                        l[n][c] *= keep[c];
-                        fresh |= high == -INFINITY;
+                    for (int b = 0; b < kBlocks; ++b) {
+                        x[b][c] -= up;
+                        x[b][c + 2] -= up;
                     }
+                }
+                l2 = fma2(l2, pair(keep[0], keep[1]), 0);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        o[n][i][0] *= keep[0];
-                        o[n][i][1] *= keep[1];
-                        o[n][i][2] *= keep[0];
-                        o[n][i][3] *= keep[1];
-                    }
+                for (int i = 0; i < MT; ++i) {
+                    o[i][0] *= keep[0];
+                    o[i][1] *= keep[1];
+                    o[i][2] *= keep[0];
+                    o[i][3] *= keep[1];
                 }
             }
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2(s[b][n][e] - ref[n][e & 1]);
-                    l[n][0] += p[0] + p[2];
-                    l[n][1] += p[1] + p[3];
-                    pb[b][n][0] = transpose8(pack2<BF>(p[0], p[1]));
-                    pb[b][n][1] = transpose8(pack2<BF>(p[2], p[3]));
-                }
+            for (int b = 0; b < kBlocks; ++b) {
+                const float p0 = ex2(x[b][0]), p1 = ex2(x[b][1]), p2 = ex2(x[b][2]), p3 = ex2(x[b][3]);
+                l2 = add2(l2, add2(pair(p0, p1), pair(p2, p3)));
+                pb[b][0] = transpose8(pack2<BF>(p0, p1));
+                pb[b][1] = transpose8(pack2<BF>(p2, p3));
+            }
         };
         const int tiles = it.hi > 0 ? j1 - j0 : 0;
         auto next_stage = [&] {
@@ -462,11 +468,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             for (int b = 0; b < kBlocks; ++b) keys(sb + at * C::kStage, b);
 #pragma unroll 1
             for (int j = j0; j < j0 + tiles; ++j) {
-                const int key_t = key_tile(a.p, it, j) << kKtLog2;
-                // tiles without a hidden token: all but the last and those at the window's ends
-                const bool edge = key_t + kKt - 1 > lim_min || (window > 0 && key_t <= lim_max - window && key_t + kKt > sinks);
                 uint8_t *here = sb + at * C::kStage;
-                weights(here, key_t + key_first, edge);
+                weights(here, (key_tile(a.p, it, j) << kKtLog2) + key_first, j < plain_lo || j >= plain_hi);
                 const bool more_tiles = j + 1 < j0 + tiles;
                 const int now = at;
                 if (more_tiles) {                        // (past the last tile its own keys go through once more, for nothing)
@@ -488,59 +491,53 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         __syncwarp();
         if (lane == 0) mbar_arrive(taken(team, buf));
         {
-            // members 2 and 3 to 0 and 1
+            // members 2 and 3 to 0 and 1; a row without a token has no reference
+            const float2 sums = unpair(l2);
+            float m[2], l[2] = {sum_g(sums.x), sum_g(sums.y)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) m[e] = l[e] == 0.f ? -INFINITY : ref[e];
             float4 *w = reinterpret_cast<float4 *>(slots + (team * (kWarps / 2) + member % (kWarps / 2)) * C::kSlot);
             auto put = [&] {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) w[(n * MT + i) * 32 + lane] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
-                    if (g == 0) w[NT * MT * 32 + 4 * n + t4] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
-                }
+                for (int i = 0; i < MT; ++i) w[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                if (g == 0) w[MT * 32 + t4] = make_float4(m[0], m[1], l[0], l[1]);
             };
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) l[n][e] = sum_g(l[n][e]);
             if (member >= kWarps / 2) put();
             bar_team(team);
             if (member < kWarps / 2) {
+                const float4 ml = w[MT * 32 + t4];
+                float own_f[2], other[2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float4 ml = w[NT * MT * 32 + 4 * n + t4];
-                    float own_f[2], other[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float mo = e ? ml.y : ml.x, top = fmaxf(m[n][e], mo), r = ref_of(top);
-                        own_f[e] = ex2(m[n][e] - r);
-                        other[e] = ex2(mo - r);
-                        m[n][e] = top;
-                        l[n][e] = l[n][e] * own_f[e] + (e ? ml.w : ml.z) * other[e];
-                    }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const float4 v = w[(n * MT + i) * 32 + lane];
-                        o[n][i][0] = o[n][i][0] * own_f[0] + v.x * other[0];
-                        o[n][i][1] = o[n][i][1] * own_f[1] + v.y * other[1];
-                        o[n][i][2] = o[n][i][2] * own_f[0] + v.z * other[0];
-                        o[n][i][3] = o[n][i][3] * own_f[1] + v.w * other[1];
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const float mo = e ? ml.y : ml.x, top = fmaxf(m[e], mo), r = ref_of(top);
+                    own_f[e] = ex2(m[e] - r);
+                    other[e] = ex2(mo - r);
+                    m[e] = top;
+                    l[e] = l[e] * own_f[e] + (e ? ml.w : ml.z) * other[e];
                 }
-                __syncwarp();                            // the last fragment of (m, l) has been read
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const float4 v = w[i * 32 + lane];
+                    o[i][0] = o[i][0] * own_f[0] + v.x * other[0];
+                    o[i][1] = o[i][1] * own_f[1] + v.y * other[1];
+                    o[i][2] = o[i][2] * own_f[0] + v.z * other[0];
+                    o[i][3] = o[i][3] * own_f[1] + v.w * other[1];
+                }
+                __syncwarp();                            // (m, l) have been read
                 put();
             }
         }
         bar_team(team);
         // every warp: fragments member, member + 4, .. of both slots
-        constexpr int F = (NT * MT + kWarps - 1) / kWarps;
+        constexpr int F = MT / kWarps;
         float4 acc[F];
         float top[F][2], sum[F][2];
 #pragma unroll
         for (int u = 0; u < F; ++u) {
-            const int f = min(member + u * kWarps, NT * MT - 1), n = f / MT;
+            const int f = member + u * kWarps;
             const float4 *w0 = reinterpret_cast<const float4 *>(slots + team * (kWarps / 2) * C::kSlot);
             const float4 *w1 = reinterpret_cast<const float4 *>(slots + (team * (kWarps / 2) + 1) * C::kSlot);
-            const float4 v0 = w0[NT * MT * 32 + 4 * n + t4], v1 = w1[NT * MT * 32 + 4 * n + t4];
+            const float4 v0 = w0[MT * 32 + t4], v1 = w1[MT * 32 + t4];
             const float4 x0 = w0[f * 32 + lane], x1 = w1[f * 32 + lane];
             top[u][0] = fmaxf(v0.x, v1.x);
             top[u][1] = fmaxf(v0.y, v1.y);
@@ -552,9 +549,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         }
         // ---------------------------------------- output, or a piece for the workspace
         auto inverse = [](float sum) { return sum == 0.f ? 0.f : 1.f / sum; };
-        // the thread's elements of row 8 n + 2 t4 + e
-        auto row_at = [&](int n, int e) -> uint16_t * {
-            const int r = 8 * n + 2 * t4 + e;
+        // the thread's elements of row 2 t4 + e
+        auto row_at = [&](int e) -> uint16_t * {
+            const int r = 2 * t4 + e;
             if (r >= rows) return nullptr;
             const int rr = r_first + r, t = a.p.group(rr);
             return a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride + (it.head * group + rr - t * group) * D + 8 * OCT * g;
@@ -564,18 +561,16 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             return pack2<BF>(x * inv, y * inv);
         };
         // elements 2 i and 2 i + 1 of the thread's words, of both its rows
-        auto store = [&](int f, const float4 &x, float l0, float l1) {
-            const int n = f / MT, i = f - n * MT;
-            if (uint16_t *dst = row_at(n, 0)) *reinterpret_cast<uint32_t *>(dst + 2 * i) = two(x.x, x.z, inverse(l0));
-            if (uint16_t *dst = row_at(n, 1)) *reinterpret_cast<uint32_t *>(dst + 2 * i) = two(x.y, x.w, inverse(l1));
+        auto store = [&](int i, const float4 &x, float l0, float l1) {
+            if (uint16_t *dst = row_at(0)) *reinterpret_cast<uint32_t *>(dst + 2 * i) = two(x.x, x.z, inverse(l0));
+            if (uint16_t *dst = row_at(1)) *reinterpret_cast<uint32_t *>(dst + 2 * i) = two(x.y, x.w, inverse(l1));
         };
         if (j0 == 0 && j1 == it.n) {
 #pragma unroll
-            for (int u = 0; u < F; ++u)
-                if (member + u * kWarps < NT * MT) store(member + u * kWarps, acc[u], sum[u][0], sum[u][1]);
+            for (int u = 0; u < F; ++u) store(member + u * kWarps, acc[u], sum[u][0], sum[u][1]);
             continue;
         }
-        // [NT][MT][32] float4 fragments, then [NT][4] (m, m, l, l) of a thread's two rows
+        // [MT][32] float4 fragments, then [4] (m, m, l, l) of a thread's two rows
         const int c0 = static_cast<uint32_t>(it.u) / sh.per, c1 = static_cast<uint32_t>(it.u + it.n - 1) / sh.per;
         auto piece = [&](int cta) {
             return reinterpret_cast<float4 *>(a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece);
@@ -584,9 +579,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
 #pragma unroll
         for (int u = 0; u < F; ++u) {
             const int f = member + u * kWarps;
-            if (f >= NT * MT) continue;
             __stcg(own_piece + f * 32 + lane, acc[u]);
-            if (f % MT == 0 && g == 0) __stcg(own_piece + NT * MT * 32 + 4 * (f / MT) + t4, make_float4(top[u][0], top[u][1], sum[u][0], sum[u][1]));
+            if (f == 0 && g == 0) __stcg(own_piece + MT * 32 + t4, make_float4(top[u][0], top[u][1], sum[u][0], sum[u][1]));
         }
         bar_team(team);
         if (member == 0 && lane == 0) {
@@ -598,26 +592,24 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         if (!*reinterpret_cast<volatile int *>(flags + team)) continue;
         // The pieces' weights first, all at once, then their fragments, eight pieces at a time; in the order of the CTAs.
         const int pieces = c1 - c0 + 1;
-        float4 *factors = reinterpret_cast<float4 *>(slots + team * (kWarps / 2) * C::kSlot);     // [n][t4]: (m, m, l, l) of all
-        float *lifts = reinterpret_cast<float *>(factors + 4 * NT);                             // [32 pieces][n][t4][2]
-        if (warp == team * kWarps) {
-            // lane: piece lane / 4 of eight, row pair t4
-            for (int n = 0; n < NT; ++n) {
-                float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float4 *factors = reinterpret_cast<float4 *>(slots + team * (kWarps / 2) * C::kSlot);     // [t4]: (m, m, l, l) of all
+        float *lifts = reinterpret_cast<float *>(factors + 4);                                    // [32 pieces][t4][2]
+        if (member == 0) {
+            // lane: pieces g, g + 8, .., row pair t4
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 #pragma unroll 4
-                for (int c = g; c < pieces; c += 8) {
-                    const float4 v = __ldcg(piece(c0 + c) + NT * MT * 32 + 4 * n + t4);
-                    const float h0 = fmaxf(m0, v.x), h1 = fmaxf(m1, v.y);
-                    l0 = l0 * ex2(m0 - ref_of(h0)) + v.z * ex2(v.x - ref_of(h0));
-                    l1 = l1 * ex2(m1 - ref_of(h1)) + v.w * ex2(v.y - ref_of(h1));
-                    m0 = h0;
-                    m1 = h1;
-                }
-                const float t0 = max_g(m0), t1 = max_g(m1);
-                l0 = sum_g(l0 * ex2(m0 - ref_of(t0)));
-                l1 = sum_g(l1 * ex2(m1 - ref_of(t1)));
-                if (g == 0) factors[4 * n + t4] = make_float4(t0, t1, l0, l1);
+            for (int c = g; c < pieces; c += 8) {
+                const float4 v = __ldcg(piece(c0 + c) + MT * 32 + t4);
+                const float h0 = fmaxf(m0, v.x), h1 = fmaxf(m1, v.y);
+                l0 = l0 * ex2(m0 - ref_of(h0)) + v.z * ex2(v.x - ref_of(h0));
+                l1 = l1 * ex2(m1 - ref_of(h1)) + v.w * ex2(v.y - ref_of(h1));
+                m0 = h0;
+                m1 = h1;
             }
+            const float t0 = max_g(m0), t1 = max_g(m1);
+            l0 = sum_g(l0 * ex2(m0 - ref_of(t0)));
+            l1 = sum_g(l1 * ex2(m1 - ref_of(t1)));
+            if (g == 0) factors[t4] = make_float4(t0, t1, l0, l1);
         }
         bar_team(team);
 #pragma unroll
@@ -625,16 +617,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
 #pragma unroll 1
         for (int cc = 0; cc < pieces; cc += 32) {
             const int here = min(32, pieces - cc);
-            for (int i = threadIdx.x % (32 * kWarps); i < here * 4 * NT; i += 32 * kWarps) {
-                const int c = i / (4 * NT), row = i - c * 4 * NT;
-                const float4 v = __ldcg(piece(c0 + cc + c) + NT * MT * 32 + row), all = factors[row];
+            if (const int i = threadIdx.x % (32 * kWarps); i < 4 * here) {
+                const float4 v = __ldcg(piece(c0 + cc + (i >> 2)) + MT * 32 + (i & 3)), all = factors[i & 3];
                 lifts[2 * i] = ex2(v.x - ref_of(all.x));
                 lifts[2 * i + 1] = ex2(v.y - ref_of(all.y));
             }
             bar_team(team);
 #pragma unroll
             for (int u = 0; u < F; ++u) {
-                const int f = min(member + u * kWarps, NT * MT - 1), n = f / MT;
+                const int f = member + u * kWarps;
 #pragma unroll 1
                 for (int c = 0; c < here; c += 8) {
                     float4 x[8];
@@ -643,7 +634,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         if (c + k >= here) continue;
-                        const float2 w = *reinterpret_cast<const float2 *>(lifts + 2 * ((c + k) * 4 * NT + 4 * n + t4));
+                        const float2 w = *reinterpret_cast<const float2 *>(lifts + 2 * (4 * (c + k) + t4));
                         acc[u].x += x[k].x * w.x;
                         acc[u].y += x[k].y * w.y;
                         acc[u].z += x[k].z * w.x;
@@ -653,13 +644,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             }
             bar_team(team);
         }
+        const float4 all = factors[t4];
 #pragma unroll
-        for (int u = 0; u < F; ++u) {
-            const int f = member + u * kWarps;
-            if (f >= NT * MT) continue;
-            const float4 all = factors[4 * (f / MT) + t4];
-            store(f, acc[u], all.z, all.w);
-        }
+        for (int u = 0; u < F; ++u) store(member + u * kWarps, acc[u], all.z, all.w);
     }
     if (!alive && lane == 0) atomicOr(a.status, kAttnTimeout);
 }
@@ -667,24 +654,21 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
 template <class C>
 cudaError_t launch(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
                    cudaStream_t st) {
-    constexpr int rows_log2 = C::NT == 1 ? 3 : 4;
-    Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), rows_log2, FastDiv(1), a.sinks},
+    Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), kRowsLog2, FastDiv(1), a.sinks},
               c, a.q, a.out, a.q_stride, a.out_stride, a.scale * 1.4426950408889634f, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_stream4_kernel<true, C> : attend_stream4_kernel<false, C>;
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) return e;
+    static std::atomic<unsigned long long> done[2];
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, done[bf16])) return e;
     kernel<<<a.ctas, C::kThreads, C::kSmem, st>>>(args);
     return cudaGetLastError();
 }
 
-// The kernel for row tiles of 8 NT rows.
-template <int NT, int TEAMS>
-cudaError_t launch_rows(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
-                        cudaStream_t st) {
-    if (s.d == 64)
-        return c.group_log2 == 5 ? launch<Cfg<64, 5, NT, TEAMS>>(s, b, c, a, bf16, st) : launch<Cfg<64, 6, NT, TEAMS>>(s, b, c, a, bf16, st);
-    return c.group_log2 == 5 ? launch<Cfg<128, 5, NT, TEAMS>>(s, b, c, a, bf16, st) : launch<Cfg<128, 6, NT, TEAMS>>(s, b, c, a, bf16, st);
-}
-
 }  // namespace
+
+cudaError_t launch_attend_stream4(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
+                                  cudaStream_t st) {
+    if (s.d == 64) return c.group_log2 == 5 ? launch<Cfg<64, 5>>(s, b, c, a, bf16, st) : launch<Cfg<64, 6>>(s, b, c, a, bf16, st);
+    return c.group_log2 == 5 ? launch<Cfg<128, 5>>(s, b, c, a, bf16, st) : launch<Cfg<128, 6>>(s, b, c, a, bf16, st);
+}
 
 }  // namespace q4

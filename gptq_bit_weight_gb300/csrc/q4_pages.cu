@@ -101,18 +101,40 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PagesView v, int32_t *co
     });
 }
 
-// Copies a chunk of page src to page dst, by the CTA.
-__device__ __forceinline__ void copy_chunk(const PageChunk &c, int src, int dst) {
-    const uint4 *from = reinterpret_cast<const uint4 *>(c.data + src * c.stride);
-    uint4 *to = reinterpret_cast<uint4 *>(c.data + dst * c.stride);
-    const int n = c.bytes / 16;
-    uint4 x[kPageChunk / 16 / kThreads];
+// A chunk of one page to another.
+struct Job {
+    const uint4 *from;
+    uint4 *to;
+    int n;                   // 16-byte vectors; 0: nothing
+};
+__device__ __forceinline__ Job job_of(const PageChunk &c, int src, int dst) {
+    return Job{reinterpret_cast<const uint4 *>(c.data + src * c.stride), reinterpret_cast<uint4 *>(c.data + dst * c.stride), c.bytes / 16};
+}
+constexpr int kVectors = kPageChunk / 16 / kThreads;         // of a thread
+__device__ __forceinline__ void load_job(const Job &j, uint4 (&x)[kVectors]) {
 #pragma unroll
-    for (int i = 0; i < kPageChunk / 16 / kThreads; ++i)
-        if (static_cast<int>(threadIdx.x) + i * kThreads < n) x[i] = __ldcs(from + threadIdx.x + i * kThreads);
+    for (int i = 0; i < kVectors; ++i)
+        if (static_cast<int>(threadIdx.x) + i * kThreads < j.n) x[i] = __ldcs(j.from + threadIdx.x + i * kThreads);
+}
+__device__ __forceinline__ void store_job(const Job &j, const uint4 (&x)[kVectors]) {
 #pragma unroll
-    for (int i = 0; i < kPageChunk / 16 / kThreads; ++i)
-        if (static_cast<int>(threadIdx.x) + i * kThreads < n) __stcs(to + threadIdx.x + i * kThreads, x[i]);
+    for (int i = 0; i < kVectors; ++i)
+        if (static_cast<int>(threadIdx.x) + i * kThreads < j.n) __stcs(j.to + threadIdx.x + i * kThreads, x[i]);
+}
+// Jobs of(w) for w = first, first + step, .. below `work`, by the CTA: where a job's data is and goes is read while the
+// job before is on its way.
+template <class F>
+__device__ __forceinline__ void copy_jobs(int64_t first, int64_t step, int64_t work, F of) {
+    if (first >= work) return;
+    Job j = of(first);
+    for (int64_t w = first; w < work; w += step) {
+        uint4 x[kVectors];
+        load_job(j, x);
+        Job next{};
+        if (w + step < work) next = of(w + step);
+        store_job(j, x);
+        j = next;
+    }
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -127,24 +149,22 @@ __global__ void __launch_bounds__(kThreads)
         else if (id >= used) id = v.hole[v.rank[id]];
         out[b * out_stride + j] = id;
     }
-    const int64_t work = static_cast<int64_t>(moves) * v.chunks;
-    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+    copy_jobs(blockIdx.x, gridDim.x, static_cast<int64_t>(moves) * v.chunks, [&](int64_t w) {
         const int m = static_cast<int>(w / v.chunks);
-        copy_chunk(v.chunk[w - static_cast<int64_t>(m) * v.chunks], v.source[m], v.hole[m]);
-    }
+        return job_of(v.chunk[w - static_cast<int64_t>(m) * v.chunks], v.source[m], v.hole[m]);
+    });
 }
 
 __global__ void __launch_bounds__(kThreads) copy_kernel(PagesView v, const int32_t *src, const int32_t *dst, int n) {
-    const int64_t work = static_cast<int64_t>(n) * v.chunks;
-    for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+    copy_jobs(blockIdx.x, gridDim.x, static_cast<int64_t>(n) * v.chunks, [&](int64_t w) {
         const int m = static_cast<int>(w / v.chunks), c = static_cast<int>(w - static_cast<int64_t>(m) * v.chunks);
         const int s = src[m], d = dst[m];
         if (s >= v.pages || d >= v.pages) {
             if (c == 0 && threadIdx.x == 0) atomicOr(v.status, kPagesBadIndex);
-        } else if (s >= 0 && d >= 0 && s != d) {
-            copy_chunk(v.chunk[c], s, d);
+            return Job{};
         }
-    }
+        return s >= 0 && d >= 0 && s != d ? job_of(v.chunk[c], s, d) : Job{};
+    });
 }
 
 // CTAs (x, i): fork i, its chunks x, x + gridDim.x, ..; x = 0 writes the row.
@@ -184,8 +204,70 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (threadIdx.x == 0) r.kv_len[c] = static_cast<int32_t>(len);
     }
-    if (part)
-        for (int k = blockIdx.x; k < v.chunks; k += gridDim.x) copy_chunk(v.chunk[k], from, to);
+    if (part) copy_jobs(blockIdx.x, gridDim.x, v.chunks, [&](int64_t k) { return job_of(v.chunk[k], from, to); });
+}
+
+// A small pool and table in one launch of one CTA: bits, their counts and what follows from them in shared memory.
+constexpr int kSmallThreads = 1024, kSmallPages = 32 * kSmallThreads, kSmallEntries = 8 * kSmallThreads;
+bool is_small(const PagesView &v, const PageRows &r) {
+    return v.pages <= kSmallPages && static_cast<int64_t>(r.batch) * r.width <= kSmallEntries;
+}
+// PLAN: a compaction's moves; else the free list.
+template <bool PLAN>
+__global__ void __launch_bounds__(kSmallThreads) small_kernel(PagesView v, PageRows r, int32_t *ids, int32_t *count) {
+    __shared__ uint32_t bits[kSmallThreads], below[kSmallThreads], of_warp[kSmallThreads / 32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    bits[tid] = 0;
+    __syncthreads();
+    const int entries = r.batch * r.width;
+#pragma unroll 4
+    for (int i = tid; i < entries; i += kSmallThreads) {
+        const int b = i / r.width, j = i - b * r.width;
+        const int id = r.table[b * r.stride + j], n = r.kv_len[b];           // (both on their way at once)
+        if (!needed(r, v.page_size, j, n)) continue;
+        if (id >= v.pages) atomicOr(v.status, kPagesBadIndex);
+        else if (id >= 0) atomicOr(bits + (id >> 5), 1u << (id & 31));
+    }
+    __syncthreads();
+    const uint32_t mine = __popc(bits[tid]);
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) of_warp[warp] = upto;
+    __syncthreads();
+    uint32_t before = 0, used = 0;
+#pragma unroll
+    for (int w = 0; w < kSmallThreads / 32; ++w) {
+        if (w < warp) before += of_warp[w];
+        used += of_warp[w];
+    }
+    below[tid] = before + upto - mine;
+    __syncthreads();
+    auto rank_of = [&](int id) { return static_cast<int>(below[id >> 5] + __popc(bits[id >> 5] & ((1u << (id & 31)) - 1))); };
+    const int n = static_cast<int>(used), free = v.pages - n, stay = n < v.pages ? rank_of(n) : n;
+    if (tid == 0) {
+        *count = PLAN ? n : free;
+        if (PLAN) *v.moves = n - stay;
+    }
+    for (int id = tid; id < v.pages; id += kSmallThreads) {
+        const bool in_use = bits[id >> 5] >> (id & 31) & 1;
+        const int rank = rank_of(id);
+        if constexpr (PLAN) {
+            if (in_use && id >= n) {
+                v.source[rank - stay] = id;
+                v.rank[id] = rank - stay;
+            } else if (!in_use && id < n) {
+                v.hole[id - rank] = id;
+            }
+        } else if (in_use) {
+            ids[free + rank] = -1;
+        } else {
+            ids[id - rank] = id;
+        }
+    }
 }
 
 int grid_of(int64_t work, int most) { return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(work, most))); }
@@ -203,6 +285,11 @@ cudaError_t launch_mark(const PagesView &v, const PageRows &r, cudaStream_t st, 
 
 cudaError_t launch_pages_free_list(const PagesView &v, const PageRows &r, int32_t *ids, int32_t *count, cudaStream_t st,
                                    int *launches) {
+    if (is_small(v, r)) {
+        small_kernel<false><<<1, kSmallThreads, 0, st>>>(v, r, ids, count);
+        *launches += 1;
+        return cudaGetLastError();
+    }
     if (cudaError_t e = launch_mark(v, r, st, launches)) return e;
     free_list_kernel<<<(v.pages + kPagesOfCta - 1) / kPagesOfCta, kThreads, 0, st>>>(v, ids, count);
     *launches += 1;
@@ -211,8 +298,12 @@ cudaError_t launch_pages_free_list(const PagesView &v, const PageRows &r, int32_
 
 cudaError_t launch_pages_compact(const PagesView &v, const PageRows &r, int32_t *out, int64_t out_stride, int32_t *count,
                                  cudaStream_t st, int *launches) {
-    if (cudaError_t e = launch_mark(v, r, st, launches)) return e;
-    plan_kernel<<<(v.pages + kPagesOfCta - 1) / kPagesOfCta, kThreads, 0, st>>>(v, count);
+    if (is_small(v, r)) {
+        small_kernel<true><<<1, kSmallThreads, 0, st>>>(v, r, nullptr, count);
+    } else {
+        if (cudaError_t e = launch_mark(v, r, st, launches)) return e;
+        plan_kernel<<<(v.pages + kPagesOfCta - 1) / kPagesOfCta, kThreads, 0, st>>>(v, count);
+    }
     *launches += 1;
     if (cudaError_t e = cudaGetLastError()) return e;
     move_kernel<<<8 * v.sms, kThreads, 0, st>>>(v, r, out, out_stride, count);

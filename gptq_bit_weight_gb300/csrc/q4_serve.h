@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <type_traits>
@@ -125,11 +126,9 @@ cudaError_t launch_attend_stream(const AttnShape &s, const AttnBatch &b, const A
 size_t attend_tc_ws_bytes(int ctas);
 cudaError_t launch_attend_tc(const AttnShape &s, const AttnBatch &b, const AttnCache &c, const AttendCall &a, bool bf16,
                              cudaStream_t st);
-// few rows over a cache of 4 bits, in row tiles of 8 and 16 (q4_attn_stream4*.cu); pieces as launch_attend_tc's
-cudaError_t launch_attend_stream4_8(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
-                                    bool bf16, cudaStream_t st);
-cudaError_t launch_attend_stream4_16(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a,
-                                     bool bf16, cudaStream_t st);
+// few rows over a cache of 4 bits (q4_attn_stream4.cu); pieces as launch_attend_tc's
+cudaError_t launch_attend_stream4(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
+                                  cudaStream_t st);
 // chunks over a cache of 4 bits; scale > 0
 cudaError_t launch_attend_tc4_64(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AttendCall &a, bool bf16,
                                  cudaStream_t st);
@@ -147,6 +146,18 @@ cudaError_t encode_queries(CUtensorMap *map, const void *ptr, const AttnShape &s
 // Tensor map of a cache's keys or values [pages][heads][page][d]: boxes of
 // 64 columns (128 bytes, swizzled) and `rows` tokens (q4_gemm_tc.cu).
 cudaError_t encode_pages(CUtensorMap *map, const void *ptr, const AttnShape &s, const AttnCache &c, uint32_t rows);
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once on each device: the call costs a small launch's host time
+// again.  done: one for each kernel, a bit for each device.
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return cudaSuccess;
+}
 
 // ------------------------------------------------------------ device helpers
 template <bool BF>

@@ -42,22 +42,21 @@ class PagePool:
                 buffers.append(gptq_q4_buffer(t.data_ptr(), size, c.struct.page_stride * t.element_size()))
         self.handle = gptq_q4_pages_make(buffers, self.pages, self.page_size)
 
-    def _ints(self, t, what: str, n: int | None = None):
-        if t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 or not t.is_contiguous() or \
-                (n is not None and t.numel() != n):
-            _refuse(f"{what} must be contiguous int32 [{'n' if n is None else n}] on {self.device}")
+    def _ints(self, t, what: str, n: int):
+        if t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
+            _refuse(f"{what} must be contiguous int32 [{n}] on {self.device}")
         return t.data_ptr()
 
     def _rows(self, table, kv_len):
-        if table.dtype != torch.int32 or table.device != self.device or table.dim() != 2 or \
-                (table.numel() and table.shape[1] > 1 and table.stride(1) != 1):
-            _refuse(f"table must be int32 [batch, width] on {self.device}, dense in its last dimension")
+        if table.dtype != torch.int32 or table.device != self.device or table.dim() != 2:
+            _refuse(f"table must be int32 [batch, width] on {self.device}")
         batch, width = table.shape
-        kv = self._ints(kv_len, "kv_len", batch)
-        stride = table.stride(0) if batch > 1 else max(table.stride(0), width)
-        if stride < width:
-            _refuse("the rows of table overlap")
-        return gptq_q4_rows(table.data_ptr(), kv, stride, width, batch)
+        stride, inner = table.stride()
+        if batch < 2:
+            stride = max(stride, width)
+        if (inner != 1 and width > 1 and batch) or stride < width:
+            _refuse("table must be dense in its last dimension, its rows apart from each other")
+        return gptq_q4_rows(table.data_ptr(), self._ints(kv_len, "kv_len", batch), stride, width, batch)
 
     def free(self, table, kv_len, window: int = 0, sinks: int = 0):
         """The pages that no row needs: (ids int32 [pages], ascending and then
@@ -76,13 +75,13 @@ class PagePool:
         fresh[i] in every cache.  Negative numbers are no fork."""
         rows = self._rows(table, kv_len)
         n = parent.numel()
-        _check(_fork(self.handle, ctypes.byref(rows), self._ints(parent, "parent"), self._ints(child, "child", n),
+        _check(_fork(self.handle, ctypes.byref(rows), self._ints(parent, "parent", n), self._ints(child, "child", n),
                      self._ints(fresh, "fresh", n), n, _stream(self.device.index)))
 
     def copy(self, src, dst) -> None:
         """Copy pages src[i] to pages dst[i] in every cache; negative numbers are no copy."""
         n = src.numel()
-        _check(_copy(self.handle, self._ints(src, "src"), self._ints(dst, "dst", n), n, _stream(self.device.index)))
+        _check(_copy(self.handle, self._ints(src, "src", n), self._ints(dst, "dst", n), n, _stream(self.device.index)))
 
     def compact(self, table, kv_len, table_out=None, window: int = 0, sinks: int = 0):
         """Move the pages in use to the lowest numbers, in every cache, and
