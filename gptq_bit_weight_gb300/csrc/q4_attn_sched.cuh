@@ -26,9 +26,11 @@ struct FastDiv {
     }
 };
 
-template <bool SINKS>
+// EXTRA: units that an item counts for besides its key tiles, for what a CTA does at its end.
+template <bool SINKS, int EXTRA = 0>
 struct SchedParamsT {
     static constexpr bool kSinks = SINKS;
+    static constexpr int kExtra = EXTRA;
     AttnBatch b;
     int hkv, page_log2, window;
     int kt_log2;      // log2 of the tokens of a key tile
@@ -48,7 +50,11 @@ struct Item {
     int near;        // if kSinks: of these, tiles of first tokens; the others are `first` tiles further on
     int u;           // the item's first unit
 };
-// The key tile that unit j of an item is.
+template <class P>
+__device__ __forceinline__ int units_of(const P &, const Item &it) {
+    return it.n + P::kExtra;
+}
+// The key tile that tile j of an item is.
 template <class P>
 __device__ __forceinline__ int key_tile(const P &, const Item &it, int j) {
     if constexpr (P::kSinks) return j < it.near ? j : it.first + j;
@@ -108,7 +114,7 @@ __device__ __forceinline__ long long tile_units(const P &p, int ql, int kv, int 
 #pragma unroll 1
     for (it.tile = i0; it.tile < tiles; it.tile += stride) {
         fill_tile(p, it);
-        sum += it.n;
+        sum += units_of(p, it);
     }
     return sum;
 }
@@ -125,7 +131,7 @@ __device__ __forceinline__ void load_item_request(const P &p, Item &it) {
 // Step to the next item; false after the last.
 template <class P>
 __device__ __forceinline__ bool next_item(const P &p, Item &it) {
-    it.u += it.n;
+    it.u += units_of(p, it);
     if (++it.tile == it.tiles) {
         it.tile = 0;
         if (++it.head == p.hkv) {
@@ -203,9 +209,12 @@ __device__ __forceinline__ void find_tile(const P &p, Item &it, int rem, int at)
 #pragma unroll 1
     for (int base = 0;; base += 32) {
         it.tile = base + lane;
-        it.n = 0;
-        if (it.tile < it.tiles) fill_tile(p, it);
-        int pre = it.n;
+        int n = 0;
+        if (it.tile < it.tiles) {
+            fill_tile(p, it);
+            n = units_of(p, it);
+        }
+        int pre = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, pre, o);
@@ -215,7 +224,7 @@ __device__ __forceinline__ void find_tile(const P &p, Item &it, int rem, int at)
         if (past) {
             const int who = __ffs(past) - 1;
             it.tile = base + who;
-            it.u = at - (rem - __shfl_sync(0xffffffffu, pre - it.n, who));
+            it.u = at - (rem - __shfl_sync(0xffffffffu, pre - n, who));
             return;
         }
         if (base + 32 >= it.tiles) {                 // cannot be: the sums said otherwise

@@ -68,8 +68,21 @@ struct Handed {
     int more;                    // 0: there is none
 };
 
+// What of an item falls to a share.  The first tile stands for two units: an item's end, and the way to the next one,
+// take a team as long as a tile does.
+struct Part {
+    int j0, j1;                  // its key tiles
+    bool whole;                  // the share has all units
+    __device__ Part(const Item &it, const Share &sh) {
+        const int r0 = max(sh.begin - it.u, 0), r1 = min(sh.end - it.u, it.n + 1);
+        j0 = r0 == 0 ? 0 : max(r0 - 1, 1);
+        j1 = it.hi > 0 ? max(r1 - 1, 1) : j0;
+        whole = r0 == 0 && r1 == it.n + 1;
+    }
+};
+
 struct Args {
-    SchedParamsT<true> p;
+    SchedParamsT<true, 1> p;
     Cache4 c;
     const uint16_t *q;
     uint16_t *out;
@@ -217,7 +230,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             uint4 q[WORDS];
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) q[w] = row ? *reinterpret_cast<const uint4 *>(src + 8 * w) : make_uint4(0, 0, 0, 0);
-            const int j0 = max(sh.begin - it.u, 0), j1 = more && it.hi > 0 ? min(sh.end - it.u, it.n) : j0;
+            const Part part(it, sh);
+            const int j0 = part.j0, j1 = more ? part.j1 : j0;
             const PageWalk walk(a.p, it, a.c.pages);
             const int boxes = kKt >> walk.box_log2, bytes = R << walk.box_log2;
             const uint8_t *head = a.c.kv + static_cast<int64_t>(it.head << a.p.page_log2) * R;
@@ -304,7 +318,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         alive = bar_and(1 + team, 32 * kWarps, alive);           // a team stays together
         if (!alive || !items[2 * team + buf].more) break;
         it = items[2 * team + buf].it;
-        const int j0 = max(sh.begin - it.u, 0), j1 = min(sh.end - it.u, it.n);
+        const Part part(it, sh);
+        const int j0 = part.j0;
         const int r_first = it.tile * kRows, rows = it.ql * group - r_first;    // of this tile: min(rows, kRows)
         uint4 qr[WORDS];
 #pragma unroll
@@ -453,7 +468,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                 pb[b][1] = transpose8(pack2<BF>(p2, p3));
             }
         };
-        const int tiles = it.hi > 0 ? j1 - j0 : 0;
+        const int tiles = part.j1 - j0;
         auto next_stage = [&] {
             if (++stage == ST) {
                 stage = 0;
@@ -565,13 +580,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             if (uint16_t *dst = row_at(0)) *reinterpret_cast<uint32_t *>(dst + 2 * i) = two(x.x, x.z, inverse(l0));
             if (uint16_t *dst = row_at(1)) *reinterpret_cast<uint32_t *>(dst + 2 * i) = two(x.y, x.w, inverse(l1));
         };
-        if (j0 == 0 && j1 == it.n) {
+        if (part.whole) {
 #pragma unroll
             for (int u = 0; u < F; ++u) store(member + u * kWarps, acc[u], sum[u][0], sum[u][1]);
             continue;
         }
         // [MT][32] float4 fragments, then [4] (m, m, l, l) of a thread's two rows
-        const int c0 = static_cast<uint32_t>(it.u) / sh.per, c1 = static_cast<uint32_t>(it.u + it.n - 1) / sh.per;
+        const int c0 = static_cast<uint32_t>(it.u) / sh.per, c1 = static_cast<uint32_t>(it.u + it.n) / sh.per;
         auto piece = [&](int cta) {
             return reinterpret_cast<float4 *>(a.ws + static_cast<size_t>(2 * cta + (cta == c0)) * C::kPiece);
         };
@@ -590,8 +605,42 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
         }
         bar_team(team);
         if (!*reinterpret_cast<volatile int *>(flags + team)) continue;
-        // The pieces' weights first, all at once, then their fragments, eight pieces at a time; in the order of the CTAs.
         const int pieces = c1 - c0 + 1;
+        if (pieces <= 8) {
+            // all of them on their way at once
+            float4 v[8], x[F][8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 *w = piece(min(c0 + k, c1));
+                v[k] = __ldcg(w + MT * 32 + t4);
+#pragma unroll
+                for (int u = 0; u < F; ++u) x[u][k] = __ldcg(w + (member + u * kWarps) * 32 + lane);
+            }
+            float t0 = -INFINITY, t1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {                // (a piece twice does no harm to a maximum)
+                t0 = fmaxf(t0, v[k].x);
+                t1 = fmaxf(t1, v[k].y);
+            }
+#pragma unroll
+            for (int u = 0; u < F; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float r0 = ref_of(t0), r1 = ref_of(t1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (k >= pieces) continue;
+                const float f0 = ex2(v[k].x - r0), f1 = ex2(v[k].y - r1);
+                l0 += v[k].z * f0;
+                l1 += v[k].w * f1;
+#pragma unroll
+                for (int u = 0; u < F; ++u)
+                    acc[u] = make_float4(acc[u].x + x[u][k].x * f0, acc[u].y + x[u][k].y * f1, acc[u].z + x[u][k].z * f0,
+                                         acc[u].w + x[u][k].w * f1);
+            }
+#pragma unroll
+            for (int u = 0; u < F; ++u) store(member + u * kWarps, acc[u], l0, l1);
+            continue;
+        }
+        // The pieces' weights first, all at once, then their fragments, eight pieces at a time; in the order of the CTAs.
         float4 *factors = reinterpret_cast<float4 *>(slots + team * (kWarps / 2) * C::kSlot);     // [t4]: (m, m, l, l) of all
         float *lifts = reinterpret_cast<float *>(factors + 4);                                    // [32 pieces][t4][2]
         if (member == 0) {
