@@ -14,6 +14,9 @@
 // A work item has 16 elements of a head.  A key's pairs (i, i + rot / 2) come from
 // two places, so the rotated elements go through shared memory, after which an
 // item holds 16 neighbours and a group is 2 or 4 lanes.
+// Three prompts of 9912 tokens, 96 heads of 128: 84 us, 4.5 TB/s, issue slots 60%
+// busy (a code at a time, with its border looked at, 137); 64 single tokens of 80
+// heads 8 us with the launch.  Reading the prompts' tokens back: 37 us, 5.4 TB/s.
 #include <algorithm>
 #include <cstdint>
 
@@ -281,7 +284,7 @@ int tokens_each(int tokens, int most) { return std::max(1, std::min(most, tokens
 
 cudaError_t launch_attn_append4(const AttnShape &s, const AttnBatch &b, const Cache4 &c, const AppendCall &a, bool bf16,
                                 cudaStream_t st) {
-    // few tokens: a CTA for every 256 items of each, so that none goes round its loop twice (64 tokens: 12.3 -> XX us)
+    // few tokens: a CTA for every 256 items of each, so that none goes round its loop twice (64 tokens: 12.3 -> 8.3 us)
     const int per = tokens_each(b.tokens, 4), passes = ((s.hq + 2 * s.hkv) * (s.d / 16) + kThreads - 1) / kThreads;
     const dim3 grid((b.tokens + per - 1) / per, std::max(1, std::min(passes, 608 / b.tokens)));
     if (bf16) append4_kernel<true><<<grid, kThreads, 0, st>>>(s, b, c, a, per);

@@ -29,6 +29,15 @@
 //   Three CTAs of one team each took as long as the slowest: some had finished
 // after 29 us and others after 67.  Teams that shared the items of a CTA met
 // too often: 88 us for 64 ragged requests.
+// 64 requests of up to 8192 tokens, 64 heads over 8 of 128, groups of 32: 70.5
+// us (the 16-bit cache: 132); two of 131071 and about 100000, groups of 64: 61
+// (103); one of 777, 32 heads: 10 (latency, as there).  Reading the cache alone
+// runs at 7.0 TB/s, the decoding and products on tiles that are there at 6.0;
+// together 5.8 in the middle of a long call, and 20 us go to its ends: lengths,
+// first tiles (3 us), the ends of items (1.5 each), the join.  Of a block of 16
+// tokens' 361 instructions 208 decode, on two pipes of half rate; issue slots
+// are 66% busy there.  Keys multiplied as codes, with step and least value
+// applied to the groups' sums, took as long.
 #include <climits>
 
 #include "q4_attn_tma.cuh"

@@ -40,6 +40,15 @@
 // softmax warps' own chain as it is compiled, spills among it (with columns of
 // their own for the weights, so that the next scores never wait for the second
 // product: 503).
+// With first tokens that stay visible (SINKS), an item's key tiles are those of
+// the first tokens and those of the window; a score's mask has the two ranges.
+// Over a cache of 4 bits (FOUR) the launch has four more warps, 512 x 128
+// registers: 256 x 184 + 256 x 72.  One warp loads records of half a tile by bulk
+// copies, six decode blocks of 32 tokens into the tiles that the MMAs read
+// (zeros for hidden tokens, so nothing is left to clean).  With two decoders it
+// was 568 us for 1024 tokens over 16384, with four to six 411 (1.30 PFLOP/s; the
+// 16-bit cache 340): two tiles fit beside the records and the queries, not two
+// and a half, and the decoders' stores share the SM with the softmax.
 // Every wait is bounded; a wait that runs out sets a status bit and its role
 // goes on without waiting.
 #pragma once
