@@ -103,6 +103,8 @@ gptq_q4_pages gptq_q4_pages_make(const gptq_q4_buffer *buffers, int n, int pages
     }
     int dev = -1;
     if (q4::api_check_device_sm103(&dev)) return nullptr;
+    for (int i = 0; i < n; ++i)
+        if (q4::api_check_device_ptr(buffers[i].data, dev, "a buffer's data")) return nullptr;
     gptq_q4_pages_s *h = new (std::nothrow) gptq_q4_pages_s();
     q4::PageChunk *host = new (std::nothrow) q4::PageChunk[std::max<int64_t>(chunks, 1)];
     if (!h || !host) {

@@ -717,8 +717,9 @@ typedef struct {
 
 /* buffers: host, n of them (0: only the numbers are managed); pages at most
  * 2^22; page_size positive.  Device memory: about 12 bytes a page.
- * Synchronizes.  NULL on error: INVALID_ARGUMENT, UNSUPPORTED (device not
- * sm_103), OUT_OF_MEMORY, CUDA_ERROR. */
+ * Synchronizes.  NULL on error: INVALID_ARGUMENT (a buffer of another device
+ * than the current one among them), UNSUPPORTED (device not sm_103),
+ * OUT_OF_MEMORY, CUDA_ERROR. */
 gptq_q4_pages gptq_q4_pages_make(const gptq_q4_buffer *buffers, int n, int pages, int page_size);
 
 /* The pages that are not in use: ids, device int32 [pages], ascending, then
