@@ -23,6 +23,7 @@ struct gptq_q4_attn_s {
     float *ws = nullptr;
     int *tickets = nullptr;
     int ctas = 0;
+    uint32_t allowed = 0;
 };
 
 namespace {
@@ -200,7 +201,8 @@ int attend(gptq_q4_attn h, const void *q, int64_t q_stride, const Cache *cache, 
     // Contexts end at 2^30 tokens, so a longer window hides nothing; differences with a shorter one fit 32 bits.
     const int seen = window < 1 << 30 ? window : 0;
     const q4::AttendCall a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), q_stride, out_stride,
-                           scale, seen, seen ? std::min(sinks, 1 << 30) : 0, batch->max_q, h->status, h->ws, h->tickets, h->ctas};
+                           scale, seen, seen ? std::min(sinks, 1 << 30) : 0, batch->max_q, h->status, h->ws, h->tickets, h->ctas,
+                           &h->allowed};
     // More query rows for each key/value head than the streaming kernel's row tile has: the tensor-core kernel
     // (which takes its maximum before scaling, so a positive scale).  Measured at 64 heads over 8, contexts of up
     // to 4096: 32 requests of 2 tokens (16 rows) 45 us streaming, 53 on tcgen05, one such request 12 and 15; 32 of 4

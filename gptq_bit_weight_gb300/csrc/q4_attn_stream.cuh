@@ -432,8 +432,7 @@ cudaError_t launch(const AttnShape &s, const AttnBatch &b, const AttnCache &c, c
     Args<SINKS> args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), kRowsLog2, FastDiv(1), a.sinks},
                      c, a.q, a.out, a.q_stride, a.out_stride, a.scale * 1.4426950408889634f, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_stream_kernel<true, C, SINKS> : attend_stream_kernel<false, C, SINKS>;
-    static std::atomic<unsigned long long> done[2];
-    if ((e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, done[bf16]))) return e;
+    if ((e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, a.allowed, SINKS ? kStreamSinks : kStream))) return e;
     kernel<<<a.ctas, kThreads, C::kSmem, st>>>(tk, tv, args);
     return cudaGetLastError();
 }

@@ -715,8 +715,7 @@ cudaError_t launch(const AttnShape &s, const AttnBatch &b, const Cache4 &c, cons
     Args args{{b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), kRowsLog2, FastDiv(1), a.sinks},
               c, a.q, a.out, a.q_stride, a.out_stride, a.scale * 1.4426950408889634f, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_stream4_kernel<true, C> : attend_stream4_kernel<false, C>;
-    static std::atomic<unsigned long long> done[2];
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, done[bf16])) return e;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, a.allowed, kStream4 + (C::GL == 6))) return e;
     kernel<<<a.ctas, C::kThreads, C::kSmem, st>>>(args);
     return cudaGetLastError();
 }

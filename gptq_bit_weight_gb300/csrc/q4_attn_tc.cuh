@@ -828,8 +828,7 @@ cudaError_t launch(const AttnShape &s, const AttnBatch &b, const Cache &c, const
         {b, s.hkv, s.page_log2, a.window, kKtLog2, FastDiv(s.group), -1, FastDiv(2 * tokens), a.sinks},
         c, a.out, a.out_stride, a.scale * 1.4426950408889634f, tokens, a.ws, a.tickets, a.status};
     auto kernel = bf16 ? attend_tc_kernel<true, C, SINKS, FOUR> : attend_tc_kernel<false, C, SINKS, FOUR>;
-    static std::atomic<unsigned long long> done[2];
-    if ((e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, done[bf16]))) return e;
+    if ((e = allow_smem(reinterpret_cast<const void *>(kernel), C::kSmem, a.allowed, FOUR ? kChunk4 + (FOUR == 6) : SINKS ? kChunkSinks : kChunk))) return e;
     kernel<<<a.ctas, threads_of(FOUR), C::kSmem, st>>>(tq, tk, tv, args);
     return cudaGetLastError();
 }

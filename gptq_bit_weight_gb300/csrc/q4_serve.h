@@ -6,7 +6,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <type_traits>
@@ -117,6 +116,7 @@ struct AttendCall {
     float *ws;                   // pieces of cut items
     int *tickets;                // [4 * ctas], zero between calls
     int ctas;                    // one for each SM
+    uint32_t *allowed;           // kernels of this handle that have their shared memory (host)
 };
 // few rows for each key/value head (q4_attn_stream.cu)
 size_t attend_stream_ws_bytes(int ctas);
@@ -147,15 +147,13 @@ cudaError_t encode_queries(CUtensorMap *map, const void *ptr, const AttnShape &s
 // 64 columns (128 bytes, swizzled) and `rows` tokens (q4_gemm_tc.cu).
 cudaError_t encode_pages(CUtensorMap *map, const void *ptr, const AttnShape &s, const AttnCache &c, uint32_t rows);
 
-// Lets `kernel` have `bytes` of dynamic shared memory, once on each device: the call costs a small launch's host time
-// again.  done: one for each kernel, a bit for each device.
-inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<unsigned long long> &done) {
-    int dev = 0;
-    if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+// Lets `kernel` have `bytes` of dynamic shared memory, once for a handle: the call costs a small launch's host time
+// again.  allowed: the handle's, a bit for each kernel that it may launch.
+enum AttnKernel { kStream, kStreamSinks, kChunk, kChunkSinks, kStream4, kChunk4 = kStream4 + 2 };     // (two of groups each)
+inline cudaError_t allow_smem(const void *kernel, int bytes, uint32_t *allowed, int bit) {
+    if (*allowed >> bit & 1) return cudaSuccess;
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
+    *allowed |= 1u << bit;
     return cudaSuccess;
 }
 

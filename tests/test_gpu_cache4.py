@@ -99,6 +99,56 @@ def test_append_and_read(q4, lens, rope, group, dtype):
 
 
 @TYPES
+def test_append_at_other_positions(q4, dtype):
+    """Rotary positions of their own; one past the table is reported, and its token left out."""
+    Hq, Hkv, D, page, lens = 4, 2, 128, 16, [(3, 20), (2, 5)]
+    step = Step(q4, lens, Hkv, D, page, dtype, 32, seed=15)
+    x = torch.randn(5, Hq + 2 * Hkv, D, generator=torch.Generator().manual_seed(16)).to(dtype)
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    att.set_rope(D, 500)
+    pos = torch.tensor([0, 499, 7, 7, 123], dtype=torch.int32)
+    att.append(x.view(5, -1).to(DEV), step.cache, step.batch, positions=pos.to(DEV))
+    att.device_error()
+    k, v = att.read(step.cache, step.batch)
+    want = rotated(x[:, Hq:Hq + Hkv], pos, D, False)
+    assert torch.equal(k.cpu(), values(*quantise(want, 32))) and torch.equal(v.cpu(), values(*quantise(x[:, Hq + Hkv:], 32)))
+    before = step.pool.clone()
+    pos[2] = 500
+    q = torch.full((5, Hq, D), 7.0, dtype=dtype, device=DEV)
+    att.append(-x.view(5, -1).to(DEV), step.cache, step.batch, positions=pos.to(DEV), q_out=q)
+    with pytest.raises(q4.GPTQ4Error):
+        att.device_error()
+    assert (q[2] == 7).all() and not (q[1] == 7).all()
+    p, slot = int(step.table[0, 19 // page]), 19 % page
+    assert torch.equal(step.pool[p, :, slot], before[p, :, slot]) and not torch.equal(step.pool[p, :, slot - 1], before[p, :, slot - 1])
+
+
+def test_two_captured_graphs_of_one_handle(q4):
+    """They share the handle's workspace, one after the other, beside calls outside."""
+    Hq, Hkv, D, page, dtype = 8, 1, 128, 16, torch.bfloat16
+    att = q4.PagedAttention(Hq, Hkv, D, page, dtype=dtype)
+    steps = [Step(q4, lens, Hkv, D, page, dtype, group, seed=17) for lens, group in (([(1, 9000), (1, 300)], 32), ([(60, 5000)], 64), ([(1, 7000)], None))]
+    g = torch.Generator().manual_seed(18)
+    qs = [torch.randn(s.tokens, Hq, D, generator=g).to(dtype).to(DEV) for s in steps]
+    want = [att.attend(q, s.cache, s.batch, window=4000, sinks=9).clone() for q, s in zip(qs, steps)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for q, s in zip(qs, steps):
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                outs.append(att.attend(q, s.cache, s.batch, window=4000, sinks=9))
+        for i in (0, 1, 2, 1, 0, 2, 2):
+            graphs[i].replay()
+            again = att.attend(qs[2 - i], steps[2 - i].cache, steps[2 - i].batch, window=4000, sinks=9)
+            assert torch.equal(outs[i], want[i]) and torch.equal(again, want[2 - i])
+    torch.cuda.synchronize()
+    att.device_error()
+
+
+@TYPES
 @GROUPS
 def test_append_of_extreme_values(q4, group, dtype):
     """Constant groups, subnormal and largest steps, borders between codes, infinities and NaN, -0; each group by itself."""

@@ -68,7 +68,7 @@ class Pool:
         return [t.cpu().clone() for t in self.buffers]
 
 
-SIZES = [(1, 16, 1, 10), (40, 16, 3, 100), (1000, 8, 40, 150), (5000, 32, 70, 2000), (33000, 64, 20, 900), (31, 1, 4, 7), (128, 24, 9, 300)]
+SIZES = [(1, 16, 1, 10), (40, 16, 3, 100), (1000, 8, 40, 150), (5000, 32, 70, 2000), (33000, 64, 20, 900), (31, 1, 4, 7), (128, 24, 9, 300), (6000, 32, 300, 900), (32768, 16, 5, 100), (32769, 16, 5, 100)]
 
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (40, 20), (1, 1), (10 ** 6, 3)])
@@ -217,6 +217,28 @@ def test_forks_that_cannot_be_done_are_left_out(q4):
             if fine:
                 ref[51] = a[5]
             assert torch.equal(b, ref)
+
+
+def test_a_million_pages(q4):
+    """Counts past a block's words, page numbers past 2^20: a few pages in use at the far end, and a few in between."""
+    pages = (1 << 20) + 77
+    k, v = (torch.zeros(pages, 1, 1, 64, dtype=torch.float16, device=DEV) for _ in "kv")
+    k[:, 0, 0, 0] = torch.arange(pages, device=DEV) % 2039
+    v[:, 0, 0, 1] = torch.arange(pages, device=DEV) % 2011
+    pool = q4.PagePool([q4.PagedCache(k, v)])
+    used = sorted(random.Random(11).sample(range(pages), 3000)) + [pages - 1]
+    table = torch.tensor([used], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([len(used)], dtype=torch.int32, device=DEV)
+    ids, count = pool.free(table, lens)
+    mark = torch.ones(pages, dtype=torch.bool)
+    mark[torch.tensor(used)] = False
+    free = mark.nonzero().flatten().to(torch.int32)
+    assert count.tolist() == [len(free)] and torch.equal(ids.cpu()[:len(free)], free) and (ids[len(free):] == -1).all()
+    old = k[table[0].long(), 0, 0, 0].clone(), v[table[0].long(), 0, 0, 1].clone()
+    n = len(set(used))
+    assert pool.compact(table, lens).tolist() == [n] and int(table.max()) == n - 1
+    assert torch.equal(k[table[0].long(), 0, 0, 0], old[0]) and torch.equal(v[table[0].long(), 0, 0, 1], old[1])
+    pool.device_error()
 
 
 def test_copy(q4):
