@@ -116,6 +116,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// With sums from 0.
+template <bool BF>
+__device__ __forceinline__ void mma16816_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+    if constexpr (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -365,11 +380,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             }
             const uint32_t p0 = *reinterpret_cast<const uint32_t *>(r0 + k_param), p1 = *reinterpret_cast<const uint32_t *>(r1 + k_param);
             const uint32_t s0 = both_low(p0), m0 = both_high(p0), s1 = both_low(p1), m1 = both_high(p1);
-            s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.f;
 #pragma unroll
             for (int w = 0; w < WORDS; ++w) {
                 const uint4 x = values_of<BF>(w0[w], s0, m0), y = values_of<BF>(w1[w], s1, m1);
-                mma16816<BF>(s[b], x.x, y.x, x.y, y.y, qr[w].x, qr[w].y);
+                if (w == 0) mma16816_0<BF>(s[b], x.x, y.x, x.y, y.y, qr[w].x, qr[w].y);
+                else mma16816<BF>(s[b], x.x, y.x, x.y, y.y, qr[w].x, qr[w].y);
                 mma16816<BF>(s[b], x.z, y.z, x.w, y.w, qr[w].z, qr[w].w);
             }
         };

@@ -5,8 +5,8 @@
 // A word of eight codes has code e at bit 4 (e / 2) + 16 (e % 2), so that
 // word >> 4 i masked by 0x000f000f holds codes 2 i and 2 i + 1 in its two
 // 16-bit halves, in the order that every operand wants them.  A code becomes a
-// 16-bit float without a conversion: as low bits of the mantissa of 1024
-// (fp16) or 128 (bf16), from which that number is then taken away, exactly;
+// 16-bit float without a conversion: as bits of the mantissa of a power of two
+// whose unit they are there, from which that power is then taken away, exactly;
 // m + s c is one fma, rounded once.
 #pragma once
 #include "q4_serve.h"
@@ -49,21 +49,20 @@ __device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask, uint32_t 
 template <bool BF>
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&c)[4]) {
     if constexpr (BF) {
-        // eight bits of mantissa: a code at bit 0, or at bit 3 for eight times its value
-        constexpr uint32_t k128 = 0x43004300u, eighth = 0x3e003e00u, m16 = 0xc180c180u;
-        const uint32_t x = w >> 1, y = w >> 8, z = w >> 9;
+        // eight bits of mantissa: a code at bit 0 of 128's, or at bit 3 of 16's
+        constexpr uint32_t k128 = 0x43004300u, k16 = 0x41804180u;
         c[0] = sub_2<true>(mask_or(w, 0x000f000fu, k128), k128);
-        c[1] = fma_2<true>(mask_or(x, 0x00780078u, k128), eighth, m16);
-        c[2] = sub_2<true>(mask_or(y, 0x000f000fu, k128), k128);
-        c[3] = fma_2<true>(mask_or(z, 0x00780078u, k128), eighth, m16);
+        c[1] = sub_2<true>(mask_or(w >> 1, 0x00780078u, k16), k16);
+        c[2] = sub_2<true>(mask_or(w >> 8, 0x000f000fu, k128), k128);
+        c[3] = sub_2<true>(mask_or(w >> 9, 0x00780078u, k16), k16);
     } else {
-        // eleven bits: at bit 0, or at bit 4 for sixteen times its value
-        constexpr uint32_t k1024 = 0x64006400u, sixteenth = 0x2c002c00u, m64 = 0xd400d400u;
+        // eleven bits: at bit 0 of 1024's, or at bit 4 of 64's
+        constexpr uint32_t k1024 = 0x64006400u, k64 = 0x54005400u;
         const uint32_t y = w >> 8;
         c[0] = sub_2<false>(mask_or(w, 0x000f000fu, k1024), k1024);
-        c[1] = fma_2<false>(mask_or(w, 0x00f000f0u, k1024), sixteenth, m64);
+        c[1] = sub_2<false>(mask_or(w, 0x00f000f0u, k64), k64);
         c[2] = sub_2<false>(mask_or(y, 0x000f000fu, k1024), k1024);
-        c[3] = fma_2<false>(mask_or(y, 0x00f000f0u, k1024), sixteenth, m64);
+        c[3] = sub_2<false>(mask_or(y, 0x00f000f0u, k64), k64);
     }
 }
 // The eight values of a word, in order; s2, m2: step and least value in both halves.
