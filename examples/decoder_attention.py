@@ -8,7 +8,8 @@
 Prompts of three requests go in together in one step, then tokens are decoded
 one a step, in a captured CUDA graph; the lengths live on the GPU, so the graph
 replays unchanged while they grow.  `python examples/decoder_attention.py`
-prints how long a step takes.
+prints how long a step takes; with `4 1024 4` as arguments, over a cache of 4
+bits, through a window of 1024 tokens with the first four visible.
 """
 import os
 import sys
@@ -49,12 +50,12 @@ class DecoderAttention:
         for part in (self.qkv, self.o, self.qkv_adapters, self.o_adapters):
             part.reserve(rows)
 
-    def step(self, x, row_slot, cache, batch):
+    def step(self, x, row_slot, cache, batch, window=0, sinks=0):
         """x [tokens, hidden]: the step's tokens, request after request; row_slot: each token's adapter."""
         qkv = self.qkv(x)
         self.qkv_adapters.add(x, row_slot, qkv, out=qkv)
         q = self.attention.append(qkv, cache, batch)
-        a = self.attention.attend(q, cache, batch).view(x.shape)
+        a = self.attention.attend(q, cache, batch, window=window, sinks=sinks).view(x.shape)
         y = self.o(a)
         return self.o_adapters.add(a, row_slot, y, out=y)
 
@@ -64,7 +65,7 @@ class DecoderAttention:
             part.device_error()
 
 
-def main(q_heads=64, kv_heads=8, head_dim=128, page_size=16, prompts=(1000, 37, 402), decoded=64):
+def main(q_heads=64, kv_heads=8, head_dim=128, page_size=16, prompts=(1000, 37, 402), decoded=64, bits=16, window=0, sinks=0):
     dtype, hidden, n = torch.bfloat16, q_heads * head_dim, len(prompts)
     layer = DecoderAttention(q_heads, kv_heads, head_dim, page_size, slots=4, max_rank=32, max_pos=8192, dtype=dtype)
     layer.reserve(sum(prompts))
@@ -77,13 +78,17 @@ def main(q_heads=64, kv_heads=8, head_dim=128, page_size=16, prompts=(1000, 37, 
 
     width = -(-(max(prompts) + decoded) // page_size)
     pages = n * width
-    cache = q4.PagedCache(*(torch.empty(pages, kv_heads, page_size, head_dim, dtype=dtype, device="cuda") for _ in "kv"))
+    if bits == 4:
+        cache = q4.PagedCache4.empty(pages, kv_heads, page_size, head_dim, dtype=dtype)
+    else:
+        cache = q4.PagedCache(*(torch.empty(pages, kv_heads, page_size, head_dim, dtype=dtype, device="cuda") for _ in "kv"))
+    seen = {"window": window, "sinks": sinks}
     table = torch.randperm(pages, device="cuda", generator=g).to(torch.int32).view(n, width)
     kv_len = torch.tensor(prompts, dtype=torch.int32, device="cuda")
     lengths = torch.tensor(prompts)
     cu = torch.tensor([0, *lengths.cumsum(0)], dtype=torch.int32, device="cuda")
     prompt = q4.PagedBatch(cu, kv_len, table, tokens=sum(prompts), max_q=max(prompts))
-    y = layer.step(normal(sum(prompts), hidden).to(dtype), slots.repeat_interleave(lengths.cuda()), cache, prompt)
+    y = layer.step(normal(sum(prompts), hidden).to(dtype), slots.repeat_interleave(lengths.cuda()), cache, prompt, **seen)
 
     x = y[cu[1:].long() - 1].clone()                               # the last token of each prompt
     one = q4.PagedBatch(torch.arange(n + 1, dtype=torch.int32, device="cuda"), kv_len, table, tokens=n, max_q=1)
@@ -91,12 +96,12 @@ def main(q_heads=64, kv_heads=8, head_dim=128, page_size=16, prompts=(1000, 37, 
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):                                  # one step outside, then capture the next
         kv_len.add_(1)
-        layer.step(x, slots, cache, one)
+        layer.step(x, slots, cache, one, **seen)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
             kv_len.add_(1)
-            x.copy_(layer.step(x, slots, cache, one))
+            x.copy_(layer.step(x, slots, cache, one, **seen))
         a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
         a.record()
         for _ in range(decoded - 1):
@@ -111,4 +116,4 @@ def main(q_heads=64, kv_heads=8, head_dim=128, page_size=16, prompts=(1000, 37, 
 
 
 if __name__ == "__main__":
-    main()
+    main(**dict(zip(("bits", "window", "sinks"), map(int, sys.argv[1:]))))

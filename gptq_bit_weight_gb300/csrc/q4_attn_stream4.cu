@@ -97,8 +97,8 @@ struct Args {
     uint16_t *out;
     int64_t q_stride, out_stride;
     float scale;                 // times log2(e)
-    float *ws;                   // [2 * CTAs] pieces
-    int *tickets;                // [CTAs], zero between calls
+    float *ws;                   // [2 * shares] pieces
+    int *tickets;                // [shares], zero between calls
     int *status;
 };
 
@@ -214,9 +214,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
     int *flags = reinterpret_cast<int *>(misc + 8 * (2 * S + 4 * T));                     // [T]
     Handed *items = reinterpret_cast<Handed *>(misc + 320);                               // [T][2]
     TeamSchedSmem<T> &sched = *reinterpret_cast<TeamSchedSmem<T> *>(misc + 1024);
-    static_assert(4 * 16 + 32 * 4 * 8 <= kWarps / 2 * C::kSlot && S >= 2 * T && S % T == 0 && 8 * (2 * S + 4 * T) + 4 * T <= 320 && 320 + 2 * T * sizeof(Handed) <= 1024 &&
+    static_assert(S >= 2 * T && S % T == 0, "stages");
+    static_assert(4 * 16 + 32 * 4 * 8 <= kWarps / 2 * C::kSlot, "what the join keeps in the slots");
+    static_assert(8 * (2 * S + 4 * T) + 4 * T <= 320 && 320 + 2 * T * sizeof(Handed) <= 1024 &&
                       1024 + sizeof(TeamSchedSmem<T>) <= C::kMisc,
-                  "shared memory");
+                  "misc region");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
