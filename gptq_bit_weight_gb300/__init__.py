@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgptq_q4.so")
@@ -467,6 +468,24 @@ def gptq_q4_pages_free(h: int | None) -> None:
 
 # --------------------------------------------------------- torch marshalling
 
+_kept = []             # (free, handle) of handles given up while a stream was captured
+
+
+def _release(free=None, handle=None) -> None:
+    """Free a handle, and those kept so far.  Freeing synchronizes, which ends
+    a capture with an error; the collector may drop a handle at any line, so
+    one given up while the current stream is captured is kept until the next
+    is made or given up outside a capture."""
+    if free is not None:
+        _kept.append((free, handle))
+    torch = sys.modules.get("torch")
+    if torch is not None and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+        return
+    while _kept:
+        free, handle = _kept.pop()
+        free(handle)
+
+
 class Q4Matrix:
     """A handle built from torch CUDA tensors (the Q4Matrix / q4_matmul pair
     of the Lorax ExLlama v1 layer).  Only moves pointers and shapes; the
@@ -484,6 +503,7 @@ class Q4Matrix:
         torch.cuda.current_stream().synchronize()
         self.K, self.N, self.groupsize, self.bits = K, N, groupsize, bits
         self.device = qweight.device
+        _release()
         make = gptq_q4_make if bits == 4 else gptq_q4_make8
         self.handle = make(qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(),
                            None if g_idx is None else g_idx.data_ptr(), K, N, groupsize)
@@ -507,6 +527,7 @@ class Q4Matrix:
         self.K, self.N, self.groupsize = K, sum(Ns), groupsize
         self.device = parts[0][0].device
         self.parts = Ns
+        _release()
         self.handle = gptq_q4_make_fused([q.data_ptr() for q, _, _ in parts], [z.data_ptr() for _, z, _ in parts],
                                          [s.data_ptr() for _, _, s in parts],
                                          None if g_idx is None else g_idx.data_ptr(), K, Ns, groupsize)
@@ -589,8 +610,8 @@ class Q4Matrix:
 
     def close(self) -> None:
         if getattr(self, "handle", None):
-            gptq_q4_free(self.handle)
-            self.handle = None
+            handle, self.handle = self.handle, None
+            _release(gptq_q4_free, handle)
 
     def __del__(self):
         try:

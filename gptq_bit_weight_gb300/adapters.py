@@ -9,8 +9,8 @@ from __future__ import annotations
 import torch
 
 from . import (GPTQ4Error, GPTQ_Q4_DTYPE_BF16, GPTQ_Q4_DTYPE_FP16, GPTQ_Q4_DTYPE_FP32, GPTQ_Q4_INVALID_ARGUMENT,
-               _check, _lib, gptq_q4_lora_device_error, gptq_q4_lora_free, gptq_q4_lora_make, gptq_q4_lora_reserve,
-               gptq_q4_lora_set)
+               _check, _lib, _release, gptq_q4_lora_device_error, gptq_q4_lora_free, gptq_q4_lora_make,
+               gptq_q4_lora_reserve, gptq_q4_lora_set)
 
 _CODES = {torch.float16: GPTQ_Q4_DTYPE_FP16, torch.bfloat16: GPTQ_Q4_DTYPE_BF16, torch.float32: GPTQ_Q4_DTYPE_FP32}
 
@@ -69,6 +69,7 @@ class LoraPool:
         self.handle = None
         self.K, self.N, self.slots, self.max_rank, self.dtype = K, N, slots, max_rank, dtype
         self.device = torch.device("cuda", torch.cuda.current_device())
+        _release()
         self.handle = gptq_q4_lora_make(K, N, slots, max_rank, _code(dtype))
 
     def set(self, slot: int, a, b, scale: float = 1.0) -> None:
@@ -115,8 +116,8 @@ class LoraPool:
 
     def close(self) -> None:
         if getattr(self, "handle", None):
-            gptq_q4_lora_free(self.handle)
-            self.handle = None
+            handle, self.handle = self.handle, None
+            _release(gptq_q4_lora_free, handle)
 
     def __del__(self):
         try:

@@ -12,8 +12,8 @@ import ctypes
 import torch
 
 from . import (GPTQ_Q4_ROPE_BANDS, GPTQ_Q4_ROPE_LINEAR, GPTQ_Q4_ROPE_NTK, GPTQ_Q4_ROPE_PLAIN, GPTQ_Q4_ROPE_YARN,
-               _check, _lib, gptq_q4_attn_device_error, gptq_q4_attn_free, gptq_q4_attn_make, gptq_q4_attn_set_rope,
-               gptq_q4_batch, gptq_q4_cache, gptq_q4_cache4, gptq_q4_rope_freqs)
+               _check, _lib, _release, gptq_q4_attn_device_error, gptq_q4_attn_free, gptq_q4_attn_make,
+               gptq_q4_attn_set_rope, gptq_q4_batch, gptq_q4_cache, gptq_q4_cache4, gptq_q4_rope_freqs)
 from .adapters import _code, _refuse, _rows, _stream
 
 _append, _attend, _read = _lib.gptq_q4_attn_append, _lib.gptq_q4_attn_attend, _lib.gptq_q4_attn_read
@@ -113,6 +113,7 @@ class PagedAttention:
         self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
         self.dtype = dtype
         self.device = torch.device("cuda", torch.cuda.current_device())
+        _release()
         self.handle = gptq_q4_attn_make(q_heads, kv_heads, head_dim, page_size, _code(dtype))
         self._q_width = q_heads * head_dim
         self._kind = (dtype, self.device, kv_heads, page_size, head_dim)
@@ -231,8 +232,8 @@ class PagedAttention:
 
     def close(self) -> None:
         if getattr(self, "handle", None):
-            gptq_q4_attn_free(self.handle)
-            self.handle = None
+            handle, self.handle = self.handle, None
+            _release(gptq_q4_attn_free, handle)
 
     def __del__(self):
         try:

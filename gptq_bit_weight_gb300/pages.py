@@ -11,8 +11,8 @@ import math
 
 import torch
 
-from . import (_check, _lib, gptq_q4_buffer, gptq_q4_pages_device_error, gptq_q4_pages_free, gptq_q4_pages_make,
-               gptq_q4_rows)
+from . import (_check, _lib, _release, gptq_q4_buffer, gptq_q4_pages_device_error, gptq_q4_pages_free,
+               gptq_q4_pages_make, gptq_q4_rows)
 from .adapters import _refuse, _stream
 from .attention import PagedCache4
 
@@ -40,6 +40,7 @@ class PagePool:
             for t in (c.kv,) if isinstance(c, PagedCache4) else (c.k, c.v):
                 size = math.prod(t.shape[1:]) * t.element_size()
                 buffers.append(gptq_q4_buffer(t.data_ptr(), size, c.struct.page_stride * t.element_size()))
+        _release()
         self.handle = gptq_q4_pages_make(buffers, self.pages, self.page_size)
 
     def _ints(self, t, what: str, n: int):
@@ -102,8 +103,8 @@ class PagePool:
 
     def close(self) -> None:
         if getattr(self, "handle", None):
-            gptq_q4_pages_free(self.handle)
-            self.handle = None
+            handle, self.handle = self.handle, None
+            _release(gptq_q4_pages_free, handle)
 
     def __del__(self):
         try:
