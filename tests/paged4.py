@@ -3,8 +3,10 @@ cache, the 4-bit format by its definition, and attention in 64 bits.
 
 Tolerance of an attention output: that of test_gpu_attention.py, whose terms hold for any 16-bit keys and values, and
 so for the values that codes stand for; and kv / 16 2^-23 of A (test_gpu_attention_long.py) for running sums."""
+import gc
 import math
 
+import pytest
 import torch
 
 DEV = "cuda:0"
@@ -126,6 +128,23 @@ def attention(step, q, scale, window=0, sinks=0):
         t = U[dt] * o.abs() + (U[dt] + 2 * d + 2.0 ** -12 + kv / 16 * 2.0 ** -23) * A + TINY[dt] * (1 + kv * vmax) * (o.abs() > 0)
         ref[rows], tol[rows] = o.reshape(ql, Hq, D), t.reshape(ql, Hq, D)
     return ref, tol
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_handles_left():
+    """Handles that a failed call's traceback keeps in a cycle are freed here, not while a later test captures a graph
+    (freeing one synchronizes, which ends a capture)."""
+    yield
+    gc.collect()
+
+
+def refused(q4, call, status=None):
+    """Whether the call raises the library's error; keeps no traceback."""
+    try:
+        call()
+    except q4.GPTQ4Error as e:
+        return status is None or e.status == status
+    return False
 
 
 def check(got, ref, tol, what):

@@ -6,6 +6,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from paged4 import no_handles_left  # noqa: E402, F401
+
 DEV = "cuda:0"
 
 

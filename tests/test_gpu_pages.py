@@ -1,11 +1,15 @@
 """Pages of a cache: free lists, forks, copies and compaction, against a plain model of a table on the host; contents
 are compared byte by byte."""
+import gc
 import random
 
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+from paged4 import no_handles_left, refused  # noqa: E402, F401
+
 DEV = "cuda:0"
 
 
@@ -191,9 +195,7 @@ def test_forks_that_cannot_be_done_are_left_out(q4):
         if fine:
             p.pool.device_error()
         else:
-            with pytest.raises(q4.GPTQ4Error) as e:
-                p.pool.device_error()
-            assert e.value.status == q4.GPTQ_Q4_DEVICE_FAULT
+            assert refused(q4, p.pool.device_error, q4.GPTQ_Q4_DEVICE_FAULT)
             p.pool.device_error()
         clash = child[1] == 0
         want = old.clone()
@@ -255,11 +257,31 @@ def test_copy(q4):
         assert torch.equal(b, ref)
     now = p.snapshot()
     p.pool.copy(ints([300, 1]), ints([2, 10 ** 9]))
-    with pytest.raises(q4.GPTQ4Error):
-        p.pool.device_error()
+    assert refused(q4, p.pool.device_error)
     assert all(torch.equal(a, b) for a, b in zip(now, p.snapshot()))
     p.pool.copy(ints([]), ints([]))
     p.pool.device_error()
+
+
+def test_pages_past_32_bit_offsets(q4):
+    """Pages that begin more than 2^32 bytes into a buffer."""
+    n, shape, stride = 12, (2, 16, 160), 1 << 29
+    far = torch.empty((n - 1) * stride + 2 * 16 * 160, dtype=torch.uint8, device=DEV).as_strided((n, *shape), (stride, 16 * 160, 160, 1))
+    want = torch.randint(0, 256, (n, *shape), dtype=torch.uint8, generator=torch.Generator().manual_seed(12))
+    far.copy_(want)
+    pool = q4.PagePool([q4.PagedCache4(far, 128)])
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)       # noqa: E731
+    pool.copy(ints(0, 11), ints(10, 1))
+    want[10], want[1] = want[0].clone(), want[11].clone()
+    assert torch.equal(far.cpu(), want)
+    table, lens = ints(9, 2, -1).view(1, 3).repeat(2, 1), ints(20, 0)
+    pool.fork(table, lens, ints(0), ints(1), ints(11))
+    want[11] = want[2]
+    assert torch.equal(far.cpu(), want) and table.tolist() == [[9, 2, -1], [9, 11, -1]] and lens.tolist() == [20, 20]
+    assert pool.compact(table, lens).tolist() == [3] and table.tolist() == [[0, 2, -1], [0, 1, -1]]
+    want[0], want[1] = want[9].clone(), want[11].clone()
+    assert torch.equal(far.cpu(), want)
+    pool.device_error()
 
 
 def test_entries_past_the_last_page_are_reported(q4):
@@ -270,14 +292,12 @@ def test_entries_past_the_last_page_are_reported(q4):
     used = {3} | {x for b in (1, 2) for x in p.rows[b]}
     ids, count = p.pool.free(p.table, p.lens)
     assert ids.tolist()[:count.item()] == [i for i in range(64) if i not in used]
-    with pytest.raises(q4.GPTQ4Error):
-        p.pool.device_error()
+    assert refused(q4, p.pool.device_error)
     p.pool.device_error()
     out = p.table.clone()
     assert p.pool.compact(p.table, p.lens, out).tolist() == [len(used)]
     assert out[0, :2].tolist() == [-1, -1] and out[0, 2] >= 0
-    with pytest.raises(q4.GPTQ4Error):
-        p.pool.device_error()
+    assert refused(q4, p.pool.device_error)
 
 
 def test_empty_batch_and_captured_graph(q4):
@@ -289,6 +309,7 @@ def test_empty_batch_and_captured_graph(q4):
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     out = torch.empty_like(p.table)
+    gc.collect()
     with torch.cuda.stream(side):
         p.pool.free(p.table, p.lens)
         torch.cuda.synchronize()
