@@ -172,16 +172,16 @@ __global__ void __launch_bounds__(kThreads, 4) copy_kernel(PagesView v, const in
 }
 
 // CTAs (x, i): fork i, its chunks x, x + gridDim.x, ..; x = 0 writes the row.
-// Each finds out for itself whether the fork is to be done, from what no CTA writes: rows of
-// parents are not written, since no child is a parent.
+// Each finds out for itself whether the fork is to be done, from what no CTA writes: rows and
+// lengths of parents are not written, since no child is a parent.
 __global__ void __launch_bounds__(kThreads, 5)
     fork_kernel(PagesView v, PageRows r, const int32_t *parent, const int32_t *child, const int32_t *fresh, int n) {
     __shared__ int s_sum[kThreads / 32];
     const int i = blockIdx.y, p = parent[i], c = child[i];
     if (p < 0 || c < 0 || p == c) return;
     const bool rows_ok = p < r.batch && c < r.batch;
-    const int64_t len = rows_ok ? r.kv_len[p] : 0;
-    bool ok = rows_ok && len >= 0 && len <= static_cast<int64_t>(r.width) * v.page_size;
+    const int64_t len = rows_ok ? r.kv_len[p] : 0, most = static_cast<int64_t>(r.width) * v.page_size;
+    bool ok = rows_ok && len >= 0 && len <= most;
     const int64_t last = len / v.page_size;
     const bool part = ok && len % v.page_size;
     const int from = part ? r.table[p * r.stride + last] : 0, to = part ? fresh[i] : 0;
@@ -194,7 +194,11 @@ __global__ void __launch_bounds__(kThreads, 5)
                 clash |= pk >= 0 && pk == ck && pk == c;             // a row that is to stay
                 continue;
             }
-            clash |= pk == c || (k < i && (ck == c || (part && fresh[k] == to)));
+            clash |= pk == c || (k < i && ck == c);
+            if (part && k < i && fresh[k] == to && pk < r.batch) {   // an earlier fork's, if that needs one
+                const int64_t lk = r.kv_len[pk];
+                clash |= lk >= 0 && lk <= most && lk % v.page_size != 0;
+            }
         }
     if (sum_all(clash, s_sum)) ok = false;
     if (!ok) {

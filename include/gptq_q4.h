@@ -730,12 +730,14 @@ int gptq_q4_pages_free_list(gptq_q4_pages h, const gptq_q4_rows *rows, int windo
 /* Rows child[i] become copies of rows parent[i], i < n: the entries up to the
  * parent's length (-1 past them) and the length.  A page that the parent has
  * filled in part is not shared: its contents go to page fresh[i] in every
- * buffer, and the child's entry is fresh[i] (not read where the length is a
- * multiple of page_size).  A negative parent or child, or parent = child, is
- * no fork.  Left out, and reported by gptq_q4_pages_device_error: a fork whose
- * row numbers, parent's length or pages are outside their range, whose child
- * is the parent of another or the child of an earlier one, or whose fresh page
- * is that of an earlier one.  fresh pages have to be free.  parent, child, fresh:
+ * buffer, and the child's entry is fresh[i] (which may be anything where the
+ * length is a multiple of page_size).  A negative parent or child, or parent =
+ * child, is no fork.  Left out, and reported by gptq_q4_pages_device_error: a
+ * fork whose row numbers, parent's length or pages are outside their range,
+ * whose child is the parent of another, is to stay (parent = child elsewhere)
+ * or is the child of an earlier one, or whose fresh page an earlier one needs
+ * (with a parent's number and length in their range).  fresh pages have to be
+ * free.  parent, child, fresh:
  * device int32 [n], n at most 4096.  Errors: INVALID_ARGUMENT, UNSUPPORTED (n),
  * CUDA_ERROR. */
 int gptq_q4_pages_fork(gptq_q4_pages h, const gptq_q4_rows *rows, const int32_t *parent, const int32_t *child,
