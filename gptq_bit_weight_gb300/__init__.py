@@ -472,17 +472,21 @@ _kept = []             # (free, handle) of handles given up while a stream was c
 
 
 def _release(free=None, handle=None) -> None:
-    """Free a handle, and those kept so far.  Freeing synchronizes, which ends
-    a capture with an error; the collector may drop a handle at any line, so
-    one given up while the current stream is captured is kept until the next
-    is made or given up outside a capture."""
+    """Free a handle, and those kept so far.  The collector may drop a handle
+    at any line; one given up while the current stream is captured, whose
+    calls so far may be of the capture, is kept until the next is made or
+    given up outside a capture.  Freeing itself ends no capture, of this
+    thread or another."""
     if free is not None:
         _kept.append((free, handle))
     torch = sys.modules.get("torch")
     if torch is not None and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
         return
-    while _kept:
-        free, handle = _kept.pop()
+    while True:
+        try:
+            free, handle = _kept.pop()
+        except IndexError:               # empty, or another thread has taken the last
+            return
         free(handle)
 
 

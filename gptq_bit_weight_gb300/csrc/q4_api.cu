@@ -110,24 +110,20 @@ int dev_alloc(T **p, size_t count, gptq_q4_s *h, const char *what) {
 
 void release(gptq_q4_s *h) {
     if (!h) return;
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (h->device >= 0) cudaSetDevice(h->device);
-    cudaDeviceSynchronize();
+    const q4::FreeScope scope(h->device);
+    cudaFree(h->status);                                  // the first: see FreeScope
     cudaFree(h->wp);
     cudaFree(h->s2);
     cudaFree(h->zeros);
     cudaFree(h->perm);
     cudaFree(h->inv8);
     cudaFree(h->bias_store);
-    cudaFree(h->status);
     cudaFree(h->ws);
     cudaFree(h->tickets);
     cudaFree(h->temp_state);
     cudaFree(h->rowscale);
     cudaFree(h->part);
     q4::api_free_retired(h->retired);
-    if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
 

@@ -107,16 +107,12 @@ q4::Cache4 cache_view(const gptq_q4_cache4 *c) {
 
 void release(gptq_q4_attn_s *h) {
     if (!h) return;
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (h->device >= 0) cudaSetDevice(h->device);
-    cudaDeviceSynchronize();
+    const q4::FreeScope scope(h->device);
+    cudaFree(h->status);                                  // the first: see FreeScope
     cudaFree(h->rope);
     q4::api_free_retired(h->retired);
-    cudaFree(h->status);
     cudaFree(h->ws);
     cudaFree(h->tickets);
-    if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
 

@@ -1,5 +1,7 @@
 // The handle behind gptq_q4_handle, shared by the C-ABI translation units.
 #pragma once
+#include <cuda_runtime.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -14,6 +16,28 @@ struct Retired {
         void *p;
         Node *next;
     } *head = nullptr;
+};
+
+// For a scope that frees a handle, which may be in a thread that captures a stream, or beside one that does.  In the
+// relaxed mode a capture goes on past cudaFree; cudaDeviceSynchronize would end any capture of the device, in every mode.
+// cudaFree of memory from cudaMalloc waits for all kernels in flight, of memory from cudaMallocAsync it does not: the
+// status word, which every handle has from cudaMalloc, goes first.
+class FreeScope {
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+    int device_ = -1;
+
+public:
+    explicit FreeScope(int device) {
+        cudaThreadExchangeStreamCaptureMode(&mode_);
+        cudaGetDevice(&device_);
+        if (device >= 0) cudaSetDevice(device);
+    }
+    ~FreeScope() {
+        if (device_ >= 0) cudaSetDevice(device_);
+        cudaThreadExchangeStreamCaptureMode(&mode_);
+    }
+    FreeScope(const FreeScope &) = delete;
+    FreeScope &operator=(const FreeScope &) = delete;
 };
 }  // namespace q4
 

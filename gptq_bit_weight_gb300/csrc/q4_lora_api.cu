@@ -39,17 +39,13 @@ int check(gptq_q4_lora h) {
 
 void release(gptq_q4_lora_s *h) {
     if (!h) return;
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (h->device >= 0) cudaSetDevice(h->device);
-    cudaDeviceSynchronize();
+    const q4::FreeScope scope(h->device);
+    cudaFree(h->status);                                  // the first: see FreeScope
     cudaFree(h->a);
     cudaFree(h->b);
     cudaFree(h->slot);
-    cudaFree(h->status);
     cudaFree(h->t);
     q4::api_free_retired(h->retired);
-    if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
 

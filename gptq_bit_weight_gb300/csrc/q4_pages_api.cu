@@ -61,15 +61,11 @@ q4::PageRows rows_view(const gptq_q4_rows *r, int window, int sinks) {
 
 void release(gptq_q4_pages_s *h) {
     if (!h) return;
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (h->device >= 0) cudaSetDevice(h->device);
-    cudaDeviceSynchronize();
+    const q4::FreeScope scope(h->device);
+    cudaFree(h->view.status);                                  // the first: see FreeScope
     cudaFree(h->chunk);
     cudaFree(h->view.used);
     cudaFree(h->view.rank);
-    cudaFree(h->view.status);
-    if (cur >= 0) cudaSetDevice(cur);
     delete h;
 }
 

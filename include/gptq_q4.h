@@ -395,8 +395,8 @@ int gptq_q4_info(gptq_q4_handle h, int *K, int *N, int *groupsize, int *G,
  * a failed internal check), else GPTQ_Q4_OK.  Clears the word. */
 int gptq_q4_device_error(gptq_q4_handle h);
 
-/* Release everything the handle owns (synchronizes its device).  NULL is a
- * no-op.  Lifecycle only; the pages' nearest passage is "Inference
+/* Release everything the handle owns (waits for its device; ends no stream
+ * capture).  NULL is a no-op.  Lifecycle only; the pages' nearest passage is "Inference
  * Backends", "Runtime cache lifetime" (native runtime storage belongs to the
  * handle, and nothing outlives it). */
 void gptq_q4_free(gptq_q4_handle h);
