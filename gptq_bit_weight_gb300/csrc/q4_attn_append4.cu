@@ -8,13 +8,22 @@
 // to even of (x - m) / s.
 //   A code changes where (x - m) / s passes a half, so what goes in has to be the
 //   same number wherever it is computed: the rotation carries the errors of its
-//   two products and of their sum (fma and two-sum), so that its fp32 result is
-//   the exact one rounded once; and the quotient is corrected by its remainder,
-//   one exact fma.
+//   two products and of their sum (Dekker's and Knuth's, by fma and two-sum), so
+//   that its fp32 result is the exact one rounded once; the quotient is corrected
+//   by its remainder, one exact fma (Markstein's); and a difference that fp32
+//   cannot hold keeps its error.
+//   That error says something only where the rounded difference is a half step
+//   h s exactly: h s has at most 16 bits, so rounding to fp32 keeps the order of
+//   x - m and h s otherwise.  fp32 loses bits of x - m if one of the two is below
+//   2^-13 of the difference (2^-16 in bf16).  A tiny m is seen at once; where x
+//   is tiny and x - m a half step, -m / s is within 2^-13 of a half.  Groups of
+//   either sort go through code that compares with the error, and so does the
+//   span's, which decides where a fifteenth of the rounded span is exact (prompts
+//   84 -> 87 us).
 // A work item has 16 elements of a head.  A key's pairs (i, i + rot / 2) come from
 // two places, so the rotated elements go through shared memory, after which an
 // item holds 16 neighbours and a group is 2 or 4 lanes.
-// Three prompts of 9912 tokens, 96 heads of 128: 84 us, 4.5 TB/s, issue slots 60%
+// Three prompts of 9912 tokens, 96 heads of 128: 87 us, 4.4 TB/s, issue slots 60%
 // busy (a code at a time, with its border looked at, 137); 64 single tokens of 80
 // heads 8 us with the launch.  Reading the prompts' tokens back: 37 us, 5.4 TB/s.
 #include <algorithm>
@@ -71,10 +80,41 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// What the rounded difference d of x and y lacks, exactly (two-sum).
+__device__ __forceinline__ float lost(float x, float y, float d) {
+    const float b = __fsub_rn(d, x);
+    return __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(y, b));
+}
 // x / 15, rounded once, for x >= 1e-30: the product with the rounded reciprocal, corrected by its remainder.
 __device__ __forceinline__ float fifteenth(float x) {
     const float r = 1.f / 15.f, q = __fmul_rn(x, r);
     return __fmaf_rn(__fmaf_rn(-q, 15.f, x), r, q);
+}
+
+// Codes of sixteen 16-bit values, and s and m, of a group from lo to hi, whatever the differences lack in fp32.  Not
+// inlined: few groups come here.
+template <bool BF>
+__device__ __noinline__ uint3 quantise_exactly(uint4 v0, uint4 v1, float lo, float hi) {
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    const float span = __fsub_rn(hi, lo), rest = lost(hi, lo, span);
+    const bool small = span < 1e-30f;
+    float part = small ? __fdiv_rn(span, 15.f) : fifteenth(span);
+    // A fifteenth without remainder ends in three zeros or more, so one unit up or down passes no border of the type and
+    // leaves one that it stands on, to the side of what the span lacks.
+    if (rest != 0.f && __fmaf_rn(-part, 15.f, span) == 0.f) part = __int_as_float(__float_as_int(part) + (rest > 0.f ? 1 : -1));
+    const uint32_t sm = pack2<BF>(part, lo);
+    const float up = small ? 0x1p64f : 1.f, s = unpack2<BF>(sm).x * up, inv = s > 0.f ? __fdividef(1.f, s) : 0.f;  // in range
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float2 f = unpack2<BF>(w[e >> 1]);
+        const float x = e & 1 ? f.y : f.x, d0 = __fsub_rn(x, lo), d = d0 * up, k = fminf(floorf(d * inv), 15.f);
+        const float past = __fmaf_rn(-(k + 0.5f), s, d) + lost(x, lo, d0) * up;     // of the half after k
+        const int n = static_cast<int>(k);
+        const int code = s > 0.f ? min(n + (past > 0.f || (past == 0.f && (n & 1))), 15) : 0;
+        c[e >> 3] |= static_cast<uint32_t>(code) << (4 * ((e & 7) >> 1) + 16 * (e & 1));
+    }
+    return make_uint3(c[0], c[1], sm);
 }
 
 // Sixteen 16-bit values in two vectors -> their codes; s and m of the group (`lanes` lanes).
@@ -89,23 +129,29 @@ __device__ __forceinline__ uint2 quantise(const uint4 &v0, const uint4 &v1, int 
     }
     uint32_t ends = min_2<BF>(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));     // (least, -greatest)
     for (int o = 1; o < lanes; o <<= 1) ends = min_2<BF>(ends, __shfl_xor_sync(mask, ends, o));
-    const float lo = unpack2<BF>(ends).x, span = __fsub_rn(-unpack2<BF>(ends).y, lo);
+    const float lo = unpack2<BF>(ends).x, hi = -unpack2<BF>(ends).y, span = __fsub_rn(hi, lo);
     if (!(span < INFINITY)) {
         const float nan = __int_as_float(0x7fffffff);
         sm = pack2<BF>(nan, nan);
         return make_uint2(0, 0);
     }
-    const bool small = span < 1e-30f;
-    sm = pack2<BF>(small ? __fdiv_rn(span, 15.f) : fifteenth(span), lo);
+    sm = pack2<BF>(fifteenth(span), lo);
     const float step = unpack2<BF>(sm).x, by = __fdividef(1.f, step);
+    constexpr float kRound = 12582912.f;
+    // Whether fp32 may lack bits of a difference that matter: beside a tiny end (15 steps are the span but for the step's
+    // rounding; a greatest element only bears on the step, whose borders bf16's spans miss), or where 0 is near a half
+    // step.  A step of 0 makes `off` NaN.
+    const float low = (BF ? 15.125f * 0x1p-16f : 15.125f * 0x1p-13f) * step;
+    const float to0 = __fmaf_rn(-lo, by, -0.5f), off = __fsub_rn(to0, __fsub_rn(__fadd_rn(to0, kRound), kRound));
+    const bool whole = span >= 1e-30f && (lo == 0.f || fabsf(lo) >= low) && (BF || hi == 0.f || fabsf(hi) >= low) &&
+                       fabsf(off) > (BF ? 0x1p-12f : 0x1p-9f);
     // d / s to its last bit, the approximate quotient corrected by its remainder, so that a half is a half (in bf16 every
     // other warp has one); to the nearest by adding 1.5 2^23.  Four codes of a half word add up in fp32 as digits of base
     // 16.
-    constexpr float kRound = 12582912.f;
     const uint64_t least2 = pair(-lo, -lo), by2 = pair(by, by), step2 = pair(-step, -step), round2 = pair(kRound, kRound);
     const uint64_t back2 = pair(-kRound, -kRound), base2 = pair(16.f, 16.f), whole2 = pair(8388608.f, 8388608.f);
     uint32_t c[2];
-    float last = 0.f;
+    float last = whole ? 0.f : 16.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint64_t sum = 0;
@@ -121,20 +167,11 @@ __device__ __forceinline__ uint2 quantise(const uint4 &v0, const uint4 &v1, int 
         const float2 digits = unpair(add2(sum, whole2));
         c[h] = __byte_perm(__float_as_uint(digits.x), __float_as_uint(digits.y), 0x5410);
     }
-    if (!small && step > 0.f && last <= 15.f) return make_uint2(c[0], c[1]);
-    // values past the last code (of a step that is a multiple of the type's least number), the smallest steps and none
-    const float up = small ? 0x1p64f : 1.f, s = step * up, inv = s > 0.f ? __fdividef(1.f, s) : 0.f;   // 1 / s in range
-    c[0] = c[1] = 0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float2 f = unpack2<BF>(w[e >> 1]);
-        const float d = __fsub_rn(e & 1 ? f.y : f.x, lo) * up, k = fminf(floorf(d * inv), 15.f);
-        const float past = __fmaf_rn(-(k + 0.5f), s, d);                 // of the half after k
-        const int n = static_cast<int>(k);
-        const int code = s > 0.f ? min(n + (past > 0.f || (past == 0.f && (n & 1))), 15) : 0;
-        c[e >> 3] |= static_cast<uint32_t>(code) << (4 * ((e & 7) >> 1) + 16 * (e & 1));
-    }
-    return make_uint2(c[0], c[1]);
+    if (last <= 15.f) return make_uint2(c[0], c[1]);
+    // also values past the last code (of a step that is a multiple of the type's least number), the smallest steps and none
+    const uint3 r = quantise_exactly<BF>(v0, v1, lo, hi);
+    sm = r.z;
+    return make_uint2(r.x, r.y);
 }
 
 template <bool BF>
