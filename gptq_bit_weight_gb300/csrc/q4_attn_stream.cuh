@@ -6,9 +6,11 @@
 // two of 131071 and about 100000: 103 us, 6.3 TB/s; one of 777, 32 heads: 11
 // us, latency (lengths, page table, keys, the join of the pieces).
 //
-//   scores s = scale log2(e) q . k in fp32; running maximum m and sum l,
+//   scores s = scale log2(e) q . k in fp32; reference m and sum l,
 //   p = 2^(s - m) rounded to 16 bits for its product with v (l sums the
-//   unrounded ones), o = sum p v in fp32; o / l rounded once.
+//   unrounded ones), o = sum p v in fp32; o / l rounded once.  m is the running
+//   maximum, in fp16 less weight_lift, so that a long tail far below it is not
+//   lost beside l.
 //   One 16-bit part of p, as in the kernel for chunks, where a second would cost:
 //   either kernel rounds alike.  The result's error against 64 bits is 1.04 to
 //   1.08 times that of rounding the exact result (relative, bf16 1.7e-3, fp16
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
                     top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-                    top[h] = fmaxf(top[h], m[h]);
+                    top[h] = fmaxf(top[h] - weight_lift<BF>, m[h]);
                     keep[h] = ex2(m[h] - ref_of(top[h]));
                     m[h] = top[h];
                 }

@@ -5,9 +5,10 @@
 //
 //   scores s = scale log2(e) q . k in fp32; reference m and sum l of each row,
 //   p = 2^(s - m) rounded to 16 bits for its product with v (l sums the
-//   unrounded ones), o = sum p v in fp32; o / l rounded once.  m is raised only
-//   when a score is more than 2^8 above it: any m gives the same result as long
-//   as p fits 16 bits.
+//   unrounded ones), o = sum p v in fp32; o / l rounded once.  m is the greatest
+//   score, in fp16 less weight_lift, and is raised only when a score is more than
+//   2^8 above that: any m gives the same result as long as p fits 16 bits at both
+//   ends.
 //
 // Both products are turned round, keys (and the value's elements) as the rows
 // of the MMA and the query rows as its columns: eight of them fill a tile,
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
             float top = -INFINITY;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) top = max3(max3(top, x[b][0], x[b][1]), x[b][2], x[b][3]);
-            if (__any_sync(0xffffffffu, top > kRescale || unseen[0] || unseen[1])) {
+            if (__any_sync(0xffffffffu, top > kRescale + weight_lift<BF> || unseen[0] || unseen[1])) {
                 float keep[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) attend_stream4_kernel(Args a) 
                     for (int b = 0; b < kBlocks; ++b) high = max3(high, x[b][c], x[b][c + 2]);
                     high = max_g(high);
                     // to the greatest so far; a row's first token sets it, up or down
-                    const float up = high == -INFINITY ? 0.f : unseen[c] ? high : fmaxf(high, 0.f);
+                    const float over = high - weight_lift<BF>, up = high == -INFINITY ? 0.f : unseen[c] ? over : fmaxf(over, 0.f);
                     keep[c] = unseen[c] ? 1.f : ex2(-up);
                     unseen[c] = unseen[c] && high == -INFINITY;
                     ref[c] += up;

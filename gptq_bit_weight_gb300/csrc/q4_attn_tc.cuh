@@ -6,7 +6,8 @@
 //   with v (l sums the unrounded ones); o = sum p v in fp32; o / l rounded
 //   once.  m is the maximum of the row's first key tile, and is raised to a
 //   later tile's only when that is more than 2^8 away: any m gives the same
-//   result as long as p fits 16 bits, so most tiles rescale no output.
+//   result as long as p fits 16 bits at both ends, so most tiles rescale no
+//   output.  In fp16 p is 2^weight_lift of that.
 //   The tensor cores take 16-bit operands: p in two parts would be half as much
 //   again of the whole work.  In one, the result's error against 64 bits is 1.4
 //   times that of rounding the exact result (relative, 512 tokens over 8192:
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(threads_of(FOUR), 1)
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m * c;
+                    const float ref = m == -INFINITY ? 0.f : fmaf(m, c, -weight_lift<BF>);
                     const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll

@@ -8,6 +8,13 @@ namespace q4 {
 
 constexpr int kKtLog2 = 7, kKt = 1 << kKtLog2;   // tokens of a key tile
 
+// log2 of the weight that a score at the reference gets, the same everywhere, so that it cancels in o / l.  Weights are
+// rounded to the cache's type for their product with the values while l sums them unrounded: in fp16 one below 2^-25 is
+// none, and 2^17 tokens 2^-25.5 below a dominant one would be lost from o (0.28% of l).  At 2^7 a weight is off by 2^-32 of
+// the reference's at most; the kernels that let weights grow by 2^8 past it then reach 2^15.  bf16 has fp32's range.
+template <bool BF>
+constexpr float weight_lift = BF ? 0.f : 7.f;
+
 // One lane of a converged warp.  The compiler knows a region behind it to be
 // one thread's, so the operands of tcgen05.mma and of TMA copies go to uniform
 // registers directly.  Behind a test of the lane number, or issued by many
