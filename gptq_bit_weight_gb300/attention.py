@@ -195,7 +195,7 @@ class PagedAttention:
         """Attention of the new tokens' queries q [tokens, q_heads, head_dim]
         over the cache, a PagedCache or PagedCache4; scale defaults to
         head_dim ** -0.5, window 0 is none; with a window, the first `sinks`
-        tokens of each context stay visible."""
+        tokens of each context stay visible, at their positions in the text."""
         self._check(cache, batch)
         x, rows, xs = self._token_rows(q, "q", self.q_heads)
         if out is None:

@@ -618,7 +618,9 @@ int gptq_q4_attn_attend(gptq_q4_attn h, const void *q, int64_t q_stride, const g
                         cudaStream_t stream);
 
 /* gptq_q4_attn_attend with the first `sinks` tokens of each context visible
- * besides the window: token j <= i is seen if j > i - window or j < sinks.
+ * besides the window: token j <= i is seen if j > i - window or j < sinks.  Keys
+ * stay as they were appended, rotated to their positions in the text: the first
+ * tokens are not moved up to the window.
  * Pages that hold neither a token below `sinks` nor one of a window are not
  * read, and their table entries may be anything.  sinks = 0, or window = 0
  * (all tokens are visible), is gptq_q4_attn_attend.  The sums, and their
@@ -662,12 +664,16 @@ typedef struct {
     int group;
 } gptq_q4_cache4;
 
-/* gptq_q4_attn_append into a cache of 4 bits.  Keys are rotated and rounded to
- * the handle's type (in enough precision that the rounding is of the exact
- * products' sum) and values taken as they are; then for each group
+/* gptq_q4_attn_append into a cache of 4 bits.  Keys are rotated (the exact sum
+ * of products with the fp32 cosines and sines, rounded to fp32 and from there to
+ * the handle's type) and values taken as they are; then for each group
  *   m = the least element,  s = (greatest - m) / 15 rounded to the type,
  *   c = (x - m) / s rounded to the nearest (ties to even), at most 15;  0 where s is 0.
- * A group with an infinity or NaN, or whose span is past fp32, reads as NaN throughout. */
+ * all of them of the exact differences and quotients.  A group with an infinity
+ * or NaN, or whose span is past fp32, reads as NaN throughout.  A rounded step
+ * may be too large by 2^-11 of itself (bf16: 2^-8), so the greatest elements of
+ * a group whose greatest + 2^-11 (2^-8) * (greatest - m) is past the type's
+ * largest number may read as infinity (fp16: 0 and 65504; 15 * 4368 = 65520). */
 int gptq_q4_attn_append4(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, const gptq_q4_cache4 *cache,
                          const gptq_q4_batch *batch, const int32_t *positions, void *q_out, int64_t q_stride,
                          cudaStream_t stream);

@@ -113,3 +113,35 @@ def test_differences_that_do_not_fit_fp32(q4, group, dtype):
             got = params[:, side].reshape(-1, 2)[i]
             assert (Fraction(float(got[0])), Fraction(float(got[1]))) == (s, m), (i, groups[i], got)
             assert c[i].tolist() == [code[j] for j in way.tolist()], (i, s, m)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64])
+def test_which_finite_groups_read_back_finite(q4, group, dtype):
+    """Those whose greatest element and the step's rounding, u of the span at most, stay within the type; past it the
+    greatest may be infinite, as zeros and the largest fp16 number are.  Spans that fp32 has."""
+    D, page = 128, 16
+    big, u = Fraction(torch.finfo(dtype).max), Fraction(1, 2 ** BITS[dtype][0])
+    r = random.Random(3)
+    groups = []
+    for i in range(400):
+        lo = nearest(big * Fraction(r.uniform(-0.99, 0.99)), dtype)
+        hi = nearest((big + u * lo) / (1 + u), dtype)
+        while hi + u * (hi - lo) > big or hi - lo > Fraction(torch.finfo(torch.float32).max):
+            hi -= unit(hi, dtype)
+        groups.append([lo, hi] + [max(lo, nearest(lo + (hi - lo) * Fraction(r.random()), dtype)) for _ in range(group - 2)])
+    groups.append([Fraction(0), Fraction(65504)] * (group // 2))
+    per = D // group
+    T = -(-len(groups) // per)
+    flat = torch.tensor([[float(v) for v in g] for g in groups], dtype=torch.float64).to(dtype)
+    flat = torch.cat([flat, torch.zeros(T * per - len(groups), group, dtype=dtype)])
+    x = torch.zeros(T, 3, D, dtype=dtype)
+    x[:, 1] = x[:, 2] = flat.view(T, D)
+    step = Step(q4, [(T, T)], 1, D, page, dtype, group, seed=2)
+    att = q4.PagedAttention(1, 1, D, page, dtype=dtype)
+    att.append(x.view(T, -1).to(DEV), step.cache, step.batch)
+    for got in att.read(step.cache, step.batch):
+        got = got.cpu().reshape(-1, group)[:len(groups)]
+        assert torch.isfinite(got[:-1]).all()
+        assert torch.isinf(got[-1]).any() == (dtype == torch.float16)
+    att.device_error()
