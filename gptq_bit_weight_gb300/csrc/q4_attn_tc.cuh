@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(threads_of(FOUR), 1)
                             }
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : fmaf(m, c, -weight_lift<BF>);
+                    // (upwards in fp16, so that no weight is past 2^(kRescale + weight_lift), however large the scores)
+                    const float ref = m == -INFINITY ? 0.f : BF ? m * c : __fmaf_ru(m, c, -weight_lift<BF>);
                     const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
                     uint64_t sum[2] = {0, 0};
 #pragma unroll

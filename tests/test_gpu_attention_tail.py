@@ -68,3 +68,35 @@ def test_a_tail_below_a_dominant_key(q4, group, D, max_q, window, at, dtype):
     assert float(o.min()) > 20 * float(tol.max() - (o * U[dtype]).max())        # the tail is there to be seen
     err = (got.view(n, ql, Hq, D) - o).abs() / tol
     assert bool((err <= 1).all()), f"worst error / tolerance {float(err.max()):.3f}"
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("max_q", [1, 100000], ids=["stream", "chunk"])
+@pytest.mark.parametrize("step", [4, 8, 32])
+@pytest.mark.parametrize("group", [32, None], ids=["4bit", "16bit"])
+def test_weights_stay_finite_under_huge_scores(q4, group, step, max_q, dtype):
+    """Scores of about 2^25 that rise a little every other tile: fp32 holds them in steps of 4, so a reference may be off
+    by units of the exponent.  Whatever the weights are then, the result lies between the values."""
+    kv, H, D, page, n, ql = 1024, 16, 64, 64, 160, 2                  # an item whole, or nearly so, in a CTA
+    k, v = torch.zeros(kv, 1, D), 0.5 + 0.5 * torch.rand(kv, 1, 1, generator=torch.Generator().manual_seed(2)).expand(kv, 1, D)
+    k[:, :, 0] = 4096
+    k[:, :, 32] = (torch.arange(kv) // 256 * step / 4)[:, None]       # a group of its own
+    k, v = k.to(dtype), v.to(dtype)
+    if group:
+        kc, vc = quantise(k, group), quantise(v, group)
+        cache = q4.PagedCache4(record(kc, vc).view(kv // page, page, 1, -1).transpose(1, 2).contiguous().to(DEV), D, group, dtype)
+        v = values(*vc)
+    else:
+        cache = q4.PagedCache(*(t.reshape(kv // page, page, 1, D).transpose(1, 2).contiguous().to(DEV) for t in (k, v)))
+    q = torch.zeros(n * ql, H, D)
+    q[:, :, 0] = 8192 + 64 * (torch.arange(n * ql * H) % 61).view(n * ql, H)
+    q[:, :, 32] = 4
+    i32 = dict(dtype=torch.int32, device=DEV)
+    att = q4.PagedAttention(H, 1, D, page, dtype=dtype)
+    batch = q4.PagedBatch(torch.arange(n + 1, **i32) * ql, torch.full((n,), kv, **i32), torch.arange(kv // page, **i32).repeat(n, 1),
+                          tokens=n * ql, max_q=max_q)
+    for scale in (1.366, 1.0, 0.5):
+        got = att.attend(q.to(dtype).to(DEV), cache, batch, scale=scale).float().cpu()
+        edge = 1 + 4 * U[dtype]
+        assert bool(((got >= float(v.min()) / edge) & (got <= float(v.max()) * edge)).all()), scale
+    att.device_error()
