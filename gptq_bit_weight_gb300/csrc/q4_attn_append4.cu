@@ -23,9 +23,10 @@
 // A work item has 16 elements of a head.  A key's pairs (i, i + rot / 2) come from
 // two places, so the rotated elements go through shared memory, after which an
 // item holds 16 neighbours and a group is 2 or 4 lanes.
-// Three prompts of 9912 tokens, 96 heads of 128: 87 us, 4.4 TB/s, issue slots 60%
-// busy (a code at a time, with its border looked at, 137); 64 single tokens of 80
-// heads 8 us with the launch.  Reading the prompts' tokens back: 37 us, 5.4 TB/s.
+// Three prompts of 9912 tokens, 96 heads of 128: 87 us, 4.4 TB/s, issue slots 58%
+// busy, bound by the latency of a token's loads and what follows them (a code at a
+// time, with its border looked at, 137); 64 single tokens of 80 heads 8 us with the
+// launch.  Reading the prompts' tokens back: 37 us, 5.4 TB/s.
 #include <algorithm>
 #include <cstdint>
 

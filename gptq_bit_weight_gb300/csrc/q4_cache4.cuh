@@ -5,9 +5,9 @@
 // A word of eight codes has code e at bit 4 (e / 2) + 16 (e % 2), so that
 // word >> 4 i masked by 0x000f000f holds codes 2 i and 2 i + 1 in its two
 // 16-bit halves, in the order that every operand wants them.  A code becomes a
-// 16-bit float without a conversion: as bits of the mantissa of a power of two
-// whose unit they are there, from which that power is then taken away, exactly;
-// m + s c is one fma, rounded once.
+// 16-bit float without a conversion, in the way that is usual for weights of few
+// bits: as bits of the mantissa of a power of two whose unit they are there, from
+// which that power is then taken away, exactly; m + s c is one fma, rounded once.
 #pragma once
 #include "q4_serve.h"
 

@@ -600,8 +600,9 @@ int gptq_q4_attn_append(gptq_q4_attn h, const void *qkv, int64_t qkv_stride, con
  *           out_stride; 16-byte aligned, strides multiples of 8, not overlapping
  * Cache slots past kv_len (and pages before the window) are not part of any
  * result, whatever they hold.  Scores, softmax and sums are fp32; each
- * weight p is rounded to 16 bits for its product with v; the output is
- * rounded once.  Rows that no request owns are left alone.  The order of the
+ * weight p is rounded to 16 bits for its product with v (in fp16 one far below
+ * the row's largest is off by at most 2^-32 of that); the output is rounded
+ * once.  Rows that no request owns are left alone.  The order of the
  * sums depends on the lengths of the whole batch, not on timing: the same
  * call gives the same bits.  A NaN or infinity in a key reaches the rows that
  * see it.  One in a value reaches those, and may reach new tokens of the same
