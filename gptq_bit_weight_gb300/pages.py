@@ -73,7 +73,8 @@ class PagePool:
     def fork(self, table, kv_len, parent, child, fresh) -> None:
         """Make rows child[i] of table and kv_len forks of rows parent[i]: they
         share full pages, and a partly filled last page is copied to page
-        fresh[i] in every cache.  Negative numbers are no fork."""
+        fresh[i] in every cache (else fresh[i] may be anything).  Negative
+        numbers are no fork."""
         rows = self._rows(table, kv_len)
         n = parent.numel()
         _check(_fork(self.handle, ctypes.byref(rows), self._ints(parent, "parent", n), self._ints(child, "child", n),
